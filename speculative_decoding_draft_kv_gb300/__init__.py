@@ -2,8 +2,9 @@
 
 The computation lives in the CUDA library ``_lib/libdflash_ring.so`` behind the C ABI of
 ``include/dflash_ring.h``; :mod:`.ring` is the thin binding with the same names, and
-:mod:`.build` compiles the library.  Importing this package does not load the library;
-the first call into :mod:`.ring` does, and fails loudly if it was not built.
+:mod:`.build` compiles the library.  :mod:`.paged` binds the operators over a paged cache
+(``include/dflash_paged.h``, the same library).  Importing this package does not load the
+library; the first call into :mod:`.ring` or :mod:`.paged` does, and fails loudly if it was not built.
 """
 
 from .ring import (  # noqa: F401
@@ -38,3 +39,15 @@ from .ring import (  # noqa: F401
     ring_set_producer,
     ring_step,
 )
+
+# names of .paged, which needs PyTorch (building and loading the library do not): imported on
+# first use
+_PAGED = ("PagedBatch", "PagedCache", "PagedRope", "paged_append", "paged_attend", "paged_attend_workspace",
+          "paged_device_error", "paged_gather", "paged_last_error", "paged_norm_rope", "rope_frequencies")
+
+
+def __getattr__(name):
+    if name in _PAGED:
+        from . import paged
+        return getattr(paged, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

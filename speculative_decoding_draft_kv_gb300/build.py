@@ -22,7 +22,8 @@ LIB_NAME = "libdflash_ring.so"
 LIB_PATH = os.path.join(LIB_DIR, LIB_NAME)
 
 SOURCES = ["ring_host.cu", "ring_kernels.cu", "attn_kernels.cu", "step_kernels.cu",
-           "static_attend.cu", "produce_kernels.cu", "produce_tc.cu"]
+           "static_attend.cu", "produce_kernels.cu", "produce_tc.cu", "paged_host.cu",
+           "paged_rows.cu", "paged_attend_f16.cu", "paged_attend_bf16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
@@ -49,7 +50,7 @@ def _stale() -> bool:
         return True
     t = os.path.getmtime(LIB_PATH)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    deps.append(os.path.join(INCLUDE, "dflash_ring.h"))
+    deps += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     deps.append(os.path.abspath(__file__))
     return any(os.path.getmtime(f) > t for f in deps if os.path.exists(f))
 

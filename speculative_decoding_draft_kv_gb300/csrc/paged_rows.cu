@@ -1,0 +1,467 @@
+// Head rows on their way into and out of a paged cache: RMS norm and position rotation
+// (paged_norm_rope), the same with quantisation and the scatter into pages (paged_append),
+// and the way back (paged_gather).
+//
+// A row is one head of one token: head_dim values, eight to a lane (16 bytes of a 16-bit
+// type), so 16 lanes hold a row of 128 and a warp two of them.  A warp's task is one token
+// and a run of its query, key or value heads; everything that belongs to the token (its
+// sequence, position, page, and the cosines and sines of its angles) is worked out once per
+// task and serves all the heads of it.
+//
+// Angles: position times frequency, less whole turns.  A frequency is held as turns per
+// position in units of 2^-64, so the product's whole turns fall off the top of a 64-bit
+// integer multiplication, exactly, and float32 sees only the rest (at most half a turn):
+// no float64 and no large arguments, for any position.
+#include "paged.h"
+
+#include <algorithm>
+#include <type_traits>
+
+namespace dflash {
+namespace {
+
+constexpr int kRowThreads = 256;
+
+template <int T> struct RowType;
+template <> struct RowType<PAGED_F16> { using type = __half; };
+template <> struct RowType<PAGED_BF16> { using type = __nv_bfloat16; };
+template <> struct RowType<PAGED_F32> { using type = float; };
+
+// Eight consecutive values as loaded (one or two 16-byte words).
+template <int T> struct Raw8 { uint4 w[T == PAGED_F32 ? 2 : 1]; };
+
+template <int T>
+__device__ __forceinline__ Raw8<T> load8(const void *base, int64_t elem) {
+    Raw8<T> r;
+    const uint4 *p = reinterpret_cast<const uint4 *>(reinterpret_cast<const typename RowType<T>::type *>(base) + elem);
+    r.w[0] = __ldcs(p);
+    if constexpr (T == PAGED_F32) r.w[1] = __ldcs(p + 1);
+    return r;
+}
+
+__device__ __forceinline__ float2 unpack2(uint32_t w, std::integral_constant<int, PAGED_F16>) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w, std::integral_constant<int, PAGED_BF16>) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, std::integral_constant<int, PAGED_F16>) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, std::integral_constant<int, PAGED_BF16>) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+template <int T>
+__device__ __forceinline__ void widen(const Raw8<T> &r, float (&x)[8]) {
+    if constexpr (T == PAGED_F32) {
+        const float *f = reinterpret_cast<const float *>(&r);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = f[e];
+    } else {
+        const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack2(w[e], std::integral_constant<int, T>{});
+            x[2 * e] = f.x;
+            x[2 * e + 1] = f.y;
+        }
+    }
+}
+
+template <int T>
+__device__ __forceinline__ void store8(void *base, int64_t elem, const float (&x)[8]) {
+    uint4 *p = reinterpret_cast<uint4 *>(reinterpret_cast<typename RowType<T>::type *>(base) + elem);
+    if constexpr (T == PAGED_F32) {
+        p[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+        p[1] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+    } else {
+        const std::integral_constant<int, T> t{};
+        *p = make_uint4(pack2(x[0], x[1], t), pack2(x[2], x[3], t), pack2(x[4], x[5], t), pack2(x[6], x[7], t));
+    }
+}
+
+__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 e4m3_unpair(uint32_t codes) {   // low 16 bits
+    uint32_t h;
+    asm("{.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"(codes));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
+// The sequence that row t belongs to (the last s with q_start[s] <= t), and its fields;
+// -1 for a row in front of the first or behind the last sequence.  Lanes take 32 entries
+// at a time, so the loads of a long table do not wait for one another.
+__device__ __forceinline__ int owner_of(const PagedBatchDev &b, int t, int lane) {
+    int count = 0;
+    for (int i = 0; i < b.n_seq; i += 32) {
+        const int v = i + lane < b.n_seq ? b.q_start[i + lane] : 0x7fffffff;
+        count += __popc(__ballot_sync(0xffffffffu, v <= t));
+    }
+    if (count == 0 || t >= b.q_start[b.n_seq]) return -1;
+    return count - 1;
+}
+
+// cos and sin (times the magnitude) of p * turn, turn in 2^-64 turns
+__device__ __forceinline__ float2 turn_cs(int p, uint64_t turn, float magnitude) {
+    const int32_t frac = (int32_t)((uint64_t)(int64_t)p * turn >> 32);   // whole turns gone
+    float sn, cs;
+    sincospif((float)frac * 0x1p-31f, &sn, &cs);
+    return make_float2(cs * magnitude, sn * magnitude);
+}
+
+// Norm and rotation of one row spread over LPR lanes (lane c: values 8c .. 8c+7).
+template <int D>
+struct Turner {
+    static constexpr int LPR = D / 8;
+    float cs[8], sn[8];      // half: of this lane's eight elements; interleaved: of its 4 pairs
+    float w[8];              // norm weights
+    int c, rot, layout, shift;
+    bool norm;
+
+    __device__ void angles(const PagedRowsArgs &a, int p) {
+        rot = a.rot;
+        layout = a.layout;
+        const int e0 = 8 * c, half = rot / 2;
+        shift = 0;
+        if (e0 >= rot) return;
+        if (layout == PAGED_HALF) {
+            const int j = e0 < half ? e0 : e0 - half;
+            shift = e0 < half ? half / 8 : -(half / 8);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float2 r = turn_cs(p, a.turn[j + e], a.magnitude);
+                cs[e] = r.x;
+                sn[e] = r.y;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 r = turn_cs(p, a.turn[e0 / 2 + e], a.magnitude);
+                cs[e] = r.x;
+                sn[e] = r.y;
+            }
+        }
+    }
+    __device__ void weights(const float *wt) {
+        norm = wt != nullptr;
+        if (!norm) return;
+        const float4 a = reinterpret_cast<const float4 *>(wt)[2 * c], b = reinterpret_cast<const float4 *>(wt)[2 * c + 1];
+        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+        w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+    }
+    __device__ __forceinline__ void apply(float (&x)[8], float eps, int lane) const {
+        if (norm) {
+            float ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+            for (int d = LPR / 2; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+            const float inv = rsqrtf(ss * (1.f / D) + eps);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * w[e];
+        }
+        if (rot == 0) return;
+        if (layout == PAGED_HALF) {
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(0xffffffffu, x[e], lane + shift);
+            if (8 * c < rot) {
+                const float sg = shift > 0 ? -1.f : 1.f;     // first half: x cos - y sin
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = fmaf(x[e], cs[e], sg * y[e] * sn[e]);
+            }
+        } else if (8 * c < rot) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float x1 = x[2 * e], x2 = x[2 * e + 1];
+                x[2 * e] = fmaf(x1, cs[e], -x2 * sn[e]);
+                x[2 * e + 1] = fmaf(x1, sn[e], x2 * cs[e]);
+            }
+        }
+    }
+};
+
+// One row's eight values per lane into a page: 16-bit values, or codes with the row's scale.
+template <int T, int LPR>
+__device__ __forceinline__ void store_page(const PagedPool &pool, uint8_t *base, float *scales, int64_t off,
+                                           int64_t soff, int c, bool live, const float (&x)[8]) {
+    if (pool.format == PAGED_F16 || pool.format == PAGED_BF16) {
+        if (live) store8<T>(base, off + 8 * c, x);
+        return;
+    }
+    // the largest magnitude; as integers, magnitudes order as the floats do and NaN is above all
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+#pragma unroll
+    for (int d = LPR / 2; d; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const float full = pool.format == PAGED_INT8 ? 127.f : 448.f;
+    const float amax = __uint_as_float(top);
+    const bool finite = top < 0x7f800000u, any = amax >= 1e-30f;
+    const float inv = finite && any ? full / amax : 0.f;
+    const float scale = !finite ? __int_as_float(0x7fc00000) : (any ? amax / full : 0.f);
+    uint2 w = make_uint2(0u, 0u);
+    if (finite) {
+        if (pool.format == PAGED_INT8) {
+            uint32_t b[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) b[e] = (uint32_t)__float2int_rn(x[e] * inv) & 0xffu;   // |x inv| <= 127 + 2^-16
+            w.x = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
+            w.y = b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24;
+        } else {
+            w.x = e4m3_pair(x[0] * inv, x[1] * inv) | e4m3_pair(x[2] * inv, x[3] * inv) << 16;
+            w.y = e4m3_pair(x[4] * inv, x[5] * inv) | e4m3_pair(x[6] * inv, x[7] * inv) << 16;
+        }
+    }
+    if (live) {
+        *reinterpret_cast<uint2 *>(base + off + 8 * c) = w;
+        if (c == 0) scales[soff] = scale;
+    }
+}
+
+template <int T, int D, bool PAGED>
+__global__ void __launch_bounds__(kRowThreads)
+k_paged_rows(const __grid_constant__ PagedRowsArgs a) {
+    constexpr int LPR = D / 8, RPW = 32 / LPR, U = 4;      // rows a warp step, steps in flight
+    const int lane = threadIdx.x & 31;
+    const int64_t gw = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+    const int tasks = a.cq + a.ck + a.cv;
+    const int64_t t64 = gw / tasks;
+    if (t64 >= a.n_rows) return;
+    const int t = (int)t64;
+    int task = (int)(gw - t64 * tasks);
+    const int kind = task < a.cq ? 0 : (task < a.cq + a.ck ? 1 : 2);
+    task -= kind == 0 ? 0 : (kind == 1 ? a.cq : a.cq + a.ck);
+    const int heads = kind == 0 ? a.nq : (kind == 1 ? a.nk : a.nv);
+    const int h0 = task * a.iters * RPW, h1 = min(heads, h0 + a.iters * RPW);
+    const void *src = kind == 0 ? a.q : (kind == 1 ? a.k : a.v);
+    const int64_t src_hs = kind == 0 ? a.q_hs : (kind == 1 ? a.k_hs : a.v_hs);
+    const int64_t src0 = (int64_t)t * (kind == 0 ? a.q_rs : (kind == 1 ? a.k_rs : a.v_rs));
+    const int sub = lane / LPR, c = lane % LPR;
+
+    // the first rows are on their way while the token's place is looked up
+    Raw8<T> raw[U];
+    auto load = [&](int h) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int hh = h + u * RPW + sub;
+            if (hh < h1) raw[u] = load8<T>(src, src0 + hh * src_hs + 8 * c);
+            else raw[u].w[0] = make_uint4(0, 0, 0, 0);
+        }
+    };
+    load(h0);
+
+    int pos = 0;
+    bool mapped = true;
+    int64_t off = 0, soff = 0;
+    if constexpr (PAGED) {
+        const int s = owner_of(a.batch, t, lane);
+        if (s < 0) return;
+        const PagedSeq q = paged_seq(a.batch, a.pool.page_shift, s);
+        pos = q.kv - q.n + (t - q.row0);
+        const int cap = a.batch.max_pages << a.pool.page_shift;
+        mapped = pos >= 0 && pos < cap && t >= q.row0 && t < q.row0 + q.n && q.ok;
+        if (mapped) {
+            const int page = a.batch.pages[(int64_t)s * a.batch.pages_stride + (pos >> a.pool.page_shift)];
+            const int slot = pos & ((1 << a.pool.page_shift) - 1);
+            mapped = page >= 0 && page < a.pool.n_pages;
+            off = (int64_t)page * a.pool.page_stride + slot * a.pool.row_stride;
+            soff = (int64_t)page * a.pool.s_page_stride + slot;
+        }
+        if (!mapped && lane == 0) atomicOr(a.err, (uint32_t)PAGED_ERR_PAGE);
+    }
+    Turner<D> tr;
+    tr.c = c;
+    tr.norm = false;
+    tr.rot = 0;
+    if (kind < 2) {
+        tr.weights(kind == 0 ? a.q_norm : a.k_norm);
+        if (a.rot) tr.angles(a, a.positions ? a.positions[t] : pos);
+    }
+    const bool to_rows = kind == 0 || !PAGED;
+    void *dst = kind == 0 ? a.qo : a.ko;
+    const int64_t dst_hs = kind == 0 ? a.qo_hs : a.ko_hs;
+    const int64_t dst0 = (int64_t)t * (kind == 0 ? a.qo_rs : a.ko_rs);
+    for (int h = h0; h < h1; h += U * RPW) {
+        if (h != h0) load(h);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (h + u * RPW >= h1) break;                      // uniform over the warp
+            const int hh = h + u * RPW + sub;
+            float x[8];
+            widen(raw[u], x);
+            tr.apply(x, a.eps, lane);
+            if (to_rows) {
+                if (hh < h1) store8<T>(dst, dst0 + hh * dst_hs + 8 * c, x);
+            } else if constexpr (PAGED) {
+                store_page<T, LPR>(a.pool, kind == 1 ? a.pool.k : a.pool.v, kind == 1 ? a.pool.ks : a.pool.vs,
+                                   off + hh * a.pool.head_stride, soff + hh * a.pool.s_head_stride, c,
+                                   hh < h1 && mapped, x);
+            }
+        }
+    }
+}
+
+// Rows of K and V read back: the same split of lanes and tasks.
+template <int T, int D>
+__global__ void __launch_bounds__(kRowThreads)
+k_paged_gather(const __grid_constant__ PagedGatherArgs a) {
+    constexpr int LPR = D / 8, RPW = 32 / LPR, U = 4;
+    const int lane = threadIdx.x & 31;
+    const int64_t gw = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+    const int64_t t64 = gw / a.chunks;
+    if (t64 >= a.batch.n_rows) return;
+    const int t = (int)t64;
+    const int s = owner_of(a.batch, t, lane);
+    if (s < 0) return;
+    const PagedSeq q = paged_seq(a.batch, a.pool.page_shift, s);
+    const int pos = q.kv - q.n + (t - q.row0);
+    const int cap = a.batch.max_pages << a.pool.page_shift;
+    bool mapped = pos >= 0 && pos < cap && t >= q.row0 && t < q.row0 + q.n && q.ok;
+    int page = 0;
+    if (mapped) {
+        page = a.batch.pages[(int64_t)s * a.batch.pages_stride + (pos >> a.pool.page_shift)];
+        mapped = page >= 0 && page < a.pool.n_pages;
+    }
+    if (!mapped) {
+        page = 0;
+        if (lane == 0) atomicOr(a.err, (uint32_t)PAGED_ERR_PAGE);
+    }
+    const int slot = mapped ? pos & ((1 << a.pool.page_shift) - 1) : 0;
+    const int64_t off = (int64_t)page * a.pool.page_stride + slot * a.pool.row_stride;
+    const int64_t soff = (int64_t)page * a.pool.s_page_stride + slot;
+    const int sub = lane / LPR, c = lane % LPR;
+    // the 2 n_head_kv rows of the token: K heads, then V heads
+    const int heads = a.pool.n_head_kv, rows = 2 * heads;
+    const int r0 = (int)(gw - t64 * a.chunks) * a.iters * RPW, r1 = min(rows, r0 + a.iters * RPW);
+    const bool wide = a.pool.format == PAGED_F16 || a.pool.format == PAGED_BF16;
+    for (int r = r0; r < r1; r += U * RPW) {
+        uint4 w[U];
+        float sc[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int rr = r + u * RPW + sub;
+            w[u] = make_uint4(0, 0, 0, 0);
+            sc[u] = 0.f;
+            if (rr < r1 && mapped) {
+                const int h = rr < heads ? rr : rr - heads;
+                const uint8_t *base = rr < heads ? a.pool.k : a.pool.v;
+                const int64_t e = off + h * a.pool.head_stride + 8 * c;
+                if (wide) {
+                    w[u] = __ldcs(reinterpret_cast<const uint4 *>(base + 2 * e));
+                } else {
+                    const uint2 x = __ldcs(reinterpret_cast<const uint2 *>(base + e));
+                    w[u].x = x.x;
+                    w[u].y = x.y;
+                    sc[u] = __ldg((rr < heads ? a.pool.ks : a.pool.vs) + soff + h * a.pool.s_head_stride);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int rr = r + u * RPW + sub;
+            if (rr >= r1) continue;
+            const int h = rr < heads ? rr : rr - heads;
+            void *dst = rr < heads ? a.k : a.v;
+            const int64_t e = (rr < heads ? (int64_t)t * a.k_rs + h * a.k_hs : (int64_t)t * a.v_rs + h * a.v_hs) + 8 * c;
+            if (wide) {
+                *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(dst) + e) = w[u];
+                continue;
+            }
+            float x[8];
+            const uint32_t ww[2] = {w[u].x, w[u].y};
+            if (a.pool.format == PAGED_INT8) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = (float)(int8_t)(ww[i >> 2] >> (8 * (i & 3))) * sc[u];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = e4m3_unpair((ww[i >> 1] >> (16 * (i & 1))) & 0xffffu);
+                    x[2 * i] = f.x * sc[u];
+                    x[2 * i + 1] = f.y * sc[u];
+                }
+            }
+            store8<T>(dst, e, x);
+        }
+    }
+}
+
+// Warp steps per task: whole tokens when there are plenty (their angles are worked out once),
+// single steps when there are few and latency counts.
+int steps_per_task(int64_t rows_total, int rpw, int sms) {
+    const int64_t steps = (rows_total + rpw - 1) / rpw;
+    const int64_t warps = (int64_t)sms * 32;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(16, steps / warps));
+}
+
+int sm_count() {
+    int dev = 0, sms = 1;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms;
+}
+
+template <int T, int D>
+cudaError_t rows_t(PagedRowsArgs a, bool paged, cudaStream_t st) {
+    constexpr int rpw = 32 / (D / 8);
+    a.iters = steps_per_task(a.n_rows * (a.nq + a.nk + a.nv), rpw, sm_count());
+    const int per = a.iters * rpw;
+    a.cq = (a.nq + per - 1) / per;
+    a.ck = (a.nk + per - 1) / per;
+    a.cv = (a.nv + per - 1) / per;
+    const int64_t warps = a.n_rows * (a.cq + a.ck + a.cv);
+    const int64_t blocks = (warps + kRowThreads / 32 - 1) / (kRowThreads / 32);
+    if (blocks <= 0) return cudaSuccess;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    if (paged) {
+        if constexpr (T != PAGED_F32) k_paged_rows<T, D, true><<<(unsigned)blocks, kRowThreads, 0, st>>>(a);
+    } else {
+        k_paged_rows<T, D, false><<<(unsigned)blocks, kRowThreads, 0, st>>>(a);
+    }
+    return cudaGetLastError();
+}
+
+template <int T, int D>
+cudaError_t gather_t(PagedGatherArgs a, cudaStream_t st) {
+    constexpr int rpw = 32 / (D / 8);
+    a.iters = steps_per_task(a.batch.n_rows * 2 * a.pool.n_head_kv, rpw, sm_count());
+    a.chunks = (2 * a.pool.n_head_kv + a.iters * rpw - 1) / (a.iters * rpw);
+    const int64_t warps = a.batch.n_rows * a.chunks;
+    const int64_t blocks = (warps + kRowThreads / 32 - 1) / (kRowThreads / 32);
+    if (blocks <= 0) return cudaSuccess;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    k_paged_gather<T, D><<<(unsigned)blocks, kRowThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_rows(const PagedRowsArgs &a, int dtype, int head_dim, bool paged, cudaStream_t st) {
+    switch (dtype * 1000 + head_dim) {
+    case PAGED_F16 * 1000 + 64: return rows_t<PAGED_F16, 64>(a, paged, st);
+    case PAGED_F16 * 1000 + 128: return rows_t<PAGED_F16, 128>(a, paged, st);
+    case PAGED_BF16 * 1000 + 64: return rows_t<PAGED_BF16, 64>(a, paged, st);
+    case PAGED_BF16 * 1000 + 128: return rows_t<PAGED_BF16, 128>(a, paged, st);
+    case PAGED_F32 * 1000 + 64: return rows_t<PAGED_F32, 64>(a, paged, st);
+    case PAGED_F32 * 1000 + 128: return rows_t<PAGED_F32, 128>(a, paged, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_paged_gather(const PagedGatherArgs &a, int dtype, int head_dim, cudaStream_t st) {
+    switch (dtype * 1000 + head_dim) {
+    case PAGED_F16 * 1000 + 64: return gather_t<PAGED_F16, 64>(a, st);
+    case PAGED_F16 * 1000 + 128: return gather_t<PAGED_F16, 128>(a, st);
+    case PAGED_BF16 * 1000 + 64: return gather_t<PAGED_BF16, 64>(a, st);
+    case PAGED_BF16 * 1000 + 128: return gather_t<PAGED_BF16, 128>(a, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace dflash
