@@ -146,11 +146,12 @@ def test_append_writes_the_rows_bit_for_bit(fmt, dtype, dim, page, order, lens):
                 assert torch.equal(got, x)
                 continue
             top = x.float().abs().amax(-1, keepdim=True)
-            full = TOP[w.store]
+            # as a tensor: PyTorch divides by (and into) a plain number through a reciprocal
+            full = torch.full_like(top, TOP[w.store])
             y = x.float() * torch.where(top > 0, full / top, 0.0)
             codes = y.round().to(torch.int8) if w.store == torch.int8 else y.to(w.store)
             assert torch.equal(got.view(torch.uint8), codes.view(torch.uint8))
-            assert torch.equal(scale[page_id, :, slot], top[..., 0] / full)
+            assert torch.equal(scale[page_id, :, slot], (top / full)[..., 0])
 
 
 @pytest.mark.parametrize("fmt,dtype", [("f16", "f16"), ("bf16", "bf16"), ("int8", "f16"), ("e4m3", "bf16")])
