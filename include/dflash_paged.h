@@ -22,7 +22,7 @@
  *     Rows that such an entry names are not written, or read as zeros, and a bit is set in
  *     the device error word (paged_device_error).
  *   - "Rows" tensors are [n_rows][heads][head_dim] with the innermost index contiguous and
- *     any row and head strides (in elements) that keep every head 16-byte aligned, so that
+ *     positive row and head strides (in elements) that keep every head 16-byte aligned, so that
  *     queries, keys and values may be slices of one projection's output.
  */
 #ifndef DFLASH_PAGED_H

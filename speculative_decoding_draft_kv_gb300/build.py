@@ -23,7 +23,8 @@ LIB_PATH = os.path.join(LIB_DIR, LIB_NAME)
 
 SOURCES = ["ring_host.cu", "ring_kernels.cu", "attn_kernels.cu", "step_kernels.cu",
            "static_attend.cu", "produce_kernels.cu", "produce_tc.cu", "paged_host.cu",
-           "paged_rows.cu", "paged_attend_f16.cu", "paged_attend_bf16.cu"]
+           "paged_rows.cu", "paged_attend_f16.cu", "paged_attend_bf16.cu", "paged_prefill_f16.cu",
+           "paged_prefill_bf16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

@@ -90,13 +90,19 @@ struct PagedAttendArgs {
     float *part_acc;                  // [ctas][2][rows][head_dim] numerators
     float2 *part_ml;                  // [ctas][2][rows] (max in log2 units, sum)
     int4 *desc;                       // [ctas] the item whose first part is the CTA's last one
-    int n_head, group, mask, window;
-    int ctas, min_tiles, tile_rows;
+    int n_head, group, mask, window, max_q;
+    int ctas, min_tiles;
+    int tile_tokens, tile_rows;       // tokens and rows (tokens times group, at most) of an item
     float scale_log2;
 };
 template <int T> cudaError_t paged_attend_setup_t();
 template <int T>
 cudaError_t launch_paged_attend_t(const PagedAttendArgs &a, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                                   int head_dim, cudaStream_t st);
+
+template <int T> cudaError_t paged_prefill_setup_t();
+template <int T>
+cudaError_t launch_paged_prefill_t(const PagedAttendArgs &a, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
+                                   const CUtensorMap &tm_q, int head_dim, cudaStream_t st);
 
 }  // namespace dflash

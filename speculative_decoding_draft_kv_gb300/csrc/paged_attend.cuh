@@ -103,12 +103,12 @@ k_paged_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     pdl_trigger();                       // the join may settle; it waits for this grid's end
-    const PagedShare share = paged_share<kDecTile, C::kThreads>(a, C::kRows, s_plan);
+    const PagedShare share = paged_share<kDecTile, C::kThreads>(a, s_plan);
     if (threadIdx.x == 0 && share.begin >= share.end) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
     if (share.begin >= share.end) return;
 
     PagedWalk<kDecTile> w;
-    w.init(a, share, C::kRows);
+    w.init(a, share);
     int it = 0;                          // tiles so far: stage it % S, use it / S
 
     if (warp == 4) {
@@ -118,7 +118,7 @@ k_paged_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         const int nb = kDecTile / br;                          // boxes along a tile
         const int boxes = nb * C::kHalves;                     // per tensor
         bool alive = true;
-        while (alive && w.next(a, C::kRows)) {
+        while (alive && w.next(a)) {
             const int hi = w.sh.hi(w.rt), lo = w.sh.lo(w.rt);
             const int64_t row = (int64_t)w.seq * a.batch.pages_stride;
             // lane b: the page of box b of tile t (-1: not needed, or not to be had)
@@ -194,14 +194,13 @@ k_paged_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     float *sx = reinterpret_cast<float *>(smem + C::kOffX);
     float2 *sml = reinterpret_cast<float2 *>(smem + C::kOffMl);
     bool began = false;                  // this CTA starts an item that another one finishes
-    while (w.next(a, C::kRows)) {
+    while (w.next(a)) {
         const PagedSeq &q = w.sh.q;
-        const int flat0 = w.rt * C::kRows;           // first (token, head) row of the tile
-        const int flat_n = q.n * a.group;
+        const int flat_n = q.n * a.group;            // a row is (token, query head), token by token
         float qscale[2] = {a.scale_log2, a.scale_log2};
         // queries of this kv head into shared memory; rows that are not there are zeros
         for (int u = threadIdx.x; u < C::kRows * (D / 8); u += 128) {
-            const int r = u / (D / 8), ch = u % (D / 8), f = flat0 + r;
+            const int r = u / (D / 8), ch = u % (D / 8), f = r;
             uint4 x = make_uint4(0, 0, 0, 0);
             if (f < flat_n) {
                 const int tok = f / a.group, hh = f - tok * a.group;
@@ -265,7 +264,7 @@ k_paged_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         const int ctx = w.sh.ctx, item_lo = w.sh.lo(w.rt), item_hi = w.sh.hi(w.rt);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int f = flat0 + (j ? r1 : r0), tok = f / a.group;
+            const int f = j ? r1 : r0, tok = f / a.group;
             rlo[j] = rhi[j] = 0;
             if (f < flat_n) {
                 if (a.mask == PAGED_CAUSAL) {
@@ -286,7 +285,7 @@ k_paged_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         uint64_t any_word = ~0ull;
         if (a.mask == PAGED_TREE) {
             uint32_t lo32 = 0, hi32 = 0;
-            const int f = flat0 + lane;
+            const int f = lane;
             if (lane < C::kRows && f < flat_n) {
                 const uint64_t x = (uint64_t)a.tree[q.row0 + f / a.group];
                 lo32 = (uint32_t)x;
@@ -598,7 +597,7 @@ k_paged_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             const int64_t part = ((int64_t)blockIdx.x * 2 + (w.first ? 1 : 0)) * C::kRows;
 #pragma unroll
             for (int jj = 0; jj < 2; ++jj) {
-                const int r = jj ? r1 : r0, f = flat0 + r;
+                const int r = jj ? r1 : r0, f = r;
                 if (f >= flat_n) continue;
                 if (whole) {
                     const float inv = L[jj] > 0.f || L[jj] != L[jj] ? 1.f / L[jj] : 0.f;

@@ -5,6 +5,22 @@
 
 namespace dflash {
 
+// The join settles while the attention runs, and waits for its end.
+template <int T>
+cudaError_t launch_join(const PagedAttendArgs &a, int rows, int head_dim, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.ctas, (unsigned)((rows + 7) / 8), 1);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return head_dim == 64 ? cudaLaunchKernelEx(&cfg, k_paged_join<64, T>, a, rows)
+                          : cudaLaunchKernelEx(&cfg, k_paged_join<128, T>, a, rows);
+}
+
 // fn(kernel, its shared memory, threads, rows) for one of the instances
 template <int T, int D, int MT, int FMT, class F>
 cudaError_t with_attend(F &&fn) {
@@ -41,18 +57,7 @@ cudaError_t launch_paged_attend_t(const PagedAttendArgs &a, const CUtensorMap &t
         kernel<<<a.ctas, threads, smem, st>>>(tm_k, tm_v, a);
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
-        // the join settles while the attention runs, and waits for its end
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)a.ctas, (unsigned)((rows + 7) / 8), 1);
-        cfg.blockDim = dim3(256);
-        cfg.stream = st;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        return head_dim == 64 ? cudaLaunchKernelEx(&cfg, k_paged_join<64, T>, a, rows)
-                              : cudaLaunchKernelEx(&cfg, k_paged_join<128, T>, a, rows);
+        return launch_join<T>(a, rows, head_dim, st);
     };
     const int mt = a.tile_rows <= 16 ? 1 : 2;
     return head_dim == 64 ? pick_attend<T, 64>(a.pool.format, mt, go) : pick_attend<T, 128>(a.pool.format, mt, go);

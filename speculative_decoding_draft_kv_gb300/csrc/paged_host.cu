@@ -47,6 +47,8 @@ int device_info(const char *who, DeviceInfo *out) {
         if (e == cudaSuccess) e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
         if (e == cudaSuccess) e = paged_attend_setup_t<PAGED_F16>();
         if (e == cudaSuccess) e = paged_attend_setup_t<PAGED_BF16>();
+        if (e == cudaSuccess) e = paged_prefill_setup_t<PAGED_F16>();
+        if (e == cudaSuccess) e = paged_prefill_setup_t<PAGED_BF16>();
         if (e != cudaSuccess) return fail(RING_ECUDA, "%s: set-up: %s", who, cudaGetErrorString(e));
         d.err = static_cast<uint32_t *>(p);
         d.ready = true;
@@ -75,9 +77,11 @@ EncodeTiled encode_fn() {
 bool is16(int t) { return t == PAGED_F16 || t == PAGED_BF16; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// rows tensors: 16-byte alignment of every head
-bool rows_ok(const void *p, int64_t rs, int64_t hs, int esize) {
-    return aligned16(p) && (rs * esize) % 16 == 0 && (hs * esize) % 16 == 0 && rs >= 0 && hs >= 0;
+// rows tensors: 16-byte alignment of every head, and strides that say something where there is
+// more than one of a kind
+bool rows_ok(const void *p, int64_t rs, int64_t hs, int esize, int64_t n_rows, int heads) {
+    return aligned16(p) && (rs * esize) % 16 == 0 && (hs * esize) % 16 == 0 && rs >= (n_rows > 1) && hs >= (heads > 1) &&
+           rs < (int64_t)1 << 38 && hs < (int64_t)1 << 38;
 }
 
 int check_cache(const char *who, const paged_cache *c) {
@@ -201,13 +205,43 @@ bool encode_pool(CUtensorMap *tm, const paged_cache *c, void *base, int rows) {
               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows per item and CTAs: what the workspace and the launch go by.
+// Queries as [n_rows][n_head][head_dim], boxes of 64 values by the heads of one kv head by tokens
+bool encode_queries(CUtensorMap *tm, const paged_attend_args *g, int head_dim, int group, int tokens) {
+    const EncodeTiled fn = encode_fn();
+    if (!fn) return false;
+    // a stride of a dimension of one entry is never walked, but has to be one
+    const int64_t hs = g->n_head > 1 ? g->q_head_stride : head_dim;
+    const int64_t rs = g->n_rows > 1 ? g->q_row_stride : (int64_t)head_dim * g->n_head;
+    cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)g->n_head, (cuuint64_t)g->n_rows};
+    cuuint64_t strides[2] = {(cuuint64_t)hs * 2, (cuuint64_t)rs * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)tokens};
+    cuuint32_t unit[3] = {1, 1, 1};
+    return fn(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(g->q), dims, strides, box, unit,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Which kernel serves a batch, its rows per item and its CTAs: what the workspace and the launch
+// go by.  Up to 32 query rows per kv head: the streaming kernel; more: the tensor-core one, whose
+// items are two blocks of as many whole tokens as 128 rows take.
+// No more CTAs than the bounds leave work for.
 struct AttendPlan {
-    int rows, ctas;
+    int rows, tokens, ctas, min_tiles;
+    bool wide;
 };
-AttendPlan plan_of(const paged_batch *b, int group, int sms) {
+AttendPlan plan_of(const paged_cache *c, const paged_batch *b, int group, int sms) {
     const int64_t rows = (int64_t)b->max_q * group;
-    return {rows <= 16 ? 16 : 32, 2 * sms};
+    AttendPlan p{};
+    p.wide = rows > 32;
+    p.rows = rows <= 16 ? 16 : (rows <= 32 ? 32 : 2 * (128 / group) * group);
+    p.tokens = p.wide ? p.rows / group : std::max(1, b->max_q);
+    p.min_tiles = p.wide ? 1 : 2;
+    const int64_t keys = b->max_kv > 0 ? b->max_kv : (int64_t)b->max_pages * c->page_size;
+    const int64_t tiles = keys / (p.wide ? 128 : 64) + 2;          // of an item, wherever it begins
+    const int64_t items = (int64_t)b->n_seq * c->n_head_kv * ((b->max_q + p.tokens - 1) / p.tokens);
+    const int64_t most = std::max<int64_t>(1, (items * tiles + p.min_tiles - 1) / p.min_tiles);
+    p.ctas = (int)std::min<int64_t>(most, p.wide ? sms : 2 * sms);
+    return p;
 }
 
 int64_t up256(int64_t x) { return (x + 255) & ~(int64_t)255; }
@@ -246,11 +280,11 @@ extern "C" int paged_norm_rope(const paged_norm_rope_args *g, void *stream) {
     if (!(g->eps >= 0.f)) return fail(RING_EINVAL, "%s: eps must not be negative", who);
     TRY(check_rope(who, g->rope, g->head_dim));
     const int es = g->dtype == PAGED_F32 ? 4 : 2;
-    if (g->n_head_q && (!g->q || !g->q_out || !rows_ok(g->q, g->q_row_stride, g->q_head_stride, es) ||
-                        !rows_ok(g->q_out, g->qo_row_stride, g->qo_head_stride, es)))
+    if (g->n_head_q && (!g->q || !g->q_out || !rows_ok(g->q, g->q_row_stride, g->q_head_stride, es, g->n_rows, g->n_head_q) ||
+                        !rows_ok(g->q_out, g->qo_row_stride, g->qo_head_stride, es, g->n_rows, g->n_head_q)))
         return fail(RING_EINVAL, "%s: q and q_out must be given with every head 16-byte aligned", who);
-    if (g->n_head_k && (!g->k || !g->k_out || !rows_ok(g->k, g->k_row_stride, g->k_head_stride, es) ||
-                        !rows_ok(g->k_out, g->ko_row_stride, g->ko_head_stride, es)))
+    if (g->n_head_k && (!g->k || !g->k_out || !rows_ok(g->k, g->k_row_stride, g->k_head_stride, es, g->n_rows, g->n_head_k) ||
+                        !rows_ok(g->k_out, g->ko_row_stride, g->ko_head_stride, es, g->n_rows, g->n_head_k)))
         return fail(RING_EINVAL, "%s: k and k_out must be given with every head 16-byte aligned", who);
     if ((g->q_norm && !aligned16(g->q_norm)) || (g->k_norm && !aligned16(g->k_norm)))
         return fail(RING_EINVAL, "%s: norm weights must be 16-byte aligned", who);
@@ -291,11 +325,11 @@ extern "C" int paged_append(const paged_append_args *g, void *stream) {
     if (g->n_head_q < 0 || g->n_head_q > 65536) return fail(RING_EINVAL, "%s: n_head_q out of range", who);
     if (!(g->eps >= 0.f)) return fail(RING_EINVAL, "%s: eps must not be negative", who);
     TRY(check_rope(who, g->rope, g->cache->head_dim));
-    if (!g->k || !g->v || !rows_ok(g->k, g->k_row_stride, g->k_head_stride, 2) ||
-        !rows_ok(g->v, g->v_row_stride, g->v_head_stride, 2))
+    if (!g->k || !g->v || !rows_ok(g->k, g->k_row_stride, g->k_head_stride, 2, g->n_rows, g->cache->n_head_kv) ||
+        !rows_ok(g->v, g->v_row_stride, g->v_head_stride, 2, g->n_rows, g->cache->n_head_kv))
         return fail(RING_EINVAL, "%s: k and v must be given with every head 16-byte aligned", who);
-    if (g->n_head_q && (!g->q || !g->q_out || !rows_ok(g->q, g->q_row_stride, g->q_head_stride, 2) ||
-                        !rows_ok(g->q_out, g->qo_row_stride, g->qo_head_stride, 2)))
+    if (g->n_head_q && (!g->q || !g->q_out || !rows_ok(g->q, g->q_row_stride, g->q_head_stride, 2, g->n_rows, g->n_head_q) ||
+                        !rows_ok(g->q_out, g->qo_row_stride, g->qo_head_stride, 2, g->n_rows, g->n_head_q)))
         return fail(RING_EINVAL, "%s: q and q_out must be given with every head 16-byte aligned", who);
     if ((g->q_norm && !aligned16(g->q_norm)) || (g->k_norm && !aligned16(g->k_norm)))
         return fail(RING_EINVAL, "%s: norm weights must be 16-byte aligned", who);
@@ -334,8 +368,8 @@ extern "C" int paged_gather(const paged_gather_args *g, void *stream) {
     if (!is16(g->dtype)) return fail(RING_EINVAL, "%s: rows must be F16 or BF16", who);
     if (is16(g->cache->format) && g->cache->format != g->dtype)
         return fail(RING_EINVAL, "%s: rows and 16-bit pages must have one type", who);
-    if (!g->k || !g->v || !rows_ok(g->k, g->k_row_stride, g->k_head_stride, 2) ||
-        !rows_ok(g->v, g->v_row_stride, g->v_head_stride, 2))
+    if (!g->k || !g->v || !rows_ok(g->k, g->k_row_stride, g->k_head_stride, 2, g->n_rows, g->cache->n_head_kv) ||
+        !rows_ok(g->v, g->v_row_stride, g->v_head_stride, 2, g->n_rows, g->cache->n_head_kv))
         return fail(RING_EINVAL, "%s: k and v must be given with every head 16-byte aligned", who);
     if (g->n_rows == 0 || g->batch->n_seq == 0) return RING_OK;
     DeviceInfo d;
@@ -360,7 +394,7 @@ extern "C" int paged_attend_workspace(const paged_cache *cache, const paged_batc
     TRY(check_heads(who, cache, n_head));
     DeviceInfo d;
     TRY(device_info(who, &d));
-    *bytes = workspace_of(plan_of(batch, n_head / cache->n_head_kv, d.sms), cache->head_dim);
+    *bytes = workspace_of(plan_of(cache, batch, n_head / cache->n_head_kv, d.sms), cache->head_dim);
     return RING_OK;
 }
 
@@ -381,14 +415,14 @@ extern "C" int paged_attend(const paged_attend_args *g, void *stream) {
         return fail(RING_EINVAL, "%s: a token tree has at most 64 nodes, max_q is %d", who, g->batch->max_q);
     if (g->window < 0) return fail(RING_EINVAL, "%s: negative window", who);
     if (!(g->scale >= 0.f) || !std::isfinite(g->scale)) return fail(RING_EINVAL, "%s: scale must be finite and not negative", who);
-    if (!g->q || !g->o || !rows_ok(g->q, g->q_row_stride, g->q_head_stride, 2) ||
-        !rows_ok(g->o, g->o_row_stride, g->o_head_stride, 2))
+    if (!g->q || !g->o || !rows_ok(g->q, g->q_row_stride, g->q_head_stride, 2, g->n_rows, g->n_head) ||
+        !rows_ok(g->o, g->o_row_stride, g->o_head_stride, 2, g->n_rows, g->n_head))
         return fail(RING_EINVAL, "%s: q and o must be given with every head 16-byte aligned", who);
     if (g->n_rows == 0 || g->batch->n_seq == 0 || g->batch->max_q == 0) return RING_OK;
     DeviceInfo d;
     TRY(device_info(who, &d));
     const int group = g->n_head / g->cache->n_head_kv;
-    const AttendPlan p = plan_of(g->batch, group, d.sms);
+    const AttendPlan p = plan_of(g->cache, g->batch, group, d.sms);
     const int64_t need = workspace_of(p, g->cache->head_dim);
     if (!g->workspace || (reinterpret_cast<uintptr_t>(g->workspace) & 255) || g->workspace_bytes < need)
         return fail(RING_EINVAL, "%s: needs %lld bytes of 256-byte aligned workspace", who, (long long)need);
@@ -413,17 +447,25 @@ extern "C" int paged_attend(const paged_attend_args *g, void *stream) {
     a.group = group;
     a.mask = g->mask;
     a.window = g->window;
+    a.max_q = g->batch->max_q;
     a.ctas = p.ctas;
-    a.min_tiles = 2;
+    a.min_tiles = p.min_tiles;
+    a.tile_tokens = p.tokens;
     a.tile_rows = p.rows;
     const double scale = g->scale > 0.f ? (double)g->scale : 1.0 / std::sqrt((double)g->cache->head_dim);
     a.scale_log2 = (float)(scale * 1.4426950408889634);
-    CUtensorMap tk, tv;
-    if (!encode_pool(&tk, g->cache, g->cache->k, 64) || !encode_pool(&tv, g->cache, g->cache->v, 64))
+    CUtensorMap tk, tv, tq;
+    const int box = p.wide ? 128 : 64;
+    if (!encode_pool(&tk, g->cache, g->cache->k, box) || !encode_pool(&tv, g->cache, g->cache->v, box) ||
+        (p.wide && !encode_queries(&tq, g, g->cache->head_dim, group, 128 / group)))
         return fail(RING_ECUDA, "%s: cuTensorMapEncodeTiled failed", who);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = g->dtype == PAGED_F16 ? launch_paged_attend_t<PAGED_F16>(a, tk, tv, g->cache->head_dim, st)
-                                                : launch_paged_attend_t<PAGED_BF16>(a, tk, tv, g->cache->head_dim, st);
+    const bool f16 = g->dtype == PAGED_F16;
+    const int dim = g->cache->head_dim;
+    const cudaError_t e = p.wide ? (f16 ? launch_paged_prefill_t<PAGED_F16>(a, tk, tv, tq, dim, st)
+                                        : launch_paged_prefill_t<PAGED_BF16>(a, tk, tv, tq, dim, st))
+                                 : (f16 ? launch_paged_attend_t<PAGED_F16>(a, tk, tv, dim, st)
+                                        : launch_paged_attend_t<PAGED_BF16>(a, tk, tv, dim, st));
     return e == cudaSuccess ? RING_OK : fail(RING_ECUDA, "%s: launch: %s", who, cudaGetErrorString(e));
 }
 

@@ -19,44 +19,69 @@
 
 namespace dflash {
 
-// Row tiles and key ranges of one sequence; TR query rows a row tile, KT keys a key tile.
+// sum over i < n of floor((a i + b) / m), a, b >= 0, m > 0: whole parts of a / m and b / m first,
+// then the lattice points under the line counted along the other axis
+__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+    int64_t sum = 0;
+    while (true) {
+        if (a >= m) {
+            sum += (n - 1) * n / 2 * (a / m);
+            a %= m;
+        }
+        if (b >= m) {
+            sum += n * (b / m);
+            b %= m;
+        }
+        const int64_t y = a * n + b;
+        if (y < m) return sum;
+        n = y / m;
+        b = y % m;
+        const int64_t t = m;
+        m = a;
+        a = t;
+    }
+}
+
+// Row tiles and key ranges of one sequence: TT tokens a row tile, KT keys a key tile.
 template <int KT>
 struct PagedShape {
     PagedSeq q;
-    int group, tile_rows, mask, window, ctx, heads;
+    int tokens, mask, window, ctx, heads;
 
-    __device__ __forceinline__ void load(const PagedAttendArgs &a, int s, int rows_per_tile) {
+    // a sequence whose lengths contradict each other has no tiles: its rows stay as they are
+    __device__ __forceinline__ void load(const PagedAttendArgs &a, int s) {
         q = paged_seq(a.batch, a.pool.page_shift, s);
-        group = a.group;
-        tile_rows = rows_per_tile;
+        q.ok = q.ok && q.n <= a.max_q;
+        if (!q.ok) q.n = 0;
+        tokens = a.tile_tokens;
         mask = a.mask;
         window = a.window;
         ctx = q.kv - q.n;
         heads = a.pool.n_head_kv;
     }
-    __device__ __forceinline__ int row_tiles() const { return (q.n * group + tile_rows - 1) / tile_rows; }
-    __device__ __forceinline__ int first_token(int rt) const { return rt * tile_rows / group; }
-    __device__ __forceinline__ int last_token(int rt) const {
-        return min(q.n - 1, (rt * tile_rows + tile_rows - 1) / group);
-    }
-    // positions that some row of the tile sees lie in [lo, hi)
+    __device__ __forceinline__ int row_tiles() const { return (q.n + tokens - 1) / tokens; }
+    // positions that some row of the tile sees lie in [lo, hi); 0 <= lo < hi
     __device__ __forceinline__ int lo(int rt) const {
         if (window == 0) return 0;
-        return max(0, mask == PAGED_CAUSAL ? ctx + first_token(rt) - window + 1 : ctx - window);
+        return max(0, mask == PAGED_CAUSAL ? ctx + rt * tokens - window + 1 : ctx - window);
     }
     __device__ __forceinline__ int hi(int rt) const {
-        return mask == PAGED_CAUSAL ? max(0, min(q.kv, ctx + last_token(rt) + 1)) : q.kv;
+        return mask == PAGED_CAUSAL ? min(q.kv, ctx + (rt + 1) * tokens) : q.kv;
     }
-    // every row tile has a key tile at least, so that rows seeing nothing get their zeros
     __device__ __forceinline__ int tile0(int rt) const { return lo(rt) / KT; }
-    __device__ __forceinline__ int tiles(int rt) const {
-        const int t0 = tile0(rt), t1 = (hi(rt) + KT - 1) / KT;
-        return max(1, t1 - t0);
-    }
+    __device__ __forceinline__ int tiles(int rt) const { return (hi(rt) + KT - 1) / KT - lo(rt) / KT; }
     __device__ __forceinline__ int64_t head_tiles() const {
-        int64_t w = 0;
         const int n = row_tiles();
-        for (int rt = 0; rt < n; ++rt) w += tiles(rt);
+        if (n == 0) return 0;
+        if (n == 1 || mask != PAGED_CAUSAL) return (int64_t)n * tiles(0);
+        // ceil(hi / KT) of all row tiles but the last, whose hi is kv ...
+        int64_t w = floor_sum(n - 1, KT, tokens, ctx + tokens + KT - 1) + (q.kv + KT - 1) / KT;
+        // ... less floor(lo / KT) of those whose lo is above 0
+        if (window) {
+            const int64_t first = ctx - window + 1;
+            const int64_t i0 = first >= 0 ? 0 : (-first + tokens - 1) / tokens;
+            if (i0 < n) w -= floor_sum(n - i0, KT, tokens, first + i0 * tokens);
+        }
         return w;
     }
 };
@@ -68,9 +93,9 @@ struct PagedShare {
 };
 
 // Block-wide: every thread calls it, every thread gets the CTA's share.  scratch: shared
-// memory of 40 int64.
+// memory of THREADS / 32 + 2 int64.
 template <int KT, int THREADS>
-__device__ __forceinline__ PagedShare paged_share(const PagedAttendArgs &a, int tile_rows, int64_t *scratch) {
+__device__ __forceinline__ PagedShare paged_share(const PagedAttendArgs &a, int64_t *scratch) {
     constexpr int WARPS = THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per_thread = (a.batch.n_seq + THREADS - 1) / THREADS;
@@ -79,7 +104,7 @@ __device__ __forceinline__ PagedShare paged_share(const PagedAttendArgs &a, int 
     int64_t sum = 0;
     bool ok = true;
     for (int s = s0; s < s1; ++s) {
-        sh.load(a, s, tile_rows);
+        sh.load(a, s);
         ok = ok && sh.q.ok;
         sum += sh.head_tiles() * sh.heads;
     }
@@ -107,7 +132,7 @@ __device__ __forceinline__ PagedShare paged_share(const PagedAttendArgs &a, int 
     if (r.begin < r.end && mine <= r.begin && r.begin < mine + sum) {
         int64_t at = mine;
         for (int s = s0; s < s1; ++s) {
-            sh.load(a, s, tile_rows);
+            sh.load(a, s);
             const int64_t w = sh.head_tiles() * sh.heads;
             if (r.begin < at + w) {
                 scratch[WARPS] = at;
@@ -124,7 +149,8 @@ __device__ __forceinline__ PagedShare paged_share(const PagedAttendArgs &a, int 
     return r;
 }
 
-// Walks a share item by item.  Every warp role runs its own copy over the same share.
+// Walks a share item by item.  Every warp role runs its own copy over the same share; init takes
+// whole warps.
 template <int KT>
 struct PagedWalk {
     PagedShape<KT> sh;
@@ -134,25 +160,44 @@ struct PagedWalk {
     int t0, nt, item_tiles;          // first key tile (absolute), their number; the item's
     bool first, last;                // the piece has the item's first / last tile
 
-    __device__ __forceinline__ void init(const PagedAttendArgs &a, const PagedShare &r, int tile_rows) {
+    __device__ __forceinline__ void init(const PagedAttendArgs &a, const PagedShare &r) {
         cur = r.begin;
         end = r.end;
         per = r.per;
         seq = r.seq;
         head = rt = off = 0;
         if (cur >= end) return;
-        sh.load(a, seq, tile_rows);
+        sh.load(a, seq);
         const int64_t per_head = sh.head_tiles();
         int64_t rem = cur - r.seq_begin;
         head = (int)(rem / per_head);
         rem -= head * per_head;
-        while (rem >= sh.tiles(rt)) {
-            rem -= sh.tiles(rt);
-            ++rt;
+        // the row tile that holds tile rem of the head, 32 row tiles at a time
+        const int lane = threadIdx.x & 31, n = sh.row_tiles();
+        while (true) {
+            const int mine = rt + lane < n ? sh.tiles(rt + lane) : 0;
+            int64_t incl = mine;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, incl, d);
+                if (lane >= d) incl += v;
+            }
+            const uint32_t beyond = __ballot_sync(0xffffffffu, rem < incl);
+            if (beyond) {
+                const int at = __ffs(beyond) - 1;
+                off = (int)(rem - __shfl_sync(0xffffffffu, incl - mine, at));
+                rt += at;
+                return;
+            }
+            rem -= __shfl_sync(0xffffffffu, incl, 31);
+            rt += 32;
+            if (rt >= n) {                           // not reached: rem < per_head
+                end = cur;
+                return;
+            }
         }
-        off = (int)rem;
     }
-    __device__ __forceinline__ bool next(const PagedAttendArgs &a, int tile_rows) {
+    __device__ __forceinline__ bool next(const PagedAttendArgs &a) {
         if (cur >= end) return false;
         if (off < 0) {                               // the item before this one is done
             off = 0;
@@ -162,7 +207,7 @@ struct PagedWalk {
                     head = 0;
                     do {
                         if (++seq >= a.batch.n_seq) return false;
-                        sh.load(a, seq, tile_rows);
+                        sh.load(a, seq);
                     } while (sh.q.n == 0);
                 }
             }

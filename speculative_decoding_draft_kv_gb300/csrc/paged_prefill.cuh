@@ -1,0 +1,826 @@
+// Attention of new tokens over a paged cache: the kernel for many query rows per kv head (prompt
+// chunks, large trees, mixed batches), on the 5th-generation tensor cores.
+//
+// With 128 query rows and more a cached byte takes part in 128 flops and up, and the pass is
+// bound by the tensor cores, then by the exponentials beside them.  An item is up to 256 query
+// rows -- two blocks of 128 TMEM lanes, a row being a (token, query head) of one kv head -- and
+// its key tiles of 128.  Per tile and block, with all accumulators in tensor memory:
+//   S = Q K^T   128 x 128 in TMEM, A and B from shared memory;
+//   P = 2^(S scale - m) by the block's four softmax warps, a thread per row, written back over S
+//               as 16-bit values;
+//   O += P V    A = P from TMEM, B = V from shared memory as it lies (rows along the keys).
+// The two blocks take turns: while the tensor cores work for one, the softmax warps of the other
+// have the exponentials.  One thread issues, per tile, O0 += P0 V, S0 = Q0 K', O1 += P1 V,
+// S1 = Q1 K': the tensor pipe runs them in that order, so S may overwrite the P that the product
+// in front of it reads, and a block's S being there means its O is up to date.
+//
+// The softmax reference moves only when a row outgrows it by 2^8 (see paged_attend.cuh), so O is
+// read back and rescaled in few tiles.
+//
+// An item of at most 128 rows (a verify block, a tree, a single token in a mixed batch) fills one
+// block only: then both blocks take the same queries, block 0 the even key tiles and block 1 the
+// odd ones, so that products and exponentials still take turns, and the two states join in shared
+// memory at the end.
+//
+// Quantised pages: four more warps turn code tiles into F16 tiles in shared memory (a thread per
+// key), exactly; scales are applied where the streaming kernel applies them, K's to the scores,
+// V's to the probabilities relative to a power of two.  bf16 queries are turned to F16 in shared
+// memory, a power of two per row taken out, by the threads that own the rows.
+//
+// Roles: warps 0-3 and 4-7 the blocks' rows, warp 8 copies (queries by one box of heads x tokens,
+// K and V a box per page), warp 9 issues products, warps 10-13 convert codes.
+#pragma once
+
+#include "paged_attend.cuh"
+
+namespace dflash {
+
+constexpr int kPreTile = 128;
+constexpr int kScaleRing = 8;            // key tiles whose scales are kept (see below)
+
+template <int D, int FMT>
+struct PreCfg {
+    static constexpr bool kCodes = FMT != kFmt16;
+    static constexpr int kThreads = kCodes ? 448 : 320;
+    static constexpr int kHalves = D / 64;                       // 128-byte columns of a 16-bit row
+    static constexpr int kHalfBytes = kPreTile * 128;
+    static constexpr int kSlotBytes = kHalves * kHalfBytes;      // 128 rows of D 16-bit values
+    static constexpr int kSlots = kCodes ? (D == 128 ? 3 : 4) : (D == 128 ? 5 : 8);   // K and V tiles in turn
+    static constexpr int kCodeBytes = kPreTile * D;
+    static constexpr int kCodeSlots = kCodes ? 3 : 0;
+    static constexpr int kOffQ = kSlots * kSlotBytes;
+    static constexpr int kOffCodes = kOffQ + 2 * kSlotBytes;
+    static constexpr int kOffCodeScale = kOffCodes + kCodeSlots * kCodeBytes;   // as loaded, per code slot
+    static constexpr int kOffScale = kOffCodeScale + kCodeSlots * kPreTile * 4;  // [ring][K, V][128]
+    static constexpr int kOffTop = kOffScale + (kCodes ? kScaleRing * 2 * kPreTile * 4 : 0);   // [ring][4]
+    static constexpr int kOffRow = kOffTop + (kCodes ? kScaleRing * 16 : 0);     // row values
+    static constexpr int kOffBars = kOffRow + 128 * 8;
+    static constexpr int kSmem = 1024 + kOffBars + 256;
+    static constexpr int kCols = kCodes ? 32 : 64;               // scores of a row in registers at once
+    static_assert(kSmem <= 227 * 1024, "one CTA per SM");
+    static_assert(2 * kSlotBytes == 128 * D * 4, "a block's numerators fit where the queries were");
+};
+
+// two float32 at a time
+__device__ __forceinline__ uint64_t pk2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void upk2(uint64_t x, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+template <int D, int FMT, int T>
+__global__ void __launch_bounds__(PreCfg<D, FMT>::kThreads, 1)
+k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ PagedAttendArgs a) {
+    using C = PreCfg<D, FMT>;
+    constexpr int NS = C::kSlots;
+    constexpr bool kCodes = C::kCodes;
+    constexpr int OT = kCodes ? PAGED_F16 : T;                       // operand type
+    constexpr bool kQTurned = kCodes && T == PAGED_BF16;
+    constexpr uint32_t kIdescQK = tc_idesc(128, kPreTile, OT == PAGED_BF16, false);
+    constexpr uint32_t kIdescPV = tc_idesc(128, D, OT == PAGED_BF16, true);
+    constexpr int CODE_ROW = D < 128 ? D : 128;                      // bytes of a row of codes
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t bars = smem_u32(smem + C::kOffBars);
+    const uint32_t full = bars, empty = bars + 8 * NS;               // [NS] each
+    const uint32_t q_full = bars + 16 * NS, q_empty = q_full + 8, q_ready = q_full + 16;
+    const uint32_t s_full = q_full + 24, p_full = s_full + 16, o_full = p_full + 16;   // [2] each
+    const uint32_t landed = o_full + 16, drain = landed + 8, odd_done = landed + 16;
+    const uint32_t c_full = landed + 24, c_empty = c_full + 8 * 3;   // [3] each
+    __shared__ int64_t s_plan[18];
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        prefetch_tensormap(&tm_k);
+        prefetch_tensormap(&tm_v);
+        prefetch_tensormap(&tm_q);
+        for (int k = 0; k < NS; ++k) {
+            mbar_init(full + 8 * k, kCodes ? 4 : 1);     // the converting warps, or the copy
+            mbar_init(empty + 8 * k, 1);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 9);                           // the products, and the rows' eight warps
+        mbar_init(q_ready, 8);                           // the rows' warps (a dealt item: block 0's, twice)
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(s_full + 8 * b, 1);
+            mbar_init(p_full + 8 * b, 4);
+            mbar_init(o_full + 8 * b, 1);
+        }
+        mbar_init(landed, 1);
+        mbar_init(drain, 1);
+        mbar_init(odd_done, 4);
+        for (int k = 0; k < C::kCodeSlots; ++k) {
+            mbar_init(c_full + 8 * k, 33);
+            mbar_init(c_empty + 8 * k, 4);
+        }
+        s_abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 9) {
+        tmem_alloc(smem_u32(&s_tmem), 512);
+        tmem_relinquish();
+    }
+    pdl_trigger();                       // the join may settle; it waits for this grid's end
+    tc_fence_before();
+    const PagedShare share = paged_share<kPreTile, C::kThreads>(a, s_plan);   // synchronises
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const int block_tokens = a.tile_tokens / 2, block_rows = block_tokens * a.group;
+    auto timed_out = [&]() {
+        atomicOr(a.err, (uint32_t)PAGED_ERR_WAIT);
+        s_abort = 1;
+    };
+
+    PagedWalk<kPreTile> w;
+    w.init(a, share);
+    // the item has rows for one block only: its key tiles are dealt to both
+    auto dealt = [&]() { return w.sh.q.n - w.rt * a.tile_tokens <= block_tokens; };
+    // some position of key tile t that no token of the sequence sees (its V row is cleared)
+    auto ragged = [&](int t) {
+        const int base = t * kPreTile;
+        return base < w.sh.lo(0) || base + kPreTile > w.sh.q.kv || (a.mask == PAGED_TREE && base + kPreTile > w.sh.ctx);
+    };
+    // tree positions that some token of the sequence sees (whole warp)
+    auto tree_union = [&]() {
+        if (a.mask != PAGED_TREE) return ~0ull;
+        uint32_t lo32 = 0, hi32 = 0;
+        for (int i = lane; i < w.sh.q.n; i += 32) {
+            const uint64_t x = (uint64_t)a.tree[w.sh.q.row0 + i];
+            lo32 |= (uint32_t)x;
+            hi32 |= (uint32_t)(x >> 32);
+        }
+        lo32 = __reduce_or_sync(0xffffffffu, lo32);
+        hi32 = __reduce_or_sync(0xffffffffu, hi32);
+        return (unsigned long long)((uint64_t)hi32 << 32 | lo32);
+    };
+    auto seen = [&](int p, uint64_t any_word) {
+        if (p < w.sh.lo(0) || p >= w.sh.q.kv) return false;
+        const int t = p - w.sh.ctx;
+        return a.mask != PAGED_TREE || t < 0 || (t < 64 && ((any_word >> t) & 1ull));
+    };
+
+    if (warp == 8) {
+        // ---------------- copies ----------------
+        constexpr int N = kCodes ? C::kCodeSlots : NS;           // stages of this ring
+        constexpr int BYTES = kCodes ? C::kCodeBytes : C::kSlotBytes;
+        constexpr int HALVES = kCodes ? 1 : C::kHalves;
+        const uint32_t ring_full = kCodes ? c_full : full, ring_empty = kCodes ? c_empty : empty;
+        const int ps = a.pool.page_shift;
+        const int br = min(1 << ps, kPreTile), nb = kPreTile / br, boxes = nb * HALVES;
+        int slot = 0, items = 0;
+        uint32_t lph = 0, wrap = 0;      // parities: of the cleared tiles, of the slot's use
+        bool alive = true;
+        while (alive && w.next(a)) {
+            const PagedSeq &q = w.sh.q;
+            const int hi = w.sh.hi(w.rt), lo = w.sh.lo(w.rt), nblk = dealt() ? 1 : 2;
+            const int64_t row = (int64_t)w.seq * a.batch.pages_stride;
+            if (lane == 0) {
+                if (!mbar_wait(q_empty, ((uint32_t)items & 1u) ^ 1u)) timed_out();
+                if (!s_abort) {
+                    mbar_expect_tx(q_full, (uint32_t)(nblk * C::kHalves * block_rows * 128));
+                    for (int b = 0; b < nblk; ++b)
+                        for (int h = 0; h < C::kHalves; ++h)
+                            tma_load_3d(smem_u32(smem + C::kOffQ) + b * C::kSlotBytes + h * C::kHalfBytes, &tm_q, h * 64,
+                                        w.head * a.group, q.row0 + w.rt * a.tile_tokens + b * block_tokens, q_full);
+                }
+            }
+            ++items;
+            auto lookup = [&](int t) {
+                const int p = t * kPreTile + lane * br;
+                if (lane >= nb || p >= hi || p + br <= lo) return -1;
+                const int id = a.batch.pages[row + (p >> ps)];
+                if (id < 0 || id >= a.pool.n_pages) {
+                    atomicOr(a.err, (uint32_t)PAGED_ERR_PAGE);
+                    return -1;
+                }
+                return id;
+            };
+            const uint64_t any_word = kCodes ? 0ull : tree_union();
+            int id = lookup(w.t0);
+            for (int j = 0; j < w.nt && alive; ++j) {
+                const int t = w.t0 + j;
+                const int id_now = id;
+                id = j + 1 < w.nt ? lookup(t + 1) : -1;
+                const int u = lane % boxes, b = u % nb, h = u / nb;
+                const int page = __shfl_sync(0xffffffffu, id_now, b);
+                for (int kv = 0; kv < 2; ++kv) {
+                    // a V tile with rows to clear lands on a barrier of this warp's own first (codes
+                    // are cleared where they are converted)
+                    const bool clear = !kCodes && kv && ragged(t);
+                    const uint32_t bar = clear ? landed : ring_full + 8 * slot;
+                    int ok = 1;
+                    if (lane == 0) {
+                        if (!mbar_wait(ring_empty + 8 * slot, wrap ^ 1u)) timed_out();
+                        ok = !s_abort;
+                        if (ok) mbar_expect_tx(bar, BYTES);
+                    }
+                    if (!__shfl_sync(0xffffffffu, ok, 0)) {
+                        alive = false;
+                        break;
+                    }
+                    uint8_t *dst = smem + (kCodes ? C::kOffCodes : 0) + slot * BYTES;
+                    if (lane < boxes)
+                        tma_load_4d(smem_u32(dst) + h * C::kHalfBytes + b * br * (kCodes ? CODE_ROW : 128), kv ? &tm_v : &tm_k, h * 64,
+                                    (t * kPreTile) & ((1 << ps) - 1), w.head, page < 0 ? a.pool.n_pages : page, bar);
+                    if constexpr (kCodes) {
+                        const int key = lane * 4;
+                        const int kp = __shfl_sync(0xffffffffu, id_now, key / br);
+                        const float *src = (kv ? a.pool.vs : a.pool.ks) + (int64_t)max(kp, 0) * a.pool.s_page_stride +
+                                           (int64_t)w.head * a.pool.s_head_stride + ((t * kPreTile + key) & ((1 << ps) - 1));
+                        cp_async16(smem_u32(smem + C::kOffCodeScale + slot * kPreTile * 4) + key * 4, src, kp < 0 ? 0 : 16);
+                        cp_async_arrive(bar);
+                    }
+                    if (clear) {
+                        // what nobody sees must not reach the product: 0 * NaN
+                        if (!__all_sync(0xffffffffu, mbar_wait(landed, lph))) {
+                            if (lane == 0) timed_out();
+                            alive = false;
+                            break;
+                        }
+                        lph ^= 1u;
+                        for (int r = lane; r < kPreTile; r += 32)
+                            if (!seen(t * kPreTile + r, any_word))
+                                for (int c = 0; c < C::kHalves * 8; ++c)
+                                    *reinterpret_cast<uint4 *>(dst + (c >> 3) * C::kHalfBytes + r * 128 + (c & 7) * 16) =
+                                        make_uint4(0, 0, 0, 0);
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(full + 8 * slot);
+                    }
+                    if (++slot == N) {
+                        slot = 0;
+                        wrap ^= 1u;
+                    }
+                }
+            }
+        }
+        // no copy may land after the CTA is gone: every one that was issued has been waited for by
+        // its reader, but on the way out of a failure
+        if (lane == 0 && s_abort) {
+            for (int k = 0; k < N; ++k) {
+                const int sl = (slot + k) % N;
+                const uint32_t par = slot + k >= N ? wrap : wrap ^ 1u;
+                if (!mbar_wait(ring_full + 8 * sl, par, 100000000ull)) break;
+            }
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        // ---------------- products ----------------
+        if (lane == 0) {
+            int slot = 0, items = 0;
+            uint32_t wrap = 0, pph[2] = {0, 0};  // parity of the slots' use, and of the blocks' P
+            bool alive = true;
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                if (!alive) return;
+                if (!mbar_wait(bar, parity)) {
+                    timed_out();
+                    alive = false;
+                }
+                if (s_abort) alive = false;
+                tc_fence_after();
+            };
+            auto step = [&]() {
+                if (++slot == NS) {
+                    slot = 0;
+                    wrap ^= 1u;
+                }
+            };
+            const uint32_t sq = smem_u32(smem + C::kOffQ), skv = smem_u32(smem);
+            // block b's S from queries qb
+            auto qk = [&](int b, int qb, int s) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = (kk >> 2) * C::kHalfBytes + (kk & 3) * 32;
+                    tc_mma_f16(tmem + b * 128, tc_desc_sw128(sq + qb * C::kSlotBytes + off),
+                               tc_desc_sw128(skv + s * C::kSlotBytes + off), kIdescQK, kk != 0);
+                }
+                tc_commit(s_full + 8 * b);
+            };
+            auto pv = [&](int b, int s, bool acc) {
+                wait(p_full + 8 * b, pph[b]);
+                pph[b] ^= 1u;
+                if (!alive) return;
+#pragma unroll
+                for (int kk = 0; kk < kPreTile / 16; ++kk)
+                    tc_mma_ts(tmem + 256 + b * 128, tmem + b * 128 + kk * 8,
+                              tc_desc_mn_sw128(skv + s * C::kSlotBytes + kk * 2048, C::kHalfBytes), kIdescPV, acc || kk != 0);
+            };
+            while (alive && w.next(a)) {
+                wait(kQTurned ? q_ready : q_full, (uint32_t)items & 1u);
+                ++items;
+                if (!dealt()) {
+                    wait(full + 8 * slot, wrap);
+                    if (!alive) break;
+                    qk(0, 0, slot);
+                    qk(1, 1, slot);
+                    tc_commit(empty + 8 * slot);
+                    step();
+                    if (w.nt == 1) tc_commit(q_empty);
+                    for (int j = 0; j < w.nt && alive; ++j) {
+                        const int vs = slot;
+                        const uint32_t vw = wrap;
+                        step();
+                        const bool more = j + 1 < w.nt;
+                        wait(full + 8 * vs, vw);
+                        pv(0, vs, j > 0);
+                        if (more) wait(full + 8 * slot, wrap);
+                        if (!alive) break;
+                        if (more) qk(0, 0, slot);
+                        else tc_commit(o_full);
+                        pv(1, vs, j > 0);
+                        if (!alive) break;
+                        tc_commit(empty + 8 * vs);
+                        if (more) {
+                            qk(1, 1, slot);
+                            tc_commit(empty + 8 * slot);
+                            step();
+                            if (j + 2 == w.nt) tc_commit(q_empty);
+                        } else {
+                            tc_commit(o_full + 8);
+                        }
+                    }
+                } else {
+                    // slots in the order K0 V0 K1 V1 ...; products in the order
+                    // QK0 QK1 PV0 QK2 PV1 QK3 ...
+                    const int s0 = slot;
+                    const uint32_t w0 = wrap;
+                    auto at = [&](int n, uint32_t &par) {      // slot and parity of the item's n-th tile
+                        const int x = s0 + n;
+                        par = w0 ^ ((uint32_t)(x / NS) & 1u);
+                        return x % NS;
+                    };
+                    auto qk_of = [&](int j) {
+                        uint32_t par;
+                        const int s = at(2 * j, par);
+                        wait(full + 8 * s, par);
+                        if (!alive) return;
+                        qk(j & 1, 0, s);
+                        tc_commit(empty + 8 * s);
+                        if (j == w.nt - 1) tc_commit(q_empty);
+                    };
+                    qk_of(0);
+                    if (w.nt > 1) qk_of(1);
+                    for (int j = 0; j < w.nt && alive; ++j) {
+                        uint32_t par;
+                        const int s = at(2 * j + 1, par);
+                        wait(full + 8 * s, par);
+                        pv(j & 1, s, j > 1);
+                        if (!alive) break;
+                        tc_commit(empty + 8 * s);
+                        if (j + 2 < w.nt) qk_of(j + 2);
+                        else tc_commit(o_full + 8 * (j & 1));
+                    }
+                    uint32_t par;
+                    slot = at(2 * w.nt, par);
+                    wrap = par;
+                }
+            }
+            tc_commit(drain);
+            if (!mbar_wait(drain, 0)) timed_out();
+        }
+        __syncwarp();
+    } else if (kCodes && warp >= 10) {
+        // ---------------- codes to F16 ----------------
+        // The ring of scales needs no barrier of its own: with 3 or 4 F16 slots and 3 code slots the
+        // tile at hand here is less than 6 tiles ahead of the one that the slower block's rows read
+        // (its V slot and all later ones are taken).
+        const int r = (int)threadIdx.x - 320;              // the thread's key
+        int slot = 0, cs = 0;
+        uint32_t wrap = 0, cwrap = 0;
+        int tile = 0;                                      // tiles so far: its place in the ring
+        bool alive = true;
+        while (alive && w.next(a)) {
+            const uint64_t any_word = tree_union();
+            for (int j = 0; j < w.nt && alive; ++j, ++tile) {
+                const int t = w.t0 + j;
+                for (int kv = 0; kv < 2; ++kv) {
+                    const bool ok = mbar_wait(c_full + 8 * cs, cwrap) && mbar_wait(empty + 8 * slot, wrap ^ 1u);
+                    if (!__all_sync(0xffffffffu, ok) || s_abort) {
+                        if (lane == 0) timed_out();
+                        alive = false;
+                        break;
+                    }
+                    const uint8_t *src = smem + C::kOffCodes + cs * C::kCodeBytes;
+                    uint8_t *dst = smem + slot * C::kSlotBytes;
+                    const bool live = seen(t * kPreTile + r, any_word);
+                    float sc = reinterpret_cast<const float *>(smem + C::kOffCodeScale)[cs * kPreTile + r];
+                    if (!live) sc = 0.f;
+                    reinterpret_cast<float *>(smem + C::kOffScale)[((tile % kScaleRing) * 2 + kv) * kPreTile + r] = sc;
+                    if (kv) {
+                        const uint32_t bits = __float_as_uint(sc) & 0x7fffffffu;
+                        const uint32_t top = __reduce_max_sync(0xffffffffu, bits < 0x7f800000u ? bits : 0u);
+                        if (lane == 0)
+                            reinterpret_cast<uint32_t *>(smem + C::kOffTop)[(tile % kScaleRing) * 4 + warp - 10] = top;
+                    }
+#pragma unroll
+                    for (int ch = 0; ch < D / 16; ++ch) {
+                        uint4 x = *reinterpret_cast<const uint4 *>(src + swz_row<CODE_ROW>(r, ch));
+                        if (!live) x = make_uint4(0, 0, 0, 0);
+                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                        uint32_t y[8];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if constexpr (FMT == kFmtInt8) {
+                                const uint32_t xf = xs[i] ^ 0x80808080u;
+                                y[2 * i] = int8_pair(xf, 0x5140u);
+                                y[2 * i + 1] = int8_pair(xf, 0x7362u);
+                            } else {
+                                y[2 * i] = e4m3_pair_f16(xs[i]);
+                                y[2 * i + 1] = e4m3_pair_f16(xs[i] >> 16);
+                            }
+                        }
+                        uint8_t *row = dst + (ch >> 2) * C::kHalfBytes;
+                        *reinterpret_cast<uint4 *>(row + swz_row<128>(r, (2 * ch) & 7)) = make_uint4(y[0], y[1], y[2], y[3]);
+                        *reinterpret_cast<uint4 *>(row + swz_row<128>(r, (2 * ch + 1) & 7)) = make_uint4(y[4], y[5], y[6], y[7]);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(full + 8 * slot);
+                        mbar_arrive(c_empty + 8 * cs);
+                    }
+                    if (++slot == NS) {
+                        slot = 0;
+                        wrap ^= 1u;
+                    }
+                    if (++cs == C::kCodeSlots) {
+                        cs = 0;
+                        cwrap ^= 1u;
+                    }
+                }
+            }
+        }
+    } else {
+        // ---------------- softmax rows ----------------
+        constexpr int CH = C::kCols;
+        const int blk = warp >> 2, r = (warp & 3) * 32 + lane;
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lane_base + blk * 128, to = tmem + lane_base + 256 + blk * 128;
+        float *row_scale = reinterpret_cast<float *>(smem + C::kOffRow);              // [2][128]
+        float2 *odd_ml = reinterpret_cast<float2 *>(smem + C::kOffRow);               // [128]
+        uint32_t sph = 0, oph = 0, dph = 0;
+        bool began = false;                                 // this CTA starts an item that another finishes
+        int items = 0, tile0 = 0;                          // pieces and tiles so far
+        int vslot = 1;                                     // running number of tile tile0's V in the slots
+        while (w.next(a)) {
+            const bool deal = dealt();
+            const PagedSeq &q = w.sh.q;
+            const int my_blk = deal ? 0 : blk;             // whose rows these are
+            const int local = my_blk * block_rows + r, f = w.rt * a.tile_tokens * a.group + local;
+            const int tok = f / a.group;
+            const bool valid = r < block_rows && f < q.n * a.group;
+            const bool busy = __any_sync(0xffffffffu, valid);
+            float qscale = a.scale_log2;
+            if constexpr (kQTurned) {
+                // this block's queries to F16, unless the other block does it
+                if (my_blk == blk) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(q_full, (uint32_t)items & 1u))) {
+                        if (lane == 0) timed_out();
+                        break;
+                    }
+                    uint8_t *qr = smem + C::kOffQ + blk * C::kSlotBytes;
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int ch = 0; ch < D / 8; ++ch) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(qr + (ch >> 3) * C::kHalfBytes + swz_row<128>(r, ch & 7));
+                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) top = max(top, max(xs[i] & 0x7fffu, (xs[i] >> 16) & 0x7fffu));
+                    }
+                    const int e = min(254, max(1, (int)(top >> 7)));
+                    const float down = e == 254 ? 0x1p-127f : __uint_as_float((uint32_t)(254 - e) << 23);
+                    const float up = __uint_as_float((uint32_t)e << 23);
+#pragma unroll
+                    for (int ch = 0; ch < D / 8; ++ch) {
+                        uint4 *at = reinterpret_cast<uint4 *>(qr + (ch >> 3) * C::kHalfBytes + swz_row<128>(r, ch & 7));
+                        const uint4 x = *at;
+                        uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            xs[i] = pack_half2(__uint_as_float(xs[i] << 16) * down, __uint_as_float(xs[i] & 0xffff0000u) * down);
+                        *at = make_uint4(xs[0], xs[1], xs[2], xs[3]);
+                    }
+                    row_scale[blk * 128 + r] = up;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(q_ready);
+                        if (deal) mbar_arrive(q_ready);
+                    }
+                }
+                if (!__all_sync(0xffffffffu, mbar_wait(q_ready, (uint32_t)items & 1u))) {
+                    if (lane == 0) timed_out();
+                    break;
+                }
+                qscale *= row_scale[my_blk * 128 + r];
+            }
+            ++items;
+            // the queries may go with the last product; in a dealt item only after their memory has
+            // carried the odd tiles' state.  (Every warp arrives once an item, so that no warp falls
+            // a whole item behind the barriers it waits on.)
+            if (!deal && lane == 0) mbar_arrive(q_empty);
+            // what the row sees: [rlo, rhi) and, for a tree, bits from ctx on
+            const int ctx = w.sh.ctx;
+            int rlo = 0, rhi = 0;
+            uint64_t word = 0;
+            if (valid) {
+                if (a.mask == PAGED_CAUSAL) {
+                    rlo = a.window ? max(0, ctx + tok - a.window + 1) : 0;
+                    rhi = min(q.kv, ctx + tok + 1);
+                } else {
+                    rlo = a.window ? max(0, ctx - a.window) : 0;
+                    rhi = a.mask == PAGED_FULL ? q.kv : min(ctx, q.kv);
+                    if (a.mask == PAGED_TREE) word = (uint64_t)a.tree[q.row0 + tok];
+                }
+            }
+            const int all_lo = __reduce_max_sync(0xffffffffu, valid ? rlo : 0);
+            const int all_hi = __reduce_min_sync(0xffffffffu, valid ? rhi : 0x7fffffff);
+            float m = -INFINITY, l = 0.f, vref = 0.f;
+            bool alive = true;
+            const int j0 = deal ? blk : 0, dj = deal ? 2 : 1;
+            for (int j = j0; j < w.nt; j += dj) {
+                const int base = (w.t0 + j) * kPreTile;
+                bool ok = mbar_wait(s_full + 8 * blk, sph);
+                if constexpr (kCodes) {
+                    // the tile's V scales (K's came with S)
+                    const int vn = vslot + 2 * j;
+                    ok = ok && mbar_wait(full + 8 * (vn % NS), (uint32_t)(vn / NS) & 1u);
+                }
+                if (!__all_sync(0xffffffffu, ok)) {
+                    if (lane == 0) timed_out();
+                    alive = false;
+                    break;
+                }
+                sph ^= 1u;
+                tc_fence_after();
+                if (busy) {
+                    const int ring = (tile0 + j) % kScaleRing;
+                    const float4 *ks4 = reinterpret_cast<const float4 *>(smem + C::kOffScale) + ring * 2 * (kPreTile / 4);
+                    const float4 *vs4 = ks4 + kPreTile / 4;
+                    // CH scores of a row at a time, masked; read twice (for the maximum, then for the
+                    // exponentials) rather than held: 128 registers of scores would spill
+                    const bool partly = base < all_lo || base + kPreTile > all_hi;
+                    auto scores = [&](int c, uint64_t (&s)[CH / 2]) {
+                        uint32_t u[CH / 32][32];
+#pragma unroll
+                        for (int i = 0; i < CH / 32; ++i) tmem_ld32(ts + CH * c + 32 * i, u[i]);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < CH / 2; ++e)
+                            s[e] = (uint64_t)u[e >> 4][(2 * e + 1) & 31] << 32 | u[e >> 4][(2 * e) & 31];
+                        if constexpr (kCodes) {
+#pragma unroll
+                            for (int e = 0; e < CH / 4; ++e) {
+                                const float4 k = ks4[c * (CH / 4) + e];
+                                s[2 * e] = mul2(s[2 * e], pk2(k.x, k.y));
+                                s[2 * e + 1] = mul2(s[2 * e + 1], pk2(k.z, k.w));
+                            }
+                        }
+                        if (partly) {
+                            const int at = base + CH * c, lo = rlo - at, tr = ctx - at, n = q.kv - ctx;
+                            const uint32_t wide = (uint32_t)(rhi - rlo);
+#pragma unroll
+                            for (int e = 0; e < CH / 2; ++e) {
+                                float x, y;
+                                upk2(s[e], x, y);
+                                bool vx = (uint32_t)(2 * e - lo) < wide, vy = (uint32_t)(2 * e + 1 - lo) < wide;
+                                if (a.mask == PAGED_TREE) {
+                                    const uint32_t ix = (uint32_t)(2 * e - tr), iy = ix + 1u;
+                                    if (ix < (uint32_t)min(n, 64)) vx = (word >> ix) & 1ull;
+                                    if (iy < (uint32_t)min(n, 64)) vy = (word >> iy) & 1ull;
+                                }
+                                s[e] = pk2(vx ? x : -INFINITY, vy ? y : -INFINITY);
+                            }
+                        }
+                    };
+                    float x0 = -INFINITY, x1 = x0, x2 = x0, x3 = x0;
+#pragma unroll
+                    for (int c = 0; c < 128 / CH; ++c) {
+                        uint64_t s[CH / 2];
+                        scores(c, s);
+#pragma unroll
+                        for (int e = 0; e < CH / 2; e += 2) {
+                            float y0, y1, y2, y3;
+                            upk2(s[e], y0, y1);
+                            upk2(s[e + 1], y2, y3);
+                            x0 = fmaxf(x0, y0);
+                            x1 = fmaxf(x1, y1);
+                            x2 = fmaxf(x2, y2);
+                            x3 = fmaxf(x3, y3);
+                        }
+                    }
+                    const float mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * qscale;
+                    bool move = valid && mx > m + kLazyMove;
+                    float vnew = vref;
+                    if constexpr (kCodes) {
+                        const uint4 t4 = *reinterpret_cast<const uint4 *>(smem + C::kOffTop + ring * 16);
+                        const uint32_t top = max(max(t4.x, t4.y), max(t4.z, t4.w));
+                        // the next power of two above the largest scale, at most 2^127
+                        if (__uint_as_float(top) > vref)
+                            vnew = __uint_as_float(min((top & 0x7f800000u) + 0x00800000u, 0x7f000000u));
+                    }
+                    if (__any_sync(0xffffffffu, move) || vnew != vref) {
+                        const float mnew = move ? mx : m;
+                        float alpha = mnew == -INFINITY || m == mnew ? 1.f : exp2f(m - mnew);
+                        m = mnew;
+                        l *= alpha;
+                        if constexpr (kCodes) {
+                            alpha *= vref / vnew;
+                            vref = vnew;
+                        }
+                        if (j > j0) {
+#pragma unroll
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t u[32];
+                                tmem_ld32(to + 32 * c, u);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
+                                tmem_st32(to + 32 * c, u);
+                            }
+                        }
+                    }
+                    const float mu = m == -INFINITY ? 0.f : m;
+                    const uint64_t scale2 = pk2(qscale, qscale), minus2 = pk2(-mu, -mu);
+                    const float vinv = kCodes && vref > 0.f ? 1.f / vref : 0.f;
+                    const uint64_t vinv2 = pk2(vinv, vinv);
+                    uint64_t sum = pk2(0.f, 0.f), sum1 = sum;
+                    uint32_t u[32];
+#pragma unroll
+                    for (int c = 0; c < 128 / CH; ++c) {
+                        uint64_t s[CH / 2];
+                        scores(c, s);                   // the P of columns 64h .. lies in 32h ..: read by now
+#pragma unroll
+                        for (int e = 0; e < CH / 2; ++e) {
+                            float x, y;
+                            upk2(fma2(s[e], scale2, minus2), x, y);
+                            uint64_t p2 = pk2(ex2_approx(x), ex2_approx(y));
+                            if (e & 1) sum1 = add2(sum1, p2);
+                            else sum = add2(sum, p2);
+                            if constexpr (kCodes) {
+                                const float2 v = reinterpret_cast<const float2 *>(vs4)[c * (CH / 2) + e];
+                                p2 = mul2(p2, mul2(pk2(v.x, v.y), vinv2));
+                            }
+                            upk2(p2, x, y);
+                            u[(c * (CH / 2) + e) & 31] = pack16<OT>(x, y);
+                        }
+                        if ((c + 1) * CH % 64 == 0) tmem_st32(ts + ((c + 1) * CH / 64 - 1) * 32, u);
+                    }
+                    float s0, s1;
+                    upk2(add2(sum, sum1), s0, s1);
+                    l += s0 + s1;
+                    tmem_st_wait();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + 8 * blk);
+            }
+            tile0 += w.nt;
+            vslot += 2 * w.nt;
+            if (!alive || s_abort) break;
+            const bool mine = j0 < w.nt;                   // this block had a tile
+            if (mine) {
+                if (!__all_sync(0xffffffffu, mbar_wait(o_full + 8 * blk, oph))) {
+                    if (lane == 0) timed_out();
+                    break;
+                }
+                oph ^= 1u;
+                tc_fence_after();
+            }
+            // dealt items: the odd tiles' state goes to block 0 through the queries' memory, a column
+            // of 128 rows after the other
+            float *odd = reinterpret_cast<float *>(smem + C::kOffQ);
+            if (deal && w.nt > 1) {
+                if (blk == 1) {
+                    if (busy) {
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t u[32];
+                            tmem_ld32(to + 32 * c, u);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                odd[(32 * c + e) * 128 + r] = kCodes ? __uint_as_float(u[e]) * vref : __uint_as_float(u[e]);
+                        }
+                        odd_ml[r] = make_float2(m, l);
+                    }
+                    tc_fence_before();
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(odd_done);
+                        mbar_arrive(q_empty);
+                    }
+                    continue;
+                }
+                if (!__all_sync(0xffffffffu, mbar_wait(odd_done, dph))) {
+                    if (lane == 0) timed_out();
+                    break;
+                }
+                dph ^= 1u;
+            } else if (deal && blk == 1) {
+                if (lane == 0) mbar_arrive(q_empty);
+                continue;
+            }
+            if (busy) {
+                float keep = 1.f, add = 0.f;               // weights of this block's numerators and the odd ones
+                if (kCodes) keep = vref;
+                if (deal && w.nt > 1) {
+                    const float2 x = odd_ml[r];
+                    const float mm = fmaxf(m, x.x), mu = mm == -INFINITY ? 0.f : mm;
+                    const float e0 = m == -INFINITY ? (l != l ? l : 0.f) : exp2f(m - mu);
+                    add = x.x == -INFINITY ? (x.y != x.y ? x.y : 0.f) : exp2f(x.x - mu);
+                    l = l * e0 + x.y * add;
+                    keep *= e0;
+                    m = mm;
+                }
+                const bool whole = w.first && w.last;
+                const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+                const int head = w.head * a.group + f - tok * a.group;
+                const int64_t part = ((int64_t)blockIdx.x * 2 + (w.first ? 1 : 0)) * a.tile_rows + local;
+                uint16_t *o = a.o + (int64_t)(q.row0 + tok) * a.o_rs + (int64_t)head * a.o_hs;
+                float *acc = a.part_acc + part * D;
+                if (whole) {
+                    keep *= inv;
+                    add *= inv;
+                }
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t u[32];
+                    __syncwarp();
+                    tmem_ld32(to + 32 * c, u);
+                    tmem_ld_wait();
+                    if (!valid) continue;
+                    float x[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(u[e]) * keep;
+                    if (deal && w.nt > 1) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[e] = fmaf(odd[(32 * c + e) * 128 + r], add, x[e]);
+                    }
+                    if (whole) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            *reinterpret_cast<uint4 *>(o + 32 * c + e) =
+                                make_uint4(pack16<T>(x[e], x[e + 1]), pack16<T>(x[e + 2], x[e + 3]),
+                                           pack16<T>(x[e + 4], x[e + 5]), pack16<T>(x[e + 6], x[e + 7]));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4 *>(acc + 32 * c + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                    }
+                }
+                if (valid) {
+                    if (whole) {
+                        if (a.lse)
+                            a.lse[(int64_t)(q.row0 + tok) * a.n_head + head] =
+                                l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                    } else {
+                        a.part_ml[part] = make_float2(m, l);
+                    }
+                }
+                tc_fence_before();
+            }
+            if (deal) {
+                // the queries' memory is free again
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_empty);
+            }
+            if (threadIdx.x == 0 && w.first && !w.last) {
+                began = true;
+                a.desc[blockIdx.x] = make_int4(w.seq, w.head, w.rt, w.last_cta());
+            }
+        }
+        if (threadIdx.x == 0 && !began) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace dflash

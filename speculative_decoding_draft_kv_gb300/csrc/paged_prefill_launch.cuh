@@ -1,0 +1,47 @@
+// Choice and launch of the tensor-core attention kernels of one query type.
+#pragma once
+
+#include "paged_attend_launch.cuh"
+#include "paged_prefill.cuh"
+
+namespace dflash {
+
+template <int T, class F>
+cudaError_t pick_prefill(int head_dim, int format, F &&fn) {
+    auto with = [&](auto d, auto fmt) {
+        using C = PreCfg<d.value, fmt.value>;
+        return fn(k_paged_prefill<d.value, fmt.value, T>, C::kSmem, C::kThreads);
+    };
+    auto dim = [&](auto fmt) {
+        return head_dim == 64 ? with(std::integral_constant<int, 64>{}, fmt) : with(std::integral_constant<int, 128>{}, fmt);
+    };
+    if (format == PAGED_INT8) return dim(std::integral_constant<int, kFmtInt8>{});
+    if (format == PAGED_E4M3) return dim(std::integral_constant<int, kFmtE4m3>{});
+    return dim(std::integral_constant<int, kFmt16>{});
+}
+
+template <int T>
+cudaError_t paged_prefill_setup_t() {
+    auto allow = [](auto kernel, int smem, int) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    };
+    const int formats[3] = {T, PAGED_INT8, PAGED_E4M3};
+    for (int f : formats)
+        for (int d = 64; d <= 128; d += 64) {
+            const cudaError_t e = pick_prefill<T>(d, f, allow);
+            if (e != cudaSuccess) return e;
+        }
+    return cudaSuccess;
+}
+
+template <int T>
+cudaError_t launch_paged_prefill_t(const PagedAttendArgs &a, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
+                                   const CUtensorMap &tm_q, int head_dim, cudaStream_t st) {
+    return pick_prefill<T>(head_dim, a.pool.format, [&](auto kernel, int smem, int threads) {
+        kernel<<<a.ctas, threads, smem, st>>>(tm_k, tm_v, tm_q, a);
+        const cudaError_t e = cudaGetLastError();
+        return e == cudaSuccess ? launch_join<T>(a, a.tile_rows, head_dim, st) : e;
+    });
+}
+
+}  // namespace dflash

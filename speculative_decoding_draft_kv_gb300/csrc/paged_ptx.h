@@ -60,4 +60,28 @@ __device__ __forceinline__ uint32_t e4m3_pair_f16(uint32_t w) {
     return r;
 }
 
+// Shared-memory descriptor of an operand whose rows run along K (K rows of 64 contiguous M or N
+// values each, 128-byte swizzle): atoms of 8 K rows x 128 bytes, 1024 bytes apart along K
+// (stride offset), `lead` bytes apart along M or N (leading offset).
+__device__ __forceinline__ uint64_t tc_desc_mn_sw128(uint32_t addr, uint32_t lead) {
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
+}
+
+// Instruction descriptor of kind::f16 as tc_idesc_f16, for F16 or BF16 operands (formats at bits
+// 7 and 10) and a B operand stored along N (bit 16).
+__host__ __device__ constexpr uint32_t tc_idesc(int m, int n, bool bf16, bool b_along_n) {
+    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_along_n ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(m >> 4) << 24);
+}
+
+// D (TMEM) = A (TMEM) B (+ D), issued by one thread.
+__device__ __forceinline__ void tc_mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(tmem_d), "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
 }  // namespace dflash
