@@ -223,7 +223,7 @@ bool encode_queries(CUtensorMap *tm, const paged_attend_args *g, int head_dim, i
 
 // Which kernel serves a batch, its rows per item and its CTAs: what the workspace and the launch
 // go by.  Up to 32 query rows per kv head: the streaming kernel; more: the tensor-core one, whose
-// items are two blocks of as many whole tokens as 128 rows take.
+// items are one or two blocks of as many whole tokens as 128 rows take.
 // No more CTAs than the bounds leave work for.
 struct AttendPlan {
     int rows, tokens, ctas, min_tiles;
@@ -233,7 +233,8 @@ AttendPlan plan_of(const paged_cache *c, const paged_batch *b, int group, int sm
     const int64_t rows = (int64_t)b->max_q * group;
     AttendPlan p{};
     p.wide = rows > 32;
-    p.rows = rows <= 16 ? 16 : (rows <= 32 ? 32 : 2 * (128 / group) * group);
+    const int block = 128 / group;                                 // whole tokens of a tensor-core block
+    p.rows = rows <= 16 ? 16 : (rows <= 32 ? 32 : (b->max_q <= block ? 1 : 2) * block * group);
     p.tokens = p.wide ? p.rows / group : std::max(1, b->max_q);
     p.min_tiles = p.wide ? 1 : 2;
     const int64_t keys = b->max_kv > 0 ? b->max_kv : (int64_t)b->max_pages * c->page_size;

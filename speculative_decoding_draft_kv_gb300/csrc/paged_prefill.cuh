@@ -14,13 +14,16 @@
 // S1 = Q1 K': the tensor pipe runs them in that order, so S may overwrite the P that the product
 // in front of it reads, and a block's S being there means its O is up to date.
 //
-// The softmax reference moves only when a row outgrows it by 2^8 (see paged_attend.cuh), so O is
-// read back and rescaled in few tiles.
+// The softmax reference moves only when a row outgrows it by 2^15 (probabilities up to there are as
+// exact in F16 as smaller ones): a row of scores is read once, a piece at a time, its piece's
+// maximum compared, its probabilities made and written back.  The move, in few tiles after a row's
+// first, is by a whole power of two and takes along the sums, O, and the probabilities of the
+// tile's earlier pieces.
 //
 // An item of at most 128 rows (a verify block, a tree, a single token in a mixed batch) fills one
 // block only: then both blocks take the same queries, block 0 the even key tiles and block 1 the
-// odd ones, so that products and exponentials still take turns, and the two states join in shared
-// memory at the end.
+// odd ones, so that products and exponentials still take turns, and block 0 joins the two states at
+// the end.  A batch with no larger item runs the variant with memory for one block of queries.
 //
 // Quantised pages: four more warps turn code tiles into F16 tiles in shared memory (a thread per
 // key), exactly; scales are applied where the streaming kernel applies them, K's to the scores,
@@ -36,29 +39,31 @@
 namespace dflash {
 
 constexpr int kPreTile = 128;
+// how far (log2) a score may pass the reference before that moves: 2^15 is within F16
+constexpr float kFarMove = 15.f;
 constexpr int kScaleRing = 8;            // key tiles whose scales are kept (see below)
 
-template <int D, int FMT>
+template <int D, int FMT, bool ONE>
 struct PreCfg {
     static constexpr bool kCodes = FMT != kFmt16;
     static constexpr int kThreads = kCodes ? 448 : 320;
     static constexpr int kHalves = D / 64;                       // 128-byte columns of a 16-bit row
     static constexpr int kHalfBytes = kPreTile * 128;
     static constexpr int kSlotBytes = kHalves * kHalfBytes;      // 128 rows of D 16-bit values
-    static constexpr int kSlots = kCodes ? (D == 128 ? 3 : 4) : (D == 128 ? 5 : 8);   // K and V tiles in turn
+    static constexpr int kBlocks = ONE ? 1 : 2;                  // of queries
+    // K and V tiles in turn: what fits
+    static constexpr int kSlots = kCodes ? (D == 128 && !ONE ? 3 : 4) : (D == 128 ? (ONE ? 6 : 5) : 10);
     static constexpr int kCodeBytes = kPreTile * D;
     static constexpr int kCodeSlots = kCodes ? 3 : 0;
     static constexpr int kOffQ = kSlots * kSlotBytes;
-    static constexpr int kOffCodes = kOffQ + 2 * kSlotBytes;
+    static constexpr int kOffCodes = kOffQ + kBlocks * kSlotBytes;
     static constexpr int kOffCodeScale = kOffCodes + kCodeSlots * kCodeBytes;   // as loaded, per code slot
     static constexpr int kOffScale = kOffCodeScale + kCodeSlots * kPreTile * 4;  // [ring][K, V][128]
     static constexpr int kOffTop = kOffScale + (kCodes ? kScaleRing * 2 * kPreTile * 4 : 0);   // [ring][4]
     static constexpr int kOffRow = kOffTop + (kCodes ? kScaleRing * 16 : 0);     // row values
     static constexpr int kOffBars = kOffRow + 128 * 8;
-    static constexpr int kSmem = 1024 + kOffBars + 256;
-    static constexpr int kCols = kCodes ? 32 : 64;               // scores of a row in registers at once
+    static constexpr int kSmem = 1024 + kOffBars + 384;
     static_assert(kSmem <= 227 * 1024, "one CTA per SM");
-    static_assert(2 * kSlotBytes == 128 * D * 4, "a block's numerators fit where the queries were");
 };
 
 // two float32 at a time
@@ -84,11 +89,22 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     return r;
 }
 
-template <int D, int FMT, int T>
-__global__ void __launch_bounds__(PreCfg<D, FMT>::kThreads, 1)
+// two 16-bit values times a float32 factor (which may lie below their own type's range)
+template <int T>
+__device__ __forceinline__ uint32_t scale16(uint32_t x, float by) {
+    if constexpr (T == PAGED_F16) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x));
+        return pack_half2(f.x * by, f.y * by);
+    } else {
+        return pack_bf162(__uint_as_float(x << 16) * by, __uint_as_float(x & 0xffff0000u) * by);
+    }
+}
+
+template <int D, int FMT, int T, bool ONE>
+__global__ void __launch_bounds__(PreCfg<D, FMT, ONE>::kThreads, 1)
 k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                 const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ PagedAttendArgs a) {
-    using C = PreCfg<D, FMT>;
+    using C = PreCfg<D, FMT, ONE>;
     constexpr int NS = C::kSlots;
     constexpr bool kCodes = C::kCodes;
     constexpr int OT = kCodes ? PAGED_F16 : T;                       // operand type
@@ -103,8 +119,8 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     const uint32_t full = bars, empty = bars + 8 * NS;               // [NS] each
     const uint32_t q_full = bars + 16 * NS, q_empty = q_full + 8, q_ready = q_full + 16;
     const uint32_t s_full = q_full + 24, p_full = s_full + 16, o_full = p_full + 16;   // [2] each
-    const uint32_t landed = o_full + 16, drain = landed + 8, odd_done = landed + 16;
-    const uint32_t c_full = landed + 24, c_empty = c_full + 8 * 3;   // [3] each
+    const uint32_t landed = o_full + 16, drain = landed + 8, odd_done = landed + 16, odd_free = landed + 24;
+    const uint32_t c_full = landed + 32, c_empty = c_full + 8 * 3;   // [3] each
     __shared__ int64_t s_plan[18];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
@@ -129,6 +145,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         mbar_init(landed, 1);
         mbar_init(drain, 1);
         mbar_init(odd_done, 4);
+        mbar_init(odd_free, 4);
         for (int k = 0; k < C::kCodeSlots; ++k) {
             mbar_init(c_full + 8 * k, 33);
             mbar_init(c_empty + 8 * k, 4);
@@ -146,7 +163,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     const PagedShare share = paged_share<kPreTile, C::kThreads>(a, s_plan);   // synchronises
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    const int block_tokens = a.tile_tokens / 2, block_rows = block_tokens * a.group;
+    const int block_tokens = a.tile_tokens / C::kBlocks, block_rows = block_tokens * a.group;
     auto timed_out = [&]() {
         atomicOr(a.err, (uint32_t)PAGED_ERR_WAIT);
         s_abort = 1;
@@ -155,7 +172,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     PagedWalk<kPreTile> w;
     w.init(a, share);
     // the item has rows for one block only: its key tiles are dealt to both
-    auto dealt = [&]() { return w.sh.q.n - w.rt * a.tile_tokens <= block_tokens; };
+    auto dealt = [&]() { return ONE || w.sh.q.n - w.rt * a.tile_tokens <= block_tokens; };
     // some position of key tile t that no token of the sequence sees (its V row is cleared)
     auto ragged = [&](int t) {
         const int base = t * kPreTile;
@@ -402,9 +419,9 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         __syncwarp();
     } else if (kCodes && warp >= 10) {
         // ---------------- codes to F16 ----------------
-        // The ring of scales needs no barrier of its own: with 3 or 4 F16 slots and 3 code slots the
-        // tile at hand here is less than 6 tiles ahead of the one that the slower block's rows read
-        // (its V slot and all later ones are taken).
+        // The ring of scales needs no barrier of its own: the V slot of the tile that the slower
+        // block's rows are at is taken, and with it every later one, so with 3 or 4 slots the tile
+        // at hand here is at most 2 ahead of that one.
         const int r = (int)threadIdx.x - 320;              // the thread's key
         int slot = 0, cs = 0;
         uint32_t wrap = 0, cwrap = 0;
@@ -473,18 +490,28 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         }
     } else {
         // ---------------- softmax rows ----------------
-        constexpr int CH = C::kCols;
+        constexpr int CH = 32;                             // scores of a row at a time: more would spill
         const int blk = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lane_base + blk * 128, to = tmem + lane_base + 256 + blk * 128;
         float *row_scale = reinterpret_cast<float *>(smem + C::kOffRow);              // [2][128]
         float2 *odd_ml = reinterpret_cast<float2 *>(smem + C::kOffRow);               // [128]
+        float *odd_ref = reinterpret_cast<float *>(smem + C::kOffBars + 376);
         uint32_t sph = 0, oph = 0, dph = 0;
         bool began = false;                                 // this CTA starts an item that another finishes
+        bool owed = false;                                 // block 0 has yet to read this block's state
         int items = 0, tile0 = 0;                          // pieces and tiles so far
         int vslot = 1;                                     // running number of tile tile0's V in the slots
         while (w.next(a)) {
             const bool deal = dealt();
+            if (owed) {
+                if (!__all_sync(0xffffffffu, mbar_wait(odd_free, dph))) {
+                    if (lane == 0) timed_out();
+                    break;
+                }
+                dph ^= 1u;
+                owed = false;
+            }
             const PagedSeq &q = w.sh.q;
             const int my_blk = deal ? 0 : blk;             // whose rows these are
             const int local = my_blk * block_rows + r, f = w.rt * a.tile_tokens * a.group + local;
@@ -536,10 +563,9 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 qscale *= row_scale[my_blk * 128 + r];
             }
             ++items;
-            // the queries may go with the last product; in a dealt item only after their memory has
-            // carried the odd tiles' state.  (Every warp arrives once an item, so that no warp falls
-            // a whole item behind the barriers it waits on.)
-            if (!deal && lane == 0) mbar_arrive(q_empty);
+            // the queries may go with the last product.  (Every warp arrives once an item, so that no
+            // warp falls a whole item behind the barriers it waits on.)
+            if (lane == 0) mbar_arrive(q_empty);
             // what the row sees: [rlo, rhi) and, for a tree, bits from ctx on
             const int ctx = w.sh.ctx;
             int rlo = 0, rhi = 0;
@@ -578,17 +604,16 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     const int ring = (tile0 + j) % kScaleRing;
                     const float4 *ks4 = reinterpret_cast<const float4 *>(smem + C::kOffScale) + ring * 2 * (kPreTile / 4);
                     const float4 *vs4 = ks4 + kPreTile / 4;
-                    // CH scores of a row at a time, masked; read twice (for the maximum, then for the
-                    // exponentials) rather than held: 128 registers of scores would spill
+                    uint32_t raw[2][CH];                   // a piece at hand and, with registers to spare, the next
+                    // CH scores of the row, masked
                     const bool partly = base < all_lo || base + kPreTile > all_hi;
                     auto scores = [&](int c, uint64_t (&s)[CH / 2]) {
-                        uint32_t u[CH / 32][32];
-#pragma unroll
-                        for (int i = 0; i < CH / 32; ++i) tmem_ld32(ts + CH * c + 32 * i, u[i]);
+                        if (kCodes || c == 0) tmem_ld32(ts + CH * c, raw[c & 1]);
                         tmem_ld_wait();
+                        if (!kCodes && c + 1 < 128 / CH) tmem_ld32(ts + CH * (c + 1), raw[(c + 1) & 1]);
 #pragma unroll
                         for (int e = 0; e < CH / 2; ++e)
-                            s[e] = (uint64_t)u[e >> 4][(2 * e + 1) & 31] << 32 | u[e >> 4][(2 * e) & 31];
+                            s[e] = pk2(__uint_as_float(raw[c & 1][2 * e]), __uint_as_float(raw[c & 1][2 * e + 1]));
                         if constexpr (kCodes) {
 #pragma unroll
                             for (int e = 0; e < CH / 4; ++e) {
@@ -614,81 +639,85 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                             }
                         }
                     };
-                    float x0 = -INFINITY, x1 = x0, x2 = x0, x3 = x0;
+                    // O times a factor per row
+                    auto rescale = [&](float by) {
+#pragma unroll 1
+                        for (int c = 0; c < D / 16; ++c) {     // rare: small pieces spare registers
+                            uint32_t u[16];
+                            tmem_ld16(to + 16 * c, u);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * by);
+                            tmem_st16(to + 16 * c, u);
+                        }
+                    };
+                    if constexpr (kCodes) {
+                        // the numerators' power of two: the next one above the largest scale
+                        const uint4 t4 = *reinterpret_cast<const uint4 *>(smem + C::kOffTop + ring * 16);
+                        const uint32_t top = max(max(t4.x, t4.y), max(t4.z, t4.w));
+                        if (__uint_as_float(top) > vref) {
+                            const float vnew = __uint_as_float(min((top & 0x7f800000u) + 0x00800000u, 0x7f000000u));
+                            if (j > j0) rescale(vref / vnew);
+                            vref = vnew;
+                        }
+                    }
+                    const float vinv = kCodes && vref > 0.f ? 1.f / vref : 0.f;
+                    const uint64_t scale2 = pk2(qscale, qscale), vinv2 = pk2(vinv, vinv);
+                    uint64_t sa = pk2(0.f, 0.f), sb = sa;
 #pragma unroll
                     for (int c = 0; c < 128 / CH; ++c) {
                         uint64_t s[CH / 2];
                         scores(c, s);
+                        float x0 = -INFINITY, x1 = x0;
 #pragma unroll
-                        for (int e = 0; e < CH / 2; e += 2) {
-                            float y0, y1, y2, y3;
+                        for (int e = 0; e < CH / 2; ++e) {
+                            float y0, y1;
                             upk2(s[e], y0, y1);
-                            upk2(s[e + 1], y2, y3);
                             x0 = fmaxf(x0, y0);
                             x1 = fmaxf(x1, y1);
-                            x2 = fmaxf(x2, y2);
-                            x3 = fmaxf(x3, y3);
                         }
-                    }
-                    const float mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * qscale;
-                    bool move = valid && mx > m + kLazyMove;
-                    float vnew = vref;
-                    if constexpr (kCodes) {
-                        const uint4 t4 = *reinterpret_cast<const uint4 *>(smem + C::kOffTop + ring * 16);
-                        const uint32_t top = max(max(t4.x, t4.y), max(t4.z, t4.w));
-                        // the next power of two above the largest scale, at most 2^127
-                        if (__uint_as_float(top) > vref)
-                            vnew = __uint_as_float(min((top & 0x7f800000u) + 0x00800000u, 0x7f000000u));
-                    }
-                    if (__any_sync(0xffffffffu, move) || vnew != vref) {
-                        const float mnew = move ? mx : m;
-                        float alpha = mnew == -INFINITY || m == mnew ? 1.f : exp2f(m - mnew);
-                        m = mnew;
-                        l *= alpha;
-                        if constexpr (kCodes) {
-                            alpha *= vref / vnew;
-                            vref = vnew;
-                        }
-                        if (j > j0) {
-#pragma unroll
-                            for (int c = 0; c < D / 32; ++c) {
-                                uint32_t u[32];
-                                tmem_ld32(to + 32 * c, u);
+                        const float mx = fmaxf(x0, x1) * qscale;
+                        const bool far = valid && mx > m + kFarMove;
+                        if (__any_sync(0xffffffffu, far)) {
+                            // the reference moves, by a whole power of two that P takes exactly
+                            const float mnew = far ? (m == -INFINITY ? mx : m + ceilf(mx - m)) : m;
+                            const float alpha = far ? exp2f(m - mnew) : 1.f;
+                            m = mnew;
+                            sa = mul2(sa, pk2(alpha, alpha));
+                            sb = mul2(sb, pk2(alpha, alpha));
+                            l *= alpha;
+                            if (j > j0) rescale(alpha);
+#pragma unroll 1
+                            for (int cc = 0; cc < c * CH / 32; ++cc) {
+                                uint32_t u[16];
+                                tmem_ld16(ts + 16 * cc, u);
                                 tmem_ld_wait();
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
-                                tmem_st32(to + 32 * c, u);
+                                for (int e = 0; e < 16; ++e) u[e] = scale16<OT>(u[e], alpha);
+                                tmem_st16(ts + 16 * cc, u);
                             }
                         }
-                    }
-                    const float mu = m == -INFINITY ? 0.f : m;
-                    const uint64_t scale2 = pk2(qscale, qscale), minus2 = pk2(-mu, -mu);
-                    const float vinv = kCodes && vref > 0.f ? 1.f / vref : 0.f;
-                    const uint64_t vinv2 = pk2(vinv, vinv);
-                    uint64_t sum = pk2(0.f, 0.f), sum1 = sum;
-                    uint32_t u[32];
-#pragma unroll
-                    for (int c = 0; c < 128 / CH; ++c) {
-                        uint64_t s[CH / 2];
-                        scores(c, s);                   // the P of columns 64h .. lies in 32h ..: read by now
+                        const float mu = m == -INFINITY ? 0.f : m;
+                        const uint64_t minus2 = pk2(-mu, -mu);
+                        uint32_t u[CH / 2];
 #pragma unroll
                         for (int e = 0; e < CH / 2; ++e) {
                             float x, y;
                             upk2(fma2(s[e], scale2, minus2), x, y);
                             uint64_t p2 = pk2(ex2_approx(x), ex2_approx(y));
-                            if (e & 1) sum1 = add2(sum1, p2);
-                            else sum = add2(sum, p2);
+                            if (e & 1) sb = add2(sb, p2);
+                            else sa = add2(sa, p2);
                             if constexpr (kCodes) {
                                 const float2 v = reinterpret_cast<const float2 *>(vs4)[c * (CH / 2) + e];
                                 p2 = mul2(p2, mul2(pk2(v.x, v.y), vinv2));
                             }
                             upk2(p2, x, y);
-                            u[(c * (CH / 2) + e) & 31] = pack16<OT>(x, y);
+                            u[e] = pack16<OT>(x, y);
                         }
-                        if ((c + 1) * CH % 64 == 0) tmem_st32(ts + ((c + 1) * CH / 64 - 1) * 32, u);
+                        tmem_st(ts + c * (CH / 2), u);     // over scores that have been read
                     }
                     float s0, s1;
-                    upk2(add2(sum, sum1), s0, s1);
+                    upk2(add2(sa, sb), s0, s1);
                     l += s0 + s1;
                     tmem_st_wait();
                 }
@@ -708,45 +737,32 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 oph ^= 1u;
                 tc_fence_after();
             }
-            // dealt items: the odd tiles' state goes to block 0 through the queries' memory, a column
-            // of 128 rows after the other
-            float *odd = reinterpret_cast<float *>(smem + C::kOffQ);
-            if (deal && w.nt > 1) {
-                if (blk == 1) {
-                    if (busy) {
-#pragma unroll
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t u[32];
-                            tmem_ld32(to + 32 * c, u);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                odd[(32 * c + e) * 128 + r] = kCodes ? __uint_as_float(u[e]) * vref : __uint_as_float(u[e]);
-                        }
-                        odd_ml[r] = make_float2(m, l);
-                    }
+            // dealt items: block 0 joins the two states; both blocks' lanes are the same, so it reads
+            // the odd tiles' numerators where they are
+            if (deal && blk == 1) {
+                if (w.nt > 1) {
+                    odd_ml[r] = make_float2(m, l);
+                    if (kCodes && threadIdx.x == 128) *odd_ref = vref;
                     tc_fence_before();
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(odd_done);
-                        mbar_arrive(q_empty);
-                    }
-                    continue;
+                    if (lane == 0) mbar_arrive(odd_done);
+                    owed = true;
                 }
+                continue;
+            }
+            const bool joins = deal && w.nt > 1;
+            if (joins) {
                 if (!__all_sync(0xffffffffu, mbar_wait(odd_done, dph))) {
                     if (lane == 0) timed_out();
                     break;
                 }
                 dph ^= 1u;
-            } else if (deal && blk == 1) {
-                if (lane == 0) mbar_arrive(q_empty);
-                continue;
+                tc_fence_after();
             }
             if (busy) {
                 float keep = 1.f, add = 0.f;               // weights of this block's numerators and the odd ones
                 if (kCodes) keep = vref;
-                if (deal && w.nt > 1) {
+                if (joins) {
                     const float2 x = odd_ml[r];
                     const float mm = fmaxf(m, x.x), mu = mm == -INFINITY ? 0.f : mm;
                     const float e0 = m == -INFINITY ? (l != l ? l : 0.f) : exp2f(m - mu);
@@ -754,6 +770,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     l = l * e0 + x.y * add;
                     keep *= e0;
                     m = mm;
+                    if (kCodes) add *= *odd_ref;
                 }
                 const bool whole = w.first && w.last;
                 const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
@@ -767,17 +784,18 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 }
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
-                    uint32_t u[32];
+                    uint32_t u[32], v[32];
                     __syncwarp();
                     tmem_ld32(to + 32 * c, u);
+                    if (joins) tmem_ld32(to + 128 + 32 * c, v);
                     tmem_ld_wait();
                     if (!valid) continue;
                     float x[32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(u[e]) * keep;
-                    if (deal && w.nt > 1) {
+                    if (joins) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] = fmaf(odd[(32 * c + e) * 128 + r], add, x[e]);
+                        for (int e = 0; e < 32; ++e) x[e] = fmaf(__uint_as_float(v[e]), add, x[e]);
                     }
                     if (whole) {
 #pragma unroll
@@ -802,11 +820,10 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 }
                 tc_fence_before();
             }
-            if (deal) {
-                // the queries' memory is free again
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            if (joins) {
+                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(q_empty);
+                if (lane == 0) mbar_arrive(odd_free);
             }
             if (threadIdx.x == 0 && w.first && !w.last) {
                 began = true;

@@ -6,14 +6,16 @@
 
 namespace dflash {
 
+// one: every item fits a block
 template <int T, class F>
-cudaError_t pick_prefill(int head_dim, int format, F &&fn) {
-    auto with = [&](auto d, auto fmt) {
-        using C = PreCfg<d.value, fmt.value>;
-        return fn(k_paged_prefill<d.value, fmt.value, T>, C::kSmem, C::kThreads);
+cudaError_t pick_prefill(int head_dim, int format, bool one, F &&fn) {
+    auto with = [&](auto d, auto fmt, auto single) {
+        using C = PreCfg<d.value, fmt.value, single.value>;
+        return fn(k_paged_prefill<d.value, fmt.value, T, single.value>, C::kSmem, C::kThreads);
     };
+    auto blocks = [&](auto d, auto fmt) { return one ? with(d, fmt, std::true_type{}) : with(d, fmt, std::false_type{}); };
     auto dim = [&](auto fmt) {
-        return head_dim == 64 ? with(std::integral_constant<int, 64>{}, fmt) : with(std::integral_constant<int, 128>{}, fmt);
+        return head_dim == 64 ? blocks(std::integral_constant<int, 64>{}, fmt) : blocks(std::integral_constant<int, 128>{}, fmt);
     };
     if (format == PAGED_INT8) return dim(std::integral_constant<int, kFmtInt8>{});
     if (format == PAGED_E4M3) return dim(std::integral_constant<int, kFmtE4m3>{});
@@ -27,17 +29,18 @@ cudaError_t paged_prefill_setup_t() {
     };
     const int formats[3] = {T, PAGED_INT8, PAGED_E4M3};
     for (int f : formats)
-        for (int d = 64; d <= 128; d += 64) {
-            const cudaError_t e = pick_prefill<T>(d, f, allow);
-            if (e != cudaSuccess) return e;
-        }
+        for (int d = 64; d <= 128; d += 64)
+            for (int one = 0; one < 2; ++one) {
+                const cudaError_t e = pick_prefill<T>(d, f, one != 0, allow);
+                if (e != cudaSuccess) return e;
+            }
     return cudaSuccess;
 }
 
 template <int T>
 cudaError_t launch_paged_prefill_t(const PagedAttendArgs &a, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                                    const CUtensorMap &tm_q, int head_dim, cudaStream_t st) {
-    return pick_prefill<T>(head_dim, a.pool.format, [&](auto kernel, int smem, int threads) {
+    return pick_prefill<T>(head_dim, a.pool.format, a.tile_rows <= 128, [&](auto kernel, int smem, int threads) {
         kernel<<<a.ctas, threads, smem, st>>>(tm_k, tm_v, tm_q, a);
         const cudaError_t e = cudaGetLastError();
         return e == cudaSuccess ? launch_join<T>(a, a.tile_rows, head_dim, st) : e;
