@@ -104,8 +104,8 @@ k_paged_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     }
     pdl_trigger();                       // the join may settle; it waits for this grid's end
     const PagedShare share = paged_share<kDecTile, C::kThreads>(a, s_plan);
-    if (threadIdx.x == 0 && share.begin >= share.end) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    if (share.begin >= share.end) return;
+    if (threadIdx.x == 0 && share.tiles == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (share.tiles == 0) return;
 
     PagedWalk<kDecTile> w;
     w.init(a, share);
@@ -119,7 +119,7 @@ k_paged_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         const int boxes = nb * C::kHalves;                     // per tensor
         bool alive = true;
         while (alive && w.next(a)) {
-            const int hi = w.sh.hi(w.rt), lo = w.sh.lo(w.rt);
+            const int hi = w.sh.hi(a, w.rt), lo = w.sh.lo(a, w.rt);
             const int64_t row = (int64_t)w.seq * a.batch.pages_stride;
             // lane b: the page of box b of tile t (-1: not needed, or not to be had)
             auto lookup = [&](int t) {
@@ -261,7 +261,7 @@ k_paged_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         int rlo[2], rhi[2];
         uint64_t word[2] = {0ull, 0ull};
         int all_lo = 0, all_hi = 0x7fffffff;
-        const int ctx = w.sh.ctx, item_lo = w.sh.lo(w.rt), item_hi = w.sh.hi(w.rt);
+        const int ctx = w.sh.ctx, item_lo = w.sh.lo(a, w.rt), item_hi = w.sh.hi(a, w.rt);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int f = j ? r1 : r0, tok = f / a.group;

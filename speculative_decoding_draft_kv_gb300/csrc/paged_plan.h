@@ -42,53 +42,53 @@ __device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, in
     }
 }
 
-// Row tiles and key ranges of one sequence: TT tokens a row tile, KT keys a key tile.
+// Row tiles and key ranges of one sequence: a.tile_tokens tokens a row tile, KT keys a key tile.
 template <int KT>
 struct PagedShape {
     PagedSeq q;
-    int tokens, mask, window, ctx, heads;
+    int ctx;
 
     // a sequence whose lengths contradict each other has no tiles: its rows stay as they are
     __device__ __forceinline__ void load(const PagedAttendArgs &a, int s) {
         q = paged_seq(a.batch, a.pool.page_shift, s);
         q.ok = q.ok && q.n <= a.max_q;
         if (!q.ok) q.n = 0;
-        tokens = a.tile_tokens;
-        mask = a.mask;
-        window = a.window;
         ctx = q.kv - q.n;
-        heads = a.pool.n_head_kv;
     }
-    __device__ __forceinline__ int row_tiles() const { return (q.n + tokens - 1) / tokens; }
+    __device__ __forceinline__ int row_tiles(const PagedAttendArgs &a) const {
+        return (q.n + a.tile_tokens - 1) / a.tile_tokens;
+    }
     // positions that some row of the tile sees lie in [lo, hi); 0 <= lo < hi
-    __device__ __forceinline__ int lo(int rt) const {
-        if (window == 0) return 0;
-        return max(0, mask == PAGED_CAUSAL ? ctx + rt * tokens - window + 1 : ctx - window);
+    __device__ __forceinline__ int lo(const PagedAttendArgs &a, int rt) const {
+        if (a.window == 0) return 0;
+        return max(0, a.mask == PAGED_CAUSAL ? ctx + rt * a.tile_tokens - a.window + 1 : ctx - a.window);
     }
-    __device__ __forceinline__ int hi(int rt) const {
-        return mask == PAGED_CAUSAL ? min(q.kv, ctx + (rt + 1) * tokens) : q.kv;
+    __device__ __forceinline__ int hi(const PagedAttendArgs &a, int rt) const {
+        return a.mask == PAGED_CAUSAL ? min(q.kv, ctx + (rt + 1) * a.tile_tokens) : q.kv;
     }
-    __device__ __forceinline__ int tile0(int rt) const { return lo(rt) / KT; }
-    __device__ __forceinline__ int tiles(int rt) const { return (hi(rt) + KT - 1) / KT - lo(rt) / KT; }
-    __device__ __forceinline__ int64_t head_tiles() const {
-        const int n = row_tiles();
+    __device__ __forceinline__ int tile0(const PagedAttendArgs &a, int rt) const { return lo(a, rt) / KT; }
+    __device__ __forceinline__ int tiles(const PagedAttendArgs &a, int rt) const {
+        return (hi(a, rt) + KT - 1) / KT - lo(a, rt) / KT;
+    }
+    __device__ __forceinline__ int64_t head_tiles(const PagedAttendArgs &a) const {
+        const int n = row_tiles(a);
         if (n == 0) return 0;
-        if (n == 1 || mask != PAGED_CAUSAL) return (int64_t)n * tiles(0);
+        if (n == 1 || a.mask != PAGED_CAUSAL) return (int64_t)n * tiles(a, 0);
         // ceil(hi / KT) of all row tiles but the last, whose hi is kv ...
-        int64_t w = floor_sum(n - 1, KT, tokens, ctx + tokens + KT - 1) + (q.kv + KT - 1) / KT;
+        int64_t w = floor_sum(n - 1, KT, a.tile_tokens, ctx + a.tile_tokens + KT - 1) + (q.kv + KT - 1) / KT;
         // ... less floor(lo / KT) of those whose lo is above 0
-        if (window) {
-            const int64_t first = ctx - window + 1;
-            const int64_t i0 = first >= 0 ? 0 : (-first + tokens - 1) / tokens;
-            if (i0 < n) w -= floor_sum(n - i0, KT, tokens, first + i0 * tokens);
+        if (a.window) {
+            const int64_t first = ctx - a.window + 1;
+            const int64_t i0 = first >= 0 ? 0 : (-first + a.tile_tokens - 1) / a.tile_tokens;
+            if (i0 < n) w -= floor_sum(n - i0, KT, a.tile_tokens, first + i0 * a.tile_tokens);
         }
         return w;
     }
 };
 
 struct PagedShare {
-    int64_t begin, end, seq_begin;   // this CTA's tiles, and the first tile of sequence seq
-    int64_t per;                     // tiles per CTA
+    int64_t rem;                     // the CTA's first tile, counted from sequence seq's first
+    int tiles, per;                  // this CTA's tiles, and those of a full share
     int seq;
 };
 
@@ -106,7 +106,7 @@ __device__ __forceinline__ PagedShare paged_share(const PagedAttendArgs &a, int6
     for (int s = s0; s < s1; ++s) {
         sh.load(a, s);
         ok = ok && sh.q.ok;
-        sum += sh.head_tiles() * sh.heads;
+        sum += sh.head_tiles(a) * a.pool.n_head_kv;
     }
     if (!ok && blockIdx.x == 0) atomicOr(a.err, (uint32_t)PAGED_ERR_PAGE);
     int64_t incl = sum;
@@ -125,17 +125,16 @@ __device__ __forceinline__ PagedShare paged_share(const PagedAttendArgs &a, int6
         total += scratch[w];
     }
     const int64_t mine = base + incl - sum;       // tiles in front of this thread's sequences
-    PagedShare r;
-    r.per = max((int64_t)a.min_tiles, (total + a.ctas - 1) / a.ctas);
-    r.begin = min(total, (int64_t)blockIdx.x * r.per);
-    r.end = min(total, r.begin + r.per);
-    if (r.begin < r.end && mine <= r.begin && r.begin < mine + sum) {
+    // a share of 2^31 tiles would take hours: 32 bits are enough for one
+    const int64_t per = max((int64_t)a.min_tiles, (total + a.ctas - 1) / a.ctas);
+    const int64_t begin = min(total, (int64_t)blockIdx.x * per), end = min(total, begin + per);
+    if (begin < end && mine <= begin && begin < mine + sum) {
         int64_t at = mine;
         for (int s = s0; s < s1; ++s) {
             sh.load(a, s);
-            const int64_t w = sh.head_tiles() * sh.heads;
-            if (r.begin < at + w) {
-                scratch[WARPS] = at;
+            const int64_t w = sh.head_tiles(a) * a.pool.n_head_kv;
+            if (begin < at + w) {
+                scratch[WARPS] = begin - at;
                 scratch[WARPS + 1] = s;
                 break;
             }
@@ -143,9 +142,11 @@ __device__ __forceinline__ PagedShare paged_share(const PagedAttendArgs &a, int6
         }
     }
     __syncthreads();
-    r.seq_begin = scratch[WARPS];
+    PagedShare r;
+    r.rem = scratch[WARPS];
     r.seq = (int)scratch[WARPS + 1];
-    if (r.seq < 0) r.end = r.begin;
+    r.tiles = r.seq < 0 ? 0 : (int)(end - begin);
+    r.per = (int)per;
     return r;
 }
 
@@ -154,28 +155,27 @@ __device__ __forceinline__ PagedShare paged_share(const PagedAttendArgs &a, int6
 template <int KT>
 struct PagedWalk {
     PagedShape<KT> sh;
-    int64_t cur, end, per;
+    int left, per;                   // tiles to come
     int seq, head, rt, off;          // the item, and the tile of it that comes next
     // the piece at hand
-    int t0, nt, item_tiles;          // first key tile (absolute), their number; the item's
+    int t0, nt, rest;                // first key tile (absolute), their number; the item's beyond them
     bool first, last;                // the piece has the item's first / last tile
 
     __device__ __forceinline__ void init(const PagedAttendArgs &a, const PagedShare &r) {
-        cur = r.begin;
-        end = r.end;
+        left = r.tiles;
         per = r.per;
         seq = r.seq;
         head = rt = off = 0;
-        if (cur >= end) return;
+        if (left == 0) return;
         sh.load(a, seq);
-        const int64_t per_head = sh.head_tiles();
-        int64_t rem = cur - r.seq_begin;
+        const int64_t per_head = sh.head_tiles(a);
+        int64_t rem = r.rem;
         head = (int)(rem / per_head);
         rem -= head * per_head;
         // the row tile that holds tile rem of the head, 32 row tiles at a time
-        const int lane = threadIdx.x & 31, n = sh.row_tiles();
+        const int lane = threadIdx.x & 31, n = sh.row_tiles(a);
         while (true) {
-            const int mine = rt + lane < n ? sh.tiles(rt + lane) : 0;
+            const int mine = rt + lane < n ? sh.tiles(a, rt + lane) : 0;
             int64_t incl = mine;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -192,18 +192,18 @@ struct PagedWalk {
             rem -= __shfl_sync(0xffffffffu, incl, 31);
             rt += 32;
             if (rt >= n) {                           // not reached: rem < per_head
-                end = cur;
+                left = 0;
                 return;
             }
         }
     }
     __device__ __forceinline__ bool next(const PagedAttendArgs &a) {
-        if (cur >= end) return false;
+        if (left <= 0) return false;
         if (off < 0) {                               // the item before this one is done
             off = 0;
-            if (++rt >= sh.row_tiles()) {
+            if (++rt >= sh.row_tiles(a)) {
                 rt = 0;
-                if (++head >= sh.heads) {
+                if (++head >= a.pool.n_head_kv) {
                     head = 0;
                     do {
                         if (++seq >= a.batch.n_seq) return false;
@@ -212,19 +212,18 @@ struct PagedWalk {
                 }
             }
         }
-        item_tiles = sh.tiles(rt);
-        t0 = sh.tile0(rt) + off;
-        nt = (int)min((int64_t)(item_tiles - off), end - cur);
+        const int item = sh.tiles(a, rt);
+        t0 = sh.tile0(a, rt) + off;
+        nt = min(item - off, left);
         first = off == 0;
-        last = off + nt == item_tiles;
-        cur += nt;
+        rest = item - off - nt;
+        last = rest == 0;
+        left -= nt;
         off = last ? -1 : off + nt;
         return true;
     }
-    // the CTA that has the item's last tile, for the piece at hand (off already advanced)
-    __device__ __forceinline__ int last_cta() const {
-        return last ? (int)blockIdx.x : (int)((cur + (item_tiles - off) - 1) / per);
-    }
+    // the CTA that has the item's last tile (a piece that leaves some ends its CTA's share)
+    __device__ __forceinline__ int last_cta() const { return (int)blockIdx.x + (rest + per - 1) / per; }
 };
 
 }  // namespace dflash

@@ -30,8 +30,8 @@
 // V's to the probabilities relative to a power of two.  bf16 queries are turned to F16 in shared
 // memory, a power of two per row taken out, by the threads that own the rows.
 //
-// Roles: warps 0-3 and 4-7 the blocks' rows, warp 8 copies (queries by one box of heads x tokens,
-// K and V a box per page), warp 9 issues products, warps 10-13 convert codes.
+// Roles: warps 0-3 and 4-7 the blocks' rows, warps 8 and 10 copies (queries by one box of heads x
+// tokens, K and V a box per page), warp 9 issues products, warps 12-15 convert codes.
 #pragma once
 
 #include "paged_attend.cuh"
@@ -46,7 +46,7 @@ constexpr int kScaleRing = 8;            // key tiles whose scales are kept (see
 template <int D, int FMT, bool ONE>
 struct PreCfg {
     static constexpr bool kCodes = FMT != kFmt16;
-    static constexpr int kThreads = kCodes ? 448 : 320;
+    static constexpr int kThreads = kCodes ? 512 : 352;
     static constexpr int kHalves = D / 64;                       // 128-byte columns of a 16-bit row
     static constexpr int kHalfBytes = kPreTile * 128;
     static constexpr int kSlotBytes = kHalves * kHalfBytes;      // 128 rows of D 16-bit values
@@ -121,7 +121,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     const uint32_t s_full = q_full + 24, p_full = s_full + 16, o_full = p_full + 16;   // [2] each
     const uint32_t landed = o_full + 16, drain = landed + 8, odd_done = landed + 16, odd_free = landed + 24;
     const uint32_t c_full = landed + 32, c_empty = c_full + 8 * 3;   // [3] each
-    __shared__ int64_t s_plan[18];
+    __shared__ int64_t s_plan[20];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -176,7 +176,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     // some position of key tile t that no token of the sequence sees (its V row is cleared)
     auto ragged = [&](int t) {
         const int base = t * kPreTile;
-        return base < w.sh.lo(0) || base + kPreTile > w.sh.q.kv || (a.mask == PAGED_TREE && base + kPreTile > w.sh.ctx);
+        return base < w.sh.lo(a, 0) || base + kPreTile > w.sh.q.kv || (a.mask == PAGED_TREE && base + kPreTile > w.sh.ctx);
     };
     // tree positions that some token of the sequence sees (whole warp)
     auto tree_union = [&]() {
@@ -192,27 +192,31 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         return (unsigned long long)((uint64_t)hi32 << 32 | lo32);
     };
     auto seen = [&](int p, uint64_t any_word) {
-        if (p < w.sh.lo(0) || p >= w.sh.q.kv) return false;
+        if (p < w.sh.lo(a, 0) || p >= w.sh.q.kv) return false;
         const int t = p - w.sh.ctx;
         return a.mask != PAGED_TREE || t < 0 || (t < 64 && ((any_word >> t) & 1ull));
     };
 
-    if (warp == 8) {
-        // ---------------- copies ----------------
+    if (warp == 8 || warp == 10) {
+        // ---------------- copies: warp 8 queries and K, warp 10 V ----------------
+        // (two, since boxes leave a warp one lane after the other: 16 of them, of pages of 16, took
+        // one warp longer than memory takes for their bytes)
         constexpr int N = kCodes ? C::kCodeSlots : NS;           // stages of this ring
         constexpr int BYTES = kCodes ? C::kCodeBytes : C::kSlotBytes;
         constexpr int HALVES = kCodes ? 1 : C::kHalves;
         const uint32_t ring_full = kCodes ? c_full : full, ring_empty = kCodes ? c_empty : empty;
+        const int kv = warp == 10;
+        const CUtensorMap *tm = kv ? &tm_v : &tm_k;
         const int ps = a.pool.page_shift;
         const int br = min(1 << ps, kPreTile), nb = kPreTile / br, boxes = nb * HALVES;
-        int slot = 0, items = 0;
-        uint32_t lph = 0, wrap = 0;      // parities: of the cleared tiles, of the slot's use
+        int turn = kv, items = 0;        // place in the order K0 V0 K1 V1 ...
+        uint32_t lph = 0;                // parity of the cleared tiles
         bool alive = true;
         while (alive && w.next(a)) {
             const PagedSeq &q = w.sh.q;
-            const int hi = w.sh.hi(w.rt), lo = w.sh.lo(w.rt), nblk = dealt() ? 1 : 2;
+            const int hi = w.sh.hi(a, w.rt), lo = w.sh.lo(a, w.rt), nblk = dealt() ? 1 : 2;
             const int64_t row = (int64_t)w.seq * a.batch.pages_stride;
-            if (lane == 0) {
+            if (!kv && lane == 0) {
                 if (!mbar_wait(q_empty, ((uint32_t)items & 1u) ^ 1u)) timed_out();
                 if (!s_abort) {
                     mbar_expect_tx(q_full, (uint32_t)(nblk * C::kHalves * block_rows * 128));
@@ -233,73 +237,72 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 }
                 return id;
             };
-            const uint64_t any_word = kCodes ? 0ull : tree_union();
+            const uint64_t any_word = !kCodes && kv ? tree_union() : 0ull;
             int id = lookup(w.t0);
-            for (int j = 0; j < w.nt && alive; ++j) {
+            for (int j = 0; j < w.nt; ++j) {
                 const int t = w.t0 + j;
                 const int id_now = id;
                 id = j + 1 < w.nt ? lookup(t + 1) : -1;
                 const int u = lane % boxes, b = u % nb, h = u / nb;
                 const int page = __shfl_sync(0xffffffffu, id_now, b);
-                for (int kv = 0; kv < 2; ++kv) {
-                    // a V tile with rows to clear lands on a barrier of this warp's own first (codes
-                    // are cleared where they are converted)
-                    const bool clear = !kCodes && kv && ragged(t);
-                    const uint32_t bar = clear ? landed : ring_full + 8 * slot;
-                    int ok = 1;
-                    if (lane == 0) {
-                        if (!mbar_wait(ring_empty + 8 * slot, wrap ^ 1u)) timed_out();
-                        ok = !s_abort;
-                        if (ok) mbar_expect_tx(bar, BYTES);
-                    }
-                    if (!__shfl_sync(0xffffffffu, ok, 0)) {
+                const int slot = turn % N;
+                const uint32_t par = (uint32_t)(turn / N) & 1u;
+                turn += 2;
+                // a V tile with rows to clear lands on a barrier of this warp's own first (codes are
+                // cleared where they are converted)
+                const bool clear = !kCodes && kv && ragged(t);
+                const uint32_t bar = clear ? landed : ring_full + 8 * slot;
+                int ok = 1;
+                if (lane == 0) {
+                    if (!mbar_wait(ring_empty + 8 * slot, par ^ 1u)) timed_out();
+                    ok = !s_abort;
+                    if (ok) mbar_expect_tx(bar, BYTES);
+                }
+                if (!__shfl_sync(0xffffffffu, ok, 0)) {
+                    alive = false;
+                    turn -= 2;                             // not issued
+                    break;
+                }
+                uint8_t *dst = smem + (kCodes ? C::kOffCodes : 0) + slot * BYTES;
+                if (lane < boxes)
+                    tma_load_4d(smem_u32(dst) + h * C::kHalfBytes + b * br * (kCodes ? CODE_ROW : 128), tm, h * 64,
+                                (t * kPreTile) & ((1 << ps) - 1), w.head, page < 0 ? a.pool.n_pages : page, bar);
+                if constexpr (kCodes) {
+                    const int key = lane * 4;
+                    const int kp = __shfl_sync(0xffffffffu, id_now, key / br);
+                    const float *src = (kv ? a.pool.vs : a.pool.ks) + (int64_t)max(kp, 0) * a.pool.s_page_stride +
+                                       (int64_t)w.head * a.pool.s_head_stride + ((t * kPreTile + key) & ((1 << ps) - 1));
+                    cp_async16(smem_u32(smem + C::kOffCodeScale + slot * kPreTile * 4) + key * 4, src, kp < 0 ? 0 : 16);
+                    cp_async_arrive(bar);
+                }
+                if (clear) {
+                    // what nobody sees must not reach the product: 0 * NaN
+                    if (!__all_sync(0xffffffffu, mbar_wait(landed, lph))) {
+                        if (lane == 0) timed_out();
                         alive = false;
                         break;
                     }
-                    uint8_t *dst = smem + (kCodes ? C::kOffCodes : 0) + slot * BYTES;
-                    if (lane < boxes)
-                        tma_load_4d(smem_u32(dst) + h * C::kHalfBytes + b * br * (kCodes ? CODE_ROW : 128), kv ? &tm_v : &tm_k, h * 64,
-                                    (t * kPreTile) & ((1 << ps) - 1), w.head, page < 0 ? a.pool.n_pages : page, bar);
-                    if constexpr (kCodes) {
-                        const int key = lane * 4;
-                        const int kp = __shfl_sync(0xffffffffu, id_now, key / br);
-                        const float *src = (kv ? a.pool.vs : a.pool.ks) + (int64_t)max(kp, 0) * a.pool.s_page_stride +
-                                           (int64_t)w.head * a.pool.s_head_stride + ((t * kPreTile + key) & ((1 << ps) - 1));
-                        cp_async16(smem_u32(smem + C::kOffCodeScale + slot * kPreTile * 4) + key * 4, src, kp < 0 ? 0 : 16);
-                        cp_async_arrive(bar);
-                    }
-                    if (clear) {
-                        // what nobody sees must not reach the product: 0 * NaN
-                        if (!__all_sync(0xffffffffu, mbar_wait(landed, lph))) {
-                            if (lane == 0) timed_out();
-                            alive = false;
-                            break;
-                        }
-                        lph ^= 1u;
-                        for (int r = lane; r < kPreTile; r += 32)
-                            if (!seen(t * kPreTile + r, any_word))
-                                for (int c = 0; c < C::kHalves * 8; ++c)
-                                    *reinterpret_cast<uint4 *>(dst + (c >> 3) * C::kHalfBytes + r * 128 + (c & 7) * 16) =
-                                        make_uint4(0, 0, 0, 0);
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(full + 8 * slot);
-                    }
-                    if (++slot == N) {
-                        slot = 0;
-                        wrap ^= 1u;
-                    }
+                    lph ^= 1u;
+                    for (int r = lane; r < kPreTile; r += 32)
+                        if (!seen(t * kPreTile + r, any_word))
+                            for (int c = 0; c < C::kHalves * 8; ++c)
+                                *reinterpret_cast<uint4 *>(dst + (c >> 3) * C::kHalfBytes + r * 128 + (c & 7) * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full + 8 * slot);
                 }
             }
         }
         // no copy may land after the CTA is gone: every one that was issued has been waited for by
-        // its reader, but on the way out of a failure
+        // its reader, but on the way out of a failure.  (A tile for clearing lands elsewhere: there
+        // the wait for its slot just runs its 50 ms.)
         if (lane == 0 && s_abort) {
-            for (int k = 0; k < N; ++k) {
-                const int sl = (slot + k) % N;
-                const uint32_t par = slot + k >= N ? wrap : wrap ^ 1u;
-                if (!mbar_wait(ring_full + 8 * sl, par, 100000000ull)) break;
+            for (int k = 1; k <= N; ++k) {                 // this warp's last turns
+                const int n = turn - 2 * k;
+                if (n >= 0) mbar_wait(ring_full + 8 * (n % N), (uint32_t)(n / N) & 1u, 50000000ull);
             }
+            if (!kv && items > 0) mbar_wait(q_full, (uint32_t)(items - 1) & 1u, 50000000ull);
         }
         __syncwarp();
     } else if (warp == 9) {
@@ -417,12 +420,12 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             if (!mbar_wait(drain, 0)) timed_out();
         }
         __syncwarp();
-    } else if (kCodes && warp >= 10) {
+    } else if (kCodes && warp >= 12) {
         // ---------------- codes to F16 ----------------
         // The ring of scales needs no barrier of its own: the V slot of the tile that the slower
         // block's rows are at is taken, and with it every later one, so with 3 or 4 slots the tile
         // at hand here is at most 2 ahead of that one.
-        const int r = (int)threadIdx.x - 320;              // the thread's key
+        const int r = (int)threadIdx.x - 384;              // the thread's key
         int slot = 0, cs = 0;
         uint32_t wrap = 0, cwrap = 0;
         int tile = 0;                                      // tiles so far: its place in the ring
@@ -448,7 +451,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                         const uint32_t bits = __float_as_uint(sc) & 0x7fffffffu;
                         const uint32_t top = __reduce_max_sync(0xffffffffu, bits < 0x7f800000u ? bits : 0u);
                         if (lane == 0)
-                            reinterpret_cast<uint32_t *>(smem + C::kOffTop)[(tile % kScaleRing) * 4 + warp - 10] = top;
+                            reinterpret_cast<uint32_t *>(smem + C::kOffTop)[(tile % kScaleRing) * 4 + warp - 12] = top;
                     }
 #pragma unroll
                     for (int ch = 0; ch < D / 16; ++ch) {
@@ -488,7 +491,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 }
             }
         }
-    } else {
+    } else if (warp < 8) {
         // ---------------- softmax rows ----------------
         constexpr int CH = 32;                             // scores of a row at a time: more would spill
         const int blk = warp >> 2, r = (warp & 3) * 32 + lane;
@@ -519,13 +522,16 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             const bool valid = r < block_rows && f < q.n * a.group;
             const bool busy = __any_sync(0xffffffffu, valid);
             float qscale = a.scale_log2;
+            // Every warp waits for every item's queries, whether it reads them or not, before it says
+            // that they may go: else a block without a tile (block 1 of a dealt item of one) would
+            // run on and speak twice for one item.
+            if (!__all_sync(0xffffffffu, mbar_wait(q_full, (uint32_t)items & 1u))) {
+                if (lane == 0) timed_out();
+                break;
+            }
             if constexpr (kQTurned) {
                 // this block's queries to F16, unless the other block does it
                 if (my_blk == blk) {
-                    if (!__all_sync(0xffffffffu, mbar_wait(q_full, (uint32_t)items & 1u))) {
-                        if (lane == 0) timed_out();
-                        break;
-                    }
                     uint8_t *qr = smem + C::kOffQ + blk * C::kSlotBytes;
                     uint32_t top = 0;
 #pragma unroll
@@ -563,8 +569,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 qscale *= row_scale[my_blk * 128 + r];
             }
             ++items;
-            // the queries may go with the last product.  (Every warp arrives once an item, so that no
-            // warp falls a whole item behind the barriers it waits on.)
+            // the queries may go with the last product
             if (lane == 0) mbar_arrive(q_empty);
             // what the row sees: [rlo, rhi) and, for a tree, bits from ctx on
             const int ctx = w.sh.ctx;

@@ -170,3 +170,18 @@ def test_many_sequences():
 
 def test_one_long_sequence_among_short_ones():
     check(World([(1, 5)] * 20 + [(2, 9000)] + [(1, 30)] * 7, seed=16))
+
+
+@pytest.mark.parametrize("fmt,dtype", FORMATS)
+@pytest.mark.parametrize("n,long", [(1, 4), (9, 4), (40, 4), (70, 3)])
+def test_many_tiles_and_items_a_cta(fmt, dtype, n, long):
+    """Enough work that every CTA's stages come round several times, with whole items of one tile
+    between long ones."""
+    lens = [(1 + (i * 7) % n, 1 + (i * 7) % n + (i * 611) % (1200 * (1 if i % long else 4))) for i in range(48)]
+    check(World(lens, heads=32, kv_heads=8, page=32, fmt=fmt, dtype=dtype, seed=n))
+
+
+@pytest.mark.parametrize("fmt,dtype", [("f16", "f16"), ("e4m3", "bf16")])
+def test_every_item_of_one_tile(fmt, dtype):
+    lens = [(1 + i % 35, 1 + i % 35 + (i * 13) % 80) for i in range(150)]
+    check(World(lens, heads=32, kv_heads=8, page=16, fmt=fmt, dtype=dtype, seed=3))
