@@ -307,118 +307,131 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         __syncwarp();
     } else if (warp == 9) {
         // ---------------- products ----------------
-        if (lane == 0) {
-            int slot = 0, items = 0;
-            uint32_t wrap = 0, pph[2] = {0, 0};  // parity of the slots' use, and of the blocks' P
-            bool alive = true;
-            auto wait = [&](uint32_t bar, uint32_t parity) {
-                if (!alive) return;
-                if (!mbar_wait(bar, parity)) {
-                    timed_out();
-                    alive = false;
-                }
-                if (s_abort) alive = false;
-                tc_fence_after();
-            };
-            auto step = [&]() {
-                if (++slot == NS) {
-                    slot = 0;
-                    wrap ^= 1u;
-                }
-            };
-            const uint32_t sq = smem_u32(smem + C::kOffQ), skv = smem_u32(smem);
-            // block b's S from queries qb
-            auto qk = [&](int b, int qb, int s) {
+        // The whole warp keeps the order and waits; one lane issues.  Descriptors differ by constants
+        // from one base per operand: an address step adds its sixteenth to the low word (computed
+        // anew for each product they took longer than the products).
+        int slot = 0, items = 0;
+        uint32_t wrap = 0, pph[2] = {0, 0};      // parity of the slots' use, and of the blocks' P
+        bool alive = true;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            if (!alive) return;
+            if (!__all_sync(0xffffffffu, mbar_wait(bar, parity))) {
+                if (lane == 0) timed_out();
+                alive = false;
+            }
+            if (__any_sync(0xffffffffu, s_abort)) alive = false;
+            tc_fence_after();
+        };
+        auto step = [&]() {
+            if (++slot == NS) {
+                slot = 0;
+                wrap ^= 1u;
+            }
+        };
+        auto commit = [&](uint32_t bar) {
+            if (elect_one()) tc_commit(bar);
+        };
+        const uint64_t q_desc = tc_desc_sw128(smem_u32(smem + C::kOffQ));
+        const uint64_t k_desc = tc_desc_sw128(smem_u32(smem));
+        const uint64_t v_desc = tc_desc_mn_sw128(smem_u32(smem), C::kHalfBytes);
+        // block b's S from queries qb and slot s
+        auto qk = [&](int b, int qb, int s) {
+            const uint64_t qd = q_desc + (uint32_t)(qb * (C::kSlotBytes >> 4));
+            const uint64_t kd = k_desc + (uint32_t)(s * (C::kSlotBytes >> 4));
+            if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (kk >> 2) * C::kHalfBytes + (kk & 3) * 32;
-                    tc_mma_f16(tmem + b * 128, tc_desc_sw128(sq + qb * C::kSlotBytes + off),
-                               tc_desc_sw128(skv + s * C::kSlotBytes + off), kIdescQK, kk != 0);
+                    const uint32_t off = ((kk >> 2) * C::kHalfBytes + (kk & 3) * 32) >> 4;
+                    tc_mma_f16(tmem + b * 128, qd + off, kd + off, kIdescQK, kk != 0);
                 }
                 tc_commit(s_full + 8 * b);
-            };
-            auto pv = [&](int b, int s, bool acc) {
-                wait(p_full + 8 * b, pph[b]);
-                pph[b] ^= 1u;
-                if (!alive) return;
+            }
+            __syncwarp();
+        };
+        auto pv = [&](int b, int s, bool acc) {
+            wait(p_full + 8 * b, pph[b]);
+            pph[b] ^= 1u;
+            if (!alive) return;
+            const uint64_t vd = v_desc + (uint32_t)(s * (C::kSlotBytes >> 4));
+            if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < kPreTile / 16; ++kk)
-                    tc_mma_ts(tmem + 256 + b * 128, tmem + b * 128 + kk * 8,
-                              tc_desc_mn_sw128(skv + s * C::kSlotBytes + kk * 2048, C::kHalfBytes), kIdescPV, acc || kk != 0);
-            };
-            while (alive && w.next(a)) {
-                wait(kQTurned ? q_ready : q_full, (uint32_t)items & 1u);
-                ++items;
-                if (!dealt()) {
-                    wait(full + 8 * slot, wrap);
-                    if (!alive) break;
-                    qk(0, 0, slot);
-                    qk(1, 1, slot);
-                    tc_commit(empty + 8 * slot);
-                    step();
-                    if (w.nt == 1) tc_commit(q_empty);
-                    for (int j = 0; j < w.nt && alive; ++j) {
-                        const int vs = slot;
-                        const uint32_t vw = wrap;
-                        step();
-                        const bool more = j + 1 < w.nt;
-                        wait(full + 8 * vs, vw);
-                        pv(0, vs, j > 0);
-                        if (more) wait(full + 8 * slot, wrap);
-                        if (!alive) break;
-                        if (more) qk(0, 0, slot);
-                        else tc_commit(o_full);
-                        pv(1, vs, j > 0);
-                        if (!alive) break;
-                        tc_commit(empty + 8 * vs);
-                        if (more) {
-                            qk(1, 1, slot);
-                            tc_commit(empty + 8 * slot);
-                            step();
-                            if (j + 2 == w.nt) tc_commit(q_empty);
-                        } else {
-                            tc_commit(o_full + 8);
-                        }
-                    }
-                } else {
-                    // slots in the order K0 V0 K1 V1 ...; products in the order
-                    // QK0 QK1 PV0 QK2 PV1 QK3 ...
-                    const int s0 = slot;
-                    const uint32_t w0 = wrap;
-                    auto at = [&](int n, uint32_t &par) {      // slot and parity of the item's n-th tile
-                        const int x = s0 + n;
-                        par = w0 ^ ((uint32_t)(x / NS) & 1u);
-                        return x % NS;
-                    };
-                    auto qk_of = [&](int j) {
-                        uint32_t par;
-                        const int s = at(2 * j, par);
-                        wait(full + 8 * s, par);
-                        if (!alive) return;
-                        qk(j & 1, 0, s);
-                        tc_commit(empty + 8 * s);
-                        if (j == w.nt - 1) tc_commit(q_empty);
-                    };
-                    qk_of(0);
-                    if (w.nt > 1) qk_of(1);
-                    for (int j = 0; j < w.nt && alive; ++j) {
-                        uint32_t par;
-                        const int s = at(2 * j + 1, par);
-                        wait(full + 8 * s, par);
-                        pv(j & 1, s, j > 1);
-                        if (!alive) break;
-                        tc_commit(empty + 8 * s);
-                        if (j + 2 < w.nt) qk_of(j + 2);
-                        else tc_commit(o_full + 8 * (j & 1));
-                    }
-                    uint32_t par;
-                    slot = at(2 * w.nt, par);
-                    wrap = par;
-                }
+                    tc_mma_ts(tmem + 256 + b * 128, tmem + b * 128 + kk * 8, vd + (uint32_t)(kk * (2048 >> 4)), kIdescPV,
+                              kk != 0 || acc);
             }
-            tc_commit(drain);
-            if (!mbar_wait(drain, 0)) timed_out();
+            __syncwarp();
+        };
+        while (alive && w.next(a)) {
+            wait(kQTurned ? q_ready : q_full, (uint32_t)items & 1u);
+            ++items;
+            if (!dealt()) {
+                wait(full + 8 * slot, wrap);
+                if (!alive) break;
+                qk(0, 0, slot);
+                qk(1, 1, slot);
+                commit(empty + 8 * slot);
+                step();
+                if (w.nt == 1) commit(q_empty);
+                for (int j = 0; j < w.nt && alive; ++j) {
+                    const int vs = slot;
+                    const uint32_t vw = wrap;
+                    step();
+                    const bool more = j + 1 < w.nt;
+                    wait(full + 8 * vs, vw);
+                    pv(0, vs, j > 0);
+                    if (more) wait(full + 8 * slot, wrap);
+                    if (!alive) break;
+                    if (more) qk(0, 0, slot);
+                    else commit(o_full);
+                    pv(1, vs, j > 0);
+                    if (!alive) break;
+                    commit(empty + 8 * vs);
+                    if (more) {
+                        qk(1, 1, slot);
+                        commit(empty + 8 * slot);
+                        step();
+                        if (j + 2 == w.nt) commit(q_empty);
+                    } else {
+                        commit(o_full + 8);
+                    }
+                }
+            } else {
+                // slots in the order K0 V0 K1 V1 ...; products in the order QK0 QK1 PV0 QK2 PV1 QK3 ...
+                const int s0 = slot;
+                const uint32_t w0 = wrap;
+                auto at = [&](int n, uint32_t &par) {          // slot and parity of the item's n-th tile
+                    const int x = s0 + n;
+                    par = w0 ^ ((uint32_t)(x / NS) & 1u);
+                    return x % NS;
+                };
+                auto qk_of = [&](int j) {
+                    uint32_t par;
+                    const int s = at(2 * j, par);
+                    wait(full + 8 * s, par);
+                    if (!alive) return;
+                    qk(j & 1, 0, s);
+                    commit(empty + 8 * s);
+                    if (j == w.nt - 1) commit(q_empty);
+                };
+                qk_of(0);
+                if (w.nt > 1) qk_of(1);
+                for (int j = 0; j < w.nt && alive; ++j) {
+                    uint32_t par;
+                    const int s = at(2 * j + 1, par);
+                    wait(full + 8 * s, par);
+                    pv(j & 1, s, j > 1);
+                    if (!alive) break;
+                    commit(empty + 8 * s);
+                    if (j + 2 < w.nt) qk_of(j + 2);
+                    else commit(o_full + 8 * (j & 1));
+                }
+                uint32_t par;
+                slot = at(2 * w.nt, par);
+                wrap = par;
+            }
         }
+        commit(drain);
+        if (!mbar_wait(drain, 0) && lane == 0) timed_out();
         __syncwarp();
     } else if (kCodes && warp >= 12) {
         // ---------------- codes to F16 ----------------
@@ -453,9 +466,13 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                         if (lane == 0)
                             reinterpret_cast<uint32_t *>(smem + C::kOffTop)[(tile % kScaleRing) * 4 + warp - 12] = top;
                     }
+                    uint4 row_codes[D / 16];                // loads first: stores might be to the same place
+#pragma unroll
+                    for (int ch = 0; ch < D / 16; ++ch)
+                        row_codes[ch] = *reinterpret_cast<const uint4 *>(src + swz_row<CODE_ROW>(r, ch));
 #pragma unroll
                     for (int ch = 0; ch < D / 16; ++ch) {
-                        uint4 x = *reinterpret_cast<const uint4 *>(src + swz_row<CODE_ROW>(r, ch));
+                        uint4 x = row_codes[ch];
                         if (!live) x = make_uint4(0, 0, 0, 0);
                         const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
                         uint32_t y[8];
@@ -493,7 +510,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         }
     } else if (warp < 8) {
         // ---------------- softmax rows ----------------
-        constexpr int CH = 32;                             // scores of a row at a time: more would spill
+        constexpr int CH = kCodes ? 16 : 32;               // scores of a row at a time: more would spill
         const int blk = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lane_base + blk * 128, to = tmem + lane_base + 256 + blk * 128;
@@ -609,13 +626,13 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     const int ring = (tile0 + j) % kScaleRing;
                     const float4 *ks4 = reinterpret_cast<const float4 *>(smem + C::kOffScale) + ring * 2 * (kPreTile / 4);
                     const float4 *vs4 = ks4 + kPreTile / 4;
-                    uint32_t raw[2][CH];                   // a piece at hand and, with registers to spare, the next
+                    uint32_t raw[2][CH];                   // the piece at hand and, with registers to spare, the next
                     // CH scores of the row, masked
                     const bool partly = base < all_lo || base + kPreTile > all_hi;
                     auto scores = [&](int c, uint64_t (&s)[CH / 2]) {
-                        if (kCodes || c == 0) tmem_ld32(ts + CH * c, raw[c & 1]);
+                        if (kCodes || c == 0) tmem_ld(ts + CH * c, raw[c & 1]);
                         tmem_ld_wait();
-                        if (!kCodes && c + 1 < 128 / CH) tmem_ld32(ts + CH * (c + 1), raw[(c + 1) & 1]);
+                        if (!kCodes && c + 1 < 128 / CH) tmem_ld(ts + CH * (c + 1), raw[(c + 1) & 1]);
 #pragma unroll
                         for (int e = 0; e < CH / 2; ++e)
                             s[e] = pk2(__uint_as_float(raw[c & 1][2 * e]), __uint_as_float(raw[c & 1][2 * e + 1]));
@@ -693,13 +710,13 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                             l *= alpha;
                             if (j > j0) rescale(alpha);
 #pragma unroll 1
-                            for (int cc = 0; cc < c * CH / 32; ++cc) {
-                                uint32_t u[16];
-                                tmem_ld16(ts + 16 * cc, u);
+                            for (int cc = 0; cc < c * CH / 16; ++cc) {
+                                uint32_t u[8];
+                                tmem_ld(ts + 8 * cc, u);
                                 tmem_ld_wait();
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) u[e] = scale16<OT>(u[e], alpha);
-                                tmem_st16(ts + 16 * cc, u);
+                                for (int e = 0; e < 8; ++e) u[e] = scale16<OT>(u[e], alpha);
+                                tmem_st(ts + 8 * cc, u);
                             }
                         }
                         const float mu = m == -INFINITY ? 0.f : m;
