@@ -14,11 +14,8 @@
 // S1 = Q1 K': the tensor pipe runs them in that order, so S may overwrite the P that the product
 // in front of it reads, and a block's S being there means its O is up to date.
 //
-// The softmax reference moves only when a row outgrows it by 2^15 (probabilities up to there are as
-// exact in F16 as smaller ones): a row of scores is read once, a piece at a time, its piece's
-// maximum compared, its probabilities made and written back.  The move, in few tiles after a row's
-// first, is by a whole power of two and takes along the sums, O, and the probabilities of the
-// tile's earlier pieces.
+// The softmax reference moves only when a row outgrows it by 2^8 (see paged_attend.cuh), so O is
+// read back and rescaled in few tiles.
 //
 // An item of at most 128 rows (a verify block, a tree, a single token in a mixed batch) fills one
 // block only: then both blocks take the same queries, block 0 the even key tiles and block 1 the
@@ -39,8 +36,6 @@
 namespace dflash {
 
 constexpr int kPreTile = 128;
-// how far (log2) a score may pass the reference before that moves: 2^15 is within F16
-constexpr float kFarMove = 15.f;
 constexpr int kScaleRing = 8;            // key tiles whose scales are kept (see below)
 
 template <int D, int FMT, bool ONE>
@@ -83,21 +78,15 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
-}
-
-// two 16-bit values times a float32 factor (which may lie below their own type's range)
-template <int T>
-__device__ __forceinline__ uint32_t scale16(uint32_t x, float by) {
-    if constexpr (T == PAGED_F16) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x));
-        return pack_half2(f.x * by, f.y * by);
-    } else {
-        return pack_bf162(__uint_as_float(x << 16) * by, __uint_as_float(x & 0xffff0000u) * by);
-    }
 }
 
 template <int D, int FMT, int T, bool ONE>
@@ -626,16 +615,34 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     const int ring = (tile0 + j) % kScaleRing;
                     const float4 *ks4 = reinterpret_cast<const float4 *>(smem + C::kOffScale) + ring * 2 * (kPreTile / 4);
                     const float4 *vs4 = ks4 + kPreTile / 4;
-                    uint32_t raw[2][CH];                   // the piece at hand and, with registers to spare, the next
-                    // CH scores of the row, masked
                     const bool partly = base < all_lo || base + kPreTile > all_hi;
-                    auto scores = [&](int c, uint64_t (&s)[CH / 2]) {
-                        if (kCodes || c == 0) tmem_ld(ts + CH * c, raw[c & 1]);
+                    // O times a factor per row
+                    auto rescale = [&](float by) {
+#pragma unroll 1
+                        for (int c = 0; c < D / 16; ++c) {     // rare: small pieces spare registers
+                            uint32_t u[16];
+                            tmem_ld16(to + 16 * c, u);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * by);
+                            tmem_st16(to + 16 * c, u);
+                        }
+                    };
+                    // The row twice, CH scores at a time: its maximum, then, against a reference that
+                    // is settled, its probabilities, without a branch to hold up the exponentials.
+                    uint32_t raw[2][CH];                   // the piece at hand and, with registers to spare, the next
+                    auto begin = [&]() {
+                        if (!kCodes) tmem_ld(ts, raw[0]);
+                    };
+                    auto scores = [&](int c, const bool masked, uint64_t (&s)[CH / 2]) {
+                        const bool ahead = !kCodes && !masked;
+                        const int at = ahead ? c & 1 : 0;
+                        if (!ahead) tmem_ld(ts + CH * c, raw[0]);
                         tmem_ld_wait();
-                        if (!kCodes && c + 1 < 128 / CH) tmem_ld(ts + CH * (c + 1), raw[(c + 1) & 1]);
+                        if (ahead && c + 1 < 128 / CH) tmem_ld(ts + CH * (c + 1), raw[at ^ 1]);
 #pragma unroll
                         for (int e = 0; e < CH / 2; ++e)
-                            s[e] = pk2(__uint_as_float(raw[c & 1][2 * e]), __uint_as_float(raw[c & 1][2 * e + 1]));
+                            s[e] = pk2(__uint_as_float(raw[at][2 * e]), __uint_as_float(raw[at][2 * e + 1]));
                         if constexpr (kCodes) {
 #pragma unroll
                             for (int e = 0; e < CH / 4; ++e) {
@@ -644,8 +651,8 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                                 s[2 * e + 1] = mul2(s[2 * e + 1], pk2(k.z, k.w));
                             }
                         }
-                        if (partly) {
-                            const int at = base + CH * c, lo = rlo - at, tr = ctx - at, n = q.kv - ctx;
+                        if (masked) {
+                            const int p = base + CH * c, lo = rlo - p, tr = ctx - p, n = q.kv - ctx;
                             const uint32_t wide = (uint32_t)(rhi - rlo);
 #pragma unroll
                             for (int e = 0; e < CH / 2; ++e) {
@@ -661,86 +668,77 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                             }
                         }
                     };
-                    // O times a factor per row
-                    auto rescale = [&](float by) {
-#pragma unroll 1
-                        for (int c = 0; c < D / 16; ++c) {     // rare: small pieces spare registers
-                            uint32_t u[16];
-                            tmem_ld16(to + 16 * c, u);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * by);
-                            tmem_st16(to + 16 * c, u);
-                        }
-                    };
+                    float factor = 1.f;                    // what O needs for this tile's reference
                     if constexpr (kCodes) {
                         // the numerators' power of two: the next one above the largest scale
                         const uint4 t4 = *reinterpret_cast<const uint4 *>(smem + C::kOffTop + ring * 16);
                         const uint32_t top = max(max(t4.x, t4.y), max(t4.z, t4.w));
                         if (__uint_as_float(top) > vref) {
                             const float vnew = __uint_as_float(min((top & 0x7f800000u) + 0x00800000u, 0x7f000000u));
-                            if (j > j0) rescale(vref / vnew);
+                            factor = vref / vnew;
                             vref = vnew;
                         }
                     }
                     const float vinv = kCodes && vref > 0.f ? 1.f / vref : 0.f;
                     const uint64_t scale2 = pk2(qscale, qscale), vinv2 = pk2(vinv, vinv);
-                    uint64_t sa = pk2(0.f, 0.f), sb = sa;
-#pragma unroll
-                    for (int c = 0; c < 128 / CH; ++c) {
-                        uint64_t s[CH / 2];
-                        scores(c, s);
+                    auto tile = [&](auto kind) {
+                        constexpr bool masked = kind.value;
+                        constexpr int kUnroll = masked ? 1 : 128 / CH;   // (the masked one is rare)
                         float x0 = -INFINITY, x1 = x0;
+                        if (!masked) begin();
+#pragma unroll kUnroll
+                        for (int c = 0; c < 128 / CH; ++c) {
+                            uint64_t s[CH / 2];
+                            scores(c, masked, s);
 #pragma unroll
-                        for (int e = 0; e < CH / 2; ++e) {
-                            float y0, y1;
-                            upk2(s[e], y0, y1);
-                            x0 = fmaxf(x0, y0);
-                            x1 = fmaxf(x1, y1);
-                        }
-                        const float mx = fmaxf(x0, x1) * qscale;
-                        const bool far = valid && mx > m + kFarMove;
-                        if (__any_sync(0xffffffffu, far)) {
-                            // the reference moves, by a whole power of two that P takes exactly
-                            const float mnew = far ? (m == -INFINITY ? mx : m + ceilf(mx - m)) : m;
-                            const float alpha = far ? exp2f(m - mnew) : 1.f;
-                            m = mnew;
-                            sa = mul2(sa, pk2(alpha, alpha));
-                            sb = mul2(sb, pk2(alpha, alpha));
-                            l *= alpha;
-                            if (j > j0) rescale(alpha);
-#pragma unroll 1
-                            for (int cc = 0; cc < c * CH / 16; ++cc) {
-                                uint32_t u[8];
-                                tmem_ld(ts + 8 * cc, u);
-                                tmem_ld_wait();
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) u[e] = scale16<OT>(u[e], alpha);
-                                tmem_st(ts + 8 * cc, u);
+                            for (int e = 0; e < CH / 2; e += 2) {
+                                float y0, y1, y2, y3;
+                                upk2(s[e], y0, y1);
+                                upk2(s[e + 1], y2, y3);
+                                x0 = max3(x0, y0, y1);
+                                x1 = max3(x1, y2, y3);
                             }
+                        }
+                        if (!masked) begin();
+                        const float mx = fmaxf(x0, x1) * qscale;
+                        const bool move = valid && mx > m + kLazyMove;
+                        if (__any_sync(0xffffffffu, move || factor != 1.f)) {
+                            const float mnew = move ? mx : m;
+                            const float alpha = move ? exp2f(m - mnew) : 1.f;
+                            m = mnew;
+                            l *= alpha;
+                            if (j > j0) rescale(alpha * factor);
                         }
                         const float mu = m == -INFINITY ? 0.f : m;
                         const uint64_t minus2 = pk2(-mu, -mu);
-                        uint32_t u[CH / 2];
+                        uint64_t sa = pk2(0.f, 0.f), sb = sa;
+#pragma unroll kUnroll
+                        for (int c = 0; c < 128 / CH; ++c) {
+                            uint64_t s[CH / 2];
+                            scores(c, masked, s);
+                            uint32_t u[CH / 2];
 #pragma unroll
-                        for (int e = 0; e < CH / 2; ++e) {
-                            float x, y;
-                            upk2(fma2(s[e], scale2, minus2), x, y);
-                            uint64_t p2 = pk2(ex2_approx(x), ex2_approx(y));
-                            if (e & 1) sb = add2(sb, p2);
-                            else sa = add2(sa, p2);
-                            if constexpr (kCodes) {
-                                const float2 v = reinterpret_cast<const float2 *>(vs4)[c * (CH / 2) + e];
-                                p2 = mul2(p2, mul2(pk2(v.x, v.y), vinv2));
+                            for (int e = 0; e < CH / 2; ++e) {
+                                float x, y;
+                                upk2(fma2(s[e], scale2, minus2), x, y);
+                                uint64_t p2 = pk2(ex2_approx(x), ex2_approx(y));
+                                if (e & 1) sb = add2(sb, p2);
+                                else sa = add2(sa, p2);
+                                if constexpr (kCodes) {
+                                    const float2 v = reinterpret_cast<const float2 *>(vs4)[c * (CH / 2) + e];
+                                    p2 = mul2(p2, mul2(pk2(v.x, v.y), vinv2));
+                                }
+                                upk2(p2, x, y);
+                                u[e] = pack16<OT>(x, y);
                             }
-                            upk2(p2, x, y);
-                            u[e] = pack16<OT>(x, y);
+                            tmem_st(ts + c * (CH / 2), u);     // over scores that have been read
                         }
-                        tmem_st(ts + c * (CH / 2), u);     // over scores that have been read
-                    }
-                    float s0, s1;
-                    upk2(add2(sa, sb), s0, s1);
-                    l += s0 + s1;
+                        float s0, s1;
+                        upk2(add2(sa, sb), s0, s1);
+                        l += s0 + s1;
+                    };
+                    if (partly) tile(std::true_type{});
+                    else tile(std::false_type{});
                     tmem_st_wait();
                 }
                 tc_fence_before();
