@@ -242,10 +242,11 @@ k_paged_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 for (int j = 0; j < 2; ++j) {
                     top[j] = max(top[j], __shfl_xor_sync(0xffffffffu, top[j], 1));
                     top[j] = max(top[j], __shfl_xor_sync(0xffffffffu, top[j], 2));
-                    const int e = min(254, max(1, (int)(top[j] >> 7)));          // biased exponent
+                    const int e = top[j] ? min(254, max(1, (int)(top[j] >> 7))) : 127;   // biased exponent
                     const float down = e == 254 ? 0x1p-127f : __uint_as_float((uint32_t)(254 - e) << 23);
                     const float up = __uint_as_float((uint32_t)e << 23);
-                    qscale[j] = a.scale_log2 * up;
+                    // (never 0, which would make NaN of what the mask leaves out; scores that small are 0)
+                    qscale[j] = fmaxf(a.scale_log2 * up, 0x1p-120f);
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll

@@ -23,8 +23,10 @@
 // the end.  A batch with no larger item runs the variant with memory for one block of queries.
 //
 // Quantised pages: four more warps turn code tiles into F16 tiles in shared memory (a thread per
-// key), exactly; scales are applied where the streaming kernel applies them, K's to the scores,
-// V's to the probabilities relative to a power of two.  bf16 queries are turned to F16 in shared
+// key), code times scale rounded once, relative to a power of two per tile that the rows' threads
+// put back.  (Exact codes with the scales on scores and probabilities, as the streaming kernel has
+// them, took 96 reads of scales per row and tile out of the same shared memory that feeds the
+// products: 197 us instead of the figure below.)  bf16 queries are turned to F16 in shared
 // memory, a power of two per row taken out, by the threads that own the rows.
 //
 // Roles: warps 0-3 and 4-7 the blocks' rows, warps 8 and 10 copies (queries by one box of heads x
@@ -36,7 +38,7 @@
 namespace dflash {
 
 constexpr int kPreTile = 128;
-constexpr int kScaleRing = 8;            // key tiles whose scales are kept (see below)
+constexpr int kUnitRing = 8;             // key tiles whose units are kept (see below)
 
 template <int D, int FMT, bool ONE>
 struct PreCfg {
@@ -53,9 +55,8 @@ struct PreCfg {
     static constexpr int kOffQ = kSlots * kSlotBytes;
     static constexpr int kOffCodes = kOffQ + kBlocks * kSlotBytes;
     static constexpr int kOffCodeScale = kOffCodes + kCodeSlots * kCodeBytes;   // as loaded, per code slot
-    static constexpr int kOffScale = kOffCodeScale + kCodeSlots * kPreTile * 4;  // [ring][K, V][128]
-    static constexpr int kOffTop = kOffScale + (kCodes ? kScaleRing * 2 * kPreTile * 4 : 0);   // [ring][4]
-    static constexpr int kOffRow = kOffTop + (kCodes ? kScaleRing * 16 : 0);     // row values
+    static constexpr int kOffUnit = kOffCodeScale + kCodeSlots * kPreTile * 4;   // [ring][K, V]
+    static constexpr int kOffRow = kOffUnit + (kCodes ? kUnitRing * 8 : 0);      // row values
     static constexpr int kOffBars = kOffRow + 128 * 8;
     static constexpr int kSmem = 1024 + kOffBars + 384;
     static_assert(kSmem <= 227 * 1024, "one CTA per SM");
@@ -424,7 +425,10 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         __syncwarp();
     } else if (kCodes && warp >= 12) {
         // ---------------- codes to F16 ----------------
-        // The ring of scales needs no barrier of its own: the V slot of the tile that the slower
+        // A row is its codes times its scale, rounded to F16 -- the value that a 16-bit page would
+        // hold -- in units of a power of two: K's for a tile, so that its largest scale is in (1/2, 1],
+        // V's the largest so far of the item, which O is kept in.  Scales of any size fit F16 so.
+        // The ring of units needs no barrier of its own: the V slot of the tile that the slower
         // block's rows are at is taken, and with it every later one, so with 3 or 4 slots the tile
         // at hand here is at most 2 ahead of that one.
         const int r = (int)threadIdx.x - 384;              // the thread's key
@@ -434,8 +438,10 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         bool alive = true;
         while (alive && w.next(a)) {
             const uint64_t any_word = tree_union();
+            float v_unit = 0.f;
             for (int j = 0; j < w.nt && alive; ++j, ++tile) {
                 const int t = w.t0 + j;
+                const bool edge = ragged(t);
                 for (int kv = 0; kv < 2; ++kv) {
                     const bool ok = mbar_wait(c_full + 8 * cs, cwrap) && mbar_wait(empty + 8 * slot, wrap ^ 1u);
                     if (!__all_sync(0xffffffffu, ok) || s_abort) {
@@ -445,40 +451,49 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     }
                     const uint8_t *src = smem + C::kOffCodes + cs * C::kCodeBytes;
                     uint8_t *dst = smem + slot * C::kSlotBytes;
-                    const bool live = seen(t * kPreTile + r, any_word);
-                    float sc = reinterpret_cast<const float *>(smem + C::kOffCodeScale)[cs * kPreTile + r];
-                    if (!live) sc = 0.f;
-                    reinterpret_cast<float *>(smem + C::kOffScale)[((tile % kScaleRing) * 2 + kv) * kPreTile + r] = sc;
-                    if (kv) {
-                        const uint32_t bits = __float_as_uint(sc) & 0x7fffffffu;
-                        const uint32_t top = __reduce_max_sync(0xffffffffu, bits < 0x7f800000u ? bits : 0u);
-                        if (lane == 0)
-                            reinterpret_cast<uint32_t *>(smem + C::kOffTop)[(tile % kScaleRing) * 4 + warp - 12] = top;
+                    const float *scales = reinterpret_cast<const float *>(smem + C::kOffCodeScale) + cs * kPreTile;
+                    const bool live = !edge || seen(t * kPreTile + r, any_word);
+                    // the tile's largest scale among the rows that count (four to a lane)
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t bits = __float_as_uint(scales[4 * lane + i]) & 0x7fffffffu;
+                        if (bits < 0x7f800000u && (!edge || seen(t * kPreTile + 4 * lane + i, any_word))) top = max(top, bits);
                     }
-                    uint4 row_codes[D / 16];                // loads first: stores might be to the same place
+                    top = __reduce_max_sync(0xffffffffu, top);
+                    // the power of two above it, at most 2^127; 0 stays
+                    float unit = top ? __uint_as_float(min((top & 0x7f800000u) + 0x00800000u, 0x7f000000u)) : 0.f;
+                    if (kv) unit = v_unit = fmaxf(v_unit, unit);
+                    else if (!top) unit = 1.f;
+                    const float sc = live && unit > 0.f ? scales[r] / unit : 0.f;
+                    if (warp == 12 && lane == 0)
+                        reinterpret_cast<float *>(smem + C::kOffUnit)[(tile % kUnitRing) * 2 + kv] = unit;
+                    const uint64_t sc2 = pk2(sc, sc);
 #pragma unroll
-                    for (int ch = 0; ch < D / 16; ++ch)
-                        row_codes[ch] = *reinterpret_cast<const uint4 *>(src + swz_row<CODE_ROW>(r, ch));
+                    for (int half = 0; half < 2; ++half) {
+                        uint4 row[D / 32];                 // loads first: stores might be to the same place
 #pragma unroll
-                    for (int ch = 0; ch < D / 16; ++ch) {
-                        uint4 x = row_codes[ch];
-                        if (!live) x = make_uint4(0, 0, 0, 0);
-                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-                        uint32_t y[8];
+                        for (int i = 0; i < D / 32; ++i)
+                            row[i] = *reinterpret_cast<const uint4 *>(src + swz_row<CODE_ROW>(r, half * (D / 32) + i));
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if constexpr (FMT == kFmtInt8) {
-                                const uint32_t xf = xs[i] ^ 0x80808080u;
-                                y[2 * i] = int8_pair(xf, 0x5140u);
-                                y[2 * i + 1] = int8_pair(xf, 0x7362u);
-                            } else {
-                                y[2 * i] = e4m3_pair_f16(xs[i]);
-                                y[2 * i + 1] = e4m3_pair_f16(xs[i] >> 16);
+                        for (int i = 0; i < D / 32; ++i) {
+                            const int ch = half * (D / 32) + i;
+                            const uint32_t xs[4] = {row[i].x, row[i].y, row[i].z, row[i].w};
+                            uint32_t y[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                uint32_t h;
+                                if constexpr (FMT == kFmtInt8) h = int8_pair(xs[k >> 1] ^ 0x80808080u, k & 1 ? 0x7362u : 0x5140u);
+                                else h = e4m3_pair_f16(xs[k >> 1] >> (16 * (k & 1)));
+                                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+                                float a0, a1;
+                                upk2(mul2(pk2(f.x, f.y), sc2), a0, a1);
+                                y[k] = live ? pack_half2(a0, a1) : 0u;
                             }
+                            uint8_t *at = dst + (ch >> 2) * C::kHalfBytes;
+                            *reinterpret_cast<uint4 *>(at + swz_row<128>(r, (2 * ch) & 7)) = make_uint4(y[0], y[1], y[2], y[3]);
+                            *reinterpret_cast<uint4 *>(at + swz_row<128>(r, (2 * ch + 1) & 7)) = make_uint4(y[4], y[5], y[6], y[7]);
                         }
-                        uint8_t *row = dst + (ch >> 2) * C::kHalfBytes;
-                        *reinterpret_cast<uint4 *>(row + swz_row<128>(r, (2 * ch) & 7)) = make_uint4(y[0], y[1], y[2], y[3]);
-                        *reinterpret_cast<uint4 *>(row + swz_row<128>(r, (2 * ch + 1) & 7)) = make_uint4(y[4], y[5], y[6], y[7]);
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
@@ -547,7 +562,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 #pragma unroll
                         for (int i = 0; i < 4; ++i) top = max(top, max(xs[i] & 0x7fffu, (xs[i] >> 16) & 0x7fffu));
                     }
-                    const int e = min(254, max(1, (int)(top >> 7)));
+                    const int e = top ? min(254, max(1, (int)(top >> 7))) : 127;
                     const float down = e == 254 ? 0x1p-127f : __uint_as_float((uint32_t)(254 - e) << 23);
                     const float up = __uint_as_float((uint32_t)e << 23);
 #pragma unroll
@@ -600,7 +615,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 const int base = (w.t0 + j) * kPreTile;
                 bool ok = mbar_wait(s_full + 8 * blk, sph);
                 if constexpr (kCodes) {
-                    // the tile's V scales (K's came with S)
+                    // the tile's V unit (K's came with S)
                     const int vn = vslot + 2 * j;
                     ok = ok && mbar_wait(full + 8 * (vn % NS), (uint32_t)(vn / NS) & 1u);
                 }
@@ -612,9 +627,9 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 sph ^= 1u;
                 tc_fence_after();
                 if (busy) {
-                    const int ring = (tile0 + j) % kScaleRing;
-                    const float4 *ks4 = reinterpret_cast<const float4 *>(smem + C::kOffScale) + ring * 2 * (kPreTile / 4);
-                    const float4 *vs4 = ks4 + kPreTile / 4;
+                    // quantised: the units of this tile's K and V
+                    float2 unit = make_float2(1.f, 1.f);
+                    if constexpr (kCodes) unit = reinterpret_cast<const float2 *>(smem + C::kOffUnit)[(tile0 + j) % kUnitRing];
                     const bool partly = base < all_lo || base + kPreTile > all_hi;
                     // O times a factor per row
                     auto rescale = [&](float by) {
@@ -643,14 +658,6 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 #pragma unroll
                         for (int e = 0; e < CH / 2; ++e)
                             s[e] = pk2(__uint_as_float(raw[at][2 * e]), __uint_as_float(raw[at][2 * e + 1]));
-                        if constexpr (kCodes) {
-#pragma unroll
-                            for (int e = 0; e < CH / 4; ++e) {
-                                const float4 k = ks4[c * (CH / 4) + e];
-                                s[2 * e] = mul2(s[2 * e], pk2(k.x, k.y));
-                                s[2 * e + 1] = mul2(s[2 * e + 1], pk2(k.z, k.w));
-                            }
-                        }
                         if (masked) {
                             const int p = base + CH * c, lo = rlo - p, tr = ctx - p, n = q.kv - ctx;
                             const uint32_t wide = (uint32_t)(rhi - rlo);
@@ -669,18 +676,13 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                         }
                     };
                     float factor = 1.f;                    // what O needs for this tile's reference
-                    if constexpr (kCodes) {
-                        // the numerators' power of two: the next one above the largest scale
-                        const uint4 t4 = *reinterpret_cast<const uint4 *>(smem + C::kOffTop + ring * 16);
-                        const uint32_t top = max(max(t4.x, t4.y), max(t4.z, t4.w));
-                        if (__uint_as_float(top) > vref) {
-                            const float vnew = __uint_as_float(min((top & 0x7f800000u) + 0x00800000u, 0x7f000000u));
-                            factor = vref / vnew;
-                            vref = vnew;
-                        }
+                    if (kCodes && unit.y != vref) {
+                        factor = vref / unit.y;
+                        vref = unit.y;
                     }
-                    const float vinv = kCodes && vref > 0.f ? 1.f / vref : 0.f;
-                    const uint64_t scale2 = pk2(qscale, qscale), vinv2 = pk2(vinv, vinv);
+                    // (never 0, which would make NaN of what the mask leaves out; scores that small are 0)
+                    const float tscale = kCodes ? fmaxf(qscale * unit.x, 0x1p-120f) : qscale;
+                    const uint64_t scale2 = pk2(tscale, tscale);
                     auto tile = [&](auto kind) {
                         constexpr bool masked = kind.value;
                         constexpr int kUnroll = masked ? 1 : 128 / CH;   // (the masked one is rare)
@@ -700,7 +702,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                             }
                         }
                         if (!masked) begin();
-                        const float mx = fmaxf(x0, x1) * qscale;
+                        const float mx = fmaxf(x0, x1) * tscale;
                         const bool move = valid && mx > m + kLazyMove;
                         if (__any_sync(0xffffffffu, move || factor != 1.f)) {
                             const float mnew = move ? mx : m;
@@ -721,13 +723,9 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                             for (int e = 0; e < CH / 2; ++e) {
                                 float x, y;
                                 upk2(fma2(s[e], scale2, minus2), x, y);
-                                uint64_t p2 = pk2(ex2_approx(x), ex2_approx(y));
+                                const uint64_t p2 = pk2(ex2_approx(x), ex2_approx(y));
                                 if (e & 1) sb = add2(sb, p2);
                                 else sa = add2(sa, p2);
-                                if constexpr (kCodes) {
-                                    const float2 v = reinterpret_cast<const float2 *>(vs4)[c * (CH / 2) + e];
-                                    p2 = mul2(p2, mul2(pk2(v.x, v.y), vinv2));
-                                }
                                 upk2(p2, x, y);
                                 u[e] = pack16<OT>(x, y);
                             }

@@ -114,7 +114,7 @@ class World:
             h = torch.where(p >= c, ((word >> (p - c).clamp(0, 63)) & 1) == 0, h)
         return h
 
-    def attend(self, q, mask="causal", window=0, tree=None, scale=None):
+    def attend(self, q, mask="causal", window=0, tree=None, scale=None, wide=False):
         """(o, lse, tolerance of o, tolerance of lse) in float64, rows behind the batch left out.
 
         The tolerances are a kernel's that multiplies exactly, adds in float32 and rounds
@@ -126,7 +126,10 @@ class World:
           numerator u + d, denominator d, relative to A = sum softmax |v|; the sums over the
             keys, in float32, in runs of at most a few thousand terms: 2^-12 u more, kept in 2 d;
           F16's smallest step 2^-25 on each probability against at most the largest |v|;
-          the output U |o|."""
+          the output U |o|;
+          wide (more than 32 query rows per kv head) over quantised pages: K and V rows are rounded
+            to F16 first, by at most 2^-11 of each element, which moves a score by at most 2^-11 T
+            and the numerator by 2^-11 A."""
         scale = 1 / math.sqrt(self.dim) if scale is None else scale
         o = torch.zeros(self.total, self.heads, self.dim, dtype=torch.float64, device="cuda")
         lse = torch.full((self.total, self.heads), -math.inf, dtype=torch.float64, device="cuda")
@@ -147,8 +150,10 @@ class World:
             o[r] = torch.einsum("hip,phd->ihd", p, v)
             T = (torch.einsum("ihd,phd->hip", x.abs(), k.abs()).amax(-1) * scale).T     # [n, heads]
             d = T * (self.dim + 8) * 2.0 ** -24 + 2.0 ** -21
+            more = UNIT[torch.float16] if wide and self.store in TOP else 0.0
+            d = d + more * T
             A = torch.einsum("hip,phd->ihd", p, v.abs())
             tiny = kv * 2.0 ** -25 * v.abs().amax() if operand == torch.float16 else 0.0
-            tol[r] = (UNIT[operand] + 3 * d[..., None]) * A + UNIT[self.dtype] * o[r].abs() + tiny + 1e-30
+            tol[r] = (UNIT[operand] + more + 3 * d[..., None]) * A + UNIT[self.dtype] * o[r].abs() + tiny + 1e-30
             ltol[r] = 2 * d + 2.0 ** -22 * lse[r].abs().nan_to_num(posinf=0.0)
         return o, lse, tol, ltol

@@ -38,7 +38,8 @@ def check(w, mask="causal", window=0, tree=None, scale=None, q=None, max_q=None,
         o = wide[:, 1:1 + w.heads, :w.dim]
     ls = torch.full((w.rows, w.heads), 7.0, device="cuda") if lse else None
     P.paged_attend(cache, batch, q, o, mask=mask, window=window, scale=scale or 0.0, tree=tree, lse=ls)
-    want, wl, tol, ltol = w.attend(q, mask, window, tree, scale)
+    wide = max(n for n, _ in w.lens) * (w.heads // w.kv_heads) > 32 if max_q is None else max_q * w.heads > 32 * w.kv_heads
+    want, wl, tol, ltol = w.attend(q, mask, window, tree, scale, wide)
     assert P.paged_device_error() == 0
     got = o[:w.total].double()
     bad = ~((got - want).abs() <= tol)
@@ -185,3 +186,15 @@ def test_many_tiles_and_items_a_cta(fmt, dtype, n, long):
 def test_every_item_of_one_tile(fmt, dtype):
     lens = [(1 + i % 35, 1 + i % 35 + (i * 13) % 80) for i in range(150)]
     check(World(lens, heads=32, kv_heads=8, page=16, fmt=fmt, dtype=dtype, seed=3))
+
+
+@pytest.mark.parametrize("fmt,dtype", FORMATS)
+@pytest.mark.parametrize("n", [3, 40])
+def test_rows_of_zeros_and_tiny_scales(fmt, dtype, n):
+    """Queries of zeros weigh what they see alike; a scale next to nothing does the same."""
+    w = World([(n, 200), (n, n)], fmt=fmt, dtype=dtype, seed=17)
+    q = w.randn(w.heads)
+    q[1] = 0
+    q[n, 2] = 0
+    check(w, q=q)
+    check(w, q=q, scale=1e-30)
