@@ -468,32 +468,31 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     const float sc = live && unit > 0.f ? scales[r] / unit : 0.f;
                     if (warp == 12 && lane == 0)
                         reinterpret_cast<float *>(smem + C::kOffUnit)[(tile % kUnitRing) * 2 + kv] = unit;
-                    const uint64_t sc2 = pk2(sc, sc);
+                    // the scale as a sum of two F16 values, good to 2^-22: code * high + (code * low), one
+                    // fused rounding, is the product's rounding but for an error far below its step
+                    const float high = __half2float(__float2half_rn(sc));
+                    const uint32_t high2 = pack_half2(high, high), low2 = pack_half2(sc - high, sc - high);
+                    uint4 row[D / 16];                     // loads first: stores might be to the same place
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        uint4 row[D / 32];                 // loads first: stores might be to the same place
+                    for (int ch = 0; ch < D / 16; ++ch)
+                        row[ch] = *reinterpret_cast<const uint4 *>(src + swz_row<CODE_ROW>(r, ch));
 #pragma unroll
-                        for (int i = 0; i < D / 32; ++i)
-                            row[i] = *reinterpret_cast<const uint4 *>(src + swz_row<CODE_ROW>(r, half * (D / 32) + i));
+                    for (int ch = 0; ch < D / 16; ++ch) {
+                        if (!live) row[ch] = make_uint4(0, 0, 0, 0);       // (an e4m3 NaN times 0)
+                        const uint32_t xs[4] = {row[ch].x, row[ch].y, row[ch].z, row[ch].w};
+                        uint32_t y[8];
 #pragma unroll
-                        for (int i = 0; i < D / 32; ++i) {
-                            const int ch = half * (D / 32) + i;
-                            const uint32_t xs[4] = {row[i].x, row[i].y, row[i].z, row[i].w};
-                            uint32_t y[8];
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                uint32_t h;
-                                if constexpr (FMT == kFmtInt8) h = int8_pair(xs[k >> 1] ^ 0x80808080u, k & 1 ? 0x7362u : 0x5140u);
-                                else h = e4m3_pair_f16(xs[k >> 1] >> (16 * (k & 1)));
-                                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-                                float a0, a1;
-                                upk2(mul2(pk2(f.x, f.y), sc2), a0, a1);
-                                y[k] = live ? pack_half2(a0, a1) : 0u;
-                            }
-                            uint8_t *at = dst + (ch >> 2) * C::kHalfBytes;
-                            *reinterpret_cast<uint4 *>(at + swz_row<128>(r, (2 * ch) & 7)) = make_uint4(y[0], y[1], y[2], y[3]);
-                            *reinterpret_cast<uint4 *>(at + swz_row<128>(r, (2 * ch + 1) & 7)) = make_uint4(y[4], y[5], y[6], y[7]);
+                        for (int k = 0; k < 8; ++k) {
+                            uint32_t h;
+                            if constexpr (FMT == kFmtInt8) h = int8_pair(xs[k >> 1] ^ 0x80808080u, k & 1 ? 0x7362u : 0x5140u);
+                            else h = e4m3_pair_f16(xs[k >> 1] >> (16 * (k & 1)));
+                            uint32_t small;
+                            asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(small) : "r"(h), "r"(low2));
+                            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y[k]) : "r"(h), "r"(high2), "r"(small));
                         }
+                        uint8_t *at = dst + (ch >> 2) * C::kHalfBytes;
+                        *reinterpret_cast<uint4 *>(at + swz_row<128>(r, (2 * ch) & 7)) = make_uint4(y[0], y[1], y[2], y[3]);
+                        *reinterpret_cast<uint4 *>(at + swz_row<128>(r, (2 * ch + 1) & 7)) = make_uint4(y[4], y[5], y[6], y[7]);
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
