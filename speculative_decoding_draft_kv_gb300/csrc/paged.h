@@ -62,7 +62,8 @@ struct PagedRowsArgs {
     float eps, magnitude;
     int nq, nk, nv;                   // heads of each kind
     int rot, layout;                  // rot 0: no rotation
-    int iters, cq, ck, cv;            // warp steps per task, tasks per token of each kind
+    int steps_q, steps_k, steps_v;    // warp steps of a token's queries, keys, values (set at launch)
+    int iters, tasks;                 // warp steps per task, tasks per token
     uint64_t turn[kPagedMaxDim / 2];  // turns per position, in 2^-64
 };
 cudaError_t launch_paged_rows(const PagedRowsArgs &a, int dtype, int head_dim, bool paged, cudaStream_t st);

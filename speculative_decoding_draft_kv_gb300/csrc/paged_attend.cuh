@@ -643,23 +643,26 @@ k_paged_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     if (threadIdx.x == 0 && !began) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
 }
 
-// Join of the items that a share's border cut: block (c, y) takes the item that CTA c began
-// and did not finish, rows 8y .. 8y+7, a warp per row; the pieces lie in CTAs c (slot 1),
-// c + 1, ... (slot 0).
-template <int D, int T>
+// Join of the items that a share's border cut: block (c, y) takes rows of the item that CTA c began
+// and did not finish; the pieces lie in CTAs c (slot 1), c + 1, ... (slot 0).  W warps share a row's
+// pieces: all eight after the streaming kernel, whose few rows are cut into many pieces, one after
+// the tensor-core kernel, where it is the other way round.
+template <int D, int T, int W>
 __global__ void __launch_bounds__(256)
-k_paged_join(const __grid_constant__ PagedAttendArgs a, int tile_rows) {
+k_paged_join(const __grid_constant__ PagedAttendArgs a) {
     constexpr int N = D / 32;
+    __shared__ float s_acc[W > 1 ? W : 1][D];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
     const int4 d = a.desc[blockIdx.x];
     if (d.x < 0) return;
-    const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int r = blockIdx.y * (8 / W) + warp / W, part = warp % W;
     const PagedSeq q = paged_seq(a.batch, a.pool.page_shift, d.x);
-    const int f = d.z * tile_rows + r;
-    if (r >= tile_rows || f >= q.n * a.group) return;
+    const int f = d.z * a.tile_rows + r;
+    if (r >= a.tile_rows || f >= q.n * a.group) return;    // whole blocks with W = 8
     const int tok = f / a.group, head = d.y * a.group + f - tok * a.group;
     const int c0 = blockIdx.x, c1 = min(d.w, a.ctas - 1);
-    auto slot = [&](int cc) { return ((int64_t)cc * 2 + (cc == c0 ? 1 : 0)) * tile_rows + r; };
+    auto slot = [&](int cc) { return ((int64_t)cc * 2 + (cc == c0 ? 1 : 0)) * a.tile_rows + r; };
     // 32 pieces' maxima and sums at a time, one to a lane
     float m = -INFINITY, l = 0.f, acc[N];
 #pragma unroll
@@ -667,6 +670,25 @@ k_paged_join(const __grid_constant__ PagedAttendArgs a, int tile_rows) {
     for (int cb = c0; cb <= c1; cb += 32) {
         const int n = min(32, c1 - cb + 1);
         const float2 ml = lane < n ? a.part_ml[slot(cb + lane)] : make_float2(-INFINITY, 0.f);
+        // this warp's numerators of the 32, four at a time, on their way before the weights are known
+        constexpr int PER = 32 / W, U = PER < 4 ? PER : 4;
+        float x[U][N];
+        auto fetch = [&](int i) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int p = part + (i + u) * W;
+                if (p >= n) continue;
+                const float *src = a.part_acc + slot(cb + p) * D + lane * N;
+                if constexpr (N == 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(src);
+                    x[u][0] = v.x; x[u][1] = v.y; x[u][2] = v.z; x[u][3] = v.w;
+                } else {
+                    const float2 v = *reinterpret_cast<const float2 *>(src);
+                    x[u][0] = v.x; x[u][1] = v.y;
+                }
+            }
+        };
+        fetch(0);
         float top = ml.x;
 #pragma unroll
         for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
@@ -681,27 +703,28 @@ k_paged_join(const __grid_constant__ PagedAttendArgs a, int tile_rows) {
 #pragma unroll
         for (int e = 0; e < N; ++e) acc[e] *= keep;
         m = mnew;
-        for (int i = 0; i < n; i += 4) {
-            float x[4][N];
+        for (int i = 0; part + i * W < n; i += U) {
+            if (i) fetch(i);
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (i + u < n) {
-                    const float *src = a.part_acc + slot(cb + i + u) * D + lane * N;
-                    if constexpr (N == 4) {
-                        const float4 v = *reinterpret_cast<const float4 *>(src);
-                        x[u][0] = v.x; x[u][1] = v.y; x[u][2] = v.z; x[u][3] = v.w;
-                    } else {
-                        const float2 v = *reinterpret_cast<const float2 *>(src);
-                        x[u][0] = v.x; x[u][1] = v.y;
-                    }
-                }
+            for (int u = 0; u < U; ++u) {
+                const int p = part + (i + u) * W;
+                const float f4 = __shfl_sync(0xffffffffu, wgt, p & 31);
+                if (p >= n) continue;
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (i + u < n) {
-                    const float f4 = __shfl_sync(0xffffffffu, wgt, i + u);
+                for (int e = 0; e < N; ++e) acc[e] = fmaf(x[u][e], f4, acc[e]);
+            }
+        }
+    }
+    if constexpr (W > 1) {
 #pragma unroll
-                    for (int e = 0; e < N; ++e) acc[e] = fmaf(x[u][e], f4, acc[e]);
-                }
+        for (int e = 0; e < N; ++e) s_acc[warp][lane * N + e] = acc[e];
+        __syncthreads();
+        if (warp) return;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            acc[e] = 0.f;
+#pragma unroll
+            for (int i = 0; i < W; ++i) acc[e] += s_acc[i][lane * N + e];
         }
     }
     const float inv = l > 0.f || l != l ? 1.f / l : 0.f;

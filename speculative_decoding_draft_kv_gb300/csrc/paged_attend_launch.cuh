@@ -3,13 +3,16 @@
 
 #include "paged_attend.cuh"
 
+#include <algorithm>
+
 namespace dflash {
 
 // The join settles while the attention runs, and waits for its end.
-template <int T>
-cudaError_t launch_join(const PagedAttendArgs &a, int rows, int head_dim, cudaStream_t st) {
+template <int T, int W>
+cudaError_t launch_join(const PagedAttendArgs &a, int head_dim, cudaStream_t st) {
+    const int rows = std::min<int64_t>(a.tile_rows, (int64_t)a.max_q * a.group);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.ctas, (unsigned)((rows + 7) / 8), 1);
+    cfg.gridDim = dim3((unsigned)a.ctas, (unsigned)((rows * W + 7) / 8), 1);
     cfg.blockDim = dim3(256);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -17,8 +20,8 @@ cudaError_t launch_join(const PagedAttendArgs &a, int rows, int head_dim, cudaSt
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return head_dim == 64 ? cudaLaunchKernelEx(&cfg, k_paged_join<64, T>, a, rows)
-                          : cudaLaunchKernelEx(&cfg, k_paged_join<128, T>, a, rows);
+    return head_dim == 64 ? cudaLaunchKernelEx(&cfg, k_paged_join<64, T, W>, a)
+                          : cudaLaunchKernelEx(&cfg, k_paged_join<128, T, W>, a);
 }
 
 // fn(kernel, its shared memory, threads, rows) for one of the instances
@@ -53,11 +56,11 @@ cudaError_t paged_attend_setup_t() {
 template <int T>
 cudaError_t launch_paged_attend_t(const PagedAttendArgs &a, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                                   int head_dim, cudaStream_t st) {
-    auto go = [&](auto kernel, int smem, int threads, int rows) {
+    auto go = [&](auto kernel, int smem, int threads, int) {
         kernel<<<a.ctas, threads, smem, st>>>(tm_k, tm_v, a);
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
-        return launch_join<T>(a, rows, head_dim, st);
+        return launch_join<T, 8>(a, head_dim, st);
     };
     const int mt = a.tile_rows <= 16 ? 1 : 2;
     return head_dim == 64 ? pick_attend<T, 64>(a.pool.format, mt, go) : pick_attend<T, 128>(a.pool.format, mt, go);

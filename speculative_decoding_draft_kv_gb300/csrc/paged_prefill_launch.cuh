@@ -43,7 +43,7 @@ cudaError_t launch_paged_prefill_t(const PagedAttendArgs &a, const CUtensorMap &
     return pick_prefill<T>(head_dim, a.pool.format, a.tile_rows <= 128, [&](auto kernel, int smem, int threads) {
         kernel<<<a.ctas, threads, smem, st>>>(tm_k, tm_v, tm_q, a);
         const cudaError_t e = cudaGetLastError();
-        return e == cudaSuccess ? launch_join<T>(a, a.tile_rows, head_dim, st) : e;
+        return e == cudaSuccess ? launch_join<T, 1>(a, head_dim, st) : e;
     });
 }
 

@@ -20,7 +20,7 @@
 namespace dflash {
 namespace {
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 256, kRowBlocks = 3;
 
 template <int T> struct RowType;
 template <> struct RowType<PAGED_F16> { using type = __half; };
@@ -115,74 +115,90 @@ __device__ __forceinline__ float2 turn_cs(int p, uint64_t turn, float magnitude)
     return make_float2(cs * magnitude, sn * magnitude);
 }
 
-// Norm and rotation of one row spread over LPR lanes (lane c: values 8c .. 8c+7).
-template <int D>
+// Norm and rotation of one row spread over LPR lanes (lane c: values 8c .. 8c+7).  With inv =
+// 1 / sqrt(mean(x^2) + eps) and x' an element's partner in its pair, both steps together are
+//   y = inv (x A + x' B),   A = w cos,  B = -+ w' sin  (A = w, B = 0 where nothing turns),
+// whose A and B belong to the token and the kind of head, not to the head.
+template <int T, int D>
 struct Turner {
     static constexpr int LPR = D / 8;
-    float cs[8], sn[8];      // half: of this lane's eight elements; interleaved: of its 4 pairs
-    float w[8];              // norm weights
-    int c, rot, layout, shift;
-    bool norm;
+    float A[8], B[8];
+    int c, shift;            // shift: lanes to the partner's (half layout; 0: in this lane, or none)
+    bool norm, turns;        // turns: this lane's elements do
 
-    __device__ void angles(const PagedRowsArgs &a, int p) {
-        rot = a.rot;
-        layout = a.layout;
-        const int e0 = 8 * c, half = rot / 2;
-        shift = 0;
-        if (e0 >= rot) return;
-        if (layout == PAGED_HALF) {
-            const int j = e0 < half ? e0 : e0 - half;
-            shift = e0 < half ? half / 8 : -(half / 8);
+    // A and B at position p under weights wt (worked out anew for queries and keys: the cosines kept
+    // between the two would spill)
+    __device__ __forceinline__ void prepare(const PagedRowsArgs &a, const float *wt, int p, int lane) {
+        norm = wt != nullptr;
+        float w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = 1.f;
+        if (norm) {
+            const float4 x = reinterpret_cast<const float4 *>(wt)[2 * c], y = reinterpret_cast<const float4 *>(wt)[2 * c + 1];
+            w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+            w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
+        }
+        const int e0 = 8 * c, half = a.rot / 2;
+        const bool halves = a.layout == PAGED_HALF, first = e0 < half;
+        turns = e0 < a.rot;
+        shift = !turns || !halves ? 0 : (first ? half / 8 : -(half / 8));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float far = __shfl_sync(0xffffffffu, w[e], lane + shift);
+            B[e] = halves ? far : w[e ^ 1];
+        }
+        if (!turns) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float2 r = turn_cs(p, a.turn[j + e], a.magnitude);
-                cs[e] = r.x;
-                sn[e] = r.y;
+                A[e] = w[e];
+                B[e] = 0.f;
+            }
+        } else if (halves) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float2 r = turn_cs(p, a.turn[(first ? e0 : e0 - half) + e], a.magnitude);
+                A[e] = w[e] * r.x;
+                B[e] *= first ? -r.y : r.y;
             }
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float2 r = turn_cs(p, a.turn[e0 / 2 + e], a.magnitude);
-                cs[e] = r.x;
-                sn[e] = r.y;
+                A[2 * e] = w[2 * e] * r.x;
+                A[2 * e + 1] = w[2 * e + 1] * r.x;
+                B[2 * e] *= -r.y;
+                B[2 * e + 1] *= r.y;
             }
         }
     }
-    __device__ void weights(const float *wt) {
-        norm = wt != nullptr;
-        if (!norm) return;
-        const float4 a = reinterpret_cast<const float4 *>(wt)[2 * c], b = reinterpret_cast<const float4 *>(wt)[2 * c + 1];
-        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-        w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-    }
-    __device__ __forceinline__ void apply(float (&x)[8], float eps, int lane) const {
+    __device__ __forceinline__ void apply(const PagedRowsArgs &a, const Raw8<T> &raw, float (&y)[8], int lane) const {
+        float x[8];
+        widen(raw, x);
+        float inv = 1.f;
         if (norm) {
             float ss = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
             for (int d = LPR / 2; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-            const float inv = rsqrtf(ss * (1.f / D) + eps);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * w[e];
+            inv = rsqrtf(ss * (1.f / D) + a.eps);
         }
-        if (rot == 0) return;
-        if (layout == PAGED_HALF) {
-            float y[8];
+        if (a.rot == 0) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(0xffffffffu, x[e], lane + shift);
-            if (8 * c < rot) {
-                const float sg = shift > 0 ? -1.f : 1.f;     // first half: x cos - y sin
+            for (int e = 0; e < 8; ++e) y[e] = x[e] * A[e] * inv;
+        } else if (a.layout == PAGED_HALF) {
+            Raw8<T> far = raw;
+            uint32_t *f = reinterpret_cast<uint32_t *>(&far);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = fmaf(x[e], cs[e], sg * y[e] * sn[e]);
-            }
-        } else if (8 * c < rot) {
+            for (int e = 0; e < (T == PAGED_F32 ? 8 : 4); ++e) f[e] = __shfl_sync(0xffffffffu, f[e], lane + shift);
+            if (!turns) far = Raw8<T>{};                   // (an infinity times 0)
+            float z[8];
+            widen(far, z);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float x1 = x[2 * e], x2 = x[2 * e + 1];
-                x[2 * e] = fmaf(x1, cs[e], -x2 * sn[e]);
-                x[2 * e + 1] = fmaf(x1, sn[e], x2 * cs[e]);
-            }
+            for (int e = 0; e < 8; ++e) y[e] = fmaf(z[e], B[e], x[e] * A[e]) * inv;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = fmaf(turns ? x[e ^ 1] : 0.f, B[e], x[e] * A[e]) * inv;
         }
     }
 };
@@ -225,37 +241,36 @@ __device__ __forceinline__ void store_page(const PagedPool &pool, uint8_t *base,
     }
 }
 
+// A warp step is RPW rows of one kind (queries, keys, values) of one token; a token's steps are laid
+// end to end and a task is `iters` of them, all of them where there are tokens enough.
 template <int T, int D, bool PAGED>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, kRowBlocks)
 k_paged_rows(const __grid_constant__ PagedRowsArgs a) {
     constexpr int LPR = D / 8, RPW = 32 / LPR, U = 4;      // rows a warp step, steps in flight
     const int lane = threadIdx.x & 31;
     const int64_t gw = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
-    const int tasks = a.cq + a.ck + a.cv;
-    const int64_t t64 = gw / tasks;
+    const int64_t t64 = gw / a.tasks;
     if (t64 >= a.n_rows) return;
     const int t = (int)t64;
-    int task = (int)(gw - t64 * tasks);
-    const int kind = task < a.cq ? 0 : (task < a.cq + a.ck ? 1 : 2);
-    task -= kind == 0 ? 0 : (kind == 1 ? a.cq : a.cq + a.ck);
-    const int heads = kind == 0 ? a.nq : (kind == 1 ? a.nk : a.nv);
-    const int h0 = task * a.iters * RPW, h1 = min(heads, h0 + a.iters * RPW);
-    const void *src = kind == 0 ? a.q : (kind == 1 ? a.k : a.v);
-    const int64_t src_hs = kind == 0 ? a.q_hs : (kind == 1 ? a.k_hs : a.v_hs);
-    const int64_t src0 = (int64_t)t * (kind == 0 ? a.q_rs : (kind == 1 ? a.k_rs : a.v_rs));
+    const int s0 = (int)(gw - t64 * a.tasks) * a.iters, s1 = min(a.steps_q + a.steps_k + a.steps_v, s0 + a.iters);
     const int sub = lane / LPR, c = lane % LPR;
+    auto kind_of = [&](int st) { return st < a.steps_q ? 0 : (st < a.steps_q + a.steps_k ? 1 : 2); };
+    auto head_of = [&](int st, int kind) { return (st - (kind == 0 ? 0 : (kind == 1 ? a.steps_q : a.steps_q + a.steps_k))) * RPW + sub; };
 
     // the first rows are on their way while the token's place is looked up
     Raw8<T> raw[U];
-    auto load = [&](int h) {
+    auto load = [&](int st) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int hh = h + u * RPW + sub;
-            if (hh < h1) raw[u] = load8<T>(src, src0 + hh * src_hs + 8 * c);
-            else raw[u].w[0] = make_uint4(0, 0, 0, 0);
+            const int kind = kind_of(st + u), h = head_of(st + u, kind);
+            const void *src = kind == 0 ? a.q : (kind == 1 ? a.k : a.v);
+            const int64_t off = (int64_t)t * (kind == 0 ? a.q_rs : (kind == 1 ? a.k_rs : a.v_rs)) +
+                                (int64_t)h * (kind == 0 ? a.q_hs : (kind == 1 ? a.k_hs : a.v_hs));
+            if (st + u < s1 && h < (kind == 0 ? a.nq : a.nk)) raw[u] = load8<T>(src, off + 8 * c);
+            else raw[u] = Raw8<T>{};
         }
     };
-    load(h0);
+    load(s0);
 
     int pos = 0;
     bool mapped = true;
@@ -276,33 +291,33 @@ k_paged_rows(const __grid_constant__ PagedRowsArgs a) {
         }
         if (!mapped && lane == 0) atomicOr(a.err, (uint32_t)PAGED_ERR_PAGE);
     }
-    Turner<D> tr;
+    Turner<T, D> tr;
     tr.c = c;
-    tr.norm = false;
-    tr.rot = 0;
-    if (kind < 2) {
-        tr.weights(kind == 0 ? a.q_norm : a.k_norm);
-        if (a.rot) tr.angles(a, a.positions ? a.positions[t] : pos);
-    }
-    const bool to_rows = kind == 0 || !PAGED;
-    void *dst = kind == 0 ? a.qo : a.ko;
-    const int64_t dst_hs = kind == 0 ? a.qo_hs : a.ko_hs;
-    const int64_t dst0 = (int64_t)t * (kind == 0 ? a.qo_rs : a.ko_rs);
-    for (int h = h0; h < h1; h += U * RPW) {
-        if (h != h0) load(h);
+    int last = 2;                                          // the kind whose A and B are at hand
+    const int at = a.rot && a.positions ? a.positions[t] : pos;
+    for (int st = s0; st < s1; st += U) {
+        if (st != s0) load(st);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (h + u * RPW >= h1) break;                      // uniform over the warp
-            const int hh = h + u * RPW + sub;
-            float x[8];
-            widen(raw[u], x);
-            tr.apply(x, a.eps, lane);
-            if (to_rows) {
-                if (hh < h1) store8<T>(dst, dst0 + hh * dst_hs + 8 * c, x);
+            if (st + u >= s1) break;                       // uniform over the warp, as kinds are
+            const int kind = kind_of(st + u), h = head_of(st + u, kind);
+            float y[8];
+            if (kind < 2) {
+                if (kind != last) {
+                    tr.prepare(a, kind == 0 ? a.q_norm : a.k_norm, at, lane);
+                    last = kind;
+                }
+                tr.apply(a, raw[u], y, lane);
+            } else {
+                widen(raw[u], y);
+            }
+            if (kind == 0) {
+                if (h < a.nq) store8<T>(a.qo, (int64_t)t * a.qo_rs + (int64_t)h * a.qo_hs + 8 * c, y);
             } else if constexpr (PAGED) {
                 store_page<T, LPR>(a.pool, kind == 1 ? a.pool.k : a.pool.v, kind == 1 ? a.pool.ks : a.pool.vs,
-                                   off + hh * a.pool.head_stride, soff + hh * a.pool.s_head_stride, c,
-                                   hh < h1 && mapped, x);
+                                   off + h * a.pool.head_stride, soff + h * a.pool.s_head_stride, c, h < a.nk && mapped, y);
+            } else {
+                if (h < a.nk) store8<T>(a.ko, (int64_t)t * a.ko_rs + (int64_t)h * a.ko_hs + 8 * c, y);
             }
         }
     }
@@ -392,12 +407,11 @@ k_paged_gather(const __grid_constant__ PagedGatherArgs a) {
     }
 }
 
-// Warp steps per task: whole tokens when there are plenty (their angles are worked out once),
-// single steps when there are few and latency counts.
-int steps_per_task(int64_t rows_total, int rpw, int sms) {
-    const int64_t steps = (rows_total + rpw - 1) / rpw;
-    const int64_t warps = (int64_t)sms * 32;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(16, steps / warps));
+// Warp steps per task: as few as still leave one wave of warps, and at most `most`.  Few tokens: one
+// step, or the few that keep the grid within a wave, since latency counts; many: whole tokens, whose
+// angles are then worked out once.
+int steps_per_task(int64_t steps, int most, int warps) {
+    return (int)std::max<int64_t>(1, std::min<int64_t>(most, (steps + warps - 1) / warps));
 }
 
 int sm_count() {
@@ -410,12 +424,13 @@ int sm_count() {
 template <int T, int D>
 cudaError_t rows_t(PagedRowsArgs a, bool paged, cudaStream_t st) {
     constexpr int rpw = 32 / (D / 8);
-    a.iters = steps_per_task(a.n_rows * (a.nq + a.nk + a.nv), rpw, sm_count());
-    const int per = a.iters * rpw;
-    a.cq = (a.nq + per - 1) / per;
-    a.ck = (a.nk + per - 1) / per;
-    a.cv = (a.nv + per - 1) / per;
-    const int64_t warps = a.n_rows * (a.cq + a.ck + a.cv);
+    a.steps_q = (a.nq + rpw - 1) / rpw;
+    a.steps_k = (a.nk + rpw - 1) / rpw;
+    a.steps_v = (a.nv + rpw - 1) / rpw;
+    const int steps = a.steps_q + a.steps_k + a.steps_v;
+    a.iters = steps_per_task(a.n_rows * steps, steps, sm_count() * kRowBlocks * (kRowThreads / 32));
+    a.tasks = (steps + a.iters - 1) / a.iters;
+    const int64_t warps = a.n_rows * a.tasks;
     const int64_t blocks = (warps + kRowThreads / 32 - 1) / (kRowThreads / 32);
     if (blocks <= 0) return cudaSuccess;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
@@ -430,7 +445,8 @@ cudaError_t rows_t(PagedRowsArgs a, bool paged, cudaStream_t st) {
 template <int T, int D>
 cudaError_t gather_t(PagedGatherArgs a, cudaStream_t st) {
     constexpr int rpw = 32 / (D / 8);
-    a.iters = steps_per_task(a.batch.n_rows * 2 * a.pool.n_head_kv, rpw, sm_count());
+    const int steps = (2 * a.pool.n_head_kv + rpw - 1) / rpw;
+    a.iters = steps_per_task(a.batch.n_rows * steps, std::min(steps, 16), sm_count() * 32);
     a.chunks = (2 * a.pool.n_head_kv + a.iters * rpw - 1) / (a.iters * rpw);
     const int64_t warps = a.batch.n_rows * a.chunks;
     const int64_t blocks = (warps + kRowThreads / 32 - 1) / (kRowThreads / 32);
