@@ -101,16 +101,19 @@ typedef struct paged_batch {
  * Position rotation: a pair (x1, x2) at position p turns to
  *   magnitude * (x1 cos a - x2 sin a, x1 sin a + x2 cos a),  a = p * inv_freq[i],
  * for the rotary_dim / 2 pairs of a head's first rotary_dim elements; the others stay.
- *   rotary_dim  a positive multiple of 16, at most head_dim.
- *   inv_freq    host double [rotary_dim / 2], >= 0: scaled frequencies are the caller's.
- * The angle's whole turns are taken off in 64-bit integers, so far positions keep their
- * angle to float32 precision.
+ *
+ * paged_rope_init -- fill *rope.  inv_freq: host double [rotary_dim / 2], 0 <= f < 1e6 (scaled
+ * frequencies are the caller's); rotary_dim: a multiple of 16 up to 128 (and up to head_dim where
+ * it is used).  The struct holds frequencies as turns per position in units of 2^-64: a product
+ * with a position loses its whole turns in 64-bit integers, so far positions keep their angle to
+ * float32 precision.  No CUDA call.  Errors: EINVAL.
  */
 typedef struct paged_rope {
-    const double *inv_freq;
-    double magnitude;
-    int32_t rotary_dim, layout;
+    uint64_t turns[64];
+    float magnitude;
+    int32_t rotary_dim, layout, reserved;
 } paged_rope;
+int paged_rope_init(paged_rope *rope, const double *inv_freq, double magnitude, int32_t rotary_dim, int32_t layout);
 
 /*
  * paged_norm_rope -- per head: y = x / sqrt(mean(x^2) + eps) * w (w = q_norm / k_norm, F32

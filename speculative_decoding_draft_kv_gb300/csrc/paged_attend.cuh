@@ -87,7 +87,7 @@ k_paged_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t bar0 = smem_u32(smem + C::kOffBars);       // full[S], empty[S]
-    __shared__ int64_t s_plan[8];
+    __shared__ int64_t s_plan[9];
     __shared__ volatile int s_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 

@@ -8,6 +8,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <cstring>
 #include <mutex>
 
 namespace dflash {
@@ -128,12 +129,8 @@ int check_rope(const char *who, const paged_rope *r, int head_dim) {
     if (!r) return RING_OK;
     if (r->rotary_dim <= 0 || r->rotary_dim % 16 || r->rotary_dim > head_dim)
         return fail(RING_EINVAL, "%s: rotary_dim %d (a multiple of 16 up to head_dim)", who, r->rotary_dim);
-    if (r->layout != PAGED_HALF && r->layout != PAGED_INTERLEAVED)
-        return fail(RING_EINVAL, "%s: unknown rotation layout %d", who, r->layout);
-    if (!r->inv_freq || !std::isfinite(r->magnitude)) return fail(RING_EINVAL, "%s: rotation without frequencies", who);
-    for (int i = 0; i < r->rotary_dim / 2; ++i)
-        if (!(r->inv_freq[i] >= 0.0) || !(r->inv_freq[i] < 1e6))
-            return fail(RING_EINVAL, "%s: inv_freq[%d] out of range", who, i);
+    if ((r->layout != PAGED_HALF && r->layout != PAGED_INTERLEAVED) || !std::isfinite(r->magnitude))
+        return fail(RING_EINVAL, "%s: the rotation is not paged_rope_init's", who);
     return RING_OK;
 }
 
@@ -153,8 +150,8 @@ uint64_t turns_of(double f) {
 void set_rope(PagedRowsArgs &a, const paged_rope *r) {
     a.rot = r ? r->rotary_dim : 0;
     a.layout = r ? r->layout : 0;
-    a.magnitude = r ? (float)r->magnitude : 1.f;
-    for (int i = 0; i < a.rot / 2; ++i) a.turn[i] = turns_of(r->inv_freq[i]);
+    a.magnitude = r ? r->magnitude : 1.f;
+    if (r) std::memcpy(a.turn, r->turns, sizeof(uint64_t) * (r->rotary_dim / 2));
 }
 
 PagedPool pool_of(const paged_cache *c) {
@@ -269,6 +266,22 @@ using namespace dflash;
         const int rc_ = (x);           \
         if (rc_ != RING_OK) return rc_; \
     } while (0)
+
+extern "C" int paged_rope_init(paged_rope *r, const double *inv_freq, double magnitude, int32_t rotary_dim, int32_t layout) {
+    static const char *who = "paged_rope_init";
+    if (!r || !inv_freq) return fail(RING_EINVAL, "%s: NULL argument", who);
+    paged_rope x{};
+    x.magnitude = (float)magnitude;
+    x.rotary_dim = rotary_dim;
+    x.layout = layout;
+    TRY(check_rope(who, &x, kPagedMaxDim));
+    for (int i = 0; i < rotary_dim / 2; ++i) {
+        if (!(inv_freq[i] >= 0.0) || !(inv_freq[i] < 1e6)) return fail(RING_EINVAL, "%s: inv_freq[%d] out of range", who, i);
+        x.turns[i] = turns_of(inv_freq[i]);
+    }
+    *r = x;
+    return RING_OK;
+}
 
 extern "C" int paged_norm_rope(const paged_norm_rope_args *g, void *stream) {
     static const char *who = "paged_norm_rope";

@@ -90,10 +90,16 @@ struct PagedShare {
     int64_t rem;                     // the CTA's first tile, counted from sequence seq's first
     int tiles, per;                  // this CTA's tiles, and those of a full share
     int seq;
+    PagedSeq q;                      // of sequence seq
 };
 
+// 64-bit numbers here are nearly always small ones, and a 64-bit division is a long way
+__device__ __forceinline__ int64_t small_div(int64_t a, int64_t b) {
+    return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // Block-wide: every thread calls it, every thread gets the CTA's share.  scratch: shared
-// memory of THREADS / 32 + 2 int64.
+// memory of THREADS / 32 + 4 int64.
 template <int KT, int THREADS>
 __device__ __forceinline__ PagedShare paged_share(const PagedAttendArgs &a, int64_t *scratch) {
     constexpr int WARPS = THREADS / 32;
@@ -126,7 +132,7 @@ __device__ __forceinline__ PagedShare paged_share(const PagedAttendArgs &a, int6
     }
     const int64_t mine = base + incl - sum;       // tiles in front of this thread's sequences
     // a share of 2^31 tiles would take hours: 32 bits are enough for one
-    const int64_t per = max((int64_t)a.min_tiles, (total + a.ctas - 1) / a.ctas);
+    const int64_t per = max((int64_t)a.min_tiles, small_div(total + a.ctas - 1, a.ctas));
     const int64_t begin = min(total, (int64_t)blockIdx.x * per), end = min(total, begin + per);
     if (begin < end && mine <= begin && begin < mine + sum) {
         int64_t at = mine;
@@ -136,6 +142,8 @@ __device__ __forceinline__ PagedShare paged_share(const PagedAttendArgs &a, int6
             if (begin < at + w) {
                 scratch[WARPS] = begin - at;
                 scratch[WARPS + 1] = s;
+                scratch[WARPS + 2] = (int64_t)sh.q.n << 32 | (uint32_t)sh.q.row0;
+                scratch[WARPS + 3] = sh.q.kv;
                 break;
             }
             at += w;
@@ -147,6 +155,10 @@ __device__ __forceinline__ PagedShare paged_share(const PagedAttendArgs &a, int6
     r.seq = (int)scratch[WARPS + 1];
     r.tiles = r.seq < 0 ? 0 : (int)(end - begin);
     r.per = (int)per;
+    r.q.row0 = (int)scratch[WARPS + 2];
+    r.q.n = (int)(scratch[WARPS + 2] >> 32);
+    r.q.kv = (int)scratch[WARPS + 3];
+    r.q.ok = true;
     return r;
 }
 
@@ -167,11 +179,16 @@ struct PagedWalk {
         seq = r.seq;
         head = rt = off = 0;
         if (left == 0) return;
-        sh.load(a, seq);
+        sh.q = r.q;
+        sh.ctx = r.q.kv - r.q.n;
         const int64_t per_head = sh.head_tiles(a);
         int64_t rem = r.rem;
-        head = (int)(rem / per_head);
+        head = (int)small_div(rem, per_head);
         rem -= head * per_head;
+        if (per_head == sh.tiles(a, 0)) {            // one row tile
+            off = (int)rem;
+            return;
+        }
         // the row tile that holds tile rem of the head, 32 row tiles at a time
         const int lane = threadIdx.x & 31, n = sh.row_tiles(a);
         while (true) {

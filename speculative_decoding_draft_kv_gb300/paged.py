@@ -27,7 +27,7 @@ LAYOUTS = {"half": PAGED_HALF, "interleaved": PAGED_INTERLEAVED}
 _TYPES = {torch.float16: PAGED_F16, torch.bfloat16: PAGED_BF16, torch.float32: PAGED_F32,
           torch.int8: PAGED_INT8, torch.float8_e4m3fn: PAGED_E4M3}
 
-EXPORTED = ("paged_norm_rope", "paged_append", "paged_gather", "paged_attend", "paged_attend_workspace",
+EXPORTED = ("paged_rope_init", "paged_norm_rope", "paged_append", "paged_gather", "paged_attend", "paged_attend_workspace",
             "paged_device_error", "paged_last_error")
 
 _vp, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
@@ -46,8 +46,8 @@ class PagedBatchArgs(ctypes.Structure):
 
 
 class PagedRopeArgs(ctypes.Structure):
-    _fields_ = [("inv_freq", ctypes.POINTER(ctypes.c_double)), ("magnitude", ctypes.c_double),
-                ("rotary_dim", _i32), ("layout", _i32)]
+    _fields_ = [("turns", ctypes.c_uint64 * 64), ("magnitude", _f32), ("rotary_dim", _i32), ("layout", _i32),
+                ("reserved", _i32)]
 
 
 class PagedNormRopeArgs(ctypes.Structure):
@@ -89,6 +89,7 @@ def _load():
         for name in ("paged_norm_rope", "paged_append", "paged_gather", "paged_attend"):
             fn = getattr(lib, name)
             fn.argtypes, fn.restype = [_vp, _vp], ctypes.c_int
+        lib.paged_rope_init.argtypes = [_vp, ctypes.POINTER(ctypes.c_double), ctypes.c_double, _i32, _i32]
         lib.paged_attend_workspace.argtypes = [_vp, _vp, _i32, ctypes.POINTER(_i64)]
         lib.paged_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint32)]
         lib.paged_last_error.restype = ctypes.c_char_p
@@ -115,39 +116,35 @@ def _device(t, name):
     return d
 
 
+# The handle of PyTorch's current stream without the Python object around it (1 us of a call of 8).
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream(stream, device):
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return _current_stream(device)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _rows(t, name, device, heads=None, head_dim=None, dtype=None, n_rows=None):
-    """(pointer, row stride, head stride) of a rows tensor [n_rows, heads, head_dim]."""
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be a CUDA tensor of the call's device")
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or (shape[2] > 1 and stride[2] != 1):
-        raise ValueError(f"{name} must be [rows, heads, head_dim] with contiguous heads")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if heads is not None and (shape[1] != heads or shape[2] != head_dim):
-        raise ValueError(f"{name} must be [rows, {heads}, {head_dim}], got {tuple(shape)}")
-    if n_rows is not None and shape[0] != n_rows:
-        raise ValueError(f"{name} must have {n_rows} rows, got {shape[0]}")
+def _rows(t, name, n, heads, dim, dtype, device):
+    """(pointer, row stride, head stride) of a rows tensor [n, heads, dim]."""
+    s = t.stride()
+    if t.shape != (n, heads, dim) or t.dtype is not dtype or t.get_device() != device or s[2] != 1:
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        raise ValueError(f"{name} must be [{n}, {heads}, {dim}] with contiguous heads on device {device}, got "
+                         f"{tuple(t.shape)} with strides {s} on device {t.get_device()}")
     # strides of dimensions of one entry say nothing
-    return t.data_ptr(), stride[0] if shape[0] > 1 else 0, stride[1] if shape[1] > 1 else 0
+    return t.data_ptr(), s[0] if n > 1 else 0, s[1] if heads > 1 else 0
 
 
 def _vector(t, name, dtype, n, device):
-    """Pointer of a contiguous vector of n entries, None for none."""
-    if t is None:
-        return None
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be a CUDA tensor of the call's device")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with {n} entries")
+    """Pointer of a contiguous tensor of n entries."""
+    if t.dtype is not dtype or t.numel() != n or t.get_device() != device or not t.is_contiguous():
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        raise ValueError(f"{name} must be contiguous with {n} entries on device {device}")
     return t.data_ptr()
 
 
@@ -249,16 +246,27 @@ class PagedRope:
         if len(inv_freq) != rotary_dim // 2:
             raise ValueError(f"inv_freq must have {rotary_dim // 2} entries, got {len(inv_freq)}")
         self.inv_freq, self.magnitude = [float(f) for f in inv_freq], float(magnitude)
-        self._table = (ctypes.c_double * len(self.inv_freq))(*self.inv_freq)
-        self.args = PagedRopeArgs(self._table, self.magnitude, rotary_dim, LAYOUTS.get(layout, layout))
+        self.args = PagedRopeArgs()
         self.address = ctypes.addressof(self.args)
+        _check(_load().paged_rope_init(self.address, (ctypes.c_double * len(self.inv_freq))(*self.inv_freq),
+                                       self.magnitude, rotary_dim, LAYOUTS.get(layout, layout)))
+
+
+_ROW_TYPES = (torch.float16, torch.bfloat16, torch.float32)
 
 
 def _one_device(cache, batch):
-    if cache.device != batch.device or cache.device != torch.cuda.current_device():
+    d = torch.cuda.current_device()
+    if cache.device != d or batch.device != d:
         raise ValueError(f"cache (device {cache.device}) and batch (device {batch.device}) must be on the current "
-                         f"device, {torch.cuda.current_device()}")
-    return cache.device
+                         f"device, {d}")
+    return d
+
+
+def _half(dtype):
+    if dtype is not torch.float16 and dtype is not torch.bfloat16:
+        raise TypeError(f"rows must be float16 or bfloat16, got {dtype}")
+    return dtype
 
 
 def paged_norm_rope(positions, rope, eps=1e-6, q=None, q_norm=None, q_out=None, k=None, k_norm=None, k_out=None,
@@ -267,30 +275,30 @@ def paged_norm_rope(positions, rope, eps=1e-6, q=None, q_norm=None, q_out=None, 
     ``*_out``: the same shape and type (or the tensor itself); ``*_norm``: float32 [head_dim] or
     None; ``positions``: int32 [rows]; ``rope``: a :class:`PagedRope` or None."""
     lead = q if q is not None else k
-    if lead is None:
-        raise ValueError("neither q nor k given")
-    if (q is None) != (q_out is None) or (k is None) != (k_out is None):
-        raise ValueError("each of q and k goes with its output")
+    if lead is None or (q is None) != (q_out is None) or (k is None) != (k_out is None):
+        raise ValueError("give q, k or both, each with its output")
     dev = _device(lead, "q" if q is not None else "k")
-    dtype = lead.dtype
-    if lead.dim() != 3 or dtype not in (torch.float16, torch.bfloat16, torch.float32):
+    dtype, shape = lead.dtype, lead.shape
+    if len(shape) != 3 or dtype not in _ROW_TYPES:
         raise TypeError("q and k must be float16, bfloat16 or float32 [rows, heads, head_dim]")
-    n, _, dim = lead.shape
-    a = PagedNormRopeArgs(n_rows=n, eps=eps, head_dim=dim, dtype=_TYPES[dtype],
-                          positions=_vector(positions, "positions", torch.int32, n, dev),
-                          rope=rope.address if rope is not None else None)
+    n, _, dim = shape
+    q_ptr = qo_ptr = k_ptr = ko_ptr = qn = kn = None
+    q_row = q_head = qo_row = qo_head = k_row = k_head = ko_row = ko_head = nq = nk = 0
     if q is not None:
-        h = q.shape[1]
-        a.n_head_q = h
-        a.q, a.q_row_stride, a.q_head_stride = _rows(q, "q", dev)
-        a.q_out, a.qo_row_stride, a.qo_head_stride = _rows(q_out, "q_out", dev, h, dim, dtype, n)
-        a.q_norm = _vector(q_norm, "q_norm", torch.float32, dim, dev)
+        nq = q.shape[1]
+        q_ptr, q_row, q_head = _rows(q, "q", n, nq, dim, dtype, dev)
+        qo_ptr, qo_row, qo_head = _rows(q_out, "q_out", n, nq, dim, dtype, dev)
+        if q_norm is not None:
+            qn = _vector(q_norm, "q_norm", torch.float32, dim, dev)
     if k is not None:
-        h = k.shape[1]
-        a.n_head_k = h
-        a.k, a.k_row_stride, a.k_head_stride = _rows(k, "k", dev, h, dim, dtype, n)
-        a.k_out, a.ko_row_stride, a.ko_head_stride = _rows(k_out, "k_out", dev, h, dim, dtype, n)
-        a.k_norm = _vector(k_norm, "k_norm", torch.float32, dim, dev)
+        nk = k.shape[1]
+        k_ptr, k_row, k_head = _rows(k, "k", n, nk, dim, dtype, dev)
+        ko_ptr, ko_row, ko_head = _rows(k_out, "k_out", n, nk, dim, dtype, dev)
+        if k_norm is not None:
+            kn = _vector(k_norm, "k_norm", torch.float32, dim, dev)
+    a = PagedNormRopeArgs(q_ptr, k_ptr, qo_ptr, ko_ptr, q_row, q_head, k_row, k_head, qo_row, qo_head, ko_row, ko_head,
+                          qn, kn, None if positions is None else _vector(positions, "positions", torch.int32, n, dev),
+                          None if rope is None else rope.address, n, eps, nq, nk, dim, _TYPES[dtype])
     _check(_load().paged_norm_rope(ctypes.addressof(a), _stream(stream, dev)))
 
 
@@ -302,25 +310,22 @@ def paged_append(cache, batch, k, v, rope=None, eps=1e-6, k_norm=None, q=None, q
     queries are normed (``q_norm``) and turned in the same pass."""
     dev = _one_device(cache, batch)
     dim, heads, n, dtype = cache.head_dim, cache.n_head_kv, k.shape[0], k.dtype
-    if dtype not in (torch.float16, torch.bfloat16):
-        raise TypeError(f"rows must be float16 or bfloat16, got {dtype}")
     if (q is None) != (q_out is None):
         raise ValueError("q goes with q_out")
-    a = PagedAppendArgs(cache.address, batch.address, n_rows=n, eps=eps, dtype=_TYPES[dtype])
-    a.k, a.k_row_stride, a.k_head_stride = _rows(k, "k", dev, heads, dim)
-    a.v, a.v_row_stride, a.v_head_stride = _rows(v, "v", dev, heads, dim, dtype, n)
-    if rope is not None:
-        a.rope = rope.address
-    if k_norm is not None:
-        a.k_norm = _vector(k_norm, "k_norm", torch.float32, dim, dev)
-    if positions is not None:
-        a.positions = _vector(positions, "positions", torch.int32, n, dev)
+    k_ptr, k_row, k_head = _rows(k, "k", n, heads, dim, _half(dtype), dev)
+    v_ptr, v_row, v_head = _rows(v, "v", n, heads, dim, dtype, dev)
+    q_ptr = qo_ptr = qn = None
+    q_row = q_head = qo_row = qo_head = nq = 0
     if q is not None:
-        a.n_head_q = q.shape[1]
-        a.q, a.q_row_stride, a.q_head_stride = _rows(q, "q", dev, q.shape[1], dim, dtype, n)
-        a.q_out, a.qo_row_stride, a.qo_head_stride = _rows(q_out, "q_out", dev, q.shape[1], dim, dtype, n)
+        nq = q.shape[1]
+        q_ptr, q_row, q_head = _rows(q, "q", n, nq, dim, dtype, dev)
+        qo_ptr, qo_row, qo_head = _rows(q_out, "q_out", n, nq, dim, dtype, dev)
         if q_norm is not None:
-            a.q_norm = _vector(q_norm, "q_norm", torch.float32, dim, dev)
+            qn = _vector(q_norm, "q_norm", torch.float32, dim, dev)
+    a = PagedAppendArgs(cache.address, batch.address, k_ptr, v_ptr, q_ptr, qo_ptr, k_row, k_head, v_row, v_head, q_row,
+                        q_head, qo_row, qo_head, None if k_norm is None else _vector(k_norm, "k_norm", torch.float32, dim, dev),
+                        qn, None if positions is None else _vector(positions, "positions", torch.int32, n, dev),
+                        None if rope is None else rope.address, n, eps, nq, _TYPES[dtype])
     _check(_load().paged_append(ctypes.addressof(a), _stream(stream, dev)))
 
 
@@ -328,10 +333,8 @@ def paged_gather(cache, batch, k, v, stream=None):
     """Read the batch's rows back into ``k``, ``v`` (float16 or bfloat16 [rows, n_head_kv, head_dim])."""
     dev = _one_device(cache, batch)
     dim, heads, n, dtype = cache.head_dim, cache.n_head_kv, k.shape[0], k.dtype
-    if dtype not in (torch.float16, torch.bfloat16):
-        raise TypeError(f"rows must be float16 or bfloat16, got {dtype}")
-    kp, kr, kh = _rows(k, "k", dev, heads, dim)
-    vp, vr, vh = _rows(v, "v", dev, heads, dim, dtype, n)
+    kp, kr, kh = _rows(k, "k", n, heads, dim, _half(dtype), dev)
+    vp, vr, vh = _rows(v, "v", n, heads, dim, dtype, dev)
     a = PagedGatherArgs(cache.address, batch.address, kp, vp, kr, kh, vr, vh, n, _TYPES[dtype], 0)
     _check(_load().paged_gather(ctypes.addressof(a), _stream(stream, dev)))
 
@@ -352,11 +355,9 @@ def paged_attend(cache, batch, q, o, mask="causal", window=0, scale=0.0, tree=No
     [rows, n_head].  ``workspace``: a uint8 tensor of :func:`paged_attend_workspace` bytes that no
     other call uses at the same time, or None for one of the call's own from PyTorch's allocator."""
     dev = _one_device(cache, batch)
-    dtype, n, heads = q.dtype, q.shape[0], q.shape[1]
-    if dtype not in (torch.float16, torch.bfloat16):
-        raise TypeError(f"q must be float16 or bfloat16, got {dtype}")
-    qp, qr, qh = _rows(q, "q", dev, heads, cache.head_dim)
-    op, orow, oh = _rows(o, "o", dev, heads, cache.head_dim, dtype, n)
+    dtype, (n, heads, _) = q.dtype, q.shape
+    qp, qr, qh = _rows(q, "q", n, heads, cache.head_dim, _half(dtype), dev)
+    op, orow, oh = _rows(o, "o", n, heads, cache.head_dim, dtype, dev)
     tp = None if tree is None else _vector(tree, "tree", torch.int64, n, dev)
     lp = None if lse is None else _vector(lse, "lse", torch.float32, n * heads, dev)
     st = _stream(stream, dev)

@@ -79,11 +79,11 @@ def batch(**kw):
 
 
 def rope(rotary_dim=128, layout=P.PAGED_HALF, freq=None, magnitude=1.0):
+    """paged_rope_init's status and struct."""
     f = freq if freq is not None else [1.0] * max(1, rotary_dim // 2)
-    t = (ctypes.c_double * len(f))(*f)
-    r = P.PagedRopeArgs(t, magnitude, rotary_dim, layout)
-    r._keep = t
-    return r
+    r = P.PagedRopeArgs()
+    rc = P._load().paged_rope_init(ctypes.addressof(r), (ctypes.c_double * len(f))(*f), magnitude, rotary_dim, layout)
+    return rc, r
 
 
 KEPT = []               # what an address was taken of lives on
@@ -194,10 +194,28 @@ ROPES = [dict(rotary_dim=0), dict(rotary_dim=24), dict(rotary_dim=144), dict(lay
 
 @pytest.mark.parametrize("bad", ROPES)
 def test_bad_rotations(lib, bad):
-    r = rope(**bad)
+    rc, r = rope(**bad)
+    assert rc == R.RING_EINVAL and r.rotary_dim == 0       # untouched
     c, b = cache(), batch()
-    refused(lib.paged_append, addr(append(c, b, rope=addr(r))), None)
+    refused(lib.paged_append, addr(append(c, b, rope=addr(r))), None)      # one that no init filled
     refused(lib.paged_norm_rope, addr(norm_rope(rope=addr(r))), None)
+    refused(lib.paged_rope_init, None, (ctypes.c_double * 8)(), 1.0, 16, 0)
+    rc, r = rope(128)
+    assert rc == R.RING_OK
+    refused(lib.paged_norm_rope, addr(norm_rope(head_dim=64, rope=addr(r))), None)
+
+
+def test_turns_are_exact_fractions(lib):
+    """inv_freq / 2 pi modulo 1 in units of 2^-64, against rational arithmetic; 1 / 2 pi to 40 digits."""
+    from fractions import Fraction
+    inv = Fraction("0.1591549430918953357688837633725143620345")
+    freq = [1.0, 0.8659643233600653, 1e-6, 0.0, 6.283185307179586, 999999.5, 2.0 ** -60, 0.1]
+    rc, r = rope(16, freq=freq)
+    assert rc == R.RING_OK
+    for f, t in zip(freq, r.turns):
+        want = int(round(Fraction(f) * inv % 1 * 2 ** 64)) % 2 ** 64
+        off = min((t - want) % 2 ** 64, (want - t) % 2 ** 64)
+        assert off <= 1 + f * 2, (f, t, want)          # the low part of 1 / 2 pi is a double itself
 
 
 def norm_rope(**kw):
@@ -214,7 +232,7 @@ def norm_rope(**kw):
 ])
 def test_bad_norm_ropes(lib, bad):
     refused(lib.paged_norm_rope, addr(norm_rope(**bad)), None)
-    r = rope()
+    _, r = rope()
     refused(lib.paged_norm_rope, addr(norm_rope(positions=None, rope=addr(r))), None)
 
 
