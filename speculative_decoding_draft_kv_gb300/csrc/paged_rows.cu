@@ -20,7 +20,7 @@
 namespace dflash {
 namespace {
 
-constexpr int kRowThreads = 256, kRowBlocks = 3;
+constexpr int kRowThreads = 128, kRowBlocks = 6;
 
 template <int T> struct RowType;
 template <> struct RowType<PAGED_F16> { using type = __half; };
@@ -94,17 +94,44 @@ __device__ __forceinline__ float2 e4m3_unpair(uint32_t codes) {   // low 16 bits
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
-// The sequence that row t belongs to (the last s with q_start[s] <= t), and its fields;
-// -1 for a row in front of the first or behind the last sequence.  Lanes take 32 entries
-// at a time, so the loads of a long table do not wait for one another.
-__device__ __forceinline__ int owner_of(const PagedBatchDev &b, int t, int lane) {
-    int count = 0;
+// Where row t lives: its sequence (the last s with q_start[s] <= t) and position, and the page and
+// row in it; found false for a row in front of the first or behind the last sequence, mapped false
+// where the arrays name no place for it.  A lane loads all that belongs to a sequence, 32 sequences
+// at a time, so that only the page number has to wait for another load.
+struct Place {
+    bool found, mapped;
+    int pos, page, slot;
+};
+__device__ __forceinline__ Place place_of(const PagedBatchDev &b, const PagedPool &pool, int t, int lane) {
+    int count = 0, r0 = 0, r1 = 0, kv = 0;
     for (int i = 0; i < b.n_seq; i += 32) {
-        const int v = i + lane < b.n_seq ? b.q_start[i + lane] : 0x7fffffff;
-        count += __popc(__ballot_sync(0xffffffffu, v <= t));
+        const bool in = i + lane < b.n_seq;
+        const int x0 = in ? b.q_start[i + lane] : 0x7fffffff, x1 = in ? b.q_start[i + lane + 1] : 0, x2 = in ? b.kv_len[i + lane] : 0;
+        const int n = __popc(__ballot_sync(0xffffffffu, x0 <= t));
+        if (n) {
+            r0 = x0;
+            r1 = x1;
+            kv = x2;
+        }
+        count += n;
     }
-    if (count == 0 || t >= b.q_start[b.n_seq]) return -1;
-    return count - 1;
+    Place p{};
+    if (count == 0) return p;
+    const int s = count - 1;
+    r0 = __shfl_sync(0xffffffffu, r0, s & 31);
+    r1 = __shfl_sync(0xffffffffu, r1, s & 31);
+    kv = __shfl_sync(0xffffffffu, kv, s & 31);
+    if (r0 > t || t >= r1) return p;
+    p.found = true;
+    const int64_t cap = (int64_t)b.max_pages << pool.page_shift, n = (int64_t)r1 - r0;
+    p.pos = (int)(kv - n + (t - r0));
+    p.mapped = r0 >= 0 && r1 <= b.n_rows && kv >= n && kv <= cap;
+    if (p.mapped) {
+        p.page = b.pages[(int64_t)s * b.pages_stride + (p.pos >> pool.page_shift)];
+        p.slot = p.pos & ((1 << pool.page_shift) - 1);
+        p.mapped = p.page >= 0 && p.page < pool.n_pages;
+    }
+    return p;
 }
 
 // cos and sin (times the magnitude) of p * turn, turn in 2^-64 turns
@@ -276,19 +303,12 @@ k_paged_rows(const __grid_constant__ PagedRowsArgs a) {
     bool mapped = true;
     int64_t off = 0, soff = 0;
     if constexpr (PAGED) {
-        const int s = owner_of(a.batch, t, lane);
-        if (s < 0) return;
-        const PagedSeq q = paged_seq(a.batch, a.pool.page_shift, s);
-        pos = q.kv - q.n + (t - q.row0);
-        const int cap = a.batch.max_pages << a.pool.page_shift;
-        mapped = pos >= 0 && pos < cap && t >= q.row0 && t < q.row0 + q.n && q.ok;
-        if (mapped) {
-            const int page = a.batch.pages[(int64_t)s * a.batch.pages_stride + (pos >> a.pool.page_shift)];
-            const int slot = pos & ((1 << a.pool.page_shift) - 1);
-            mapped = page >= 0 && page < a.pool.n_pages;
-            off = (int64_t)page * a.pool.page_stride + slot * a.pool.row_stride;
-            soff = (int64_t)page * a.pool.s_page_stride + slot;
-        }
+        const Place at = place_of(a.batch, a.pool, t, lane);
+        if (!at.found) return;
+        pos = at.pos;
+        mapped = at.mapped;
+        off = (int64_t)at.page * a.pool.page_stride + at.slot * a.pool.row_stride;
+        soff = (int64_t)at.page * a.pool.s_page_stride + at.slot;
         if (!mapped && lane == 0) atomicOr(a.err, (uint32_t)PAGED_ERR_PAGE);
     }
     Turner<T, D> tr;
@@ -333,24 +353,12 @@ k_paged_gather(const __grid_constant__ PagedGatherArgs a) {
     const int64_t t64 = gw / a.chunks;
     if (t64 >= a.batch.n_rows) return;
     const int t = (int)t64;
-    const int s = owner_of(a.batch, t, lane);
-    if (s < 0) return;
-    const PagedSeq q = paged_seq(a.batch, a.pool.page_shift, s);
-    const int pos = q.kv - q.n + (t - q.row0);
-    const int cap = a.batch.max_pages << a.pool.page_shift;
-    bool mapped = pos >= 0 && pos < cap && t >= q.row0 && t < q.row0 + q.n && q.ok;
-    int page = 0;
-    if (mapped) {
-        page = a.batch.pages[(int64_t)s * a.batch.pages_stride + (pos >> a.pool.page_shift)];
-        mapped = page >= 0 && page < a.pool.n_pages;
-    }
-    if (!mapped) {
-        page = 0;
-        if (lane == 0) atomicOr(a.err, (uint32_t)PAGED_ERR_PAGE);
-    }
-    const int slot = mapped ? pos & ((1 << a.pool.page_shift) - 1) : 0;
-    const int64_t off = (int64_t)page * a.pool.page_stride + slot * a.pool.row_stride;
-    const int64_t soff = (int64_t)page * a.pool.s_page_stride + slot;
+    const Place at = place_of(a.batch, a.pool, t, lane);
+    if (!at.found) return;
+    const bool mapped = at.mapped;
+    if (!mapped && lane == 0) atomicOr(a.err, (uint32_t)PAGED_ERR_PAGE);
+    const int64_t off = mapped ? (int64_t)at.page * a.pool.page_stride + at.slot * a.pool.row_stride : 0;
+    const int64_t soff = mapped ? (int64_t)at.page * a.pool.s_page_stride + at.slot : 0;
     const int sub = lane / LPR, c = lane % LPR;
     // the 2 n_head_kv rows of the token: K heads, then V heads
     const int heads = a.pool.n_head_kv, rows = 2 * heads;
@@ -407,11 +415,11 @@ k_paged_gather(const __grid_constant__ PagedGatherArgs a) {
     }
 }
 
-// Warp steps per task: as few as still leave one wave of warps, and at most `most`.  Few tokens: one
-// step, or the few that keep the grid within a wave, since latency counts; many: whole tokens, whose
-// angles are then worked out once.
-int steps_per_task(int64_t steps, int most, int warps) {
-    return (int)std::max<int64_t>(1, std::min<int64_t>(most, (steps + warps - 1) / warps));
+// Tasks per token: as many as fill one wave of `warps`, at most one per warp step, each of as near
+// the same number of steps as can be.  Few tokens: single steps, or the few that keep the grid within
+// the wave, since latency counts; many: whole tokens, whose angles are then worked out once.
+int tasks_per_token(int64_t tokens, int steps, int warps) {
+    return (int)std::max<int64_t>(1, std::min<int64_t>(steps, warps / std::max<int64_t>(tokens, 1)));
 }
 
 int sm_count() {
@@ -428,7 +436,8 @@ cudaError_t rows_t(PagedRowsArgs a, bool paged, cudaStream_t st) {
     a.steps_k = (a.nk + rpw - 1) / rpw;
     a.steps_v = (a.nv + rpw - 1) / rpw;
     const int steps = a.steps_q + a.steps_k + a.steps_v;
-    a.iters = steps_per_task(a.n_rows * steps, steps, sm_count() * kRowBlocks * (kRowThreads / 32));
+    a.tasks = tasks_per_token(a.n_rows, steps, sm_count() * kRowBlocks * (kRowThreads / 32));
+    a.iters = (steps + a.tasks - 1) / a.tasks;
     a.tasks = (steps + a.iters - 1) / a.iters;
     const int64_t warps = a.n_rows * a.tasks;
     const int64_t blocks = (warps + kRowThreads / 32 - 1) / (kRowThreads / 32);
@@ -446,8 +455,9 @@ template <int T, int D>
 cudaError_t gather_t(PagedGatherArgs a, cudaStream_t st) {
     constexpr int rpw = 32 / (D / 8);
     const int steps = (2 * a.pool.n_head_kv + rpw - 1) / rpw;
-    a.iters = steps_per_task(a.batch.n_rows * steps, std::min(steps, 16), sm_count() * 32);
-    a.chunks = (2 * a.pool.n_head_kv + a.iters * rpw - 1) / (a.iters * rpw);
+    a.chunks = tasks_per_token(a.batch.n_rows, steps, sm_count() * 64);
+    a.iters = (steps + a.chunks - 1) / a.chunks;
+    a.chunks = (steps + a.iters - 1) / a.iters;
     const int64_t warps = a.batch.n_rows * a.chunks;
     const int64_t blocks = (warps + kRowThreads / 32 - 1) / (kRowThreads / 32);
     if (blocks <= 0) return cudaSuccess;
