@@ -230,49 +230,59 @@ struct Turner {
     }
 };
 
-// One row's eight values per lane into a page: 16-bit values, or codes with the row's scale.
-template <int T, int LPR>
-__device__ __forceinline__ void store_page(const PagedPool &pool, uint8_t *base, float *scales, int64_t off,
-                                           int64_t soff, int c, bool live, const float (&x)[8]) {
-    if (pool.format == PAGED_F16 || pool.format == PAGED_BF16) {
-        if (live) store8<T>(base, off + 8 * c, x);
-        return;
-    }
-    // the largest magnitude; as integers, magnitudes order as the floats do and NaN is above all
-    uint32_t top = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+// Eight values per lane of a row that is LPR lanes, quantised: codes and the row's scale.
+// top: the largest magnitude's bits among this lane's values (as integers, magnitudes order as the
+// floats do, and infinities and NaN are above all).
+template <int LPR>
+__device__ __forceinline__ uint2 quantise(const float (&x)[8], uint32_t top, bool int8, float *scale) {
 #pragma unroll
     for (int d = LPR / 2; d; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const float full = pool.format == PAGED_INT8 ? 127.f : 448.f;
+    const float full = int8 ? 127.f : 448.f;
     const float amax = __uint_as_float(top);
     const bool finite = top < 0x7f800000u, any = amax >= 1e-30f;
-    const float inv = finite && any ? full / amax : 0.f;
-    const float scale = !finite ? __int_as_float(0x7fc00000) : (any ? amax / full : 0.f);
+    const float inv = any && finite ? full / amax : 0.f;
+    *scale = !finite ? __int_as_float(0x7fc00000) : (any ? amax / full : 0.f);
     uint2 w = make_uint2(0u, 0u);
-    if (finite) {
-        if (pool.format == PAGED_INT8) {
-            uint32_t b[8];
+    if (int8) {
+        // |x inv| <= 127 + 2^-16: adding 1.5 2^23 leaves the code, rounded to even, in the low byte
+        uint32_t b[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) b[e] = (uint32_t)__float2int_rn(x[e] * inv) & 0xffu;   // |x inv| <= 127 + 2^-16
-            w.x = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
-            w.y = b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24;
-        } else {
-            w.x = e4m3_pair(x[0] * inv, x[1] * inv) | e4m3_pair(x[2] * inv, x[3] * inv) << 16;
-            w.y = e4m3_pair(x[4] * inv, x[5] * inv) | e4m3_pair(x[6] * inv, x[7] * inv) << 16;
-        }
+        for (int e = 0; e < 8; ++e) b[e] = __float_as_uint(__fadd_rn(__fmul_rn(x[e], inv), 12582912.f));
+        w.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+        w.y = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+    } else {
+        w.x = e4m3_pair(x[0] * inv, x[1] * inv) | e4m3_pair(x[2] * inv, x[3] * inv) << 16;
+        w.y = e4m3_pair(x[4] * inv, x[5] * inv) | e4m3_pair(x[6] * inv, x[7] * inv) << 16;
     }
-    if (live) {
-        *reinterpret_cast<uint2 *>(base + off + 8 * c) = w;
-        if (c == 0) scales[soff] = scale;
+    if (!finite) w = make_uint2(0u, 0u);
+    return w;
+}
+
+template <int T>
+__device__ __forceinline__ uint32_t largest(const Raw8<T> &raw, const float (&x)[8], bool same) {
+    uint32_t top = 0;
+    if (T != PAGED_F32 && same) {
+        // the values are the raw ones: two 16-bit magnitudes at a time
+        const uint32_t m = 0x7fff7fffu;
+        const uint32_t a = __vimax3_u16x2(raw.w[0].x & m, raw.w[0].y & m, raw.w[0].z & m);
+        const uint32_t b = __vimax3_u16x2(a, raw.w[0].w & m, 0u);
+        const uint32_t h = max(b & 0xffffu, b >> 16);
+        if constexpr (T == PAGED_BF16) return h << 16;
+        return __float_as_uint(__half2float(__ushort_as_half((unsigned short)h)));
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+    return top;
 }
 
 // A warp step is RPW rows of one kind (queries, keys, values) of one token; a token's steps are laid
-// end to end and a task is `iters` of them, all of them where there are tokens enough.
+// end to end and a task is `iters` of them, all of them where there are tokens enough.  With plenty of
+// tokens the kernel is bound by what it issues (about 0.7 instructions a clock and scheduler), so a
+// step's addresses are two additions, and each kind has a loop of its own.
 template <int T, int D, bool PAGED>
 __global__ void __launch_bounds__(kRowThreads, kRowBlocks)
 k_paged_rows(const __grid_constant__ PagedRowsArgs a) {
+    using E = typename RowType<T>::type;
     constexpr int LPR = D / 8, RPW = 32 / LPR, U = 4;      // rows a warp step, steps in flight
     const int lane = threadIdx.x & 31;
     const int64_t gw = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
@@ -281,23 +291,39 @@ k_paged_rows(const __grid_constant__ PagedRowsArgs a) {
     const int t = (int)t64;
     const int s0 = (int)(gw - t64 * a.tasks) * a.iters, s1 = min(a.steps_q + a.steps_k + a.steps_v, s0 + a.iters);
     const int sub = lane / LPR, c = lane % LPR;
-    auto kind_of = [&](int st) { return st < a.steps_q ? 0 : (st < a.steps_q + a.steps_k ? 1 : 2); };
-    auto head_of = [&](int st, int kind) { return (st - (kind == 0 ? 0 : (kind == 1 ? a.steps_q : a.steps_q + a.steps_k))) * RPW + sub; };
 
-    // the first rows are on their way while the token's place is looked up
+    // one kind's steps of this task: [from, to) of the kind's own
+    struct Run {
+        const E *src;
+        int64_t stride;      // per step
+        int from, to, heads;
+    };
+    auto run_of = [&](const void *base, int64_t rs, int64_t hs, int before, int steps, int heads) {
+        Run r;
+        r.from = max(0, s0 - before);
+        r.to = min(steps, s1 - before);
+        r.heads = heads;
+        r.stride = (int64_t)RPW * hs;
+        r.src = reinterpret_cast<const E *>(base) + (int64_t)t * rs + (int64_t)(r.from * RPW + sub) * hs + 8 * c;
+        return r;
+    };
     Raw8<T> raw[U];
-    auto load = [&](int st) {
+    auto load = [&](const Run &r, int st) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int kind = kind_of(st + u), h = head_of(st + u, kind);
-            const void *src = kind == 0 ? a.q : (kind == 1 ? a.k : a.v);
-            const int64_t off = (int64_t)t * (kind == 0 ? a.q_rs : (kind == 1 ? a.k_rs : a.v_rs)) +
-                                (int64_t)h * (kind == 0 ? a.q_hs : (kind == 1 ? a.k_hs : a.v_hs));
-            if (st + u < s1 && h < (kind == 0 ? a.nq : a.nk)) raw[u] = load8<T>(src, off + 8 * c);
-            else raw[u] = Raw8<T>{};
+            raw[u] = Raw8<T>{};
+            if (st + u < r.to && (st + u) * RPW + sub < r.heads) raw[u] = load8<T>(r.src, (int64_t)(st + u - r.from) * r.stride);
         }
     };
-    load(s0);
+    const Run rq = run_of(a.q, a.q_rs, a.q_hs, 0, a.steps_q, a.nq);
+    const Run rk = run_of(a.k, a.k_rs, a.k_hs, a.steps_q, a.steps_k, a.nk);
+    const Run rv = run_of(a.v, a.v_rs, a.v_hs, a.steps_q + a.steps_k, a.steps_v, a.nv);
+
+    // the first rows are on their way while the token's place is looked up
+    if (rq.from < rq.to) load(rq, rq.from);
+    else if (rk.from < rk.to) load(rk, rk.from);
+    else load(rv, rv.from);
+    bool loaded = true;
 
     int pos = 0;
     bool mapped = true;
@@ -311,35 +337,59 @@ k_paged_rows(const __grid_constant__ PagedRowsArgs a) {
         soff = (int64_t)at.page * a.pool.s_page_stride + at.slot;
         if (!mapped && lane == 0) atomicOr(a.err, (uint32_t)PAGED_ERR_PAGE);
     }
+    const int at = a.rot && a.positions ? a.positions[t] : pos;
     Turner<T, D> tr;
     tr.c = c;
-    int last = 2;                                          // the kind whose A and B are at hand
-    const int at = a.rot && a.positions ? a.positions[t] : pos;
-    for (int st = s0; st < s1; st += U) {
-        if (st != s0) load(st);
+
+    // steps of one kind, fn(row's head, raw, values, turned)
+    auto walk = [&](const Run &r, bool turned, const float *wt, auto &&fn) {
+        if (r.from >= r.to) return;
+        if (turned) tr.prepare(a, wt, at, lane);
+        for (int st = r.from; st < r.to; st += U) {
+            if (!loaded) load(r, st);
+            loaded = false;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (st + u >= s1) break;                       // uniform over the warp, as kinds are
-            const int kind = kind_of(st + u), h = head_of(st + u, kind);
-            float y[8];
-            if (kind < 2) {
-                if (kind != last) {
-                    tr.prepare(a, kind == 0 ? a.q_norm : a.k_norm, at, lane);
-                    last = kind;
-                }
-                tr.apply(a, raw[u], y, lane);
-            } else {
-                widen(raw[u], y);
-            }
-            if (kind == 0) {
-                if (h < a.nq) store8<T>(a.qo, (int64_t)t * a.qo_rs + (int64_t)h * a.qo_hs + 8 * c, y);
-            } else if constexpr (PAGED) {
-                store_page<T, LPR>(a.pool, kind == 1 ? a.pool.k : a.pool.v, kind == 1 ? a.pool.ks : a.pool.vs,
-                                   off + h * a.pool.head_stride, soff + h * a.pool.s_head_stride, c, h < a.nk && mapped, y);
-            } else {
-                if (h < a.nk) store8<T>(a.ko, (int64_t)t * a.ko_rs + (int64_t)h * a.ko_hs + 8 * c, y);
+            for (int u = 0; u < U; ++u) {
+                if (st + u >= r.to) break;                 // uniform over the warp
+                float y[8];
+                if (turned) tr.apply(a, raw[u], y, lane);
+                else widen(raw[u], y);
+                fn((st + u) * RPW + sub, raw[u], y);
             }
         }
+    };
+    const bool q_turns = a.rot || a.q_norm, k_turns = a.rot || a.k_norm;
+    {
+        E *dst = reinterpret_cast<E *>(a.qo) + (int64_t)t * a.qo_rs + 8 * c;
+        walk(rq, q_turns, a.q_norm, [&](int h, const Raw8<T> &, const float (&y)[8]) {
+            if (h < a.nq) store8<T>(dst, (int64_t)h * a.qo_hs, y);
+        });
+    }
+    if constexpr (!PAGED) {
+        E *dst = reinterpret_cast<E *>(a.ko) + (int64_t)t * a.ko_rs + 8 * c;
+        walk(rk, k_turns, a.k_norm, [&](int h, const Raw8<T> &, const float (&y)[8]) {
+            if (h < a.nk) store8<T>(dst, (int64_t)h * a.ko_hs, y);
+        });
+    } else {
+        const bool wide = a.pool.format == PAGED_F16 || a.pool.format == PAGED_BF16, int8 = a.pool.format == PAGED_INT8;
+        auto put = [&](uint8_t *pool, float *scales, bool turned) {
+            return [=, &a](int h, const Raw8<T> &raw, const float (&y)[8]) {
+                const bool live = h < a.nk && mapped;
+                const int64_t e = off + (int64_t)h * a.pool.head_stride + 8 * c;
+                if (wide) {
+                    if (live) store8<T>(pool, e, y);
+                    return;
+                }
+                float scale;
+                const uint2 w = quantise<LPR>(y, largest<T>(raw, y, !turned), int8, &scale);
+                if (live) {
+                    *reinterpret_cast<uint2 *>(pool + e) = w;
+                    if (c == 0) scales[soff + (int64_t)h * a.pool.s_head_stride] = scale;
+                }
+            };
+        };
+        walk(rk, k_turns, a.k_norm, put(a.pool.k, a.pool.ks, k_turns));
+        walk(rv, false, nullptr, put(a.pool.v, a.pool.vs, false));
     }
 }
 
