@@ -74,7 +74,7 @@ struct PagedGatherArgs {
     PagedPool pool;
     PagedBatchDev batch;
     uint32_t *err;
-    int iters, chunks;
+    int steps, iters, chunks;         // warp steps of a token's K (or V), steps per task, tasks per token
 };
 cudaError_t launch_paged_gather(const PagedGatherArgs &a, int dtype, int head_dim, cudaStream_t st);
 

@@ -13,6 +13,7 @@
 // integer multiplication, exactly, and float32 sees only the rest (at most half a turn):
 // no float64 and no large arguments, for any position.
 #include "paged.h"
+#include "paged_ptx.h"
 
 #include <algorithm>
 #include <type_traits>
@@ -20,7 +21,7 @@
 namespace dflash {
 namespace {
 
-constexpr int kRowThreads = 128, kRowBlocks = 6;
+constexpr int kRowThreads = 128, kRowBlocks = 6, kGatherBlocks = 8;
 
 template <int T> struct RowType;
 template <> struct RowType<PAGED_F16> { using type = __half; };
@@ -88,12 +89,6 @@ __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ float2 e4m3_unpair(uint32_t codes) {   // low 16 bits
-    uint32_t h;
-    asm("{.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"(codes));
-    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
-}
-
 // Where row t lives: its sequence (the last s with q_start[s] <= t) and position, and the page and
 // row in it; found false for a row in front of the first or behind the last sequence, mapped false
 // where the arrays name no place for it.  A lane loads all that belongs to a sequence, 32 sequences
@@ -285,11 +280,11 @@ k_paged_rows(const __grid_constant__ PagedRowsArgs a) {
     using E = typename RowType<T>::type;
     constexpr int LPR = D / 8, RPW = 32 / LPR, U = 4;      // rows a warp step, steps in flight
     const int lane = threadIdx.x & 31;
-    const int64_t gw = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
-    const int64_t t64 = gw / a.tasks;
-    if (t64 >= a.n_rows) return;
-    const int t = (int)t64;
-    const int s0 = (int)(gw - t64 * a.tasks) * a.iters, s1 = min(a.steps_q + a.steps_k + a.steps_v, s0 + a.iters);
+    // (tokens times tasks stay below 2^31: several tasks a token only while they fit a wave)
+    const uint32_t gw = blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+    const int t = (int)(gw / (uint32_t)a.tasks);
+    if (t >= a.n_rows) return;
+    const int s0 = (int)(gw - (uint32_t)t * a.tasks) * a.iters, s1 = min(a.steps_q + a.steps_k + a.steps_v, s0 + a.iters);
     const int sub = lane / LPR, c = lane % LPR;
 
     // one kind's steps of this task: [from, to) of the kind's own
@@ -393,74 +388,71 @@ k_paged_rows(const __grid_constant__ PagedRowsArgs a) {
     }
 }
 
-// Rows of K and V read back: the same split of lanes and tasks.
+// Rows of K and V read back: the same split of lanes and tasks over a token's K steps, then V steps.
 template <int T, int D>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, kGatherBlocks)
 k_paged_gather(const __grid_constant__ PagedGatherArgs a) {
+    using E = typename RowType<T>::type;
     constexpr int LPR = D / 8, RPW = 32 / LPR, U = 4;
     const int lane = threadIdx.x & 31;
-    const int64_t gw = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
-    const int64_t t64 = gw / a.chunks;
-    if (t64 >= a.batch.n_rows) return;
-    const int t = (int)t64;
+    const uint32_t gw = blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+    const int t = (int)(gw / (uint32_t)a.chunks);
+    if (t >= a.batch.n_rows) return;
     const Place at = place_of(a.batch, a.pool, t, lane);
     if (!at.found) return;
-    const bool mapped = at.mapped;
-    if (!mapped && lane == 0) atomicOr(a.err, (uint32_t)PAGED_ERR_PAGE);
-    const int64_t off = mapped ? (int64_t)at.page * a.pool.page_stride + at.slot * a.pool.row_stride : 0;
-    const int64_t soff = mapped ? (int64_t)at.page * a.pool.s_page_stride + at.slot : 0;
+    if (!at.mapped && lane == 0) atomicOr(a.err, (uint32_t)PAGED_ERR_PAGE);
     const int sub = lane / LPR, c = lane % LPR;
-    // the 2 n_head_kv rows of the token: K heads, then V heads
-    const int heads = a.pool.n_head_kv, rows = 2 * heads;
-    const int r0 = (int)(gw - t64 * a.chunks) * a.iters * RPW, r1 = min(rows, r0 + a.iters * RPW);
-    const bool wide = a.pool.format == PAGED_F16 || a.pool.format == PAGED_BF16;
-    for (int r = r0; r < r1; r += U * RPW) {
-        uint4 w[U];
-        float sc[U];
+    const int s0 = (int)(gw - (uint32_t)t * a.chunks) * a.iters, s1 = min(2 * a.steps, s0 + a.iters);
+    const int64_t off = (int64_t)at.page * a.pool.page_stride + at.slot * a.pool.row_stride + 8 * c;
+    const int64_t soff = (int64_t)at.page * a.pool.s_page_stride + at.slot;
+    const bool wide = a.pool.format == PAGED_F16 || a.pool.format == PAGED_BF16, int8 = a.pool.format == PAGED_INT8;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int rr = r + u * RPW + sub;
-            w[u] = make_uint4(0, 0, 0, 0);
-            sc[u] = 0.f;
-            if (rr < r1 && mapped) {
-                const int h = rr < heads ? rr : rr - heads;
-                const uint8_t *base = rr < heads ? a.pool.k : a.pool.v;
-                const int64_t e = off + h * a.pool.head_stride + 8 * c;
-                if (wide) {
-                    w[u] = __ldcs(reinterpret_cast<const uint4 *>(base + 2 * e));
-                } else {
-                    const uint2 x = __ldcs(reinterpret_cast<const uint2 *>(base + e));
-                    w[u].x = x.x;
-                    w[u].y = x.y;
-                    sc[u] = __ldg((rr < heads ? a.pool.ks : a.pool.vs) + soff + h * a.pool.s_head_stride);
+    for (int kv = 0; kv < 2; ++kv) {
+        const int from = max(0, s0 - kv * a.steps), to = min(a.steps, s1 - kv * a.steps), h0 = from * RPW + sub;
+        const int64_t in_stride = (int64_t)RPW * a.pool.head_stride, sc_stride = (int64_t)RPW * a.pool.s_head_stride;
+        const int64_t out_hs = kv ? a.v_hs : a.k_hs;
+        const int64_t in0 = off + (int64_t)h0 * a.pool.head_stride;
+        const uint8_t *src = (kv ? a.pool.v : a.pool.k) + (wide ? 2 * in0 : in0);
+        const float *scales = (kv ? a.pool.vs : a.pool.ks) + soff + (int64_t)h0 * a.pool.s_head_stride;
+        E *dst = reinterpret_cast<E *>(kv ? a.v : a.k) + (int64_t)t * (kv ? a.v_rs : a.k_rs) + (int64_t)h0 * out_hs + 8 * c;
+        for (int st = from; st < to; st += U) {
+            uint4 w[U];
+            float sc[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int n = st + u - from;
+                w[u] = make_uint4(0, 0, 0, 0);
+                sc[u] = 0.f;
+                if (st + u < to && h0 + n * RPW < a.pool.n_head_kv && at.mapped) {
+                    if (wide) {
+                        w[u] = __ldcs(reinterpret_cast<const uint4 *>(src + 2 * n * in_stride));
+                    } else {
+                        const uint2 x = __ldcs(reinterpret_cast<const uint2 *>(src + n * in_stride));
+                        w[u].x = x.x;
+                        w[u].y = x.y;
+                        sc[u] = __ldg(scales + n * sc_stride);
+                    }
                 }
             }
-        }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int rr = r + u * RPW + sub;
-            if (rr >= r1) continue;
-            const int h = rr < heads ? rr : rr - heads;
-            void *dst = rr < heads ? a.k : a.v;
-            const int64_t e = (rr < heads ? (int64_t)t * a.k_rs + h * a.k_hs : (int64_t)t * a.v_rs + h * a.v_hs) + 8 * c;
-            if (wide) {
-                *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(dst) + e) = w[u];
-                continue;
-            }
-            float x[8];
-            const uint32_t ww[2] = {w[u].x, w[u].y};
-            if (a.pool.format == PAGED_INT8) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = (float)(int8_t)(ww[i >> 2] >> (8 * (i & 3))) * sc[u];
-            } else {
+            for (int u = 0; u < U; ++u) {
+                const int n = st + u - from;
+                if (st + u >= to || h0 + n * RPW >= a.pool.n_head_kv) continue;
+                if (wide) {
+                    *reinterpret_cast<uint4 *>(dst + (int64_t)n * RPW * out_hs) = w[u];
+                    continue;
+                }
+                float x[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float2 f = e4m3_unpair((ww[i >> 1] >> (16 * (i & 1))) & 0xffffu);
+                    const uint32_t v = i < 2 ? w[u].x : w[u].y;
+                    const uint32_t h = int8 ? int8_pair(v ^ 0x80808080u, i & 1 ? 0x7362u : 0x5140u) : e4m3_pair_f16(v >> (16 * (i & 1)));
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
                     x[2 * i] = f.x * sc[u];
                     x[2 * i + 1] = f.y * sc[u];
                 }
+                store8<T>(dst, (int64_t)n * RPW * out_hs, x);
             }
-            store8<T>(dst, e, x);
         }
     }
 }
@@ -504,8 +496,9 @@ cudaError_t rows_t(PagedRowsArgs a, bool paged, cudaStream_t st) {
 template <int T, int D>
 cudaError_t gather_t(PagedGatherArgs a, cudaStream_t st) {
     constexpr int rpw = 32 / (D / 8);
-    const int steps = (2 * a.pool.n_head_kv + rpw - 1) / rpw;
-    a.chunks = tasks_per_token(a.batch.n_rows, steps, sm_count() * 64);
+    a.steps = (a.pool.n_head_kv + rpw - 1) / rpw;
+    const int steps = 2 * a.steps;
+    a.chunks = tasks_per_token(a.batch.n_rows, steps, sm_count() * kGatherBlocks * (kRowThreads / 32));
     a.iters = (steps + a.chunks - 1) / a.chunks;
     a.chunks = (steps + a.iters - 1) / a.iters;
     const int64_t warps = a.batch.n_rows * a.chunks;
