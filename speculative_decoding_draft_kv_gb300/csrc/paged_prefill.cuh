@@ -438,7 +438,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         bool alive = true;
         while (alive && w.next(a)) {
             const uint64_t any_word = tree_union();
-            float v_unit = 0.f;
+            uint32_t v_unit = 0;
             for (int j = 0; j < w.nt && alive; ++j, ++tile) {
                 const int t = w.t0 + j;
                 const bool edge = ragged(t);
@@ -453,21 +453,26 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     uint8_t *dst = smem + slot * C::kSlotBytes;
                     const float *scales = reinterpret_cast<const float *>(smem + C::kOffCodeScale) + cs * kPreTile;
                     const bool live = !edge || seen(t * kPreTile + r, any_word);
-                    // the tile's largest scale among the rows that count (four to a lane)
-                    uint32_t top = 0;
+                    const float own = scales[r];
+                    // the tile's largest finite scale among the rows that count (four to a lane)
+                    const float4 four = reinterpret_cast<const float4 *>(scales)[lane];
+                    float f[4] = {fabsf(four.x), fabsf(four.y), fabsf(four.z), fabsf(four.w)};
+                    float most = fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3]));           // NaN is passed over
+                    if (edge || most == INFINITY) {
+                        most = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t bits = __float_as_uint(scales[4 * lane + i]) & 0x7fffffffu;
-                        if (bits < 0x7f800000u && (!edge || seen(t * kPreTile + 4 * lane + i, any_word))) top = max(top, bits);
+                        for (int i = 0; i < 4; ++i)
+                            if (f[i] < INFINITY && (!edge || seen(t * kPreTile + 4 * lane + i, any_word))) most = fmaxf(most, f[i]);
                     }
-                    top = __reduce_max_sync(0xffffffffu, top);
-                    // the power of two above it, at most 2^127; 0 stays
-                    float unit = top ? __uint_as_float(min((top & 0x7f800000u) + 0x00800000u, 0x7f000000u)) : 0.f;
-                    if (kv) unit = v_unit = fmaxf(v_unit, unit);
-                    else if (!top) unit = 1.f;
-                    const float sc = live && unit > 0.f ? scales[r] / unit : 0.f;
+                    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
+                    // the power of two above it, at most 2^127, and its inverse; 0 stays
+                    uint32_t unit = top ? min((top & 0x7f800000u) + 0x00800000u, 0x7f000000u) : 0u;
+                    if (kv) unit = v_unit = max(v_unit, unit);
+                    else if (!top) unit = 0x3f800000u;
+                    const float inv = unit == 0 ? 0.f : (unit == 0x7f000000u ? 0x1p-127f : __uint_as_float(0x7f000000u - unit));
+                    const float sc = live ? own * inv : 0.f;
                     if (warp == 12 && lane == 0)
-                        reinterpret_cast<float *>(smem + C::kOffUnit)[(tile % kUnitRing) * 2 + kv] = unit;
+                        reinterpret_cast<uint32_t *>(smem + C::kOffUnit)[(tile % kUnitRing) * 2 + kv] = unit;
                     // the scale as a sum of two F16 values, good to 2^-22: code * high + (code * low), one
                     // fused rounding, is the product's rounding but for an error far below its step
                     const float high = __half2float(__float2half_rn(sc));
@@ -644,6 +649,18 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     };
                     // The row twice, CH scores at a time: its maximum, then, against a reference that
                     // is settled, its probabilities, without a branch to hold up the exponentials.
+                    // bit e: the row sees position p + e
+                    auto seen_bits = [&](int p) {
+                        // positions below x of the 32 from p on
+                        auto below = [&](int x) { return x - p >= 32 ? ~0u : (x <= p ? 0u : (1u << (x - p)) - 1u); };
+                        uint32_t bits = below(rhi) & ~below(rlo);
+                        if (a.mask == PAGED_TREE) {
+                            const int at = p - ctx;        // the word's bit that p is
+                            const uint32_t tree = at >= 64 ? 0u : (at >= 0 ? (uint32_t)(word >> at) : (at > -32 ? (uint32_t)word << -at : 0u));
+                            bits |= tree & below(q.kv);
+                        }
+                        return bits;
+                    };
                     uint32_t raw[2][CH];                   // the piece at hand and, with registers to spare, the next
                     auto begin = [&]() {
                         if (!kCodes) tmem_ld(ts, raw[0]);
@@ -658,19 +675,12 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                         for (int e = 0; e < CH / 2; ++e)
                             s[e] = pk2(__uint_as_float(raw[at][2 * e]), __uint_as_float(raw[at][2 * e + 1]));
                         if (masked) {
-                            const int p = base + CH * c, lo = rlo - p, tr = ctx - p, n = q.kv - ctx;
-                            const uint32_t wide = (uint32_t)(rhi - rlo);
+                            const uint32_t bits = seen_bits(base + CH * c);
 #pragma unroll
                             for (int e = 0; e < CH / 2; ++e) {
                                 float x, y;
                                 upk2(s[e], x, y);
-                                bool vx = (uint32_t)(2 * e - lo) < wide, vy = (uint32_t)(2 * e + 1 - lo) < wide;
-                                if (a.mask == PAGED_TREE) {
-                                    const uint32_t ix = (uint32_t)(2 * e - tr), iy = ix + 1u;
-                                    if (ix < (uint32_t)min(n, 64)) vx = (word >> ix) & 1ull;
-                                    if (iy < (uint32_t)min(n, 64)) vy = (word >> iy) & 1ull;
-                                }
-                                s[e] = pk2(vx ? x : -INFINITY, vy ? y : -INFINITY);
+                                s[e] = pk2(bits & (1u << (2 * e)) ? x : -INFINITY, bits & (2u << (2 * e)) ? y : -INFINITY);
                             }
                         }
                     };
