@@ -92,7 +92,7 @@ struct PagedAttendArgs {
     float2 *part_ml;                  // [ctas][2][rows] (max in log2 units, sum)
     int4 *desc;                       // [ctas] the item whose first part is the CTA's last one
     int n_head, group, mask, window, max_q;
-    int ctas, min_tiles;
+    int ctas, min_tiles, item_cost;   // fewest units of a share; units of an item beyond its tiles
     int tile_tokens, tile_rows;       // tokens and rows (tokens times group, at most) of an item
     float scale_log2;
 };

@@ -104,8 +104,8 @@ k_paged_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     }
     pdl_trigger();                       // the join may settle; it waits for this grid's end
     const PagedShare share = paged_share<kDecTile, C::kThreads>(a, s_plan);
-    if (threadIdx.x == 0 && share.tiles == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    if (share.tiles == 0) return;
+    if (threadIdx.x == 0 && share.units == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (share.units == 0) return;
 
     PagedWalk<kDecTile> w;
     w.init(a, share);

@@ -223,7 +223,7 @@ bool encode_queries(CUtensorMap *tm, const paged_attend_args *g, int head_dim, i
 // items are one or two blocks of as many whole tokens as 128 rows take.
 // No more CTAs than the bounds leave work for.
 struct AttendPlan {
-    int rows, tokens, ctas, min_tiles;
+    int rows, tokens, ctas, min_tiles, item_cost;
     bool wide;
 };
 AttendPlan plan_of(const paged_cache *c, const paged_batch *b, int group, int sms) {
@@ -233,9 +233,12 @@ AttendPlan plan_of(const paged_cache *c, const paged_batch *b, int group, int sm
     const int block = 128 / group;                                 // whole tokens of a tensor-core block
     p.rows = rows <= 16 ? 16 : (rows <= 32 ? 32 : (b->max_q <= block ? 1 : 2) * block * group);
     p.tokens = p.wide ? p.rows / group : std::max(1, b->max_q);
-    p.min_tiles = p.wide ? 1 : 2;
+    // An item's beginning and end take the tensor-core kernel some 6,500 clocks, its tiles 2,500 to
+    // 3,500 each; the streaming kernel's overlap with its other CTA's tiles.
+    p.item_cost = p.wide ? 2 : 0;
+    p.min_tiles = (p.wide ? 1 : 2) + p.item_cost;
     const int64_t keys = b->max_kv > 0 ? b->max_kv : (int64_t)b->max_pages * c->page_size;
-    const int64_t tiles = keys / (p.wide ? 128 : 64) + 2;          // of an item, wherever it begins
+    const int64_t tiles = keys / (p.wide ? 128 : 64) + 2 + p.item_cost;   // of an item, wherever it begins
     const int64_t items = (int64_t)b->n_seq * c->n_head_kv * ((b->max_q + p.tokens - 1) / p.tokens);
     const int64_t most = std::max<int64_t>(1, (items * tiles + p.min_tiles - 1) / p.min_tiles);
     p.ctas = (int)std::min<int64_t>(most, p.wide ? sms : 2 * sms);
@@ -464,6 +467,7 @@ extern "C" int paged_attend(const paged_attend_args *g, void *stream) {
     a.max_q = g->batch->max_q;
     a.ctas = p.ctas;
     a.min_tiles = p.min_tiles;
+    a.item_cost = p.item_cost;
     a.tile_tokens = p.tokens;
     a.tile_rows = p.rows;
     const double scale = g->scale > 0.f ? (double)g->scale : 1.0 / std::sqrt((double)g->cache->head_dim);

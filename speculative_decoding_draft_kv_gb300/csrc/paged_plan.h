@@ -3,8 +3,9 @@
 //
 // An item is (sequence, row tile, kv head): a run of query rows -- the tokens of the sequence
 // times the query heads of one kv head, token by token -- and the key tiles that some row of
-// it sees.  All key tiles of all items, laid end to end (sequence, head, row tile, key tile),
-// are cut into equal shares, one per CTA.  So ragged lengths, a few long sequences among many
+// it sees.  All key tiles of all items, laid end to end (sequence, head, row tile, key tile), are
+// cut into equal shares, one per CTA; an item counts for item_cost tiles more than it has, which is
+// what its beginning and end were measured to take.  So ragged lengths, a few long sequences among many
 // short ones, and causal row tiles of uneven length all load the CTAs alike, with a grid that
 // depends on nothing but bounds known to the host.  An item inside one share is finished by
 // its CTA; an item cut by a share's border leaves one partial softmax state in each CTA that
@@ -19,24 +20,30 @@
 
 namespace dflash {
 
-// sum over i < n of floor((a i + b) / m), a, b >= 0, m > 0: whole parts of a / m and b / m first,
-// then the lattice points under the line counted along the other axis
-__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+// 64-bit numbers here are nearly always small ones, and a 64-bit division is a long way
+__device__ __forceinline__ int64_t small_div(int64_t a, int64_t b) {
+    return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
+// sum over i < n of floor((a i + b) / m), 0 <= a, b < 2^31, 0 < m, n a' < 2^32 for a' = a mod m (n is a
+// number of row tiles, m of keys in a tile): whole parts of a / m and b / m first, then the lattice
+// points under the line counted along the other axis
+__device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
     int64_t sum = 0;
     while (true) {
         if (a >= m) {
-            sum += (n - 1) * n / 2 * (a / m);
+            sum += (int64_t)n * (n - 1) / 2 * (a / m);
             a %= m;
         }
         if (b >= m) {
-            sum += n * (b / m);
+            sum += (int64_t)n * (b / m);
             b %= m;
         }
-        const int64_t y = a * n + b;
+        const uint64_t y = (uint64_t)a * n + b;
         if (y < m) return sum;
-        n = y / m;
-        b = y % m;
-        const int64_t t = m;
+        n = (uint32_t)small_div((int64_t)y, m);
+        b = (uint32_t)(y - (uint64_t)n * m);
+        const uint32_t t = m;
         m = a;
         a = t;
     }
@@ -70,16 +77,21 @@ struct PagedShape {
     __device__ __forceinline__ int tiles(const PagedAttendArgs &a, int rt) const {
         return (hi(a, rt) + KT - 1) / KT - lo(a, rt) / KT;
     }
-    __device__ __forceinline__ int64_t head_tiles(const PagedAttendArgs &a) const {
+    // units of work: an item's key tiles and what starting and ending it costs, in tiles
+    __device__ __forceinline__ int units(const PagedAttendArgs &a, int rt) const { return tiles(a, rt) + a.item_cost; }
+    __device__ __forceinline__ int64_t head_units(const PagedAttendArgs &a) const {
         const int n = row_tiles(a);
         if (n == 0) return 0;
-        if (n == 1 || a.mask != PAGED_CAUSAL) return (int64_t)n * tiles(a, 0);
+        if (n == 1 || a.mask != PAGED_CAUSAL) return (int64_t)n * units(a, 0);
+        return head_tiles(a, n) + (int64_t)n * a.item_cost;
+    }
+    __device__ __forceinline__ int64_t head_tiles(const PagedAttendArgs &a, int n) const {
         // ceil(hi / KT) of all row tiles but the last, whose hi is kv ...
         int64_t w = floor_sum(n - 1, KT, a.tile_tokens, ctx + a.tile_tokens + KT - 1) + (q.kv + KT - 1) / KT;
         // ... less floor(lo / KT) of those whose lo is above 0
         if (a.window) {
-            const int64_t first = ctx - a.window + 1;
-            const int64_t i0 = first >= 0 ? 0 : (-first + a.tile_tokens - 1) / a.tile_tokens;
+            const int first = ctx - a.window + 1;
+            const int i0 = first >= 0 ? 0 : (-first + a.tile_tokens - 1) / a.tile_tokens;
             if (i0 < n) w -= floor_sum(n - i0, KT, a.tile_tokens, first + i0 * a.tile_tokens);
         }
         return w;
@@ -87,16 +99,11 @@ struct PagedShape {
 };
 
 struct PagedShare {
-    int64_t rem;                     // the CTA's first tile, counted from sequence seq's first
-    int tiles, per;                  // this CTA's tiles, and those of a full share
+    int64_t rem;                     // the CTA's first unit, counted from sequence seq's first
+    int units, per;                  // this CTA's units, and those of a full share
     int seq;
     PagedSeq q;                      // of sequence seq
 };
-
-// 64-bit numbers here are nearly always small ones, and a 64-bit division is a long way
-__device__ __forceinline__ int64_t small_div(int64_t a, int64_t b) {
-    return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
-}
 
 // Block-wide: every thread calls it, every thread gets the CTA's share.  scratch: shared
 // memory of THREADS / 32 + 4 int64.
@@ -112,7 +119,7 @@ __device__ __forceinline__ PagedShare paged_share(const PagedAttendArgs &a, int6
     for (int s = s0; s < s1; ++s) {
         sh.load(a, s);
         ok = ok && sh.q.ok;
-        sum += sh.head_tiles(a) * a.pool.n_head_kv;
+        sum += sh.head_units(a) * a.pool.n_head_kv;
     }
     if (!ok && blockIdx.x == 0) atomicOr(a.err, (uint32_t)PAGED_ERR_PAGE);
     int64_t incl = sum;
@@ -130,7 +137,7 @@ __device__ __forceinline__ PagedShare paged_share(const PagedAttendArgs &a, int6
         if (w == warp) base = total;
         total += scratch[w];
     }
-    const int64_t mine = base + incl - sum;       // tiles in front of this thread's sequences
+    const int64_t mine = base + incl - sum;       // units in front of this thread's sequences
     // a share of 2^31 tiles would take hours: 32 bits are enough for one
     const int64_t per = max((int64_t)a.min_tiles, small_div(total + a.ctas - 1, a.ctas));
     const int64_t begin = min(total, (int64_t)blockIdx.x * per), end = min(total, begin + per);
@@ -138,7 +145,7 @@ __device__ __forceinline__ PagedShare paged_share(const PagedAttendArgs &a, int6
         int64_t at = mine;
         for (int s = s0; s < s1; ++s) {
             sh.load(a, s);
-            const int64_t w = sh.head_tiles(a) * a.pool.n_head_kv;
+            const int64_t w = sh.head_units(a) * a.pool.n_head_kv;
             if (begin < at + w) {
                 scratch[WARPS] = begin - at;
                 scratch[WARPS + 1] = s;
@@ -153,7 +160,7 @@ __device__ __forceinline__ PagedShare paged_share(const PagedAttendArgs &a, int6
     PagedShare r;
     r.rem = scratch[WARPS];
     r.seq = (int)scratch[WARPS + 1];
-    r.tiles = r.seq < 0 ? 0 : (int)(end - begin);
+    r.units = r.seq < 0 ? 0 : (int)(end - begin);
     r.per = (int)per;
     r.q.row0 = (int)scratch[WARPS + 2];
     r.q.n = (int)(scratch[WARPS + 2] >> 32);
@@ -167,32 +174,32 @@ __device__ __forceinline__ PagedShare paged_share(const PagedAttendArgs &a, int6
 template <int KT>
 struct PagedWalk {
     PagedShape<KT> sh;
-    int left, per;                   // tiles to come
-    int seq, head, rt, off;          // the item, and the tile of it that comes next
+    int left, per;                   // units to come, units of a full share
+    int seq, head, rt, off;          // the item, and the unit of it that comes next
     // the piece at hand
-    int t0, nt, rest;                // first key tile (absolute), their number; the item's beyond them
+    int t0, nt, rest;                // first key tile (absolute), their number; units beyond them
     bool first, last;                // the piece has the item's first / last tile
 
     __device__ __forceinline__ void init(const PagedAttendArgs &a, const PagedShare &r) {
-        left = r.tiles;
+        left = r.units;
         per = r.per;
         seq = r.seq;
         head = rt = off = 0;
         if (left == 0) return;
         sh.q = r.q;
         sh.ctx = r.q.kv - r.q.n;
-        const int64_t per_head = sh.head_tiles(a);
+        const int64_t per_head = sh.head_units(a);
         int64_t rem = r.rem;
         head = (int)small_div(rem, per_head);
         rem -= head * per_head;
-        if (per_head == sh.tiles(a, 0)) {            // one row tile
+        if (per_head == sh.units(a, 0)) {            // one row tile
             off = (int)rem;
             return;
         }
-        // the row tile that holds tile rem of the head, 32 row tiles at a time
+        // the row tile that holds unit rem of the head, 32 row tiles at a time
         const int lane = threadIdx.x & 31, n = sh.row_tiles(a);
         while (true) {
-            const int mine = rt + lane < n ? sh.tiles(a, rt + lane) : 0;
+            const int mine = rt + lane < n ? sh.units(a, rt + lane) : 0;
             int64_t incl = mine;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -215,29 +222,33 @@ struct PagedWalk {
         }
     }
     __device__ __forceinline__ bool next(const PagedAttendArgs &a) {
-        if (left <= 0) return false;
-        if (off < 0) {                               // the item before this one is done
-            off = 0;
-            if (++rt >= sh.row_tiles(a)) {
-                rt = 0;
-                if (++head >= a.pool.n_head_kv) {
-                    head = 0;
-                    do {
-                        if (++seq >= a.batch.n_seq) return false;
-                        sh.load(a, seq);
-                    } while (sh.q.n == 0);
+        while (left > 0) {
+            if (off < 0) {                           // the item before this one is done
+                off = 0;
+                if (++rt >= sh.row_tiles(a)) {
+                    rt = 0;
+                    if (++head >= a.pool.n_head_kv) {
+                        head = 0;
+                        do {
+                            if (++seq >= a.batch.n_seq) return false;
+                            sh.load(a, seq);
+                        } while (sh.q.n == 0);
+                    }
                 }
             }
+            // the item's first item_cost units stand for no tile
+            const int units = sh.units(a, rt), n = min(units - off, left);
+            const int from = max(0, off - a.item_cost), to = max(0, off + n - a.item_cost);
+            t0 = sh.tile0(a, rt) + from;
+            nt = to - from;
+            first = from == 0;
+            rest = units - off - n;
+            last = rest == 0;
+            left -= n;
+            off = last ? -1 : off + n;
+            if (nt > 0) return true;
         }
-        const int item = sh.tiles(a, rt);
-        t0 = sh.tile0(a, rt) + off;
-        nt = min(item - off, left);
-        first = off == 0;
-        rest = item - off - nt;
-        last = rest == 0;
-        left -= nt;
-        off = last ? -1 : off + nt;
-        return true;
+        return false;
     }
     // the CTA that has the item's last tile (a piece that leaves some ends its CTA's share)
     __device__ __forceinline__ int last_cta() const { return (int)blockIdx.x + (rest + per - 1) / per; }

@@ -49,16 +49,17 @@ struct PreCfg {
     static constexpr int kSlotBytes = kHalves * kHalfBytes;      // 128 rows of D 16-bit values
     static constexpr int kBlocks = ONE ? 1 : 2;                  // of queries
     // K and V tiles in turn: what fits
-    static constexpr int kSlots = kCodes ? (D == 128 && !ONE ? 3 : 4) : (D == 128 ? (ONE ? 6 : 5) : 10);
+    static constexpr int kSlots = kCodes ? 4 : (D == 128 ? (ONE ? 6 : 5) : 10);
     static constexpr int kCodeBytes = kPreTile * D;
-    static constexpr int kCodeSlots = kCodes ? 3 : 0;
+    static constexpr int kCodeSlots = kCodes ? (D == 128 && !ONE ? 2 : 3) : 0;
     static constexpr int kOffQ = kSlots * kSlotBytes;
     static constexpr int kOffCodes = kOffQ + kBlocks * kSlotBytes;
     static constexpr int kOffCodeScale = kOffCodes + kCodeSlots * kCodeBytes;   // as loaded, per code slot
     static constexpr int kOffUnit = kOffCodeScale + kCodeSlots * kPreTile * 4;   // [ring][K, V]
     static constexpr int kOffRow = kOffUnit + (kCodes ? kUnitRing * 8 : 0);      // row values
     static constexpr int kOffBars = kOffRow + 128 * 8;
-    static constexpr int kSmem = 1024 + kOffBars + 384;
+    static constexpr int kOffPlan = kOffBars + 304;                // what else is shared: the plan, then words
+    static constexpr int kSmem = kOffPlan + 24 * 8 + 16;
     static_assert(kSmem <= 227 * 1024, "one CTA per SM");
 };
 
@@ -102,19 +103,25 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     constexpr uint32_t kIdescQK = tc_idesc(128, kPreTile, OT == PAGED_BF16, false);
     constexpr uint32_t kIdescPV = tc_idesc(128, D, OT == PAGED_BF16, true);
     constexpr int CODE_ROW = D < 128 ? D : 128;                      // bytes of a row of codes
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // no static shared memory beside this, so its start is the CTA's, aligned for any swizzle
+    extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t bars = smem_u32(smem + C::kOffBars);
     const uint32_t full = bars, empty = bars + 8 * NS;               // [NS] each
     const uint32_t q_full = bars + 16 * NS, q_empty = q_full + 8, q_ready = q_full + 16;
     const uint32_t s_full = q_full + 24, p_full = s_full + 16, o_full = p_full + 16;   // [2] each
     const uint32_t landed = o_full + 16, drain = landed + 8, odd_done = landed + 16, odd_free = landed + 24;
-    const uint32_t c_full = landed + 32, c_empty = c_full + 8 * 3;   // [3] each
-    __shared__ int64_t s_plan[20];
-    __shared__ uint32_t s_tmem;
-    __shared__ volatile int s_abort;
+    const uint32_t c_full = landed + 32, c_empty = c_full + 8 * C::kCodeSlots;
+    int64_t *s_plan = reinterpret_cast<int64_t *>(smem + C::kOffPlan);
+    uint32_t &s_tmem = *reinterpret_cast<uint32_t *>(smem + C::kOffPlan + 24 * 8);
+    volatile int &s_abort = *reinterpret_cast<volatile int *>(smem + C::kOffPlan + 24 * 8 + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (smem_u32(smem) & 1023u) {                          // never: tiles would be read in another order
+        if (threadIdx.x == 0) {
+            atomicOr(a.err, (uint32_t)PAGED_ERR_WAIT);
+            a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        }
+        return;
+    }
 
     if (threadIdx.x == 0) {
         prefetch_tensormap(&tm_k);
@@ -429,8 +436,8 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         // hold -- in units of a power of two: K's for a tile, so that its largest scale is in (1/2, 1],
         // V's the largest so far of the item, which O is kept in.  Scales of any size fit F16 so.
         // The ring of units needs no barrier of its own: the V slot of the tile that the slower
-        // block's rows are at is taken, and with it every later one, so with 3 or 4 slots the tile
-        // at hand here is at most 2 ahead of that one.
+        // block's rows are at is taken, and with it every later one, so with 4 slots the tile at hand
+        // here is at most 2 ahead of that one.
         const int r = (int)threadIdx.x - 384;              // the thread's key
         int slot = 0, cs = 0;
         uint32_t wrap = 0, cwrap = 0;
@@ -524,7 +531,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         const uint32_t ts = tmem + lane_base + blk * 128, to = tmem + lane_base + 256 + blk * 128;
         float *row_scale = reinterpret_cast<float *>(smem + C::kOffRow);              // [2][128]
         float2 *odd_ml = reinterpret_cast<float2 *>(smem + C::kOffRow);               // [128]
-        float *odd_ref = reinterpret_cast<float *>(smem + C::kOffBars + 376);
+        float *odd_ref = reinterpret_cast<float *>(smem + C::kOffPlan + 24 * 8 + 8);
         uint32_t sph = 0, oph = 0, dph = 0;
         bool began = false;                                 // this CTA starts an item that another finishes
         bool owed = false;                                 // block 0 has yet to read this block's state
