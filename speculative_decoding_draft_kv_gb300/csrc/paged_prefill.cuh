@@ -670,10 +670,10 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     };
                     uint32_t raw[2][CH];                   // the piece at hand and, with registers to spare, the next
                     auto begin = [&]() {
-                        if (!kCodes) tmem_ld(ts, raw[0]);
+                        tmem_ld(ts, raw[0]);
                     };
                     auto scores = [&](int c, const bool masked, uint64_t (&s)[CH / 2]) {
-                        const bool ahead = !kCodes && !masked;
+                        const bool ahead = !masked;
                         const int at = ahead ? c & 1 : 0;
                         if (!ahead) tmem_ld(ts + CH * c, raw[0]);
                         tmem_ld_wait();
