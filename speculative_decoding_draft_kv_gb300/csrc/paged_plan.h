@@ -111,6 +111,38 @@ template <int KT, int THREADS>
 __device__ __forceinline__ PagedShare paged_share(const PagedAttendArgs &a, int64_t *scratch) {
     constexpr int WARPS = THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (a.batch.n_seq <= 32) {
+        // every warp for itself, a sequence to a lane; the barrier is for the caller's sake
+        PagedShape<KT> sh;
+        sh.q = PagedSeq{0, 0, 0, true};
+        int64_t mine = 0;
+        if (lane < a.batch.n_seq) {
+            sh.load(a, lane);
+            mine = sh.head_units(a) * a.pool.n_head_kv;
+            if (!sh.q.ok && blockIdx.x == 0 && warp == 0) atomicOr(a.err, (uint32_t)PAGED_ERR_PAGE);
+        }
+        int64_t incl = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += v;
+        }
+        const int64_t total = __shfl_sync(0xffffffffu, incl, 31);
+        const int64_t per = max((int64_t)a.min_tiles, small_div(total + a.ctas - 1, a.ctas));
+        const int64_t begin = min(total, (int64_t)blockIdx.x * per), end = min(total, begin + per);
+        const uint32_t beyond = __ballot_sync(0xffffffffu, begin < incl);
+        PagedShare r;
+        r.seq = beyond ? __ffs(beyond) - 1 : 0;
+        r.rem = begin - __shfl_sync(0xffffffffu, incl - mine, r.seq);
+        r.units = beyond ? (int)(end - begin) : 0;
+        r.per = (int)per;
+        r.q.row0 = __shfl_sync(0xffffffffu, sh.q.row0, r.seq);
+        r.q.n = __shfl_sync(0xffffffffu, sh.q.n, r.seq);
+        r.q.kv = __shfl_sync(0xffffffffu, sh.q.kv, r.seq);
+        r.q.ok = true;
+        __syncthreads();
+        return r;
+    }
     const int per_thread = (a.batch.n_seq + THREADS - 1) / THREADS;
     const int s0 = min(a.batch.n_seq, tid * per_thread), s1 = min(a.batch.n_seq, s0 + per_thread);
     PagedShape<KT> sh;
