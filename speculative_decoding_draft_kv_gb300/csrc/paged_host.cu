@@ -78,11 +78,16 @@ EncodeTiled encode_fn() {
 bool is16(int t) { return t == PAGED_F16 || t == PAGED_BF16; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// rows tensors: 16-byte alignment of every head, and strides that say something where there is
-// more than one of a kind
+// rows tensors: given (where there are rows: an empty tensor may have no address), 16-byte alignment
+// of every head, and strides that say something where there is more than one of a kind
 bool rows_ok(const void *p, int64_t rs, int64_t hs, int esize, int64_t n_rows, int heads) {
-    return aligned16(p) && (rs * esize) % 16 == 0 && (hs * esize) % 16 == 0 && rs >= (n_rows > 1) && hs >= (heads > 1) &&
+    return (p || n_rows == 0) && aligned16(p) && (rs * esize) % 16 == 0 && (hs * esize) % 16 == 0 && rs >= (n_rows > 1) && hs >= (heads > 1) &&
            rs < (int64_t)1 << 38 && hs < (int64_t)1 << 38;
+}
+
+// an output that is its input's tensor has its strides (a head's lanes read it whole before they write)
+bool in_place_ok(const void *in, const void *out, int64_t rs, int64_t hs, int64_t ors, int64_t ohs, int64_t n_rows, int heads) {
+    return in != out || n_rows == 0 || ((n_rows == 1 || rs == ors) && (heads <= 1 || hs == ohs));
 }
 
 int check_cache(const char *who, const paged_cache *c) {
@@ -94,6 +99,7 @@ int check_cache(const char *who, const paged_cache *c) {
     if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)))
         return fail(RING_EINVAL, "%s: page_size %d (16, 32, 64, 128 or 256)", who, c->page_size);
     if (c->n_pages <= 0 || c->n_head_kv <= 0) return fail(RING_EINVAL, "%s: the cache is empty", who);
+    if (c->n_head_kv > 65536) return fail(RING_EINVAL, "%s: more than 65536 kv heads", who);
     if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v))
         return fail(RING_EINVAL, "%s: pools must be given and 16-byte aligned", who);
     const int es = is16(c->format) ? 2 : 1;
@@ -115,6 +121,7 @@ int check_batch(const char *who, const paged_cache *c, const paged_batch *b, int
     if (b->n_seq < 0 || b->max_pages < 0 || b->max_q < 0 || b->max_kv < 0 || b->pages_stride < 0)
         return fail(RING_EINVAL, "%s: negative batch dimension", who);
     if (n_rows < 0 || n_rows > INT32_MAX / 2) return fail(RING_EINVAL, "%s: n_rows out of range", who);
+    if (b->max_q > INT32_MAX / 2) return fail(RING_EINVAL, "%s: max_q out of range", who);
     if (b->n_seq > 0 && (!b->q_start || !b->kv_len || (!b->pages && b->max_pages)))
         return fail(RING_EINVAL, "%s: NULL batch array", who);
     if (b->n_seq > 65536) return fail(RING_EINVAL, "%s: more than 65536 sequences", who);
@@ -240,8 +247,10 @@ AttendPlan plan_of(const paged_cache *c, const paged_batch *b, int group, int sm
     const int64_t keys = b->max_kv > 0 ? b->max_kv : (int64_t)b->max_pages * c->page_size;
     const int64_t tiles = keys / (p.wide ? 128 : 64) + 2 + p.item_cost;   // of an item, wherever it begins
     const int64_t items = (int64_t)b->n_seq * c->n_head_kv * ((b->max_q + p.tokens - 1) / p.tokens);
-    const int64_t most = std::max<int64_t>(1, (items * tiles + p.min_tiles - 1) / p.min_tiles);
-    p.ctas = (int)std::min<int64_t>(most, p.wide ? sms : 2 * sms);
+    // an item has min_tiles or more
+    const int64_t fit = p.wide ? sms : 2 * sms;
+    const int64_t most = items >= fit ? fit : (items * tiles + p.min_tiles - 1) / p.min_tiles;
+    p.ctas = (int)std::max<int64_t>(1, std::min(most, fit));
     return p;
 }
 
@@ -297,12 +306,17 @@ extern "C" int paged_norm_rope(const paged_norm_rope_args *g, void *stream) {
     if (!(g->eps >= 0.f)) return fail(RING_EINVAL, "%s: eps must not be negative", who);
     TRY(check_rope(who, g->rope, g->head_dim));
     const int es = g->dtype == PAGED_F32 ? 4 : 2;
-    if (g->n_head_q && (!g->q || !g->q_out || !rows_ok(g->q, g->q_row_stride, g->q_head_stride, es, g->n_rows, g->n_head_q) ||
+    if (g->n_head_q && (!rows_ok(g->q, g->q_row_stride, g->q_head_stride, es, g->n_rows, g->n_head_q) ||
                         !rows_ok(g->q_out, g->qo_row_stride, g->qo_head_stride, es, g->n_rows, g->n_head_q)))
         return fail(RING_EINVAL, "%s: q and q_out must be given with every head 16-byte aligned", who);
-    if (g->n_head_k && (!g->k || !g->k_out || !rows_ok(g->k, g->k_row_stride, g->k_head_stride, es, g->n_rows, g->n_head_k) ||
+    if (g->n_head_k && (!rows_ok(g->k, g->k_row_stride, g->k_head_stride, es, g->n_rows, g->n_head_k) ||
                         !rows_ok(g->k_out, g->ko_row_stride, g->ko_head_stride, es, g->n_rows, g->n_head_k)))
         return fail(RING_EINVAL, "%s: k and k_out must be given with every head 16-byte aligned", who);
+    if ((g->n_head_q && !in_place_ok(g->q, g->q_out, g->q_row_stride, g->q_head_stride, g->qo_row_stride, g->qo_head_stride,
+                                     g->n_rows, g->n_head_q)) ||
+        (g->n_head_k && !in_place_ok(g->k, g->k_out, g->k_row_stride, g->k_head_stride, g->ko_row_stride, g->ko_head_stride,
+                                     g->n_rows, g->n_head_k)))
+        return fail(RING_EINVAL, "%s: an output in its input's place must have its strides", who);
     if ((g->q_norm && !aligned16(g->q_norm)) || (g->k_norm && !aligned16(g->k_norm)))
         return fail(RING_EINVAL, "%s: norm weights must be 16-byte aligned", who);
     if (g->rope && !g->positions && g->n_rows) return fail(RING_EINVAL, "%s: a rotation needs positions", who);
@@ -342,12 +356,15 @@ extern "C" int paged_append(const paged_append_args *g, void *stream) {
     if (g->n_head_q < 0 || g->n_head_q > 65536) return fail(RING_EINVAL, "%s: n_head_q out of range", who);
     if (!(g->eps >= 0.f)) return fail(RING_EINVAL, "%s: eps must not be negative", who);
     TRY(check_rope(who, g->rope, g->cache->head_dim));
-    if (!g->k || !g->v || !rows_ok(g->k, g->k_row_stride, g->k_head_stride, 2, g->n_rows, g->cache->n_head_kv) ||
+    if (!rows_ok(g->k, g->k_row_stride, g->k_head_stride, 2, g->n_rows, g->cache->n_head_kv) ||
         !rows_ok(g->v, g->v_row_stride, g->v_head_stride, 2, g->n_rows, g->cache->n_head_kv))
         return fail(RING_EINVAL, "%s: k and v must be given with every head 16-byte aligned", who);
-    if (g->n_head_q && (!g->q || !g->q_out || !rows_ok(g->q, g->q_row_stride, g->q_head_stride, 2, g->n_rows, g->n_head_q) ||
+    if (g->n_head_q && (!rows_ok(g->q, g->q_row_stride, g->q_head_stride, 2, g->n_rows, g->n_head_q) ||
                         !rows_ok(g->q_out, g->qo_row_stride, g->qo_head_stride, 2, g->n_rows, g->n_head_q)))
         return fail(RING_EINVAL, "%s: q and q_out must be given with every head 16-byte aligned", who);
+    if (g->n_head_q && !in_place_ok(g->q, g->q_out, g->q_row_stride, g->q_head_stride, g->qo_row_stride, g->qo_head_stride,
+                                    g->n_rows, g->n_head_q))
+        return fail(RING_EINVAL, "%s: an output in its input's place must have its strides", who);
     if ((g->q_norm && !aligned16(g->q_norm)) || (g->k_norm && !aligned16(g->k_norm)))
         return fail(RING_EINVAL, "%s: norm weights must be 16-byte aligned", who);
     if (g->n_rows == 0 || g->batch->n_seq == 0) return RING_OK;
@@ -385,7 +402,7 @@ extern "C" int paged_gather(const paged_gather_args *g, void *stream) {
     if (!is16(g->dtype)) return fail(RING_EINVAL, "%s: rows must be F16 or BF16", who);
     if (is16(g->cache->format) && g->cache->format != g->dtype)
         return fail(RING_EINVAL, "%s: rows and 16-bit pages must have one type", who);
-    if (!g->k || !g->v || !rows_ok(g->k, g->k_row_stride, g->k_head_stride, 2, g->n_rows, g->cache->n_head_kv) ||
+    if (!rows_ok(g->k, g->k_row_stride, g->k_head_stride, 2, g->n_rows, g->cache->n_head_kv) ||
         !rows_ok(g->v, g->v_row_stride, g->v_head_stride, 2, g->n_rows, g->cache->n_head_kv))
         return fail(RING_EINVAL, "%s: k and v must be given with every head 16-byte aligned", who);
     if (g->n_rows == 0 || g->batch->n_seq == 0) return RING_OK;
@@ -431,10 +448,12 @@ extern "C" int paged_attend(const paged_attend_args *g, void *stream) {
     if (g->mask == PAGED_TREE && g->batch->max_q > 64)
         return fail(RING_EINVAL, "%s: a token tree has at most 64 nodes, max_q is %d", who, g->batch->max_q);
     if (g->window < 0) return fail(RING_EINVAL, "%s: negative window", who);
-    if (!(g->scale >= 0.f) || !std::isfinite(g->scale)) return fail(RING_EINVAL, "%s: scale must be finite and not negative", who);
-    if (!g->q || !g->o || !rows_ok(g->q, g->q_row_stride, g->q_head_stride, 2, g->n_rows, g->n_head) ||
+    // (in log2 units it has to be finite too)
+    if (!(g->scale >= 0.f) || !std::isfinite(g->scale * 1.5f)) return fail(RING_EINVAL, "%s: scale must be finite and not negative", who);
+    if (!rows_ok(g->q, g->q_row_stride, g->q_head_stride, 2, g->n_rows, g->n_head) ||
         !rows_ok(g->o, g->o_row_stride, g->o_head_stride, 2, g->n_rows, g->n_head))
         return fail(RING_EINVAL, "%s: q and o must be given with every head 16-byte aligned", who);
+    if (g->q == g->o && g->n_rows > 0) return fail(RING_EINVAL, "%s: o may not be q", who);
     if (g->n_rows == 0 || g->batch->n_seq == 0 || g->batch->max_q == 0) return RING_OK;
     DeviceInfo d;
     TRY(device_info(who, &d));
@@ -463,7 +482,8 @@ extern "C" int paged_attend(const paged_attend_args *g, void *stream) {
     a.n_head = g->n_head;
     a.group = group;
     a.mask = g->mask;
-    a.window = g->window;
+    // one that reaches back past any position is none (and sums of positions and windows stay in 32 bits)
+    a.window = g->window > INT32_MAX / 2 ? 0 : g->window;
     a.max_q = g->batch->max_q;
     a.ctas = p.ctas;
     a.min_tiles = p.min_tiles;

@@ -197,6 +197,8 @@ class PagedBatch:
             raise ValueError(f"pages must be int32 [{n}, max_pages] on the batch's device")
         if pages.shape[1] > 1 and pages.stride(1) != 1:
             raise ValueError("a row of pages must be contiguous")
+        if not (0 <= max_q < 1 << 30 and 0 <= max_kv < 1 << 30):
+            raise ValueError(f"max_q {max_q} or max_kv {max_kv} out of range")
         self.tensors = (q_start, kv_len, pages)
         self.args = PagedBatchArgs(q_start.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), pages.stride(0), n,
                                    pages.shape[1], int(max_q), int(max_kv))
@@ -360,12 +362,17 @@ def paged_attend(cache, batch, q, o, mask="causal", window=0, scale=0.0, tree=No
     op, orow, oh = _rows(o, "o", n, heads, cache.head_dim, dtype, dev)
     tp = None if tree is None else _vector(tree, "tree", torch.int64, n, dev)
     lp = None if lse is None else _vector(lse, "lse", torch.float32, n * heads, dev)
+    if not 0 <= window < 1 << 31:
+        raise ValueError(f"window {window} out of range")
     st = _stream(stream, dev)
     if workspace is None:
+        # from the pool of the stream that the work runs on, which alone may have it next
         size = paged_attend_workspace(cache, batch, heads)
-        own = torch.cuda.ExternalStream(st) if stream is not None and st else torch.cuda.current_stream(dev)
-        with torch.cuda.stream(own):
+        if stream is None:
             workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+        else:
+            with torch.cuda.stream(torch.cuda.ExternalStream(st) if st else torch.cuda.default_stream(dev)):
+                workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
     elif workspace.get_device() != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 CUDA tensor of the call's device")
     a = PagedAttendArgs(cache.address, batch.address, qp, op, qr, qh, orow, oh, tp, lp, workspace.data_ptr(),

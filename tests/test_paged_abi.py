@@ -100,17 +100,17 @@ def refused(call, *args):
 
 
 BAD_CACHES = [dict(k=None), dict(v=FAKE + 8), dict(page_size=8), dict(page_size=48), dict(page_size=512), dict(head_dim=96),
-              dict(head_dim=0), dict(format=P.PAGED_F32), dict(format=9), dict(n_pages=0), dict(n_head_kv=0),
+              dict(head_dim=0), dict(format=P.PAGED_F32), dict(format=9), dict(n_pages=0), dict(n_head_kv=0), dict(n_head_kv=65537),
               dict(row_stride=100), dict(head_stride=0), dict(page_stride=-2048), dict(page_stride=1 << 41),
               dict(format=P.PAGED_INT8), dict(format=P.PAGED_E4M3, k_scale=FAKE, v_scale=FAKE),
               dict(format=P.PAGED_INT8, k_scale=FAKE, v_scale=FAKE + 4, scale_page_stride=128, scale_head_stride=16),
               dict(format=P.PAGED_INT8, k_scale=FAKE, v_scale=FAKE, scale_page_stride=128, scale_head_stride=18)]
 BAD_BATCHES = [dict(q_start=None), dict(kv_len=None), dict(pages=None), dict(n_seq=-1), dict(n_seq=70000),
-               dict(max_q=-1), dict(max_kv=65), dict(max_pages=1 << 27, max_kv=0), dict(pages_stride=-1)]
+               dict(max_q=-1), dict(max_q=(1 << 31) - 1), dict(max_kv=65), dict(max_pages=1 << 27, max_kv=0), dict(pages_stride=-1)]
 
 
 def attend(c, b, **kw):
-    d = dict(cache=addr(c), batch=addr(b), q=FAKE, o=FAKE, q_row_stride=4096, q_head_stride=128, o_row_stride=4096,
+    d = dict(cache=addr(c), batch=addr(b), q=FAKE, o=2 * FAKE, q_row_stride=4096, q_head_stride=128, o_row_stride=4096,
              o_head_stride=128, tree=None, lse=None, workspace=FAKE, workspace_bytes=1 << 40, n_rows=16, scale=0.0,
              n_head=32, dtype=P.PAGED_F16, mask=P.PAGED_CAUSAL, window=0, reserved=0)
     d.update(kw)
@@ -160,8 +160,8 @@ def test_nothing_given(lib, name):
 @pytest.mark.parametrize("bad", [
     dict(q=None), dict(o=FAKE + 2), dict(q_row_stride=4100), dict(o_head_stride=-128), dict(n_head=30), dict(n_head=0),
     dict(n_head=8 * 65), dict(dtype=P.PAGED_BF16), dict(dtype=P.PAGED_F32), dict(mask=3), dict(mask=P.PAGED_TREE),
-    dict(tree=FAKE), dict(window=-1), dict(scale=-1.0), dict(scale=math.nan), dict(scale=math.inf), dict(n_rows=-1),
-    dict(n_rows=1 << 31),
+    dict(tree=FAKE), dict(window=-1), dict(scale=-1.0), dict(scale=math.nan), dict(scale=math.inf), dict(scale=3e38),
+    dict(n_rows=-1), dict(n_rows=1 << 31), dict(q=2 * FAKE), dict(q_row_stride=0), dict(o_head_stride=0),
 ])
 def test_bad_attention(lib, bad):
     c, b = cache(), batch()
@@ -176,6 +176,7 @@ def test_a_tree_has_at_most_64_nodes(lib):
 @pytest.mark.parametrize("bad", [
     dict(k=None), dict(v=FAKE + 8), dict(k_row_stride=1023), dict(dtype=P.PAGED_BF16), dict(dtype=P.PAGED_F32),
     dict(eps=-1.0), dict(eps=math.nan), dict(n_head_q=32), dict(n_head_q=-1), dict(k_norm=FAKE + 4),
+    dict(n_head_q=4, q=FAKE, q_out=FAKE, q_row_stride=512, q_head_stride=128, qo_row_stride=1024, qo_head_stride=128),
 ])
 def test_bad_appends(lib, bad):
     c, b = cache(), batch()
@@ -229,6 +230,7 @@ def norm_rope(**kw):
 @pytest.mark.parametrize("bad", [
     dict(dtype=P.PAGED_INT8), dict(head_dim=80), dict(n_rows=-1), dict(n_head_q=-1), dict(eps=-1.0), dict(q=None),
     dict(k_out=None), dict(q_row_stride=4095), dict(k_head_stride=-128), dict(q_norm=FAKE + 4),
+    dict(qo_row_stride=8192), dict(ko_head_stride=256),
 ])
 def test_bad_norm_ropes(lib, bad):
     refused(lib.paged_norm_rope, addr(norm_rope(**bad)), None)
@@ -241,7 +243,10 @@ def test_nothing_to_do_is_done(lib):
     for name, make in CALLS.items():
         assert getattr(lib, name)(addr(make(c, b, n_rows=0)), None) == R.RING_OK
         assert getattr(lib, name)(addr(make(c, none)), None) == R.RING_OK
+        gone = {"q": None, "o": None} if name == "paged_attend" else {"k": None, "v": None}
+        assert getattr(lib, name)(addr(make(c, b, n_rows=0, **gone)), None) == R.RING_OK     # as empty tensors are
     assert lib.paged_norm_rope(addr(norm_rope(n_rows=0)), None) == R.RING_OK
+    assert lib.paged_norm_rope(addr(norm_rope(n_rows=0, q=None, q_out=None, k=None, k_out=None, positions=None)), None) == R.RING_OK
 
 
 def test_workspace_refusals(lib):
