@@ -21,6 +21,7 @@
  *     (lengths, page numbers) is checked by the kernels: nothing out of range is followed.
  *     Rows that such an entry names are not written, or read as zeros, and a bit is set in
  *     the device error word (paged_device_error).
+ *   - An empty batch or tensor is nothing to do, its pointers are not looked at.
  *   - "Rows" tensors are [n_rows][heads][head_dim] with the innermost index contiguous and
  *     positive row and head strides (in elements) that keep every head 16-byte aligned, so that
  *     queries, keys and values may be slices of one projection's output.
@@ -88,8 +89,11 @@ typedef struct paged_cache {
  *   kv_len   device int32 [n_seq].
  *   pages    device int32 [n_seq][pages_stride]; entries of pages that a call has no need of
  *            (past the end, or in front of a window) are not looked at.
- *   max_q    upper bound of n over the sequences: chooses the kernel and its grid.
- *   max_kv   upper bound of kv_len, at most max_pages * page_size.
+ *   max_q    upper bound of n over the sequences: paged_attend chooses its kernel by it (and a
+ *            sequence of more new tokens is left alone there, PAGED_ERR_PAGE); the other calls
+ *            do not look at it.
+ *   max_kv   upper bound of kv_len, at most max_pages * page_size (0: that product): bounds
+ *            paged_attend's grid and workspace.
  */
 typedef struct paged_batch {
     const int32_t *q_start, *kv_len, *pages;
@@ -145,7 +149,8 @@ int paged_norm_rope(const paged_norm_rope_args *args, void *stream);
  *   k, v       rows [n_rows][n_head_kv][head_dim], PAGED_F16 or PAGED_BF16.
  *   k_norm, rope   K is normed and turned first, as in paged_norm_rope, at its position in
  *              the sequence, or at positions[row] where given (a token tree's depths).
- *   q, q_out   optional (n_head_q > 0): queries normed (q_norm) and turned in the same pass.
+ *   q, q_out   optional (n_head_q > 0): queries normed (q_norm) and turned in the same pass;
+ *              q_out may be q with the same strides.
  * Quantised pages: per row, A = max|x| in float32, scale = A / 127 (int8) or A / 448 (e4m3),
  * codes = x * (127 / A) or x * (448 / A) rounded to nearest even; a row with A < 1e-30 gets
  * scale 0 and codes 0, a row with an infinity or NaN gets scale NaN and codes 0 and reads
@@ -198,12 +203,17 @@ int paged_gather(const paged_gather_args *args, void *stream);
  * Per query head h (kv head h / (n_head / n_head_kv)):
  *   o = sum_p softmax_p(q . k_p * scale) v_p;  a token that sees nothing gets 0.
  * Products on the tensor cores with float32 accumulation, softmax in float32;
- * probabilities round to the operand type (F16 for quantised pages, whose codes are exact
- * in F16 and whose scales are applied in float32).
+ * probabilities round to the operand type (F16 for quantised pages).  With up to 32 query rows
+ * per kv head (max_q * n_head / n_head_kv) codes are exact F16 operands and their scales are
+ * applied in float32; with more, a row's codes times its scale are rounded to F16 once, relative
+ * to a power of two that keeps scales of any size within F16's range.
+ * A sequence whose lengths contradict each other (more new tokens than kv_len or than max_q, a
+ * length beyond the block table) is left alone: its rows of o and lse stay as they were.
  *   q, o     rows [n_rows][n_head][head_dim], PAGED_F16 or PAGED_BF16; pages of a 16-bit
  *            format have the same type.  n_head a multiple of n_head_kv, up to 64 query
  *            heads per kv head.  o may not overlap q.
- *   scale    0: 1 / sqrt(head_dim).
+ *   scale    0: 1 / sqrt(head_dim); at most 2e38.
+ *   window   0: none; one past every position is none too.
  *   tree     PAGED_TREE: device int64 [n_rows], else NULL.
  *   lse      NULL, or device F32 [n_rows][n_head]: ln of the softmax's denominator (of
  *            exp(score)), -inf for a token that sees nothing.
