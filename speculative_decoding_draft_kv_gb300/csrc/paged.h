@@ -78,7 +78,7 @@ struct PagedGatherArgs {
 };
 cudaError_t launch_paged_gather(const PagedGatherArgs &a, int dtype, int head_dim, cudaStream_t st);
 
-// Attention: what every CTA needs to find its share of the work (paged_attend.cu).
+// Attention: what every CTA needs to find its share of the work.
 struct PagedAttendArgs {
     const uint16_t *q;
     uint16_t *o;

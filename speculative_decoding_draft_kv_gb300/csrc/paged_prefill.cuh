@@ -26,8 +26,19 @@
 // key), code times scale rounded once, relative to a power of two per tile that the rows' threads
 // put back.  (Exact codes with the scales on scores and probabilities, as the streaming kernel has
 // them, took 96 reads of scales per row and tile out of the same shared memory that feeds the
-// products: 197 us instead of the figure below.)  bf16 queries are turned to F16 in shared
+// products: 197 us for the token trees below, against 191 when this form took over, and 131 now.)  bf16 queries are turned to F16 in shared
 // memory, a power of two per row taken out, by the threads that own the rows.
+//
+// Measured, 32 query and 8 kv heads: a chunk of 2,048 tokens at the end of 32,768, heads of 128, bf16:
+// 792 us, 1.35 PFLOP/s, the tensor pipe active 62 % of the time (a block's chain S -> softmax -> P -> O
+// is longer than the other block's products); 64 verify blocks of up to 9 tokens (36 rows, dealt) over
+// 2.2 GB: 357 us, 6.2 TB/s, bound by memory; two prompts of 4,097 tokens, heads of 64: 214 us, bound by
+// the exponentials and their latency (products are half as long there, exponentials as many); 16 trees
+// of up to 31 nodes over int8: 131 us, and chunks of 1,024 among single tokens, e4m3, window 2,048:
+// 243 us, both bound by the four converting warps, 1,500 to 2,300 clocks a K or V tile.  Tried and not
+// faster: eight converting warps (640 threads), registers moved between the roles (setmaxnreg), waits
+// that sleep or poll otherwise; one pass over S with the reference moved where needed was slower (914
+// us for the chunk, where two passes took 793).
 //
 // Roles: warps 0-3 and 4-7 the blocks' rows, warps 8 and 10 copies (queries by one box of heads x
 // tokens, K and V a box per page), warp 9 issues products, warps 12-15 convert codes.

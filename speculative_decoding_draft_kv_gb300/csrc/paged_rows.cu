@@ -12,6 +12,12 @@
 // position in units of 2^-64, so the product's whole turns fall off the top of a 64-bit
 // integer multiplication, exactly, and float32 sees only the rest (at most half a turn):
 // no float64 and no large arguments, for any position.
+//
+// Bytes are all that these operators cannot do without, each read and written once.  Measured, 32 query
+// and 8 kv heads of 128: norm and rotation of 16,384 bf16 tokens 66 us (5.0 TB/s, 75 % of the copy
+// rate); 22,600 F16 tokens to int8 and back 69 us (4.0 TB/s); 270,000 tokens back from e4m3 286 us (5.9
+// TB/s, 88 %).  What holds them is the instructions they issue, 0.64 to 0.74 a clock and scheduler;
+// small calls (a verify block, 64 of them) are bound by the host's call, 7 to 9 us.
 #include "paged.h"
 #include "paged_ptx.h"
 
