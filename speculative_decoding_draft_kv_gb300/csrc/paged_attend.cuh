@@ -26,10 +26,10 @@
 // 2^-24 below it.
 //
 // Measured, bf16, 32 query and 8 kv heads of 128, pages of 16, 64 sequences of 9 to 16,384 tokens
-// (2.2 GB): one token each 353 us, 6.3 TB/s (94 % of the copy rate); 8 tokens (32 rows) 402 us,
-// 5.5 TB/s, where the products' instructions begin to show.  With 9 tokens (36 rows) this kernel would
-// take two row tiles and read everything twice as often from L2: 414 us, against 357 us in the
-// tensor-core kernel, so 32 rows are the border between the two.  One token over 4,096: 12 us with the
+// (2.2 GB): one token each 353 us, 6.3 TB/s (93 % of the copy rate); 4 tokens (16 rows) 367 us.  With
+// 32 rows it took 382 us, where the products' instructions show, against the tensor-core kernel's 371:
+// 16-bit pages come here with up to 16 rows, quantised ones with up to 32 (4 tokens over int8 286 us, 3.9
+// TB/s; 8 tokens 436 us: turning codes into operands is what counts).  One token over 4,096: 12 us with the
 // join, of which bytes are 2.5: the rest is a chain of lookups (plan, page numbers), one round of
 // copies, the slices' merge and the join.
 #pragma once

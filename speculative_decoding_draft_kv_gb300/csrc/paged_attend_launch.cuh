@@ -33,9 +33,10 @@ cudaError_t with_attend(F &&fn) {
 
 template <int T, int D, class F>
 cudaError_t pick_attend(int format, int mt, F &&fn) {
+    // (16-bit pages come here with up to 16 rows only)
     if (format == PAGED_INT8) return mt == 1 ? with_attend<T, D, 1, kFmtInt8>(fn) : with_attend<T, D, 2, kFmtInt8>(fn);
     if (format == PAGED_E4M3) return mt == 1 ? with_attend<T, D, 1, kFmtE4m3>(fn) : with_attend<T, D, 2, kFmtE4m3>(fn);
-    return mt == 1 ? with_attend<T, D, 1, kFmt16>(fn) : with_attend<T, D, 2, kFmt16>(fn);
+    return with_attend<T, D, 1, kFmt16>(fn);
 }
 
 template <int T>

@@ -226,8 +226,12 @@ bool encode_queries(CUtensorMap *tm, const paged_attend_args *g, int head_dim, i
 }
 
 // Which kernel serves a batch, its rows per item and its CTAs: what the workspace and the launch
-// go by.  Up to 32 query rows per kv head: the streaming kernel; more: the tensor-core one, whose
-// items are one or two blocks of as many whole tokens as 128 rows take.
+// go by.  The streaming kernel up to a number of query rows per kv head, the tensor-core one above it,
+// whose items are one or two blocks of as many whole tokens as 128 rows take.
+// The border, measured on 64 sequences of up to 1,024 / 16,384 tokens, 8 kv heads of 128 (us):
+//   bf16 pages  16 rows: streaming 54 / 367, tensor-core 63 / 373;  32 rows: 69 / 382 and 62 / 371
+//   int8 pages  32 rows: 75 / 436 and 112 / 501 (the tensor-core kernel turns codes into F16 rows first)
+// so 16 rows over 16-bit pages and 32 over quantised ones, more than the streaming kernel has.
 // No more CTAs than the bounds leave work for.
 struct AttendPlan {
     int rows, tokens, ctas, min_tiles, item_cost;
@@ -236,18 +240,21 @@ struct AttendPlan {
 AttendPlan plan_of(const paged_cache *c, const paged_batch *b, int group, int sms) {
     const int64_t rows = (int64_t)b->max_q * group;
     AttendPlan p{};
-    p.wide = rows > 32;
+    p.wide = rows > (is16(c->format) ? 16 : 32);
     const int block = 128 / group;                                 // whole tokens of a tensor-core block
-    p.rows = rows <= 16 ? 16 : (rows <= 32 ? 32 : (b->max_q <= block ? 1 : 2) * block * group);
+    p.rows = p.wide ? (b->max_q <= block ? 1 : 2) * block * group : (rows <= 16 ? 16 : 32);
     p.tokens = p.wide ? p.rows / group : std::max(1, b->max_q);
-    // An item's beginning and end take the tensor-core kernel some 6,500 clocks, its tiles 2,500 to
-    // 3,500 each; the streaming kernel's overlap with its other CTA's tiles.
-    p.item_cost = p.wide ? 2 : 0;
-    p.min_tiles = (p.wide ? 1 : 2) + p.item_cost;
+    // What an item's beginning and end cost, in tiles: without it a share of many short items takes
+    // longer than one of as many tiles of a long item.  Tensor-core kernel: some 6,500 clocks, its tiles
+    // 2,500 to 3,500 each.  Streaming kernel, 64 sequences of up to 1,024 / 16,384 tokens, int8, 4 tokens
+    // each: 94 / 321 us at 0, 56 / 292 at 4, 53 / 286 at 6, 53 / 288 at 8; bf16 85 / 370 and 54 / 367 at 6.
+    p.item_cost = p.wide ? 2 : 6;
+    // (fewest units of a share; one token over 1,024 positions: 16 us with 2, 22 with 2 + item_cost)
+    p.min_tiles = p.wide ? 1 + p.item_cost : 2;
     const int64_t keys = b->max_kv > 0 ? b->max_kv : (int64_t)b->max_pages * c->page_size;
     const int64_t tiles = keys / (p.wide ? 128 : 64) + 2 + p.item_cost;   // of an item, wherever it begins
     const int64_t items = (int64_t)b->n_seq * c->n_head_kv * ((b->max_q + p.tokens - 1) / p.tokens);
-    // an item has min_tiles or more
+    // an item has min_tiles units or more
     const int64_t fit = p.wide ? sms : 2 * sms;
     const int64_t most = items >= fit ? fit : (items * tiles + p.min_tiles - 1) / p.min_tiles;
     p.ctas = (int)std::max<int64_t>(1, std::min(most, fit));
