@@ -22,23 +22,29 @@
 // odd ones, so that products and exponentials still take turns, and block 0 joins the two states at
 // the end.  A batch with no larger item runs the variant with memory for one block of queries.
 //
-// Quantised pages: four more warps turn code tiles into F16 tiles in shared memory (a thread per
-// key), code times scale rounded once, relative to a power of two per tile that the rows' threads
-// put back.  (Exact codes with the scales on scores and probabilities, as the streaming kernel has
-// them, took 96 reads of scales per row and tile out of the same shared memory that feeds the
-// products: 197 us for the token trees below, against 191 when this form took over, and 131 now.)  bf16 queries are turned to F16 in shared
-// memory, a power of two per row taken out, by the threads that own the rows.
+// Quantised pages: four more warps turn code tiles into F16 tiles in shared memory, a thread per key.
+// For F16 queries exactly, with K's scales multiplied on the scores and V's on the probabilities (in
+// units of a power of two), as the streaming kernel does.  For bf16 queries code times scale rounded once
+// to F16, relative to a power of two per tile that the rows' threads put back: 2^-12 of error beside an
+// output that rounds to 2^-9, and F16 tiles in four slots instead of three (the scales take 8 KiB): 213
+// us for the mixed batch below against 247 with exact codes.  For F16 outputs the rounded rows doubled
+// the relative error (4.3e-4, where the output's own rounding alone is 2.1e-4) and saved
+// nothing (130 us for the trees either way).  bf16 queries are turned to F16 in shared memory, a power
+// of two per row taken out, by the threads that own the rows.
 //
 // Measured, 32 query and 8 kv heads: a chunk of 2,048 tokens at the end of 32,768, heads of 128, bf16:
 // 792 us, 1.35 PFLOP/s, the tensor pipe active 62 % of the time (a block's chain S -> softmax -> P -> O
 // is longer than the other block's products); 64 verify blocks of up to 9 tokens (36 rows, dealt) over
-// 2.2 GB: 357 us, 6.2 TB/s, bound by memory; two prompts of 4,097 tokens, heads of 64: 214 us, bound by
+// 2.2 GB: 355 us, 6.2 TB/s, bound by memory; two prompts of 4,097 tokens, heads of 64: 214 us, bound by
 // the exponentials and their latency (products are half as long there, exponentials as many); 16 trees
-// of up to 31 nodes over int8: 131 us, and chunks of 1,024 among single tokens, e4m3, window 2,048:
-// 243 us, both bound by the four converting warps, 1,500 to 2,300 clocks a K or V tile.  Tried and not
-// faster: eight converting warps (640 threads), registers moved between the roles (setmaxnreg), waits
-// that sleep or poll otherwise; one pass over S with the reference moved where needed was slower (914
-// us for the chunk, where two passes took 793).
+// of up to 31 nodes over int8: 130 us, and chunks of 1,024 among single tokens, e4m3, window 2,048:
+// 208 us, both bound by the converting warps and the rows' warps sharing the issue slots.
+// What the kernel's parts run at the same time has to fit the instruction cache: over quantised pages the
+// rows' loops are unrolled twice, not eight times (mixed batch 243 -> 213 us, and with exact codes the
+// trees 162 -> 130), over 16-bit pages whole (two prompts: 214 us, 229 unrolled twice).
+// Tried and not faster: eight converting warps (640 threads), registers moved between the roles
+// (setmaxnreg), waits that sleep or poll otherwise; one pass over S with the reference moved where needed
+// was slower (914 us for the chunk, where two passes took 793).
 //
 // Roles: warps 0-3 and 4-7 the blocks' rows, warps 8 and 10 copies (queries by one box of heads x
 // tokens, K and V a box per page), warp 9 issues products, warps 12-15 convert codes.
@@ -49,25 +55,27 @@
 namespace dflash {
 
 constexpr int kPreTile = 128;
-constexpr int kUnitRing = 8;             // key tiles whose units are kept (see below)
+constexpr int kScaleRing = 8;            // key tiles whose scales or units are kept (see below)
 
-template <int D, int FMT, bool ONE>
+template <int D, int FMT, int T, bool ONE>
 struct PreCfg {
     static constexpr bool kCodes = FMT != kFmt16;
+    static constexpr bool kExact = kCodes && T == PAGED_F16;     // codes as they are, scales on S and P
     static constexpr int kThreads = kCodes ? 512 : 352;
     static constexpr int kHalves = D / 64;                       // 128-byte columns of a 16-bit row
     static constexpr int kHalfBytes = kPreTile * 128;
     static constexpr int kSlotBytes = kHalves * kHalfBytes;      // 128 rows of D 16-bit values
     static constexpr int kBlocks = ONE ? 1 : 2;                  // of queries
     // K and V tiles in turn: what fits
-    static constexpr int kSlots = kCodes ? 4 : (D == 128 ? (ONE ? 6 : 5) : 10);
+    static constexpr int kSlots = kCodes ? (kExact && D == 128 && !ONE ? 3 : 4) : (D == 128 ? (ONE ? 6 : 5) : 10);
     static constexpr int kCodeBytes = kPreTile * D;
-    static constexpr int kCodeSlots = kCodes ? (D == 128 && !ONE ? 2 : 3) : 0;
+    static constexpr int kCodeSlots = kCodes ? (D == 128 && !ONE && !kExact ? 2 : 3) : 0;
     static constexpr int kOffQ = kSlots * kSlotBytes;
     static constexpr int kOffCodes = kOffQ + kBlocks * kSlotBytes;
     static constexpr int kOffCodeScale = kOffCodes + kCodeSlots * kCodeBytes;   // as loaded, per code slot
-    static constexpr int kOffUnit = kOffCodeScale + kCodeSlots * kPreTile * 4;   // [ring][K, V]
-    static constexpr int kOffRow = kOffUnit + (kCodes ? kUnitRing * 8 : 0);      // row values
+    static constexpr int kOffScale = kOffCodeScale + kCodeSlots * kPreTile * 4;  // [ring][K, V][128]
+    static constexpr int kOffUnit = kOffScale + (kExact ? kScaleRing * 2 * kPreTile * 4 : 0);   // [ring][K, V]
+    static constexpr int kOffRow = kOffUnit + (kCodes ? kScaleRing * 8 : 0);     // row values
     static constexpr int kOffBars = kOffRow + 128 * 8;
     static constexpr int kOffPlan = kOffBars + 304;                // what else is shared: the plan, then words
     static constexpr int kSmem = kOffPlan + 24 * 8 + 16;
@@ -103,12 +111,12 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 }
 
 template <int D, int FMT, int T, bool ONE>
-__global__ void __launch_bounds__(PreCfg<D, FMT, ONE>::kThreads, 1)
+__global__ void __launch_bounds__(PreCfg<D, FMT, T, ONE>::kThreads, 1)
 k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                 const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ PagedAttendArgs a) {
-    using C = PreCfg<D, FMT, ONE>;
+    using C = PreCfg<D, FMT, T, ONE>;
     constexpr int NS = C::kSlots;
-    constexpr bool kCodes = C::kCodes;
+    constexpr bool kCodes = C::kCodes, kExact = C::kExact;
     constexpr int OT = kCodes ? PAGED_F16 : T;                       // operand type
     constexpr bool kQTurned = kCodes && T == PAGED_BF16;
     constexpr uint32_t kIdescQK = tc_idesc(128, kPreTile, OT == PAGED_BF16, false);
@@ -443,13 +451,16 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         __syncwarp();
     } else if (kCodes && warp >= 12) {
         // ---------------- codes to F16 ----------------
-        // A row is its codes times its scale, rounded to F16 -- the value that a 16-bit page would
-        // hold -- in units of a power of two: K's for a tile, so that its largest scale is in (1/2, 1],
-        // V's the largest so far of the item, which O is kept in.  Scales of any size fit F16 so.
+        // A row is its codes (exact) or its codes times its scale, rounded to F16.  Scales are in units of
+        // a power of two: K's (of rounded rows) for a tile, so that its largest scale is in (1/2, 1], V's
+        // the largest so far of the item, which O is kept in.  Scales of any size fit F16 so.
         // The ring of units needs no barrier of its own: the V slot of the tile that the slower
         // block's rows are at is taken, and with it every later one, so with 4 slots the tile at hand
         // here is at most 2 ahead of that one.
         const int r = (int)threadIdx.x - 384;              // the thread's key
+        // 16-byte pieces of a row at a time: all where codes are all there is to it (trees 130 us, 135
+        // two at a time), two where they are scaled (mixed batch 208 us, 213 all)
+        constexpr int kChunks = kExact ? D / 16 : 2;
         int slot = 0, cs = 0;
         uint32_t wrap = 0, cwrap = 0;
         int tile = 0;                                      // tiles so far: its place in the ring
@@ -486,36 +497,45 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     // the power of two above it, at most 2^127, and its inverse; 0 stays
                     uint32_t unit = top ? min((top & 0x7f800000u) + 0x00800000u, 0x7f000000u) : 0u;
                     if (kv) unit = v_unit = max(v_unit, unit);
-                    else if (!top) unit = 0x3f800000u;
+                    else if (kExact || !top) unit = 0x3f800000u;
                     const float inv = unit == 0 ? 0.f : (unit == 0x7f000000u ? 0x1p-127f : __uint_as_float(0x7f000000u - unit));
                     const float sc = live ? own * inv : 0.f;
                     if (warp == 12 && lane == 0)
-                        reinterpret_cast<uint32_t *>(smem + C::kOffUnit)[(tile % kUnitRing) * 2 + kv] = unit;
+                        reinterpret_cast<uint32_t *>(smem + C::kOffUnit)[(tile % kScaleRing) * 2 + kv] = unit;
+                    if constexpr (kExact) reinterpret_cast<float *>(smem + C::kOffScale)[((tile % kScaleRing) * 2 + kv) * kPreTile + r] = sc;
                     // the scale as a sum of two F16 values, good to 2^-22: code * high + (code * low), one
                     // fused rounding, is the product's rounding but for an error far below its step
                     const float high = __half2float(__float2half_rn(sc));
                     const uint32_t high2 = pack_half2(high, high), low2 = pack_half2(sc - high, sc - high);
-                    uint4 row[D / 16];                     // loads first: stores might be to the same place
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D / 16; c0 += kChunks) {
+                        uint4 row[kChunks];                // loads first: stores might be to the same place
 #pragma unroll
-                    for (int ch = 0; ch < D / 16; ++ch)
-                        row[ch] = *reinterpret_cast<const uint4 *>(src + swz_row<CODE_ROW>(r, ch));
+                        for (int i = 0; i < kChunks; ++i)
+                            row[i] = *reinterpret_cast<const uint4 *>(src + swz_row<CODE_ROW>(r, c0 + i));
 #pragma unroll
-                    for (int ch = 0; ch < D / 16; ++ch) {
-                        if (!live) row[ch] = make_uint4(0, 0, 0, 0);       // (an e4m3 NaN times 0)
-                        const uint32_t xs[4] = {row[ch].x, row[ch].y, row[ch].z, row[ch].w};
-                        uint32_t y[8];
+                        for (int i = 0; i < kChunks; ++i) {
+                            const int ch = c0 + i;
+                            if (!live) row[i] = make_uint4(0, 0, 0, 0);        // (an e4m3 NaN times 0)
+                            const uint32_t xs[4] = {row[i].x, row[i].y, row[i].z, row[i].w};
+                            uint32_t y[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            uint32_t h;
-                            if constexpr (FMT == kFmtInt8) h = int8_pair(xs[k >> 1] ^ 0x80808080u, k & 1 ? 0x7362u : 0x5140u);
-                            else h = e4m3_pair_f16(xs[k >> 1] >> (16 * (k & 1)));
-                            uint32_t small;
-                            asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(small) : "r"(h), "r"(low2));
-                            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y[k]) : "r"(h), "r"(high2), "r"(small));
+                            for (int k = 0; k < 8; ++k) {
+                                uint32_t h;
+                                if constexpr (FMT == kFmtInt8) h = int8_pair(xs[k >> 1] ^ 0x80808080u, k & 1 ? 0x7362u : 0x5140u);
+                                else h = e4m3_pair_f16(xs[k >> 1] >> (16 * (k & 1)));
+                                if constexpr (kExact) {
+                                    y[k] = h;
+                                    continue;
+                                }
+                                uint32_t small;
+                                asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(small) : "r"(h), "r"(low2));
+                                asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y[k]) : "r"(h), "r"(high2), "r"(small));
+                            }
+                            uint8_t *at = dst + (ch >> 2) * C::kHalfBytes;
+                            *reinterpret_cast<uint4 *>(at + swz_row<128>(r, (2 * ch) & 7)) = make_uint4(y[0], y[1], y[2], y[3]);
+                            *reinterpret_cast<uint4 *>(at + swz_row<128>(r, (2 * ch + 1) & 7)) = make_uint4(y[4], y[5], y[6], y[7]);
                         }
-                        uint8_t *at = dst + (ch >> 2) * C::kHalfBytes;
-                        *reinterpret_cast<uint4 *>(at + swz_row<128>(r, (2 * ch) & 7)) = make_uint4(y[0], y[1], y[2], y[3]);
-                        *reinterpret_cast<uint4 *>(at + swz_row<128>(r, (2 * ch + 1) & 7)) = make_uint4(y[4], y[5], y[6], y[7]);
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
@@ -649,9 +669,12 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 sph ^= 1u;
                 tc_fence_after();
                 if (busy) {
-                    // quantised: the units of this tile's K and V
+                    // quantised: the units of this tile's K and V, and the scales in them
+                    const int ring = (tile0 + j) % kScaleRing;
                     float2 unit = make_float2(1.f, 1.f);
-                    if constexpr (kCodes) unit = reinterpret_cast<const float2 *>(smem + C::kOffUnit)[(tile0 + j) % kUnitRing];
+                    if constexpr (kCodes) unit = reinterpret_cast<const float2 *>(smem + C::kOffUnit)[ring];
+                    const float4 *ks4 = reinterpret_cast<const float4 *>(smem + C::kOffScale) + ring * (kPreTile / 2);
+                    const float4 *vs4 = ks4 + kPreTile / 4;
                     const bool partly = base < all_lo || base + kPreTile > all_hi;
                     // O times a factor per row
                     auto rescale = [&](float by) {
@@ -692,6 +715,14 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 #pragma unroll
                         for (int e = 0; e < CH / 2; ++e)
                             s[e] = pk2(__uint_as_float(raw[at][2 * e]), __uint_as_float(raw[at][2 * e + 1]));
+                        if constexpr (kExact) {
+#pragma unroll
+                            for (int e = 0; e < CH / 4; ++e) {
+                                const float4 k = ks4[c * (CH / 4) + e];
+                                s[2 * e] = mul2(s[2 * e], pk2(k.x, k.y));
+                                s[2 * e + 1] = mul2(s[2 * e + 1], pk2(k.z, k.w));
+                            }
+                        }
                         if (masked) {
                             const uint32_t bits = seen_bits(base + CH * c);
 #pragma unroll
@@ -712,7 +743,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     const uint64_t scale2 = pk2(tscale, tscale);
                     auto tile = [&](auto kind) {
                         constexpr bool masked = kind.value;
-                        constexpr int kUnroll = masked ? 1 : 128 / CH;   // (the masked one is rare)
+                        constexpr int kUnroll = masked ? 1 : (kCodes ? 2 : 128 / CH);   // (see above; the masked one is rare)
                         float x0 = -INFINITY, x1 = x0;
                         if (!masked) begin();
 #pragma unroll kUnroll
@@ -728,8 +759,8 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                                 x1 = max3(x1, y2, y3);
                             }
                         }
-                        if (!masked) begin();
                         const float mx = fmaxf(x0, x1) * tscale;
+                        if (!masked) begin();
                         const bool move = valid && mx > m + kLazyMove;
                         if (__any_sync(0xffffffffu, move || factor != 1.f)) {
                             const float mnew = move ? mx : m;
@@ -750,9 +781,13 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                             for (int e = 0; e < CH / 2; ++e) {
                                 float x, y;
                                 upk2(fma2(s[e], scale2, minus2), x, y);
-                                const uint64_t p2 = pk2(ex2_approx(x), ex2_approx(y));
+                                uint64_t p2 = pk2(ex2_approx(x), ex2_approx(y));
                                 if (e & 1) sb = add2(sb, p2);
                                 else sa = add2(sa, p2);
+                                if constexpr (kExact) {
+                                    const float4 v = vs4[c * (CH / 4) + e / 2];
+                                    p2 = mul2(p2, e & 1 ? pk2(v.z, v.w) : pk2(v.x, v.y));
+                                }
                                 upk2(p2, x, y);
                                 u[e] = pack16<OT>(x, y);
                             }

@@ -10,7 +10,7 @@ namespace dflash {
 template <int T, class F>
 cudaError_t pick_prefill(int head_dim, int format, bool one, F &&fn) {
     auto with = [&](auto d, auto fmt, auto single) {
-        using C = PreCfg<d.value, fmt.value, single.value>;
+        using C = PreCfg<d.value, fmt.value, T, single.value>;
         return fn(k_paged_prefill<d.value, fmt.value, T, single.value>, C::kSmem, C::kThreads);
     };
     auto blocks = [&](auto d, auto fmt) { return one ? with(d, fmt, std::true_type{}) : with(d, fmt, std::false_type{}); };

@@ -127,7 +127,7 @@ class World:
             keys, in float32, in runs of at most a few thousand terms: 2^-12 u more, kept in 2 d;
           F16's smallest step 2^-25 on each probability against at most the largest |v|;
           the output U |o|;
-          wide (more than 32 query rows per kv head) over quantised pages: K and V rows are rounded
+          wide (more than 32 query rows per kv head) over quantised pages, bf16: K and V rows are rounded
             to F16 first, by at most 2^-11 of each element, which moves a score by at most 2^-11 T
             and the numerator by 2^-11 A."""
         scale = 1 / math.sqrt(self.dim) if scale is None else scale
@@ -150,7 +150,7 @@ class World:
             o[r] = torch.einsum("hip,phd->ihd", p, v)
             T = (torch.einsum("ihd,phd->hip", x.abs(), k.abs()).amax(-1) * scale).T     # [n, heads]
             d = T * (self.dim + 8) * 2.0 ** -24 + 2.0 ** -21
-            more = UNIT[torch.float16] if wide and self.store in TOP else 0.0
+            more = UNIT[torch.float16] if wide and self.store in TOP and self.dtype == torch.bfloat16 else 0.0
             d = d + more * T
             A = torch.einsum("hip,phd->ihd", p, v.abs())
             tiny = kv * 2.0 ** -25 * v.abs().amax() if operand == torch.float16 else 0.0
