@@ -42,9 +42,9 @@
 // What the kernel's parts run at the same time has to fit the instruction cache: over quantised pages the
 // rows' loops are unrolled twice, not eight times (mixed batch 243 -> 213 us, and with exact codes the
 // trees 162 -> 130), over 16-bit pages whole (two prompts: 214 us, 229 unrolled twice).
-// Tried and not faster: eight converting warps (640 threads), registers moved between the roles
-// (setmaxnreg), waits that sleep or poll otherwise; one pass over S with the reference moved where needed
-// was slower (914 us for the chunk, where two passes took 793).
+// Tried and not faster: eight converting warps (640 threads), waits that sleep or poll otherwise; one pass
+// over S with the reference moved where needed was slower (914 us for the chunk, where two passes took
+// 793).
 //
 // Roles: warps 0-3 and 4-7 the blocks' rows, warps 8 and 10 copies (queries by one box of heads x
 // tokens, K and V a box per page), warp 9 issues products, warps 12-15 convert codes.
@@ -62,6 +62,12 @@ struct PreCfg {
     static constexpr bool kCodes = FMT != kFmt16;
     static constexpr bool kExact = kCodes && T == PAGED_F16;     // codes as they are, scales on S and P
     static constexpr int kThreads = kCodes ? 512 : 352;
+    // With scales on the scores and two blocks of rows, those are what holds the kernel: their 256 threads
+    // take 168 registers, the others 88 (together the 65,536 of the launch, 512 times 128), and pieces of
+    // 32 scores (a chunk of 619 tokens at 23,810, heads of 64, int8: 314 -> 257 us).  One block, or rounded
+    // rows: no gain (trees 130 -> 137 us, mixed batch 207 -> 211).
+    static constexpr bool kMore = kExact && !ONE;
+    static constexpr int kManyRegs = 168, kFewRegs = 88;
     static constexpr int kHalves = D / 64;                       // 128-byte columns of a 16-bit row
     static constexpr int kHalfBytes = kPreTile * 128;
     static constexpr int kSlotBytes = kHalves * kHalfBytes;      // 128 rows of D 16-bit values
@@ -213,7 +219,11 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         return a.mask != PAGED_TREE || t < 0 || (t < 64 && ((any_word >> t) & 1ull));
     };
 
+    auto fewer = [&]() {
+        if constexpr (C::kMore) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kFewRegs));
+    };
     if (warp == 8 || warp == 10) {
+        fewer();
         // ---------------- copies: warp 8 queries and K, warp 10 V ----------------
         // (two, since boxes leave a warp one lane after the other: 16 of them, of pages of 16, took
         // one warp longer than memory takes for their bytes)
@@ -322,6 +332,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         }
         __syncwarp();
     } else if (warp == 9) {
+        fewer();
         // ---------------- products ----------------
         // The whole warp keeps the order and waits; one lane issues.  Descriptors differ by constants
         // from one base per operand: an address step adds its sixteenth to the low word (computed
@@ -450,6 +461,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         if (!mbar_wait(drain, 0) && lane == 0) timed_out();
         __syncwarp();
     } else if (kCodes && warp >= 12) {
+        fewer();
         // ---------------- codes to F16 ----------------
         // A row is its codes (exact) or its codes times its scale, rounded to F16.  Scales are in units of
         // a power of two: K's (of rounded rows) for a tile, so that its largest scale is in (1/2, 1], V's
@@ -555,8 +567,9 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             }
         }
     } else if (warp < 8) {
+        if constexpr (C::kMore) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kManyRegs));
         // ---------------- softmax rows ----------------
-        constexpr int CH = kCodes ? 16 : 32;               // scores of a row at a time: more would spill
+        constexpr int CH = kCodes && !C::kMore ? 16 : 32;               // scores of a row at a time: more would spill
         const int blk = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lane_base + blk * 128, to = tmem + lane_base + 256 + blk * 128;
@@ -743,7 +756,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     const uint64_t scale2 = pk2(tscale, tscale);
                     auto tile = [&](auto kind) {
                         constexpr bool masked = kind.value;
-                        constexpr int kUnroll = masked ? 1 : (kCodes ? 2 : 128 / CH);   // (see above; the masked one is rare)
+                        constexpr int kUnroll = masked ? 1 : (kCodes && !C::kMore ? 2 : 128 / CH);   // (see above; the masked one is rare)
                         float x0 = -INFINITY, x1 = x0;
                         if (!masked) begin();
 #pragma unroll kUnroll
@@ -911,6 +924,8 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             }
         }
         if (threadIdx.x == 0 && !began) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    } else {
+        fewer();
     }
     tc_fence_before();
     __syncthreads();
