@@ -245,12 +245,13 @@ AttendPlan plan_of(const paged_cache *c, const paged_batch *b, int group, int sm
     p.rows = p.wide ? (b->max_q <= block ? 1 : 2) * block * group : (rows <= 16 ? 16 : 32);
     p.tokens = p.wide ? p.rows / group : std::max(1, b->max_q);
     // What an item's beginning and end cost, in tiles: without it a share of many short items takes
-    // longer than one of as many tiles of a long item.  Tensor-core kernel: some 6,500 clocks, its tiles
-    // 2,500 to 3,500 each.  Streaming kernel, 64 sequences of up to 1,024 / 16,384 tokens, int8, 4 tokens
+    // longer than one of as many tiles of a long item.  Tensor-core kernel: two prompts of 4,097 tokens 248
+    // us at 0, 214 at 2 and 3; int8 trees and a mixed e4m3 batch 130 and 208 us at 2, 126 and 202 at 3, 127
+    // and 204 at 4.  Streaming kernel, 64 sequences of up to 1,024 / 16,384 tokens, int8, 4 tokens
     // each: 94 / 321 us at 0, 56 / 292 at 4, 53 / 286 at 6, 53 / 288 at 8; bf16 85 / 370 and 54 / 367 at 6.
-    p.item_cost = p.wide ? 2 : 6;
+    p.item_cost = p.wide ? 3 : 6;
     // (fewest units of a share; one token over 1,024 positions: 16 us with 2, 22 with 2 + item_cost)
-    p.min_tiles = p.wide ? 1 + p.item_cost : 2;
+    p.min_tiles = 2;
     const int64_t keys = b->max_kv > 0 ? b->max_kv : (int64_t)b->max_pages * c->page_size;
     const int64_t tiles = keys / (p.wide ? 128 : 64) + 2 + p.item_cost;   // of an item, wherever it begins
     const int64_t items = (int64_t)b->n_seq * c->n_head_kv * ((b->max_q + p.tokens - 1) / p.tokens);

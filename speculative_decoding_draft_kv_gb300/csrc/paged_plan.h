@@ -11,8 +11,7 @@
 // its CTA; an item cut by a share's border leaves one partial softmax state in each CTA that
 // has a piece of it, and the combine kernel joins them.
 //
-// (In the tensor-core kernel it took two prompts of 4,097 tokens, of whose items many begin and end in a
-// share, from 248 to 212 us; for the streaming one see plan_of.)
+// (What it is worth in either kernel: see plan_of.)
 //
 // A share is one run of tiles, so a CTA holds at most two such pieces: the end (or middle) of
 // an item begun earlier, slot 0, and the beginning of one that goes on, slot 1.

@@ -27,7 +27,7 @@
 // units of a power of two), as the streaming kernel does.  For bf16 queries code times scale rounded once
 // to F16, relative to a power of two per tile that the rows' threads put back: 2^-12 of error beside an
 // output that rounds to 2^-9, and F16 tiles in four slots instead of three (the scales take 8 KiB): 213
-// us for the mixed batch below against 247 with exact codes.  For F16 outputs the rounded rows doubled
+// us for the mixed batch below against 247 with exact codes (202 after later steps).  For F16 outputs the rounded rows doubled
 // the relative error (4.3e-4, where the output's own rounding alone is 2.1e-4) and saved
 // nothing (130 us for the trees either way).  bf16 queries are turned to F16 in shared memory, a power
 // of two per row taken out, by the threads that own the rows.
@@ -37,8 +37,8 @@
 // is longer than the other block's products); 64 verify blocks of up to 9 tokens (36 rows, dealt) over
 // 2.2 GB: 355 us, 6.2 TB/s, bound by memory; two prompts of 4,097 tokens, heads of 64: 214 us, bound by
 // the exponentials and their latency (products are half as long there, exponentials as many); 16 trees
-// of up to 31 nodes over int8: 130 us, and chunks of 1,024 among single tokens, e4m3, window 2,048:
-// 208 us, both bound by the converting warps and the rows' warps sharing the issue slots.
+// of up to 31 nodes over int8: 126 us, and chunks of 1,024 among single tokens, e4m3, window 2,048:
+// 202 us, both bound by the converting warps and the rows' warps sharing the issue slots.
 // What the kernel's parts run at the same time has to fit the instruction cache: over quantised pages the
 // rows' loops are unrolled twice, not eight times (mixed batch 243 -> 213 us, and with exact codes the
 // trees 162 -> 130), over 16-bit pages whole (two prompts: 214 us, 229 unrolled twice).
