@@ -10,11 +10,11 @@
 //
 // Angles: position times frequency, less whole turns.  A frequency is held as turns per
 // position in units of 2^-64, so the product's whole turns fall off the top of a 64-bit
-// integer multiplication, exactly, and float32 sees only the rest (at most half a turn):
+// integer multiplication, exactly, and float32 sees only the rest (at most half a turn, in two parts):
 // no float64 and no large arguments, for any position.
 //
 // Bytes are all that these operators cannot do without, each read and written once.  Measured, 32 query
-// and 8 kv heads of 128: norm and rotation of 16,384 bf16 tokens 66 us (5.0 TB/s, 75 % of the copy
+// and 8 kv heads of 128: norm and rotation of 16,384 bf16 tokens 67 us (5.0 TB/s, 74 % of the copy
 // rate); 22,600 F16 tokens to int8 and back 69 us (4.0 TB/s); 270,000 tokens back from e4m3 286 us (5.9
 // TB/s, 88 %).  What holds them is the instructions they issue, 0.64 to 0.74 a clock and scheduler;
 // small calls (a verify block, 64 of them) are bound by the host's call, 7 to 9 us.
@@ -135,12 +135,15 @@ __device__ __forceinline__ Place place_of(const PagedBatchDev &b, const PagedPoo
     return p;
 }
 
-// cos and sin (times the magnitude) of p * turn, turn in 2^-64 turns
+// cos and sin (times the magnitude) of p * turn, turn in 2^-64 turns.  The angle's top 20 bits are exact
+// in float32; the other 12, at most 6e-6, follow by the derivative (a float32 angle would be off by up to
+// 1e-7: of 226 million e4m3 codes 13 fell on the other side of a rounding border that way, 8 this way).
 __device__ __forceinline__ float2 turn_cs(int p, uint64_t turn, float magnitude) {
     const int32_t frac = (int32_t)((uint64_t)(int64_t)p * turn >> 32);   // whole turns gone
+    const float low = (float)(frac & 0xfff) * 1.4629180792671596e-9f;    // pi 2^-31
     float sn, cs;
-    sincospif((float)frac * 0x1p-31f, &sn, &cs);
-    return make_float2(cs * magnitude, sn * magnitude);
+    sincospif((float)(frac & ~0xfff) * 0x1p-31f, &sn, &cs);
+    return make_float2(fmaf(-sn, low, cs) * magnitude, fmaf(cs, low, sn) * magnitude);
 }
 
 // Norm and rotation of one row spread over LPR lanes (lane c: values 8c .. 8c+7).  With inv =
