@@ -495,22 +495,26 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     const float *scales = reinterpret_cast<const float *>(smem + C::kOffCodeScale) + cs * kPreTile;
                     const bool live = !edge || seen(t * kPreTile + r, any_word);
                     const float own = scales[r];
-                    // the tile's largest finite scale among the rows that count (four to a lane)
-                    const float4 four = reinterpret_cast<const float4 *>(scales)[lane];
-                    float f[4] = {fabsf(four.x), fabsf(four.y), fabsf(four.z), fabsf(four.w)};
-                    float most = fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3]));           // NaN is passed over
-                    if (edge || most == INFINITY) {
-                        most = 0.f;
+                    uint32_t unit = 0x3f800000u;
+                    float inv = 1.f;
+                    if (kv || !kExact) {
+                        // the tile's largest finite scale among the rows that count (four to a lane)
+                        const float4 four = reinterpret_cast<const float4 *>(scales)[lane];
+                        float f[4] = {fabsf(four.x), fabsf(four.y), fabsf(four.z), fabsf(four.w)};
+                        float most = fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3]));           // NaN is passed over
+                        if (edge || most == INFINITY) {
+                            most = 0.f;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (f[i] < INFINITY && (!edge || seen(t * kPreTile + 4 * lane + i, any_word))) most = fmaxf(most, f[i]);
+                            for (int i = 0; i < 4; ++i)
+                                if (f[i] < INFINITY && (!edge || seen(t * kPreTile + 4 * lane + i, any_word))) most = fmaxf(most, f[i]);
+                        }
+                        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
+                        // the power of two above it, at most 2^127, and its inverse; 0 stays
+                        unit = top ? min((top & 0x7f800000u) + 0x00800000u, 0x7f000000u) : 0u;
+                        if (kv) unit = v_unit = max(v_unit, unit);
+                        else if (!top) unit = 0x3f800000u;
+                        inv = unit == 0 ? 0.f : (unit == 0x7f000000u ? 0x1p-127f : __uint_as_float(0x7f000000u - unit));
                     }
-                    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
-                    // the power of two above it, at most 2^127, and its inverse; 0 stays
-                    uint32_t unit = top ? min((top & 0x7f800000u) + 0x00800000u, 0x7f000000u) : 0u;
-                    if (kv) unit = v_unit = max(v_unit, unit);
-                    else if (kExact || !top) unit = 0x3f800000u;
-                    const float inv = unit == 0 ? 0.f : (unit == 0x7f000000u ? 0x1p-127f : __uint_as_float(0x7f000000u - unit));
                     const float sc = live ? own * inv : 0.f;
                     if (warp == 12 && lane == 0)
                         reinterpret_cast<uint32_t *>(smem + C::kOffUnit)[(tile % kScaleRing) * 2 + kv] = unit;
