@@ -81,8 +81,11 @@ struct PreCfg {
     static constexpr int kOffCodeScale = kOffCodes + kCodeSlots * kCodeBytes;   // as loaded, per code slot
     static constexpr int kOffScale = kOffCodeScale + kCodeSlots * kPreTile * 4;  // [ring][K, V][128]
     static constexpr int kOffUnit = kOffScale + (kExact ? kScaleRing * 2 * kPreTile * 4 : 0);   // [ring][K, V]
-    static constexpr int kOffRow = kOffUnit + (kCodes ? kScaleRing * 8 : 0);     // row values
-    static constexpr int kOffBars = kOffRow + 128 * 8;
+    // a dealt item's odd tiles: maxima and sums; its queries' powers of two (in a place of their own: block 0
+    // writes those of the next item while its slower warps may still read the sums of this one)
+    static constexpr int kOffOdd = kOffUnit + (kCodes ? kScaleRing * 8 : 0);
+    static constexpr int kOffExp = kOffOdd + 128 * 8;
+    static constexpr int kOffBars = kOffExp + (kCodes && T == PAGED_BF16 ? 128 : 0);
     static constexpr int kOffPlan = kOffBars + 304;                // what else is shared: the plan, then words
     static constexpr int kSmem = kOffPlan + 24 * 8 + 16;
     static_assert(kSmem <= 227 * 1024, "one CTA per SM");
@@ -577,8 +580,8 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         const int blk = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lane_base + blk * 128, to = tmem + lane_base + 256 + blk * 128;
-        float *row_scale = reinterpret_cast<float *>(smem + C::kOffRow);              // [2][128]
-        float2 *odd_ml = reinterpret_cast<float2 *>(smem + C::kOffRow);               // [128]
+        uint8_t *row_exp = smem + C::kOffExp;                                         // [128] biased exponents
+        float2 *odd_ml = reinterpret_cast<float2 *>(smem + C::kOffOdd);               // [128]
         float *odd_ref = reinterpret_cast<float *>(smem + C::kOffPlan + 24 * 8 + 8);
         uint32_t sph = 0, oph = 0, dph = 0;
         bool began = false;                                 // this CTA starts an item that another finishes
@@ -610,7 +613,10 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 break;
             }
             if constexpr (kQTurned) {
-                // this block's queries to F16, unless the other block does it
+                // This block's queries to F16, unless the other block does it, which then leaves the rows'
+                // powers of two here.  (They stand until every warp has said that this item's queries may
+                // go: the next ones are not looked at before.)
+                int e = 127;
                 if (my_blk == blk) {
                     uint8_t *qr = smem + C::kOffQ + blk * C::kSlotBytes;
                     uint32_t top = 0;
@@ -621,9 +627,8 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 #pragma unroll
                         for (int i = 0; i < 4; ++i) top = max(top, max(xs[i] & 0x7fffu, (xs[i] >> 16) & 0x7fffu));
                     }
-                    const int e = top ? min(254, max(1, (int)(top >> 7))) : 127;
+                    if (top) e = min(254, max(1, (int)(top >> 7)));
                     const float down = e == 254 ? 0x1p-127f : __uint_as_float((uint32_t)(254 - e) << 23);
-                    const float up = __uint_as_float((uint32_t)e << 23);
 #pragma unroll
                     for (int ch = 0; ch < D / 8; ++ch) {
                         uint4 *at = reinterpret_cast<uint4 *>(qr + (ch >> 3) * C::kHalfBytes + swz_row<128>(r, ch & 7));
@@ -634,7 +639,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                             xs[i] = pack_half2(__uint_as_float(xs[i] << 16) * down, __uint_as_float(xs[i] & 0xffff0000u) * down);
                         *at = make_uint4(xs[0], xs[1], xs[2], xs[3]);
                     }
-                    row_scale[blk * 128 + r] = up;
+                    if (deal) row_exp[r] = (uint8_t)e;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) {
@@ -646,7 +651,9 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     if (lane == 0) timed_out();
                     break;
                 }
-                qscale *= row_scale[my_blk * 128 + r];
+                if (my_blk != blk) e = row_exp[r];
+                qscale *= __uint_as_float((uint32_t)e << 23);
+                __syncwarp();                              // read by every lane before lane 0 says so
             }
             ++items;
             // the queries may go with the last product

@@ -1,0 +1,37 @@
+"""The order of what the roles inside an attention CTA read and write: items one behind another in the
+same shared memory, again and again, with the same bits each time."""
+
+import pytest
+import torch
+
+from speculative_decoding_draft_kv_gb300 import paged as P
+from tests.paged_oracle import World
+from tests.test_gpu_paged_attend import check
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("fmt,dtype", [("int8", "bf16"), ("e4m3", "bf16"), ("int8", "f16"), ("bf16", "bf16")])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("chunk", [0, 150])
+def test_dealt_items_one_behind_another(fmt, dtype, dim, chunk):
+    """Verify blocks of 9 tokens, 4 heads to a kv head: 36 rows, so that of block 0's warps two have rows
+    and two run straight on into the next item, whose queries' powers of two they write while the
+    others still read the odd tiles' sums of this one.  With a chunk among them, in the variant of two blocks."""
+    lens = [(9, 140 + (i * 173) % 900) for i in range(64)]
+    if chunk:
+        lens[40] = (chunk, 700)
+    w = World(lens, heads=32, kv_heads=8, page=16, fmt=fmt, dtype=dtype, dim=dim, seed=dim + chunk)
+    # rows' magnitudes far apart, so that a power of two of another row or item does not go unseen
+    q = w.randn(w.heads) * torch.exp2(torch.randint(-3, 4, (w.rows, w.heads, 1), generator=w.g, device="cuda")).to(w.dtype)
+    want = check(w, q=q)
+    cache, batch = w.handles(P)
+    ws = torch.empty(P.paged_attend_workspace(cache, batch, w.heads), dtype=torch.uint8, device="cuda")
+    o, lse = torch.empty_like(q), torch.empty(w.rows, w.heads, device="cuda")
+    first = None
+    for _ in range(25):
+        o.fill_(7.0)
+        P.paged_attend(cache, batch, q, o, lse=lse, workspace=ws)
+        first = lse.clone() if first is None else first
+        assert torch.equal(o, want) and torch.equal(lse, first)
+    assert P.paged_device_error() == 0
