@@ -554,8 +554,8 @@ k_paged_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             sml[warp * 16 + g] = make_float2(mrow[0], lrow[0]);
             sml[warp * 16 + g + 8] = make_float2(mrow[1], lrow[1]);
         }
-        bar_sync(1, 128);
-        if (s_abort) break;              // set before the barrier or not at all: all warps agree
+        // a wait that ran out, here or in the copy warp (which may say so at any time): all four warps leave
+        if (bar_any(1, 128, s_abort != 0)) break;
         float M[2], L[2];
 #pragma unroll
         for (int jj = 0; jj < 2; ++jj) {

@@ -488,7 +488,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 const bool edge = ragged(t);
                 for (int kv = 0; kv < 2; ++kv) {
                     const bool ok = mbar_wait(c_full + 8 * cs, cwrap) && mbar_wait(empty + 8 * slot, wrap ^ 1u);
-                    if (!__all_sync(0xffffffffu, ok) || s_abort) {
+                    if (!__all_sync(0xffffffffu, ok && !s_abort)) {
                         if (lane == 0) timed_out();
                         alive = false;
                         break;
@@ -831,7 +831,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             }
             tile0 += w.nt;
             vslot += 2 * w.nt;
-            if (!alive || s_abort) break;
+            if (__any_sync(0xffffffffu, !alive || s_abort)) break;     // one answer for the warp
             const bool mine = j0 < w.nt;                   // this block had a tile
             if (mine) {
                 if (!__all_sync(0xffffffffu, mbar_wait(o_full + 8 * blk, oph))) {

@@ -108,6 +108,18 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) { tme
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16]) { tmem_st16(taddr, r); }
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[32]) { tmem_st32(taddr, r); }
 
+// A barrier of `threads` threads (whole warps) at which they also agree: true for all of them if one
+// says so.  A shared word that somebody outside the barrier may set is not the same to all that read it
+// after the barrier, and who has left is missed, without limit, at the next one.
+__device__ __forceinline__ bool bar_any(int id, int threads, bool mine) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"((uint32_t)mine), "r"(id), "r"(threads)
+                 : "memory");
+    return r != 0;
+}
+
 // One lane of the converged warp, the same one every time.  (A branch on it, rather than on the lane
 // number, keeps the operands of what it issues in uniform registers.)
 __device__ __forceinline__ bool elect_one() {

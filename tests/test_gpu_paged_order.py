@@ -1,9 +1,13 @@
 """The order of what the roles inside an attention CTA read and write: items one behind another in the
 same shared memory, again and again, with the same bits each time."""
 
+import ctypes
+import subprocess
+
 import pytest
 import torch
 
+from speculative_decoding_draft_kv_gb300 import build as B
 from speculative_decoding_draft_kv_gb300 import paged as P
 from tests.paged_oracle import World
 from tests.test_gpu_paged_attend import check
@@ -35,3 +39,51 @@ def test_dealt_items_one_behind_another(fmt, dtype, dim, chunk):
         first = lse.clone() if first is None else first
         assert torch.equal(o, want) and torch.equal(lse, first)
     assert P.paged_device_error() == 0
+
+
+PROBE = r"""
+#include "paged_ptx.h"
+using namespace dflash;
+// Four warps that meet twice a round, as the streaming kernel's do at an item's end, and a fifth that raises
+// a flag after `late` clocks; the round in which each of the four left.
+__global__ void probe(int late, int rounds, int *left) {
+    __shared__ volatile int flag;
+    if (threadIdx.x == 0) flag = 0;
+    __syncthreads();
+    const int warp = threadIdx.x >> 5;
+    if (warp == 4) {
+        const long long t0 = clock64();
+        while (clock64() - t0 < late) {}
+        if ((threadIdx.x & 31) == 0) flag = 1;
+        return;
+    }
+    int i = 0;
+    for (; i < rounds; ++i) {
+        if (bar_any(1, 128, flag != 0)) break;
+        bar_sync(1, 128);
+    }
+    if ((threadIdx.x & 31) == 0) left[blockIdx.x * 4 + warp] = i;
+}
+extern "C" int run(int late, int rounds, int blocks, int *left) {
+    probe<<<blocks, 160>>>(late, rounds, left);
+    return (int)cudaDeviceSynchronize();
+}
+"""
+
+
+def test_warps_leave_a_barrier_together(tmp_path):
+    """Whenever a flag is raised, all the warps that vote on it leave in the same round: none is left at the
+    next barrier, which has no limit.  (The rounds are limited, so every warp leaves in the end.)"""
+    src, lib = tmp_path / "probe.cu", tmp_path / "probe.so"
+    src.write_text(PROBE)
+    subprocess.run([B._nvcc(), *B.ARCH, *B.FLAGS, "-shared", str(src), "-o", str(lib)], check=True)
+    run = ctypes.CDLL(str(lib)).run
+    run.argtypes = [ctypes.c_int] * 3 + [ctypes.c_void_p]
+    rounds, blocks = 2000, 64
+    seen = set()
+    for late in list(range(0, 4000, 37)) + [1 << 30 >> k for k in range(14, 20)]:
+        left = torch.full((blocks, 4), -1, dtype=torch.int32, device="cuda")
+        assert run(late, rounds, blocks, left.data_ptr()) == 0
+        assert (left >= 0).all() and (left == left[:, :1]).all(), (late, left.tolist())
+        seen.update(left.flatten().tolist())
+    assert len(seen) > 20                        # flags raised in many different rounds
