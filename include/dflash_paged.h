@@ -204,9 +204,7 @@ int paged_gather(const paged_gather_args *args, void *stream);
  *   o = sum_p softmax_p(q . k_p * scale) v_p;  a token that sees nothing gets 0.
  * Products on the tensor cores with float32 accumulation, softmax in float32;
  * probabilities round to the operand type (F16 for quantised pages, whose codes are exact F16
- * operands and whose scales are applied in float32; but for bf16 queries with more than 32 rows
- * per kv head -- max_q * n_head / n_head_kv -- a row's codes times its scale are rounded to F16
- * once, relative to a power of two that keeps scales of any size within F16's range).
+ * operands and whose scales are applied in float32).
  * A sequence whose lengths contradict each other (more new tokens than kv_len or than max_q, a
  * length beyond the block table) is left alone: its rows of o and lse stay as they were.
  *   q, o     rows [n_rows][n_head][head_dim], PAGED_F16 or PAGED_BF16; pages of a 16-bit

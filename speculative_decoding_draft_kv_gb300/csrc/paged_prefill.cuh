@@ -22,15 +22,12 @@
 // odd ones, so that products and exponentials still take turns, and block 0 joins the two states at
 // the end.  A batch with no larger item runs the variant with memory for one block of queries.
 //
-// Quantised pages: four more warps turn code tiles into F16 tiles in shared memory, a thread per key.
-// For F16 queries exactly, with K's scales multiplied on the scores and V's on the probabilities (in
-// units of a power of two), as the streaming kernel does.  For bf16 queries code times scale rounded once
-// to F16, relative to a power of two per tile that the rows' threads put back: 2^-12 of error beside an
-// output that rounds to 2^-9, and F16 tiles in four slots instead of three (the scales take 8 KiB): 213
-// us for the mixed batch below against 247 with exact codes (202 after later steps).  For F16 outputs the rounded rows doubled
-// the relative error (4.3e-4, where the output's own rounding alone is 2.1e-4) and saved
-// nothing (130 us for the trees either way).  bf16 queries are turned to F16 in shared memory, a power
-// of two per row taken out, by the threads that own the rows.
+// Quantised pages: four more warps turn codes into F16 tiles in shared memory, exactly, a thread per key; K's
+// scales are multiplied on the scores and V's on the probabilities, in float32 (V's in units of a power of
+// two), as the streaming kernel does.  Rows of code times scale rounded to F16 would spare the rows'
+// threads three products a score (mixed batch below 202 us), but a row whose scale is 2^-14 of its tile's largest
+// would lose bits, and with F16 outputs they doubled the error.  bf16 queries are turned to F16 in shared
+// memory, a power of two per row taken out, by the threads that own the rows.
 //
 // Measured, 32 query and 8 kv heads: a chunk of 2,048 tokens at the end of 32,768, heads of 128, bf16:
 // 792 us, 1.35 PFLOP/s, the tensor pipe active 62 % of the time (a block's chain S -> softmax -> P -> O
@@ -38,10 +35,11 @@
 // 2.2 GB: 355 us, 6.2 TB/s, bound by memory; two prompts of 4,097 tokens, heads of 64: 214 us, bound by
 // the exponentials and their latency (products are half as long there, exponentials as many); 16 trees
 // of up to 31 nodes over int8: 126 us, and chunks of 1,024 among single tokens, e4m3, window 2,048:
-// 202 us, both bound by the converting warps and the rows' warps sharing the issue slots.
-// What the kernel's parts run at the same time has to fit the instruction cache: over quantised pages the
-// rows' loops are unrolled twice, not eight times (mixed batch 243 -> 213 us, and with exact codes the
-// trees 162 -> 130), over 16-bit pages whole (two prompts: 214 us, 229 unrolled twice).
+// 243 us, where neither memory nor the tensor cores nor the issue slots are full.
+// What the kernel's parts run at the same time has to fit the instruction cache: over quantised pages and one
+// block the rows' loops are unrolled twice, not eight times (trees 162 -> 130 us), else whole (two prompts
+// over 16-bit pages: 214 us, 229 unrolled twice; two blocks over quantised ones: chunk of 619 tokens
+// at 23,810 275 us against 304, but the mixed batch 243 against 230).
 // Tried and not faster: eight converting warps (640 threads), waits that sleep or poll otherwise; one pass
 // over S with the reference moved where needed was slower (914 us for the chunk, where two passes took
 // 793).
@@ -60,30 +58,29 @@ constexpr int kScaleRing = 8;            // key tiles whose scales or units are 
 template <int D, int FMT, int T, bool ONE>
 struct PreCfg {
     static constexpr bool kCodes = FMT != kFmt16;
-    static constexpr bool kExact = kCodes && T == PAGED_F16;     // codes as they are, scales on S and P
     static constexpr int kThreads = kCodes ? 512 : 352;
     // With scales on the scores and two blocks of rows, those are what holds the kernel: their 256 threads
     // take 168 registers, the others 88 (together the 65,536 of the launch, 512 times 128), and pieces of
-    // 32 scores (a chunk of 619 tokens at 23,810, heads of 64, int8: 314 -> 257 us).  One block, or rounded
-    // rows: no gain (trees 130 -> 137 us, mixed batch 207 -> 211).
-    static constexpr bool kMore = kExact && !ONE;
+    // 32 scores (a chunk of 619 tokens at 23,810, heads of 64, int8: 314 -> 257 us).  One block: no gain
+    // (trees 130 -> 137 us).
+    static constexpr bool kMore = kCodes && !ONE;
     static constexpr int kManyRegs = 168, kFewRegs = 88;
     static constexpr int kHalves = D / 64;                       // 128-byte columns of a 16-bit row
     static constexpr int kHalfBytes = kPreTile * 128;
     static constexpr int kSlotBytes = kHalves * kHalfBytes;      // 128 rows of D 16-bit values
     static constexpr int kBlocks = ONE ? 1 : 2;                  // of queries
     // K and V tiles in turn: what fits
-    static constexpr int kSlots = kCodes ? (kExact && D == 128 && !ONE ? 3 : 4) : (D == 128 ? (ONE ? 6 : 5) : 10);
+    static constexpr int kSlots = kCodes ? (D == 128 && !ONE ? 3 : 4) : (D == 128 ? (ONE ? 6 : 5) : 10);
     static constexpr int kCodeBytes = kPreTile * D;
-    static constexpr int kCodeSlots = kCodes ? (D == 128 && !ONE && !kExact ? 2 : 3) : 0;
+    static constexpr int kCodeSlots = kCodes ? 3 : 0;
     static constexpr int kOffQ = kSlots * kSlotBytes;
     static constexpr int kOffCodes = kOffQ + kBlocks * kSlotBytes;
     static constexpr int kOffCodeScale = kOffCodes + kCodeSlots * kCodeBytes;   // as loaded, per code slot
     static constexpr int kOffScale = kOffCodeScale + kCodeSlots * kPreTile * 4;  // [ring][K, V][128]
-    static constexpr int kOffUnit = kOffScale + (kExact ? kScaleRing * 2 * kPreTile * 4 : 0);   // [ring][K, V]
+    static constexpr int kOffUnit = kOffScale + (kCodes ? kScaleRing * 2 * kPreTile * 4 : 0);   // [ring]
     // a dealt item's odd tiles: maxima and sums; its queries' powers of two (in a place of their own: block 0
     // writes those of the next item while its slower warps may still read the sums of this one)
-    static constexpr int kOffOdd = kOffUnit + (kCodes ? kScaleRing * 8 : 0);
+    static constexpr int kOffOdd = kOffUnit + (kCodes ? kScaleRing * 4 : 0);
     static constexpr int kOffExp = kOffOdd + 128 * 8;
     static constexpr int kOffBars = kOffExp + (kCodes && T == PAGED_BF16 ? 128 : 0);
     static constexpr int kOffPlan = kOffBars + 304;                // what else is shared: the plan, then words
@@ -125,7 +122,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ PagedAttendArgs a) {
     using C = PreCfg<D, FMT, T, ONE>;
     constexpr int NS = C::kSlots;
-    constexpr bool kCodes = C::kCodes, kExact = C::kExact;
+    constexpr bool kCodes = C::kCodes;
     constexpr int OT = kCodes ? PAGED_F16 : T;                       // operand type
     constexpr bool kQTurned = kCodes && T == PAGED_BF16;
     constexpr uint32_t kIdescQK = tc_idesc(128, kPreTile, OT == PAGED_BF16, false);
@@ -466,16 +463,14 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     } else if (kCodes && warp >= 12) {
         fewer();
         // ---------------- codes to F16 ----------------
-        // A row is its codes (exact) or its codes times its scale, rounded to F16.  Scales are in units of
-        // a power of two: K's (of rounded rows) for a tile, so that its largest scale is in (1/2, 1], V's
-        // the largest so far of the item, which O is kept in.  Scales of any size fit F16 so.
+        // A row's codes become F16 exactly.  Its scale goes to the rows' threads, K's as it is, V's in units of a
+        // power of two, the largest so far of the item, which O is kept in: scales of any size fit F16 so.
         // The ring of units needs no barrier of its own: the V slot of the tile that the slower
         // block's rows are at is taken, and with it every later one, so with 4 slots the tile at hand
         // here is at most 2 ahead of that one.
         const int r = (int)threadIdx.x - 384;              // the thread's key
-        // 16-byte pieces of a row at a time: all where codes are all there is to it (trees 130 us, 135
-        // two at a time), two where they are scaled (mixed batch 208 us, 213 all)
-        constexpr int kChunks = kExact ? D / 16 : 2;
+        // 16-byte pieces of a row at a time: all of them (trees 130 us, 135 two at a time)
+        constexpr int kChunks = D / 16;
         int slot = 0, cs = 0;
         uint32_t wrap = 0, cwrap = 0;
         int tile = 0;                                      // tiles so far: its place in the ring
@@ -498,9 +493,8 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     const float *scales = reinterpret_cast<const float *>(smem + C::kOffCodeScale) + cs * kPreTile;
                     const bool live = !edge || seen(t * kPreTile + r, any_word);
                     const float own = scales[r];
-                    uint32_t unit = 0x3f800000u;
                     float inv = 1.f;
-                    if (kv || !kExact) {
+                    if (kv) {
                         // the tile's largest finite scale among the rows that count (four to a lane)
                         const float4 four = reinterpret_cast<const float4 *>(scales)[lane];
                         float f[4] = {fabsf(four.x), fabsf(four.y), fabsf(four.z), fabsf(four.w)};
@@ -513,19 +507,13 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                         }
                         const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
                         // the power of two above it, at most 2^127, and its inverse; 0 stays
-                        unit = top ? min((top & 0x7f800000u) + 0x00800000u, 0x7f000000u) : 0u;
-                        if (kv) unit = v_unit = max(v_unit, unit);
-                        else if (!top) unit = 0x3f800000u;
-                        inv = unit == 0 ? 0.f : (unit == 0x7f000000u ? 0x1p-127f : __uint_as_float(0x7f000000u - unit));
+                        const uint32_t unit = top ? min((top & 0x7f800000u) + 0x00800000u, 0x7f000000u) : 0u;
+                        v_unit = max(v_unit, unit);
+                        inv = v_unit == 0 ? 0.f : (v_unit == 0x7f000000u ? 0x1p-127f : __uint_as_float(0x7f000000u - v_unit));
+                        if (warp == 12 && lane == 0) reinterpret_cast<uint32_t *>(smem + C::kOffUnit)[tile % kScaleRing] = v_unit;
                     }
                     const float sc = live ? own * inv : 0.f;
-                    if (warp == 12 && lane == 0)
-                        reinterpret_cast<uint32_t *>(smem + C::kOffUnit)[(tile % kScaleRing) * 2 + kv] = unit;
-                    if constexpr (kExact) reinterpret_cast<float *>(smem + C::kOffScale)[((tile % kScaleRing) * 2 + kv) * kPreTile + r] = sc;
-                    // the scale as a sum of two F16 values, good to 2^-22: code * high + (code * low), one
-                    // fused rounding, is the product's rounding but for an error far below its step
-                    const float high = __half2float(__float2half_rn(sc));
-                    const uint32_t high2 = pack_half2(high, high), low2 = pack_half2(sc - high, sc - high);
+                    reinterpret_cast<float *>(smem + C::kOffScale)[((tile % kScaleRing) * 2 + kv) * kPreTile + r] = sc;
 #pragma unroll 1
                     for (int c0 = 0; c0 < D / 16; c0 += kChunks) {
                         uint4 row[kChunks];                // loads first: stores might be to the same place
@@ -540,16 +528,8 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                             uint32_t y[8];
 #pragma unroll
                             for (int k = 0; k < 8; ++k) {
-                                uint32_t h;
-                                if constexpr (FMT == kFmtInt8) h = int8_pair(xs[k >> 1] ^ 0x80808080u, k & 1 ? 0x7362u : 0x5140u);
-                                else h = e4m3_pair_f16(xs[k >> 1] >> (16 * (k & 1)));
-                                if constexpr (kExact) {
-                                    y[k] = h;
-                                    continue;
-                                }
-                                uint32_t small;
-                                asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(small) : "r"(h), "r"(low2));
-                                asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y[k]) : "r"(h), "r"(high2), "r"(small));
+                                if constexpr (FMT == kFmtInt8) y[k] = int8_pair(xs[k >> 1] ^ 0x80808080u, k & 1 ? 0x7362u : 0x5140u);
+                                else y[k] = e4m3_pair_f16(xs[k >> 1] >> (16 * (k & 1)));
                             }
                             uint8_t *at = dst + (ch >> 2) * C::kHalfBytes;
                             *reinterpret_cast<uint4 *>(at + swz_row<128>(r, (2 * ch) & 7)) = make_uint4(y[0], y[1], y[2], y[3]);
@@ -615,12 +595,13 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             if constexpr (kQTurned) {
                 // This block's queries to F16, unless the other block does it, which then leaves the rows'
                 // powers of two here.  (They stand until every warp has said that this item's queries may
-                // go: the next ones are not looked at before.)
+                // go: the next ones are not looked at before.  Loops not unrolled, for the instruction cache's sake:
+                // two prompts of 4,097 tokens 421 us, 466 whole.)
                 int e = 127;
                 if (my_blk == blk) {
                     uint8_t *qr = smem + C::kOffQ + blk * C::kSlotBytes;
                     uint32_t top = 0;
-#pragma unroll
+#pragma unroll 1
                     for (int ch = 0; ch < D / 8; ++ch) {
                         const uint4 x = *reinterpret_cast<const uint4 *>(qr + (ch >> 3) * C::kHalfBytes + swz_row<128>(r, ch & 7));
                         const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
@@ -629,7 +610,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     }
                     if (top) e = min(254, max(1, (int)(top >> 7)));
                     const float down = e == 254 ? 0x1p-127f : __uint_as_float((uint32_t)(254 - e) << 23);
-#pragma unroll
+#pragma unroll 1
                     for (int ch = 0; ch < D / 8; ++ch) {
                         uint4 *at = reinterpret_cast<uint4 *>(qr + (ch >> 3) * C::kHalfBytes + swz_row<128>(r, ch & 7));
                         const uint4 x = *at;
@@ -681,7 +662,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 const int base = (w.t0 + j) * kPreTile;
                 bool ok = mbar_wait(s_full + 8 * blk, sph);
                 if constexpr (kCodes) {
-                    // the tile's V unit (K's came with S)
+                    // the tile's V scales (K's came with S)
                     const int vn = vslot + 2 * j;
                     ok = ok && mbar_wait(full + 8 * (vn % NS), (uint32_t)(vn / NS) & 1u);
                 }
@@ -693,10 +674,10 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 sph ^= 1u;
                 tc_fence_after();
                 if (busy) {
-                    // quantised: the units of this tile's K and V, and the scales in them
+                    // quantised: the tile's scales, and the unit of V's
                     const int ring = (tile0 + j) % kScaleRing;
-                    float2 unit = make_float2(1.f, 1.f);
-                    if constexpr (kCodes) unit = reinterpret_cast<const float2 *>(smem + C::kOffUnit)[ring];
+                    float unit = 0.f;
+                    if constexpr (kCodes) unit = reinterpret_cast<const float *>(smem + C::kOffUnit)[ring];
                     const float4 *ks4 = reinterpret_cast<const float4 *>(smem + C::kOffScale) + ring * (kPreTile / 2);
                     const float4 *vs4 = ks4 + kPreTile / 4;
                     const bool partly = base < all_lo || base + kPreTile > all_hi;
@@ -739,7 +720,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 #pragma unroll
                         for (int e = 0; e < CH / 2; ++e)
                             s[e] = pk2(__uint_as_float(raw[at][2 * e]), __uint_as_float(raw[at][2 * e + 1]));
-                        if constexpr (kExact) {
+                        if constexpr (kCodes) {
 #pragma unroll
                             for (int e = 0; e < CH / 4; ++e) {
                                 const float4 k = ks4[c * (CH / 4) + e];
@@ -758,12 +739,12 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                         }
                     };
                     float factor = 1.f;                    // what O needs for this tile's reference
-                    if (kCodes && unit.y != vref) {
-                        factor = vref / unit.y;
-                        vref = unit.y;
+                    if (kCodes && unit != vref) {
+                        factor = vref / unit;
+                        vref = unit;
                     }
                     // (never 0, which would make NaN of what the mask leaves out; scores that small are 0)
-                    const float tscale = kCodes ? fmaxf(qscale * unit.x, 0x1p-120f) : qscale;
+                    const float tscale = kCodes ? fmaxf(qscale, 0x1p-120f) : qscale;
                     const uint64_t scale2 = pk2(tscale, tscale);
                     auto tile = [&](auto kind) {
                         constexpr bool masked = kind.value;
@@ -808,7 +789,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                                 uint64_t p2 = pk2(ex2_approx(x), ex2_approx(y));
                                 if (e & 1) sb = add2(sb, p2);
                                 else sa = add2(sa, p2);
-                                if constexpr (kExact) {
+                                if constexpr (kCodes) {
                                     const float4 v = vs4[c * (CH / 4) + e / 2];
                                     p2 = mul2(p2, e & 1 ? pk2(v.z, v.w) : pk2(v.x, v.y));
                                 }
