@@ -20,16 +20,20 @@
 //
 // Quantised pages: codes become F16 operands exactly (int8: byte permutes and a subtraction;
 // e4m3: one conversion), whatever the queries' type; K's scale multiplies the score, V's the
-// probability, relative to a power of two 2^E that follows the largest scale seen, so that
-// the scaled probability stays within F16's range for any scale.  bf16 queries enter as F16
-// after a power of two per row brings the row's largest value to [1, 2): exact but for values
-// 2^-24 below it.
+// probability.  The product of those two becomes an F16 operand in a unit that keeps it in range: the power
+// of two above the largest V scale so far, while none of the item's is below 2^-10 of that, which
+// every row's largest product is then not far below either.  Once one is (a row of zeros too), each row has
+// a unit of its own, which follows the row's largest product: what is lost below F16's smallest step is
+// small beside what counts most, whatever scales the row does not see or gives no weight.  (Units by the
+// row from the start: 4 tokens over int8 338 us instead of 291; one unit for all always: 284.)  bf16
+// queries enter as F16 after a power of two per row brings the row's largest value to [1, 2): exact but
+// for values 2^-17 below it, which are off by 2^-25 of it at most.
 //
 // Measured, bf16, 32 query and 8 kv heads of 128, pages of 16, 64 sequences of 9 to 16,384 tokens
 // (2.2 GB): one token each 353 us, 6.3 TB/s (93 % of the copy rate); 4 tokens (16 rows) 367 us.  With
 // 32 rows it took 382 us, where the products' instructions show, against the tensor-core kernel's 371:
-// 16-bit pages come here with up to 16 rows, quantised ones with up to 32 (4 tokens over int8 286 us, 3.9
-// TB/s; 8 tokens 436 us: turning codes into operands is what counts).  One token over 4,096: 12 us with the
+// 16-bit pages come here with up to 16 rows, quantised ones with up to 32 (4 tokens over int8 291 us, 3.9
+// TB/s; 8 tokens 455 us: turning codes into operands is what counts).  One token over 4,096: 12 us with the
 // join, of which bytes are 2.5: the rest is a chain of lookups (plan, page numbers), one round of
 // copies, the slices' merge and the join.
 #pragma once
@@ -74,6 +78,12 @@ template <int RB>
 __device__ __forceinline__ uint32_t swz_row(int r, int ch) {
     const int x = RB == 128 ? (r & 7) : ((r >> 1) & 3);
     return (uint32_t)(r * RB + ((ch ^ x) << 4));
+}
+
+// the largest of a row's four lanes
+__device__ __forceinline__ float quad_max(float x) {
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
 }
 
 template <int T>
@@ -313,7 +323,10 @@ k_paged_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 #pragma unroll
         for (int n = 0; n < D / 8; ++n) oacc[n][0] = oacc[n][1] = oacc[n][2] = oacc[n][3] = 0.f;
         float mrow[2] = {-INFINITY, -INFINITY}, lrow[2] = {0.f, 0.f};
-        float vref = 0.f;                // quantised: 2^E that the numerators are relative to
+        // quantised: the unit that the numerators are in; far: each row has its own, at most its largest
+        // probability times V scale so far (negative: one from before, which may be above that)
+        float vref[2] = {0.f, 0.f};
+        bool far = false;
         for (int j = 0; j < w.nt; ++j, ++it) {
             const int stg = it % S, base = (w.t0 + j) * kDecTile;
             if (!__all_sync(0xffffffffu, mbar_wait(bar0 + 8 * stg, (uint32_t)(it / S) & 1u))) {
@@ -427,6 +440,10 @@ k_paged_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                     alpha[jj] = mnew == -INFINITY ? 1.f : exp2f(mrow[jj] - mnew);
                     mrow[jj] = mnew;
                     lrow[jj] *= alpha[jj];
+                    if (FMT != kFmt16 && far) {          // the unit moves in the numerators' place
+                        vref[jj] *= alpha[jj];
+                        alpha[jj] = 1.f;
+                    }
                 }
 #pragma unroll
                 for (int n = 0; n < D / 8; ++n) {
@@ -455,37 +472,82 @@ k_paged_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             if constexpr (FMT != kFmt16) {
                 const float *vscale = reinterpret_cast<const float *>(smem + C::kOffScale + stg * C::kScaleBytes) + kDecTile;
                 float2 f[C::kNT];
-                uint32_t top = 0;
+                float top = 0.f, low = INFINITY;         // largest and smallest of this lane's scales (NaN is passed over)
 #pragma unroll
-                for (int n = 0; n < C::kNT; ++n) {
-                    f[n] = *reinterpret_cast<const float2 *>(vscale + key0 + n * 8 + 2 * c);
-                    if (ragged) {
+                for (int n = 0; n < C::kNT; ++n) f[n] = *reinterpret_cast<const float2 *>(vscale + key0 + n * 8 + 2 * c);
+                if (ragged) {
+#pragma unroll
+                    for (int n = 0; n < C::kNT; ++n) {
                         const int p = base + key0 + n * 8 + 2 * c;
-                        if (!seen_by_any(p)) f[n].x = 0.f;
-                        if (!seen_by_any(p + 1)) f[n].y = 0.f;
+                        if (seen_by_any(p)) low = fminf(low, fabsf(f[n].x));
+                        else f[n].x = 0.f;
+                        if (seen_by_any(p + 1)) low = fminf(low, fabsf(f[n].y));
+                        else f[n].y = 0.f;
                     }
-                    const uint32_t u0 = __float_as_uint(f[n].x) & 0x7fffffffu, u1 = __float_as_uint(f[n].y) & 0x7fffffffu;
-                    top = max(top, max(u0 < 0x7f800000u ? u0 : 0u, u1 < 0x7f800000u ? u1 : 0u));
-                }
-                top = __reduce_max_sync(0xffffffffu, top);
-                if (__uint_as_float(top) > vref) {
-                    // the next power of two (the exponent field plus one, at most 2^127)
-                    const float vnew = __uint_as_float(min((top & 0x7f800000u) + 0x00800000u, 0x7f000000u));
-                    const float r = vref / vnew;
-                    vref = vnew;
+                } else {
 #pragma unroll
-                    for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) oacc[n][e] *= r;
+                    for (int n = 0; n < C::kNT; ++n) low = fminf(low, fminf(fabsf(f[n].x), fabsf(f[n].y)));
                 }
-                const float inv = vref > 0.f ? 1.f / vref : 0.f;
+                float inv[2];
+                if (!far) {
+#pragma unroll
+                    for (int n = 0; n < C::kNT; ++n) top = fmaxf(top, fmaxf(fabsf(f[n].x), fabsf(f[n].y)));
+                    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+                    const bool apart = low < fmaxf(top, vref[0]) * 0x1p-10f;      // (also with an infinity among them)
+                    if (__any_sync(0xffffffffu, apart || top > vref[0])) {
+                        far = __any_sync(0xffffffffu, apart);
+                        // the next power of two (the exponent field plus one, at most 2^127)
+                        const float vnew = fmaxf(vref[0], __uint_as_float(min((__float_as_uint(top) & 0x7f800000u) + 0x00800000u, 0x7f000000u)));
+                        const float r = far ? 1.f : vref[0] / vnew;
+                        vref[0] = vref[1] = far ? -vref[0] : vnew;
+#pragma unroll
+                        for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) oacc[n][e] *= r;
+                    }
+                }
+                if (far) {
+#pragma unroll
+                    for (int jj = 0; jj < 2; ++jj) {
+                        float wt = 0.f, omax = 0.f;
+#pragma unroll
+                        for (int n = 0; n < C::kNT; ++n) {
+                            sc[n][2 * jj] *= f[n].x;
+                            sc[n][2 * jj + 1] *= f[n].y;
+                            wt = fmaxf(wt, fmaxf(fabsf(sc[n][2 * jj]), fabsf(sc[n][2 * jj + 1])));
+                        }
+                        wt = fminf(quad_max(wt), 0x1p126f);
+                        // (a unit that followed the reference's moves below F32's smallest is set anew too)
+                        const bool move = wt > 0.f && (wt > 1024.f * vref[jj] || vref[jj] < 0x1p-126f);
+                        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                            for (int n = 0; n < D / 8; ++n) omax = fmaxf(omax, fmaxf(fabsf(oacc[n][2 * jj]), fabsf(oacc[n][2 * jj + 1])));
+                            omax = quad_max(omax);
+                            // 2^-60 of the numerators is less than any product in them, and keeps them in range
+                            const float vold = fabsf(vref[jj]);
+                            const float vnew = move ? fmaxf(fmaxf(wt, 0x1p-126f), fminf(omax * vold, 0x1p126f) * 0x1p-60f) : vref[jj];
+                            if (move) {
+                                vref[jj] = vnew;
+#pragma unroll
+                                for (int n = 0; n < D / 8; ++n) {
+                                    oacc[n][2 * jj] = oacc[n][2 * jj] * vold * (1.f / vnew);
+                                    oacc[n][2 * jj + 1] = oacc[n][2 * jj + 1] * vold * (1.f / vnew);
+                                }
+                            }
+                        }
+                        inv[jj] = vref[jj] >= 0x1p-126f ? 1.f / vref[jj] : 0.f;
+                    }
+#pragma unroll
+                    for (int n = 0; n < C::kNT; ++n) f[n] = make_float2(1.f, 1.f);
+                } else {
+                    inv[0] = inv[1] = vref[0] > 0.f ? 1.f / vref[0] : 0.f;
+                }
 #pragma unroll
                 for (int n = 0; n < C::kNT; ++n) {
-                    const float fx = f[n].x * inv, fy = f[n].y * inv;
-                    sc[n][0] *= fx;
-                    sc[n][1] *= fy;
-                    sc[n][2] *= fx;
-                    sc[n][3] *= fy;
+                    sc[n][0] *= f[n].x * inv[0];
+                    sc[n][1] *= f[n].y * inv[0];
+                    sc[n][2] *= f[n].x * inv[1];
+                    sc[n][3] *= f[n].y * inv[1];
                 }
             }
 #pragma unroll
@@ -569,7 +631,7 @@ k_paged_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 L[jj] += x.x == -INFINITY ? x.y : x.y * exp2f(x.x - M[jj]);   // x.y: 0, or NaN
             }
             float f = mrow[jj] == -INFINITY ? 0.f : exp2f(mrow[jj] - M[jj]);
-            if constexpr (FMT != kFmt16) f *= vref;
+            if constexpr (FMT != kFmt16) f *= fabsf(vref[jj]);
 #pragma unroll
             for (int n = 0; n < D / 8; ++n) {
                 oacc[n][2 * jj] *= f;

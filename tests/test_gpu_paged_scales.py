@@ -13,7 +13,7 @@ pytestmark = pytest.mark.gpu
 
 #: A probability times its V scale is an F16 value in a unit of the row's own, at most this many times the
 #: largest such product of the row.
-UNIT_ABOVE_WEIGHT = 2.0 ** 8
+UNIT_ABOVE_WEIGHT = 2.0 ** 11
 
 
 def rescale(w, s, which, factor):
@@ -27,17 +27,18 @@ def rescale(w, s, which, factor):
     true[s] = true[s] * (new.double() / old.double())[..., None]
 
 
-def put_key(w, s, positions, direction, length):
-    """K rows of some positions along direction [kv_heads, dim], of scale-free length `length`."""
+def put_keys(w, s, positions, direction, lengths):
+    """K rows of some positions along direction [kv_heads, dim], each of its (signed) length."""
+    p, size = torch.as_tensor(positions, device="cuda"), torch.as_tensor(lengths, dtype=torch.float64, device="cuda")
     x = direction / direction.abs().amax(-1, keepdim=True) * 100
-    codes = x.round() if w.store == torch.int8 else x.to(w.store).float()
-    for p in positions:
-        page, slot = int(w.pages[s, p // w.page]), p % w.page
-        size = codes.double().square().sum(-1).sqrt()
-        scale = (length[p] / size).float()
-        w.k.view(torch.uint8)[page, :, slot] = codes.to(w.store).view(torch.uint8)
-        w.ks[page, :, slot] = scale
-        w.K[s][p] = codes.double() * scale.double()[:, None]
+    x = x[None] * torch.where(size < 0, -1.0, 1.0)[:, None, None]
+    codes = (x.round() if w.store == torch.int8 else x.float()).to(w.store)
+    value = codes.double()
+    scale = (size.abs()[:, None] / value.square().sum(-1).sqrt()).float()
+    page, slot = w.pages[s][p // w.page].long(), p % w.page
+    w.k.view(torch.uint8)[page, :, slot] = codes.view(torch.uint8)
+    w.ks[page, :, slot] = scale
+    w.K[s][p] = value * scale.double()[..., None]
 
 
 def queries(w, spread=0.02):
@@ -67,7 +68,7 @@ def check(w, q, mask="causal", window=0, tree=None):
         at = torch.arange(kv, device="cuda")
         vs = w.vs[w.pages[s][at // w.page].long(), :, at % w.page].double().abs().repeat_interleave(group, 1)     # [kv, heads]
         k, v = w.K[s].repeat_interleave(group, 1), w.V[s].repeat_interleave(group, 1)
-        code = v.abs() / vs[..., None]
+        code = torch.where(vs[..., None] > 0, v.abs() / vs[..., None], 0.0)
         x = q[r].double()
         z = torch.einsum("ihd,phd->hip", x, k) / math.sqrt(w.dim)
         z = z.masked_fill(w.hidden(s, mask, window, tree)[None], -math.inf)
@@ -109,5 +110,103 @@ def test_large_k_scales_out_of_sight(fmt, dtype, dim, n, power):
             f[-1] = 2.0 ** min(power, 20)
             rescale(w, s, "k", f)
         if kv > 100:
-            put_key(w, s, [5], -base, {5: 2.0 ** power})
+            put_keys(w, s, [5], base, [-(2.0 ** power)])
+    check(w, q)
+
+
+FEW = [3]
+
+
+def clamp_power(w, power):
+    """F16 outputs reach 65,504 only: what lies so far above the others lies as far below 2^12."""
+    return 2.0 ** (min(0, 12 - power) if w.dtype == torch.float16 else 0)
+
+
+@pytest.mark.parametrize("fmt,dtype", CODED)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("n", FEW)
+@pytest.mark.parametrize("power", [14, 20, 30, 100])
+@pytest.mark.parametrize("where", ["first", "middle"])
+def test_large_v_scales_without_weight(fmt, dtype, dim, n, power, where):
+    """Seen by every row, but with a score far below all others (e^-100)."""
+    w = World([(n, 500), (1, 70), (n, n + 3)], fmt=fmt, dtype=dtype, dim=dim, seed=power + n)
+    q, base = queries(w)
+    for s, (m, kv) in enumerate(w.lens):
+        at = 0 if where == "first" else kv // 2
+        put_keys(w, s, [at], base, [-100.0])
+        f = torch.ones(kv, w.kv_heads, device="cuda")
+        f[at] = 2.0 ** power
+        rescale(w, s, "v", f * clamp_power(w, power if power < 100 else 0))
+    check(w, q)
+
+
+@pytest.mark.parametrize("fmt,dtype", CODED)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("n", FEW)
+@pytest.mark.parametrize("power", [14, 20, 30, 100])
+def test_large_v_scales_out_of_sight(fmt, dtype, dim, n, power):
+    """The batch's last tokens', which the ones before them do not see, in their tile."""
+    w = World([(n, 500), (n, 130), (n, n)], fmt=fmt, dtype=dtype, dim=dim, seed=power + n)
+    q, _ = queries(w)
+    for s, (m, kv) in enumerate(w.lens):
+        f = torch.ones(kv, w.kv_heads, device="cuda")
+        f[-1] = 2.0 ** power
+        f[-2, 0] = 2.0 ** -power
+        rescale(w, s, "v", f)
+    check(w, q)
+    tree = torch.zeros(w.rows, dtype=torch.int64, device="cuda")
+    for s, (m, _) in enumerate(w.lens):
+        for i in range(m):
+            tree[int(w.q_start[s]) + i] = (1 << i) | (1 << max(0, i - 2))
+    check(w, q, "tree", tree=tree)
+
+
+@pytest.mark.parametrize("fmt,dtype", CODED)
+@pytest.mark.parametrize("n", FEW)
+@pytest.mark.parametrize("window", [0, 200])
+def test_v_scales_of_all_sizes(fmt, dtype, n, window):
+    """Forty powers of two up and down at random: what is largest counts most, the rest is small beside it."""
+    w = World([(n, 700), (1, 300), (n, n)], fmt=fmt, dtype=dtype, seed=n)
+    q, _ = queries(w, 1.0)
+    for s, (m, kv) in enumerate(w.lens):
+        up = torch.empty(kv, w.kv_heads, device="cuda").uniform_(-40, 40 if dtype == "bf16" else 10, generator=w.g)
+        rescale(w, s, "v", torch.exp2(up))
+    check(w, q, window=window)
+
+
+@pytest.mark.parametrize("fmt,dtype", CODED)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("n", FEW)
+@pytest.mark.parametrize("rise,fall", [(0.3, 0.12), (0.3, -0.1), (-0.3, -0.12), (-0.3, 0.1), (1.5, 0.2)])
+def test_weights_that_move(fmt, dtype, dim, n, rise, fall):
+    """Scores that rise or fall along the sequence while V scales fall or rise, so that the largest product
+    and the largest scale are in different places, and either moves from tile to tile."""
+    w = World([(n, 600), (n, 150)], fmt=fmt, dtype=dtype, dim=dim, seed=5 + n)
+    q, base = queries(w, 0.001)
+    for s, (m, kv) in enumerate(w.lens):
+        p = torch.arange(kv, device="cuda")
+        score = rise * (p - kv)                       # natural units
+        put_keys(w, s, p, base, score)
+        up = -fall * p
+        if dtype == "f16":                            # the largest near 1
+            up = up - up.max()
+        rescale(w, s, "v", torch.exp2(up)[:, None].expand(kv, w.kv_heads))
+    check(w, q)
+
+
+@pytest.mark.parametrize("fmt,dtype", CODED)
+@pytest.mark.parametrize("n", FEW)
+def test_v_rows_of_zeros_among_others(fmt, dtype, n):
+    """Scales of 0 (rows below 1e-30) with nearly all the weight, and negative ones."""
+    w = World([(n, 300), (1, 40)], fmt=fmt, dtype=dtype, seed=n)
+    q, base = queries(w)
+    for s, (m, kv) in enumerate(w.lens):
+        f = torch.ones(kv, w.kv_heads, device="cuda")
+        f[kv // 2::3] *= -1
+        rescale(w, s, "v", f)
+        zero = [0, kv // 3]
+        put_keys(w, s, zero, base, [12.0, 12.0])
+        page = w.pages[s][torch.tensor(zero, device="cuda") // w.page].long()
+        w.vs[page, :, torch.tensor(zero, device="cuda") % w.page] = 0.0
+        w.V[s][zero] = 0.0
     check(w, q)
