@@ -326,6 +326,7 @@ k_paged_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         // quantised: the unit that the numerators are in; far: each row has its own, at most its largest
         // probability times V scale so far (negative: one from before, which may be above that)
         float vref[2] = {0.f, 0.f};
+        float low = INFINITY;            // the smallest of the V scales that this lane has met
         bool far = false;
         for (int j = 0; j < w.nt; ++j, ++it) {
             const int stg = it % S, base = (w.t0 + j) * kDecTile;
@@ -472,7 +473,7 @@ k_paged_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             if constexpr (FMT != kFmt16) {
                 const float *vscale = reinterpret_cast<const float *>(smem + C::kOffScale + stg * C::kScaleBytes) + kDecTile;
                 float2 f[C::kNT];
-                float top = 0.f, low = INFINITY;         // largest and smallest of this lane's scales (NaN is passed over)
+                float top = 0.f;                         // the tile's largest (NaN is passed over)
 #pragma unroll
                 for (int n = 0; n < C::kNT; ++n) f[n] = *reinterpret_cast<const float2 *>(vscale + key0 + n * 8 + 2 * c);
                 if (ragged) {
@@ -493,7 +494,7 @@ k_paged_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 #pragma unroll
                     for (int n = 0; n < C::kNT; ++n) top = fmaxf(top, fmaxf(fabsf(f[n].x), fabsf(f[n].y)));
                     top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-                    const bool apart = low < fmaxf(top, vref[0]) * 0x1p-10f;      // (also with an infinity among them)
+                    const bool apart = low < fmaxf(top, vref[0]) * 0x1p-10f;         // (also with an infinity among them)
                     if (__any_sync(0xffffffffu, apart || top > vref[0])) {
                         far = __any_sync(0xffffffffu, apart);
                         // the next power of two (the exponent field plus one, at most 2^127)

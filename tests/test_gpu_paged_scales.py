@@ -210,3 +210,21 @@ def test_v_rows_of_zeros_among_others(fmt, dtype, n):
         w.vs[page, :, torch.tensor(zero, device="cuda") % w.page] = 0.0
         w.V[s][zero] = 0.0
     check(w, q)
+
+
+@pytest.mark.parametrize("fmt,dtype", CODED)
+@pytest.mark.parametrize("n", FEW)
+@pytest.mark.parametrize("block", [64, 128, 256])
+@pytest.mark.parametrize("first", [0, 1])
+def test_v_scales_by_the_tile(fmt, dtype, n, block, first):
+    """Whole tiles of scales 2^20 above the others', with a 2^-24th of their weight: neither kind has far
+    scales among its own, and both count."""
+    w = World([(n, 1100), (1, 600)], fmt=fmt, dtype=dtype, seed=block + n)
+    q, base = queries(w, 0.001)
+    for s, (m, kv) in enumerate(w.lens):
+        p = torch.arange(kv, device="cuda")
+        large = p // block % 2 == first
+        put_keys(w, s, p, base, torch.where(large, -24 * math.log(2.0), 0.1))
+        up = torch.where(large, 20.0, 0.0) - (12.0 if dtype == "f16" else 0.0)
+        rescale(w, s, "v", torch.exp2(up)[:, None].expand(kv, w.kv_heads))
+    check(w, q)
