@@ -203,8 +203,11 @@ int paged_gather(const paged_gather_args *args, void *stream);
  * Per query head h (kv head h / (n_head / n_head_kv)):
  *   o = sum_p softmax_p(q . k_p * scale) v_p;  a token that sees nothing gets 0.
  * Products on the tensor cores with float32 accumulation, softmax in float32;
- * probabilities round to the operand type (F16 for quantised pages, whose codes are exact F16
- * operands and whose scales are applied in float32).
+ * probabilities round to the operand type.  Quantised pages: codes are exact F16 operands and K's
+ * scales multiply the scores in float32; a probability times its V scale rounds to F16, off by 2^-11 of
+ * itself or by 2^-15 of the row's largest such product, whichever is more (scales that the row does not
+ * see, or gives no weight, take nothing from it, up to 2^100 above the others).  Scores (q . k * scale)
+ * above some 10^7 are beyond float32's steps, and the output may be NaN there.
  * A sequence whose lengths contradict each other (more new tokens than kv_len or than max_q, a
  * length beyond the block table) is left alone: its rows of o and lse stay as they were.
  *   q, o     rows [n_rows][n_head][head_dim], PAGED_F16 or PAGED_BF16; pages of a 16-bit

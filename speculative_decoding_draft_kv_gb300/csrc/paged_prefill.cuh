@@ -23,8 +23,8 @@
 // the end.  A batch with no larger item runs the variant with memory for one block of queries.
 //
 // Quantised pages: four more warps turn codes into F16 tiles in shared memory, exactly, a thread per key; K's
-// scales are multiplied on the scores and V's on the probabilities, in float32 (V's in units of a power of
-// two), as the streaming kernel does.  Rows of code times scale rounded to F16 would spare the rows'
+// scales are multiplied on the scores and V's on the probabilities, in float32, as the streaming kernel does,
+// with units that the F16 products are in: common ones, then the rows' own (apart_tile).  Rows of code times scale rounded to F16 would spare the rows'
 // threads three products a score (mixed batch below 202 us), but a row whose scale is 2^-14 of its tile's largest
 // would lose bits, and with F16 outputs they doubled the error.  bf16 queries are turned to F16 in shared
 // memory, a power of two per row taken out, by the threads that own the rows.
@@ -35,11 +35,12 @@
 // 2.2 GB: 355 us, 6.2 TB/s, bound by memory; two prompts of 4,097 tokens, heads of 64: 214 us, bound by
 // the exponentials and their latency (products are half as long there, exponentials as many); 16 trees
 // of up to 31 nodes over int8: 126 us, and chunks of 1,024 among single tokens, e4m3, window 2,048:
-// 243 us, where neither memory nor the tensor cores nor the issue slots are full.
+// 237 us, where neither memory nor the tensor cores nor the issue slots are full.
 // What the kernel's parts run at the same time has to fit the instruction cache: over quantised pages and one
-// block the rows' loops are unrolled twice, not eight times (trees 162 -> 130 us), else whole (two prompts
-// over 16-bit pages: 214 us, 229 unrolled twice; two blocks over quantised ones: chunk of 619 tokens
-// at 23,810 275 us against 304, but the mixed batch 243 against 230).
+// block the rows' loops are unrolled twice, not eight times (trees 162 -> 130 us), over 16-bit pages whole (two
+// prompts: 214 us, 229 unrolled twice).  Two blocks over quantised pages lie between: F16 queries whole (a
+// chunk of 619 tokens at 23,810 281 us, the second loop unrolled twice 297; the mixed batch 243 and 232), bf16
+// ones with the second loop unrolled twice (mixed batch 237 us, whole 256; chunk 296 and 285).
 // Tried and not faster: eight converting warps (640 threads), waits that sleep or poll otherwise; one pass
 // over S with the reference moved where needed was slower (914 us for the chunk, where two passes took
 // 793).
@@ -114,6 +115,114 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
+}
+
+// What a row sees: positions [lo, hi) and, for a tree, bits of its word from ctx on, below kv.
+struct RowSight {
+    int lo, hi, ctx, kv;
+    bool tree;
+    uint64_t word;
+
+    // bit e: position p + e
+    __device__ __forceinline__ uint32_t bits(int p) const {
+        // positions below x of the 32 from p on
+        auto below = [&](int x) { return x - p >= 32 ? ~0u : (x <= p ? 0u : (1u << (x - p)) - 1u); };
+        uint32_t b = below(hi) & ~below(lo);
+        if (tree) {
+            const int at = p - ctx;                        // the word's bit that p is
+            const uint32_t nodes = at >= 64 ? 0u : (at >= 0 ? (uint32_t)(word >> at) : (at > -32 ? (uint32_t)word << -at : 0u));
+            b |= nodes & below(kv);
+        }
+        return b;
+    }
+};
+
+// A row's numerators (dim columns from `to` on) times a factor.
+__device__ __forceinline__ void scale_numerators(uint32_t to, int dim, float by) {
+#pragma unroll 1
+    for (int c = 0; c < dim; c += 16) {
+        uint32_t u[16];
+        tmem_ld16(to + c, u);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * by);
+        tmem_st16(to + c, u);
+    }
+}
+
+// A row's tile over quantised pages where the item's V scales are far apart: its scores (ts) to probabilities
+// times V scales, as F16 values in a unit of the row's own.  The unit is at most the row's largest such
+// product, and not below 2^-10 of that: what is lost below F16's smallest step is small beside what counts
+// most, whatever scales the row does not see or gives no weight.  When the reference m moves the unit moves
+// with it and O stays.  (m, l, vref) before and after; vref: the unit, with a minus sign.  Rare, and in a loop of
+// its own, so that it takes no room between the loops that are not (there it cost two blocks 5 to 20 %).
+__device__ __forceinline__ float3 apart_tile(uint32_t ts, uint32_t to, int dim, bool more, RowSight sight, int base, const float4 *ks4,
+                                          float tscale, bool valid, float m, float l, float vref) {
+    const float4 *vs4 = ks4 + kPreTile / 4;
+    // fn(piece of 16, scores, masked by -inf, V scales)
+    auto pieces = [&](auto &&fn) {
+#pragma unroll 1
+        for (int c = 0; c < kPreTile / 16; ++c) {
+            uint32_t u[16];
+            tmem_ld16(ts + 16 * c, u);
+            tmem_ld_wait();
+            const uint32_t bits = sight.bits(base + 16 * c);
+            float x[16], v[16];
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                const float4 k = ks4[4 * c + e / 4], w = vs4[4 * c + e / 4];
+                x[e] = __uint_as_float(u[e]) * k.x;
+                x[e + 1] = __uint_as_float(u[e + 1]) * k.y;
+                x[e + 2] = __uint_as_float(u[e + 2]) * k.z;
+                x[e + 3] = __uint_as_float(u[e + 3]) * k.w;
+                v[e] = w.x; v[e + 1] = w.y; v[e + 2] = w.z; v[e + 3] = w.w;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = bits & (1u << e) ? x[e] : -INFINITY;
+            fn(c, x, v);
+        }
+    };
+    float mx = -INFINITY;
+    pieces([&](int, const float (&x)[16], const float (&)[16]) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) mx = fmaxf(mx, x[e]);
+    });
+    mx *= tscale;
+    float unit = fabsf(vref);
+    if (valid && mx > m + kLazyMove) {
+        const float alpha = exp2f(m - mx);
+        m = mx;
+        l *= alpha;
+        unit *= alpha;                                     // in place of O
+    }
+    const float mu = m == -INFINITY ? 0.f : m;
+    float wt = 0.f;                                        // the tile's largest product (NaN is passed over)
+    pieces([&](int, const float (&x)[16], const float (&v)[16]) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) wt = fmaxf(wt, fabsf(ex2_approx(fmaf(x[e], tscale, -mu)) * v[e]));
+    });
+    wt = fminf(wt, 0x1p126f);
+    // A unit from before, common to the item's rows: no scale was below 2^-10 of it then, so the row's largest
+    // product was not either, if it has seen any.
+    const bool first = !signbit(vref);
+    const float least = !first ? unit : (l > 0.f ? unit * 0x1p-10f : 0.f);
+    float now = least;
+    if (wt > 0.f && (first || wt > 1024.f * least || least < 0x1p-126f)) now = fmaxf(fmaxf(wt, least), 0x1p-126f);
+    const float by = now > 0.f ? (first && !(l > 0.f) ? 0.f : unit / now) : 1.f;
+    if (more && __any_sync(0xffffffffu, by != 1.f)) scale_numerators(to, dim, by);
+    const float inv = now >= 0x1p-126f ? 1.f / now : 0.f;
+    float sum = 0.f;
+    pieces([&](int c, const float (&x)[16], const float (&v)[16]) {
+        uint32_t u[8];
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+            const float p0 = ex2_approx(fmaf(x[e], tscale, -mu)), p1 = ex2_approx(fmaf(x[e + 1], tscale, -mu));
+            sum += p0 + p1;
+            u[e / 2] = pack_half2(p0 * v[e] * inv, p1 * v[e + 1] * inv);
+        }
+        tmem_st(ts + 8 * c, u);                            // over scores that have been read
+    });
+    return make_float3(m, l + sum, -now);
 }
 
 template <int D, int FMT, int T, bool ONE>
@@ -464,7 +573,8 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         fewer();
         // ---------------- codes to F16 ----------------
         // A row's codes become F16 exactly.  Its scale goes to the rows' threads, K's as it is, V's in units of a
-        // power of two, the largest so far of the item, which O is kept in: scales of any size fit F16 so.
+        // power of two, the largest so far of the item, which O is kept in.  Once the item has a V scale below
+        // 2^-10 of that (a row of zeros too), V's go as they are, and the unit as -1: see apart_tile.
         // The ring of units needs no barrier of its own: the V slot of the tile that the slower
         // block's rows are at is taken, and with it every later one, so with 4 slots the tile at hand
         // here is at most 2 ahead of that one.
@@ -478,9 +588,15 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         while (alive && w.next(a)) {
             const uint64_t any_word = tree_union();
             uint32_t v_unit = 0;
+            float v_low = INFINITY;                        // the smallest of the V scales that this lane has met
+            bool far = false;
             for (int j = 0; j < w.nt && alive; ++j, ++tile) {
                 const int t = w.t0 + j;
-                const bool edge = ragged(t);
+                // positions that no row of the item sees (some lie in pages that were not fetched for it) count
+                // for nothing
+                const int lo = w.sh.lo(a, w.rt), hi = w.sh.hi(a, w.rt);
+                const bool edge = t * kPreTile < lo || (t + 1) * kPreTile > hi || ragged(t);
+                auto counts = [&](int p) { return p >= lo && p < hi && seen(p, any_word); };
                 for (int kv = 0; kv < 2; ++kv) {
                     const bool ok = mbar_wait(c_full + 8 * cs, cwrap) && mbar_wait(empty + 8 * slot, wrap ^ 1u);
                     if (!__all_sync(0xffffffffu, ok && !s_abort)) {
@@ -491,26 +607,33 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     const uint8_t *src = smem + C::kOffCodes + cs * C::kCodeBytes;
                     uint8_t *dst = smem + slot * C::kSlotBytes;
                     const float *scales = reinterpret_cast<const float *>(smem + C::kOffCodeScale) + cs * kPreTile;
-                    const bool live = !edge || seen(t * kPreTile + r, any_word);
+                    const bool live = !edge || counts(t * kPreTile + r);
                     const float own = scales[r];
                     float inv = 1.f;
                     if (kv) {
-                        // the tile's largest finite scale among the rows that count (four to a lane)
+                        // the tile's largest and smallest scale among the rows that count (four to a lane)
                         const float4 four = reinterpret_cast<const float4 *>(scales)[lane];
-                        float f[4] = {fabsf(four.x), fabsf(four.y), fabsf(four.z), fabsf(four.w)};
+                        const float f[4] = {fabsf(four.x), fabsf(four.y), fabsf(four.z), fabsf(four.w)};
                         float most = fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3]));           // NaN is passed over
-                        if (edge || most == INFINITY) {
+                        if (!edge) {
+                            v_low = fminf(v_low, fminf(fminf(f[0], f[1]), fminf(f[2], f[3])));
+                        } else {
                             most = 0.f;
-#pragma unroll
+#pragma unroll 1
                             for (int i = 0; i < 4; ++i)
-                                if (f[i] < INFINITY && (!edge || seen(t * kPreTile + 4 * lane + i, any_word))) most = fmaxf(most, f[i]);
+                                if (counts(t * kPreTile + 4 * lane + i)) {
+                                    const float x = fabsf(scales[4 * lane + i]);
+                                    most = fmaxf(most, x);
+                                    v_low = fminf(v_low, x);
+                                }
                         }
                         const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
                         // the power of two above it, at most 2^127, and its inverse; 0 stays
-                        const uint32_t unit = top ? min((top & 0x7f800000u) + 0x00800000u, 0x7f000000u) : 0u;
-                        v_unit = max(v_unit, unit);
-                        inv = v_unit == 0 ? 0.f : (v_unit == 0x7f000000u ? 0x1p-127f : __uint_as_float(0x7f000000u - v_unit));
-                        if (warp == 12 && lane == 0) reinterpret_cast<uint32_t *>(smem + C::kOffUnit)[tile % kScaleRing] = v_unit;
+                        v_unit = max(v_unit, top ? min((top & 0x7f800000u) + 0x00800000u, 0x7f000000u) : 0u);
+                        far = __any_sync(0xffffffffu, far || v_low < __uint_as_float(v_unit) * 0x1p-10f);
+                        if (!far) inv = v_unit == 0 ? 0.f : (v_unit == 0x7f000000u ? 0x1p-127f : __uint_as_float(0x7f000000u - v_unit));
+                        if (warp == 12 && lane == 0)
+                            reinterpret_cast<float *>(smem + C::kOffUnit)[tile % kScaleRing] = far ? -1.f : __uint_as_float(v_unit);
                     }
                     const float sc = live ? own * inv : 0.f;
                     reinterpret_cast<float *>(smem + C::kOffScale)[((tile % kScaleRing) * 2 + kv) * kPreTile + r] = sc;
@@ -655,11 +778,10 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             }
             const int all_lo = __reduce_max_sync(0xffffffffu, valid ? rlo : 0);
             const int all_hi = __reduce_min_sync(0xffffffffu, valid ? rhi : 0x7fffffff);
-            float m = -INFINITY, l = 0.f, vref = 0.f;
+            float m = -INFINITY, l = 0.f, vref = 0.f;      // vref: the unit that O is in
             bool alive = true;
             const int j0 = deal ? blk : 0, dj = deal ? 2 : 1;
-            for (int j = j0; j < w.nt; j += dj) {
-                const int base = (w.t0 + j) * kPreTile;
+            auto wait_scores = [&](int j) {
                 bool ok = mbar_wait(s_full + 8 * blk, sph);
                 if constexpr (kCodes) {
                     // the tile's V scales (K's came with S)
@@ -669,15 +791,32 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 if (!__all_sync(0xffffffffu, ok)) {
                     if (lane == 0) timed_out();
                     alive = false;
-                    break;
+                    return;
                 }
                 sph ^= 1u;
                 tc_fence_after();
+            };
+            auto hand_over = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + 8 * blk);
+            };
+            const RowSight sight{rlo, rhi, w.sh.ctx, q.kv, a.mask == PAGED_TREE, word};
+            // (never 0, which would make NaN of what the mask leaves out; scores that small are 0)
+            const float tscale = kCodes ? fmaxf(qscale, 0x1p-120f) : qscale;
+            int j = j0;
+            for (; j < w.nt; j += dj) {
+                const int base = (w.t0 + j) * kPreTile;
+                wait_scores(j);
+                if (!alive) break;
                 if (busy) {
                     // quantised: the tile's scales, and the unit of V's
                     const int ring = (tile0 + j) % kScaleRing;
                     float unit = 0.f;
-                    if constexpr (kCodes) unit = reinterpret_cast<const float *>(smem + C::kOffUnit)[ring];
+                    if constexpr (kCodes) {
+                        unit = reinterpret_cast<const float *>(smem + C::kOffUnit)[ring];
+                        if (unit < 0.f) break;             // from here on V scales are far apart: below
+                    }
                     const float4 *ks4 = reinterpret_cast<const float4 *>(smem + C::kOffScale) + ring * (kPreTile / 2);
                     const float4 *vs4 = ks4 + kPreTile / 4;
                     const bool partly = base < all_lo || base + kPreTile > all_hi;
@@ -696,17 +835,6 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     // The row twice, CH scores at a time: its maximum, then, against a reference that
                     // is settled, its probabilities, without a branch to hold up the exponentials.
                     // bit e: the row sees position p + e
-                    auto seen_bits = [&](int p) {
-                        // positions below x of the 32 from p on
-                        auto below = [&](int x) { return x - p >= 32 ? ~0u : (x <= p ? 0u : (1u << (x - p)) - 1u); };
-                        uint32_t bits = below(rhi) & ~below(rlo);
-                        if (a.mask == PAGED_TREE) {
-                            const int at = p - ctx;        // the word's bit that p is
-                            const uint32_t tree = at >= 64 ? 0u : (at >= 0 ? (uint32_t)(word >> at) : (at > -32 ? (uint32_t)word << -at : 0u));
-                            bits |= tree & below(q.kv);
-                        }
-                        return bits;
-                    };
                     uint32_t raw[2][CH];                   // the piece at hand and, with registers to spare, the next
                     auto begin = [&]() {
                         tmem_ld(ts, raw[0]);
@@ -729,7 +857,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                             }
                         }
                         if (masked) {
-                            const uint32_t bits = seen_bits(base + CH * c);
+                            const uint32_t bits = sight.bits(base + CH * c);
 #pragma unroll
                             for (int e = 0; e < CH / 2; ++e) {
                                 float x, y;
@@ -743,12 +871,11 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                         factor = vref / unit;
                         vref = unit;
                     }
-                    // (never 0, which would make NaN of what the mask leaves out; scores that small are 0)
-                    const float tscale = kCodes ? fmaxf(qscale, 0x1p-120f) : qscale;
                     const uint64_t scale2 = pk2(tscale, tscale);
                     auto tile = [&](auto kind) {
                         constexpr bool masked = kind.value;
                         constexpr int kUnroll = masked ? 1 : (kCodes && !C::kMore ? 2 : 128 / CH);   // (see above; the masked one is rare)
+                        constexpr int kProducts = masked ? 1 : (kCodes && (!C::kMore || kQTurned) ? 2 : 128 / CH);
                         float x0 = -INFINITY, x1 = x0;
                         if (!masked) begin();
 #pragma unroll kUnroll
@@ -777,7 +904,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                         const float mu = m == -INFINITY ? 0.f : m;
                         const uint64_t minus2 = pk2(-mu, -mu);
                         uint64_t sa = pk2(0.f, 0.f), sb = sa;
-#pragma unroll kUnroll
+#pragma unroll kProducts
                         for (int c = 0; c < 128 / CH; ++c) {
                             uint64_t s[CH / 2];
                             scores(c, masked, s);
@@ -806,9 +933,21 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     else tile(std::false_type{});
                     tmem_st_wait();
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_full + 8 * blk);
+                hand_over();
+            }
+            if constexpr (kCodes) {
+                // the item's other tiles, the first of them waited for
+                for (bool here = true; alive && j < w.nt; j += dj, here = false) {
+                    if (!here) wait_scores(j);
+                    if (!alive) break;
+                    const float4 *ks4 = reinterpret_cast<const float4 *>(smem + C::kOffScale) + (tile0 + j) % kScaleRing * (kPreTile / 2);
+                    const float3 x = apart_tile(ts, to, D, j > j0, sight, (w.t0 + j) * kPreTile, ks4, tscale, valid, m, l, vref);
+                    m = x.x;
+                    l = x.y;
+                    vref = x.z;
+                    tmem_st_wait();
+                    hand_over();
+                }
             }
             tile0 += w.nt;
             vslot += 2 * w.nt;
@@ -826,6 +965,11 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             // the odd tiles' numerators where they are
             if (deal && blk == 1) {
                 if (w.nt > 1) {
+                    if (kCodes && busy && signbit(vref)) { // units of the rows' own are taken out: there is room for one
+                        scale_numerators(to, D, fabsf(vref));
+                        tmem_st_wait();
+                        vref = 1.f;
+                    }
                     odd_ml[r] = make_float2(m, l);
                     if (kCodes && threadIdx.x == 128) *odd_ref = vref;
                     tc_fence_before();
@@ -846,7 +990,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             }
             if (busy) {
                 float keep = 1.f, add = 0.f;               // weights of this block's numerators and the odd ones
-                if (kCodes) keep = vref;
+                if (kCodes) keep = fabsf(vref);
                 if (joins) {
                     const float2 x = odd_ml[r];
                     const float mm = fmaxf(m, x.x), mu = mm == -INFINITY ? 0.f : mm;

@@ -91,12 +91,13 @@ def check(w, q, mask="causal", window=0, tree=None):
 
 
 CODED = [("int8", "f16"), ("int8", "bf16"), ("e4m3", "f16"), ("e4m3", "bf16")]
-WIDE = [9, 50]              # new tokens, 4 query heads to a kv head: dealt items of one block, items of two
+#: new tokens, 4 query heads to a kv head: the streaming kernel, dealt items of one block, items of two blocks
+ROWS = [3, 9, 50]
 
 
 @pytest.mark.parametrize("fmt,dtype", CODED)
 @pytest.mark.parametrize("dim", [64, 128])
-@pytest.mark.parametrize("n", [3] + WIDE)
+@pytest.mark.parametrize("n", ROWS)
 @pytest.mark.parametrize("power", [12, 20, 40])
 def test_large_k_scales_out_of_sight(fmt, dtype, dim, n, power):
     """A K row with a large scale behind a row's last position, in its tile, and one in its sight that
@@ -114,9 +115,6 @@ def test_large_k_scales_out_of_sight(fmt, dtype, dim, n, power):
     check(w, q)
 
 
-FEW = [3]
-
-
 def clamp_power(w, power):
     """F16 outputs reach 65,504 only: what lies so far above the others lies as far below 2^12."""
     return 2.0 ** (min(0, 12 - power) if w.dtype == torch.float16 else 0)
@@ -124,7 +122,7 @@ def clamp_power(w, power):
 
 @pytest.mark.parametrize("fmt,dtype", CODED)
 @pytest.mark.parametrize("dim", [64, 128])
-@pytest.mark.parametrize("n", FEW)
+@pytest.mark.parametrize("n", ROWS)
 @pytest.mark.parametrize("power", [14, 20, 30, 100])
 @pytest.mark.parametrize("where", ["first", "middle"])
 def test_large_v_scales_without_weight(fmt, dtype, dim, n, power, where):
@@ -142,7 +140,7 @@ def test_large_v_scales_without_weight(fmt, dtype, dim, n, power, where):
 
 @pytest.mark.parametrize("fmt,dtype", CODED)
 @pytest.mark.parametrize("dim", [64, 128])
-@pytest.mark.parametrize("n", FEW)
+@pytest.mark.parametrize("n", ROWS)
 @pytest.mark.parametrize("power", [14, 20, 30, 100])
 def test_large_v_scales_out_of_sight(fmt, dtype, dim, n, power):
     """The batch's last tokens', which the ones before them do not see, in their tile."""
@@ -162,7 +160,7 @@ def test_large_v_scales_out_of_sight(fmt, dtype, dim, n, power):
 
 
 @pytest.mark.parametrize("fmt,dtype", CODED)
-@pytest.mark.parametrize("n", FEW)
+@pytest.mark.parametrize("n", ROWS)
 @pytest.mark.parametrize("window", [0, 200])
 def test_v_scales_of_all_sizes(fmt, dtype, n, window):
     """Forty powers of two up and down at random: what is largest counts most, the rest is small beside it."""
@@ -176,7 +174,7 @@ def test_v_scales_of_all_sizes(fmt, dtype, n, window):
 
 @pytest.mark.parametrize("fmt,dtype", CODED)
 @pytest.mark.parametrize("dim", [64, 128])
-@pytest.mark.parametrize("n", FEW)
+@pytest.mark.parametrize("n", ROWS)
 @pytest.mark.parametrize("rise,fall", [(0.3, 0.12), (0.3, -0.1), (-0.3, -0.12), (-0.3, 0.1), (1.5, 0.2)])
 def test_weights_that_move(fmt, dtype, dim, n, rise, fall):
     """Scores that rise or fall along the sequence while V scales fall or rise, so that the largest product
@@ -195,7 +193,7 @@ def test_weights_that_move(fmt, dtype, dim, n, rise, fall):
 
 
 @pytest.mark.parametrize("fmt,dtype", CODED)
-@pytest.mark.parametrize("n", FEW)
+@pytest.mark.parametrize("n", ROWS)
 def test_v_rows_of_zeros_among_others(fmt, dtype, n):
     """Scales of 0 (rows below 1e-30) with nearly all the weight, and negative ones."""
     w = World([(n, 300), (1, 40)], fmt=fmt, dtype=dtype, seed=n)
@@ -213,7 +211,7 @@ def test_v_rows_of_zeros_among_others(fmt, dtype, n):
 
 
 @pytest.mark.parametrize("fmt,dtype", CODED)
-@pytest.mark.parametrize("n", FEW)
+@pytest.mark.parametrize("n", ROWS)
 @pytest.mark.parametrize("block", [64, 128, 256])
 @pytest.mark.parametrize("first", [0, 1])
 def test_v_scales_by_the_tile(fmt, dtype, n, block, first):
