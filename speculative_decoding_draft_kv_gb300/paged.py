@@ -212,7 +212,10 @@ def rope_frequencies(rotary_dim, theta, scaling="none", factor=1.0, original_len
     factor^(r / (r - 2)), which slows the lowest frequency by ``factor`` and leaves the highest);
     "yarn" (by parts: pairs that turn more than ``beta_fast`` times within ``original_len``
     positions stay, those that turn less than ``beta_slow`` times slow down by ``factor``, a ramp
-    in the number of turns between; magnitude 0.1 ln(factor) + 1).
+    linear in the number of turns between; magnitude 0.1 ln(factor) + 1).  Programs that make the ramp
+    linear in the pair's index instead, between borders that they may round, give other
+    frequencies to the pairs between: weights that were trained or run so want those, as
+    :class:`PagedRope`'s ``inv_freq`` and ``magnitude``.
     """
     r = int(rotary_dim)
     if r <= 0 or r % 2 or not theta > 0 or not factor > 0:
