@@ -252,9 +252,13 @@ class PagedRope:
             raise ValueError(f"inv_freq must have {rotary_dim // 2} entries, got {len(inv_freq)}")
         self.inv_freq, self.magnitude = [float(f) for f in inv_freq], float(magnitude)
         self.args = PagedRopeArgs()
-        self.address = ctypes.addressof(self.args)
         _check(_load().paged_rope_init(self.address, (ctypes.c_double * len(self.inv_freq))(*self.inv_freq),
                                        self.magnitude, rotary_dim, LAYOUTS.get(layout, layout)))
+
+    @property
+    def address(self):
+        """Of the struct that this handle holds: a copy (of a model's, or sent to another process) has its own."""
+        return ctypes.addressof(self.args)
 
 
 _ROW_TYPES = (torch.float16, torch.bfloat16, torch.float32)
