@@ -85,7 +85,7 @@ typedef struct paged_cache {
  * sequence s's newest tokens, at positions kv_len[s] - n .. kv_len[s] - 1 (n of them; kv_len
  * counts them).  Position p lives in row p % page_size of page pages[s][p / page_size].
  *   q_start  device int32 [n_seq + 1], not decreasing.  Rows from q_start[n_seq] on (a padded
- *            batch) are neither read nor written.
+ *            batch) are not written, and what they hold changes nothing (their memory may be read).
  *   kv_len   device int32 [n_seq].
  *   pages    device int32 [n_seq][pages_stride]; entries of pages that a call has no need of
  *            (past the end, or in front of a window) are not looked at.
