@@ -84,7 +84,9 @@ typedef struct paged_cache {
  * A ragged batch of new tokens: rows q_start[s] .. q_start[s+1]-1 of the rows tensors are
  * sequence s's newest tokens, at positions kv_len[s] - n .. kv_len[s] - 1 (n of them; kv_len
  * counts them).  Position p lives in row p % page_size of page pages[s][p / page_size].
- *   q_start  device int32 [n_seq + 1], not decreasing.  Rows from q_start[n_seq] on (a padded
+ *   q_start  device int32 [n_seq + 1], not decreasing (paged_attend reports one that is,
+ *            PAGED_ERR_PAGE; paged_append and paged_gather look rows up as if it were not, and so may
+ *            serve a row at another place of the block table, or not at all).  Rows from q_start[n_seq] on (a padded
  *            batch) are not written, and what they hold changes nothing (their memory may be read).
  *   kv_len   device int32 [n_seq].
  *   pages    device int32 [n_seq][pages_stride]; entries of pages that a call has no need of
