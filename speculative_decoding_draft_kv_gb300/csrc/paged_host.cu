@@ -17,8 +17,9 @@ namespace {
 __device__ uint32_t g_paged_err;
 
 constexpr int kMaxDevices = 64;
+// (set_up: of the attention kernels, by kind: bf16 + 2 * wide)
 struct DeviceInfo {
-    bool ready;
+    bool ready, set_up[4];
     int sms;
     uint32_t *err;
 };
@@ -46,15 +47,30 @@ int device_info(const char *who, DeviceInfo *out) {
         void *p = nullptr;
         e = cudaGetSymbolAddress(&p, g_paged_err);
         if (e == cudaSuccess) e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
-        if (e == cudaSuccess) e = paged_attend_setup_t<PAGED_F16>();
-        if (e == cudaSuccess) e = paged_attend_setup_t<PAGED_BF16>();
-        if (e == cudaSuccess) e = paged_prefill_setup_t<PAGED_F16>();
-        if (e == cudaSuccess) e = paged_prefill_setup_t<PAGED_BF16>();
         if (e != cudaSuccess) return fail(RING_ECUDA, "%s: set-up: %s", who, cudaGetErrorString(e));
         d.err = static_cast<uint32_t *>(p);
         d.ready = true;
     }
     *out = d;
+    return RING_OK;
+}
+
+// The kernels of a kind, once per device and when first called for: one that a device cannot run fails the
+// calls that want it and no others.
+int set_up_attend(const char *who, int kind) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= kMaxDevices)
+        return fail(RING_ECUDA, "%s: cudaGetDevice: %s", who, cudaGetErrorString(e));
+    std::lock_guard<std::mutex> lock(g_mu);
+    switch (kind) {
+    case 0: e = paged_attend_setup_t<PAGED_F16>(); break;
+    case 1: e = paged_attend_setup_t<PAGED_BF16>(); break;
+    case 2: e = paged_prefill_setup_t<PAGED_F16>(); break;
+    default: e = paged_prefill_setup_t<PAGED_BF16>(); break;
+    }
+    if (e != cudaSuccess) return fail(RING_ECUDA, "%s: set-up: %s", who, cudaGetErrorString(e));
+    g_dev[dev].set_up[kind] = true;
     return RING_OK;
 }
 
@@ -467,6 +483,8 @@ extern "C" int paged_attend(const paged_attend_args *g, void *stream) {
     TRY(device_info(who, &d));
     const int group = g->n_head / g->cache->n_head_kv;
     const AttendPlan p = plan_of(g->cache, g->batch, group, d.sms);
+    const int kind = (g->dtype == PAGED_BF16) + 2 * p.wide;
+    if (!d.set_up[kind]) TRY(set_up_attend(who, kind));
     const int64_t need = workspace_of(p, g->cache->head_dim);
     if (!g->workspace || (reinterpret_cast<uintptr_t>(g->workspace) & 255) || g->workspace_bytes < need)
         return fail(RING_EINVAL, "%s: needs %lld bytes of 256-byte aligned workspace", who, (long long)need);
