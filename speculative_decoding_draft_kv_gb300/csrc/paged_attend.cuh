@@ -631,12 +631,12 @@ k_paged_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 const float2 x = sml[(s * MT + mb) * 16 + g + 8 * jj];
                 L[jj] += x.x == -INFINITY ? x.y : x.y * exp2f(x.x - M[jj]);   // x.y: 0, or NaN
             }
-            float f = mrow[jj] == -INFINITY ? 0.f : exp2f(mrow[jj] - M[jj]);
-            if constexpr (FMT != kFmt16) f *= fabsf(vref[jj]);
+            // (one factor after the other: a small unit goes with large numerators)
+            const float f = mrow[jj] == -INFINITY ? 0.f : exp2f(mrow[jj] - M[jj]), unit = FMT != kFmt16 ? fabsf(vref[jj]) : 1.f;
 #pragma unroll
             for (int n = 0; n < D / 8; ++n) {
-                oacc[n][2 * jj] *= f;
-                oacc[n][2 * jj + 1] *= f;
+                oacc[n][2 * jj] = oacc[n][2 * jj] * unit * f;
+                oacc[n][2 * jj + 1] = oacc[n][2 * jj + 1] * unit * f;
             }
         }
         // 64 columns at a time through shared memory, conflict-free

@@ -246,7 +246,8 @@ bool encode_queries(CUtensorMap *tm, const paged_attend_args *g, int head_dim, i
 // whose items are one or two blocks of as many whole tokens as 128 rows take.
 // The border, measured on 64 sequences of up to 1,024 / 16,384 tokens, 8 kv heads of 128 (us):
 //   bf16 pages  16 rows: streaming 54 / 367, tensor-core 63 / 373;  32 rows: 69 / 382 and 62 / 371
-//   int8 pages  32 rows: 75 / 436 and 112 / 501 (the tensor-core kernel turns codes into F16 rows first)
+//   int8 pages  16 rows: streaming 47 / 291, tensor-core 75 / 416;  32 rows: 70 / 454 and 74 / 415
+//   (e4m3, bf16 queries, 32 rows: 66 / 401 and 73 / 400)
 // so 16 rows over 16-bit pages and 32 over quantised ones, more than the streaming kernel has.
 // No more CTAs than the bounds leave work for.
 struct AttendPlan {
@@ -262,8 +263,7 @@ AttendPlan plan_of(const paged_cache *c, const paged_batch *b, int group, int sm
     p.tokens = p.wide ? p.rows / group : std::max(1, b->max_q);
     // What an item's beginning and end cost, in tiles: without it a share of many short items takes
     // longer than one of as many tiles of a long item.  Tensor-core kernel: two prompts of 4,097 tokens 248
-    // us at 0, 214 at 2 and 3; int8 trees and a mixed e4m3 batch 130 and 208 us at 2, 126 and 202 at 3, 127
-    // and 204 at 4.  Streaming kernel, 64 sequences of up to 1,024 / 16,384 tokens, int8, 4 tokens
+    // us at 0, 214 at 2 and 3; int8 trees 130 us at 2, 126 at 3, 127 at 4 (123 at 3 now).  Streaming kernel, 64 sequences of up to 1,024 / 16,384 tokens, int8, 4 tokens
     // each: 94 / 321 us at 0, 56 / 292 at 4, 53 / 286 at 6, 53 / 288 at 8; bf16 85 / 370 and 54 / 367 at 6.
     p.item_cost = p.wide ? 3 : 6;
     // (fewest units of a share; one token over 1,024 positions: 16 us with 2, 22 with 2 + item_cost)

@@ -32,10 +32,11 @@
 // Measured, 32 query and 8 kv heads: a chunk of 2,048 tokens at the end of 32,768, heads of 128, bf16:
 // 792 us, 1.35 PFLOP/s, the tensor pipe active 62 % of the time (a block's chain S -> softmax -> P -> O
 // is longer than the other block's products); 64 verify blocks of up to 9 tokens (36 rows, dealt) over
-// 2.2 GB: 355 us, 6.2 TB/s, bound by memory; two prompts of 4,097 tokens, heads of 64: 214 us, bound by
-// the exponentials and their latency (products are half as long there, exponentials as many); 16 trees
-// of up to 31 nodes over int8: 126 us, and chunks of 1,024 among single tokens, e4m3, window 2,048:
-// 237 us, where neither memory nor the tensor cores nor the issue slots are full.
+// 2.2 GB: 355 us, 6.2 TB/s, bound by memory; two prompts of 4,097 tokens, heads of 64: 214 us, bound by the
+// same chain (P lies over S, so the next S waits for O += P V; the exponentials alone would be 55 us, the
+// tensor pipe is active 31 % of the time); 16 trees of up to 31 nodes over int8: 123 us, and chunks of 1,024
+// among single tokens, e4m3, window 2,048: 238 us, both chains of copy, conversion, S, softmax, P and O,
+// where neither memory nor the tensor cores nor the issue slots are full.
 // What the kernel's parts run at the same time has to fit the instruction cache: over quantised pages and one
 // block the rows' loops are unrolled twice, not eight times (trees 162 -> 130 us), over 16-bit pages whole (two
 // prompts: 214 us, 229 unrolled twice).  Two blocks over quantised pages lie between: F16 queries whole (a
@@ -155,7 +156,8 @@ __device__ __forceinline__ void scale_numerators(uint32_t to, int dim, float by)
 // product, and not below 2^-10 of that: what is lost below F16's smallest step is small beside what counts
 // most, whatever scales the row does not see or gives no weight.  When the reference m moves the unit moves
 // with it and O stays.  (m, l, vref) before and after; vref: the unit, with a minus sign.  Rare, and in a loop of
-// its own, so that it takes no room between the loops that are not (there it cost two blocks 5 to 20 %).
+// its own, so that it takes no room between the loops that are not (there it cost two blocks 5 to 20 %).  Blocks
+// of up to 9 tokens over int8, one V row in 5,000 of zeros: 793 us, 414 without; chunks 2.1 times as long.
 __device__ __forceinline__ float3 apart_tile(uint32_t ts, uint32_t to, int dim, bool more, RowSight sight, int base, const float4 *ks4,
                                           float tscale, bool valid, float m, float l, float vref) {
     const float4 *vs4 = ks4 + kPreTile / 4;

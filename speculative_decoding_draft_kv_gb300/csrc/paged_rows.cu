@@ -16,8 +16,9 @@
 // Bytes are all that these operators cannot do without, each read and written once.  Measured, 32 query
 // and 8 kv heads of 128: norm and rotation of 16,384 bf16 tokens 67 us (5.0 TB/s, 74 % of the copy
 // rate); 22,600 F16 tokens to int8 and back 69 us (4.0 TB/s); 270,000 tokens back from e4m3 286 us (5.9
-// TB/s, 88 %).  What holds them is the instructions they issue, 0.64 to 0.74 a clock and scheduler;
-// small calls (a verify block, 64 of them) are bound by the host's call, 7 to 9 us.
+// TB/s, 88 %).  What holds them is instructions and their latency together: 0.64 to 0.74 a clock and scheduler
+// with 33 to 45 % of the warps, and nothing of a warp's next steps in flight while it works on these; when
+// quantising, two divisions a row on every lane of it besides.  Small calls (a verify block, 64 of them) are bound by the host's call, 7 to 9 us.
 #include "paged.h"
 #include "paged_ptx.h"
 
@@ -281,7 +282,7 @@ __device__ __forceinline__ uint32_t largest(const Raw8<T> &raw, const float (&x)
 
 // A warp step is RPW rows of one kind (queries, keys, values) of one token; a token's steps are laid
 // end to end and a task is `iters` of them, all of them where there are tokens enough.  With plenty of
-// tokens the kernel is bound by what it issues (about 0.7 instructions a clock and scheduler), so a
+// tokens what a warp issues counts (about 0.7 instructions a clock and scheduler), so a
 // step's addresses are two additions, and each kind has a loop of its own.
 template <int T, int D, bool PAGED>
 __global__ void __launch_bounds__(kRowThreads, kRowBlocks)

@@ -226,3 +226,23 @@ def test_v_scales_by_the_tile(fmt, dtype, n, block, first):
         up = torch.where(large, 20.0, 0.0) - (12.0 if dtype == "f16" else 0.0)
         rescale(w, s, "v", torch.exp2(up)[:, None].expand(kv, w.kv_heads))
     check(w, q)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("n", ROWS)
+@pytest.mark.parametrize("heavy", [3, 70, 200, 599])
+@pytest.mark.parametrize("some", [39, 130, 411])
+def test_a_row_of_zeros_with_all_the_weight(fmt, n, heavy, some):
+    """One key has all the weight and a V row of zeros, another, e^-70 of it, all that comes out (as bf16
+    values of some 1e-31), and zeros among the rest make every tile one of scales far apart."""
+    w = World([(n, 650), (n, n + 620)], fmt=fmt, dtype="bf16", seed=heavy + some)
+    q, base = queries(w, 0.001)
+    for s, (m, kv) in enumerate(w.lens):
+        p = torch.arange(kv - m, device="cuda")
+        put_keys(w, s, p, base, torch.where(p == heavy, 70.0, torch.where(p == some, 0.0, -45.0)))
+        put_keys(w, s, torch.arange(kv - m, kv, device="cuda"), base, torch.full((m,), -50.0))
+        zero = torch.cat([torch.tensor([heavy], device="cuda"), torch.arange(81, kv - m, 17, device="cuda")])
+        zero = zero[zero != some]
+        w.vs[w.pages[s][zero // w.page].long(), :, zero % w.page] = 0.0
+        w.V[s][zero] = 0.0
+    check(w, q)
