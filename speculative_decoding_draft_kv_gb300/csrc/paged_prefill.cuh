@@ -24,10 +24,11 @@
 //
 // Quantised pages: four more warps turn codes into F16 tiles in shared memory, exactly, a thread per key; K's
 // scales are multiplied on the scores and V's on the probabilities, in float32, as the streaming kernel does,
-// with units that the F16 products are in: common ones, then the rows' own (apart_tile).  Rows of code times scale rounded to F16 would spare the rows'
-// threads three products a score (mixed batch below 202 us), but a row whose scale is 2^-14 of its tile's largest
-// would lose bits, and with F16 outputs they doubled the error.  bf16 queries are turned to F16 in shared
-// memory, a power of two per row taken out, by the threads that own the rows.
+// with units that the F16 products are in: common ones, then the rows' own (apart_tile).  Rows of code
+// times scale rounded to F16 would spare the rows' threads three products a score (mixed batch below 202 us),
+// but a row whose scale is 2^-14 of its tile's largest would lose bits, and with F16 outputs they doubled
+// the error.  bf16 queries are turned to F16 in shared memory, a power of two per row taken out, by the
+// threads that own the rows.
 //
 // Measured, 32 query and 8 kv heads: a chunk of 2,048 tokens at the end of 32,768, heads of 128, bf16:
 // 792 us, 1.35 PFLOP/s, the tensor pipe active 62 % of the time (a block's chain S -> softmax -> P -> O
