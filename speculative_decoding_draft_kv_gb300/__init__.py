@@ -3,8 +3,9 @@
 The computation lives in the CUDA library ``_lib/libdflash_ring.so`` behind the C ABI of
 ``include/dflash_ring.h``; :mod:`.ring` is the thin binding with the same names, and
 :mod:`.build` compiles the library.  :mod:`.paged` binds the operators over a paged cache
-(``include/dflash_paged.h``, the same library).  Importing this package does not load the
-library; the first call into :mod:`.ring` or :mod:`.paged` does, and fails loudly if it was not built.
+(``include/dflash_paged.h``, the same library), :mod:`.delta` the gated delta rule
+(``include/dflash_delta.h``).  Importing this package does not load the library; the first call into one
+of them does, and fails loudly if it was not built.
 """
 
 from .ring import (  # noqa: F401
@@ -40,14 +41,18 @@ from .ring import (  # noqa: F401
     ring_step,
 )
 
-# names of .paged, which needs PyTorch (building and loading the library do not): imported on
-# first use
+# names of .paged and .delta, which need PyTorch (building and loading the library do not): imported
+# on first use
 _PAGED = ("PagedBatch", "PagedCache", "PagedRope", "paged_append", "paged_attend", "paged_attend_workspace",
           "paged_device_error", "paged_gather", "paged_last_error", "paged_norm_rope", "rope_frequencies")
+_DELTA = ("DeltaBatch", "DeltaState", "delta_device_error", "delta_last_error", "delta_rule", "delta_rule_workspace")
 
 
 def __getattr__(name):
     if name in _PAGED:
         from . import paged
         return getattr(paged, name)
+    if name in _DELTA:
+        from . import delta
+        return getattr(delta, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,50 @@
+// Internal declarations shared by the gated delta rule's CUDA translation units.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "dflash_delta.h"
+
+namespace dflash {
+
+struct DeltaArgs {
+    const uint16_t *q, *k, *v;
+    uint16_t *o;
+    int64_t q_rs, q_hs, k_rs, k_hs, v_rs, v_hs, o_rs, o_hs;
+    const float *g, *beta;
+    int64_t g_rs, beta_rs;
+    float *state;
+    int64_t slot_stride, head_stride;
+    const int *q_start, *slot_in, *slot_out, *save;
+    uint32_t *err;
+    int64_t n_rows;
+    float scale, eps;
+    int n_seq, max_q, n_slots, n_head, n_head_k, group;   // group: heads of a key head
+    int normalise;
+};
+
+constexpr float kDeltaLeast = -1e4f;     // log decays below it count as it: exp() of both is 0
+
+// A sequence's rows and the slot that it begins from, as far as the arrays can be believed.
+struct DeltaSeq {
+    int row0, n, slot;                   // slot negative: zeros
+    bool ok;
+};
+__device__ __forceinline__ DeltaSeq delta_seq(const DeltaArgs &a, int s, uint32_t &bits) {
+    DeltaSeq q;
+    const int64_t r0 = a.q_start[s], r1 = a.q_start[s + 1];
+    q.slot = a.slot_in[s];
+    const bool rows = r0 >= 0 && r0 <= r1 && r1 <= a.n_rows && r1 - r0 <= a.max_q, slot = q.slot < a.n_slots;
+    bits = (rows ? 0u : (uint32_t)DELTA_ERR_BATCH) | (slot ? 0u : (uint32_t)DELTA_ERR_SLOT);
+    q.ok = rows && slot;
+    q.row0 = rows ? (int)r0 : 0;
+    q.n = rows ? (int)(r1 - r0) : 0;
+    return q;
+}
+
+cudaError_t launch_delta_step(const DeltaArgs &a, int dtype, int dim_k, int dim_v, cudaStream_t st);
+
+}  // namespace dflash

@@ -1,0 +1,230 @@
+// The gated delta rule token by token, the state in registers: the kernel for few new tokens per
+// sequence, and for states that are kept behind single tokens.
+//
+//   S <- a S,  u = beta (v - S k),  S <- S + u k^T,  o = scale S q;   a = exp(g)
+//
+// Rows of S (one per value element) never meet, so a head's state is shared out by rows: a warp
+// has four rows beside one another, eight lanes to a row, each lane a run of four key elements in
+// every 32, so that a row is read and written in whole 128-byte lines.  S k and S q come out of one pass
+// over the old state, o = a (S q) + (q . k) u, whose two sums over the eight lanes are the only words
+// that lanes exchange.  Keys and queries are normed once per CTA, eight tokens at a time, in shared
+// memory.
+//
+// Bound by the state's bytes, 64 KB read and written per head of 128 x 128, as long as a sequence has
+// few tokens: a token takes 3 flops per state element beside 8 bytes of it.
+#include "delta.h"
+
+#include "ring_internal.h"
+#include "ptx.h"
+
+namespace dflash {
+namespace {
+
+constexpr int kStepThreads = 128, kStepTokens = 8;
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+template <int T> __device__ __forceinline__ float from16(uint32_t x) {
+    if constexpr (T == PAGED_F16) return __half2float(__ushort_as_half((unsigned short)x));
+    else return __uint_as_float(x << 16);
+}
+template <int T> __device__ __forceinline__ uint16_t to16(float x) {
+    if constexpr (T == PAGED_F16) return __half_as_ushort(__float2half_rn(x));
+    else return __bfloat16_as_ushort(__float2bfloat16_rn(x));
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    return x;
+}
+
+// DK key elements, DV value elements
+template <int T, int DK, int DV>
+__global__ void __launch_bounds__(kStepThreads)
+k_delta_step(const __grid_constant__ DeltaArgs a) {
+    constexpr int E = DK / 8;                          // of a lane's part of a row
+    constexpr int J = 32 / E;                          // rows of a lane
+    constexpr int kRows = 4 * 4 * J;                   // of a CTA
+    constexpr int kParts = DV / kRows;
+    constexpr int TB = kStepTokens;
+    __shared__ float s_k[TB][DK], s_q[TB][DK], s_v[TB][kRows];
+    __shared__ float s_decay[TB], s_beta[TB], s_qk[TB];
+    __shared__ int s_save[TB];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int part = blockIdx.x % kParts, sh = blockIdx.x / kParts, h = sh % a.n_head, s = sh / a.n_head;
+    uint32_t bits;
+    const DeltaSeq q = delta_seq(a, s, bits);
+    if (bits && threadIdx.x == 0 && h == 0 && part == 0) atomicOr(a.err, bits);
+    if (!q.ok) return;
+    const int sub = lane & 7, rg = lane >> 3;          // the lane's part of a row, its row of four
+    const int row0 = part * kRows + warp * 4 * J;      // the warp's rows: row0 + 4 j + rg
+    auto place = [&](int slot) {
+        return a.state + (int64_t)slot * a.slot_stride + (int64_t)h * a.head_stride + (int64_t)(row0 + rg) * DK + sub * 4;
+    };
+    uint64_t st[J][E / 2];
+    if (q.slot >= 0) {
+        const float *src = place(q.slot);
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int e = 0; e < E / 4; ++e) {
+                const float4 x = *reinterpret_cast<const float4 *>(src + j * 4 * DK + e * 32);
+                st[j][2 * e] = pack2(x.x, x.y);
+                st[j][2 * e + 1] = pack2(x.z, x.w);
+            }
+    } else {
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) st[j][e] = 0ull;
+    }
+    auto store = [&](int slot) {
+        if (slot < 0) return;
+        if (slot >= a.n_slots) {
+            if (threadIdx.x == 0 && h == 0 && part == 0) atomicOr(a.err, (uint32_t)DELTA_ERR_SLOT);
+            return;
+        }
+        float *dst = place(slot);
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int e = 0; e < E / 4; ++e) {
+                const float2 x = unpack2(st[j][2 * e]), y = unpack2(st[j][2 * e + 1]);
+                *reinterpret_cast<float4 *>(dst + j * 4 * DK + e * 32) = make_float4(x.x, x.y, y.x, y.y);
+            }
+    };
+
+    const int hk = h / a.group;
+    for (int t0 = 0; t0 < q.n; t0 += TB) {
+        const int nt = min(TB, q.n - t0);
+        if (t0) __syncthreads();                       // the tokens before these have been read
+        for (int i = warp; i < nt; i += 4) {
+            const int64_t row = q.row0 + t0 + i;
+            const uint16_t *kp = a.k + row * a.k_rs + (int64_t)hk * a.k_hs;
+            const uint16_t *qp = a.q + row * a.q_rs + (int64_t)hk * a.q_hs;
+            constexpr int N = DK / 32;                 // of a lane
+            float kx[N], qx[N], kk = 0.f, qq = 0.f, qk = 0.f;
+            uint32_t kw[N / 2], qw[N / 2];
+            if constexpr (N == 4) {
+                const uint2 x = *reinterpret_cast<const uint2 *>(kp + lane * 4), y = *reinterpret_cast<const uint2 *>(qp + lane * 4);
+                kw[0] = x.x; kw[1] = x.y; qw[0] = y.x; qw[1] = y.y;
+            } else {
+                kw[0] = *reinterpret_cast<const uint32_t *>(kp + lane * 2);
+                qw[0] = *reinterpret_cast<const uint32_t *>(qp + lane * 2);
+            }
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                kx[e] = from16<T>(e & 1 ? kw[e / 2] >> 16 : kw[e / 2] & 0xffffu);
+                qx[e] = from16<T>(e & 1 ? qw[e / 2] >> 16 : qw[e / 2] & 0xffffu);
+                kk = fmaf(kx[e], kx[e], kk);
+                qq = fmaf(qx[e], qx[e], qq);
+            }
+            float kr = 1.f, qr = a.scale;
+            if (a.normalise) {
+                kr = 1.f / sqrtf(warp_sum(kk) + a.eps);
+                qr = a.scale / sqrtf(warp_sum(qq) + a.eps);
+            }
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                kx[e] *= kr;
+                qx[e] *= qr;
+                qk = fmaf(kx[e], qx[e], qk);
+                s_k[i][lane * N + e] = kx[e];
+                s_q[i][lane * N + e] = qx[e];
+            }
+            qk = warp_sum(qk);
+            if (lane == 0) {
+                const float g = a.g[row * a.g_rs + h];
+                s_decay[i] = expf(g < kDeltaLeast ? kDeltaLeast : g);
+                s_beta[i] = a.beta[row * a.beta_rs + h];
+                s_qk[i] = qk;
+                s_save[i] = a.save ? a.save[row] : -1;
+            }
+        }
+        for (int i = threadIdx.x; i < nt * kRows; i += kStepThreads) {
+            const int t = i / kRows, r = i % kRows;
+            s_v[t][r] = from16<T>(a.v[(int64_t)(q.row0 + t0 + t) * a.v_rs + (int64_t)h * a.v_hs + part * kRows + r]);
+        }
+        __syncthreads();
+        for (int t = 0; t < nt; ++t) {
+            uint64_t kd[E / 2], ks[J], qs[J];
+#pragma unroll
+            for (int j = 0; j < J; ++j) ks[j] = qs[j] = 0ull;
+#pragma unroll
+            for (int e = 0; e < E / 4; ++e) {
+                const ulonglong2 kx = *reinterpret_cast<const ulonglong2 *>(&s_k[t][sub * 4 + e * 32]);
+                const ulonglong2 qx = *reinterpret_cast<const ulonglong2 *>(&s_q[t][sub * 4 + e * 32]);
+                kd[2 * e] = kx.x;
+                kd[2 * e + 1] = kx.y;
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    ks[j] = fma2(kx.x, st[j][2 * e], ks[j]);
+                    ks[j] = fma2(kx.y, st[j][2 * e + 1], ks[j]);
+                    qs[j] = fma2(qx.x, st[j][2 * e], qs[j]);
+                    qs[j] = fma2(qx.y, st[j][2 * e + 1], qs[j]);
+                }
+            }
+            const float decay = s_decay[t], beta = s_beta[t], qk = s_qk[t];
+            const uint64_t decay2 = pack2(decay, decay);
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const float2 x = unpack2(ks[j]), y = unpack2(qs[j]);
+                float kS = x.x + x.y, qS = y.x + y.y;
+#pragma unroll
+                for (int d = 4; d; d >>= 1) {
+                    kS += __shfl_xor_sync(0xffffffffu, kS, d);
+                    qS += __shfl_xor_sync(0xffffffffu, qS, d);
+                }
+                const float u = beta * (s_v[t][warp * 4 * J + 4 * j + rg] - decay * kS);
+                const uint64_t u2 = pack2(u, u);
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) st[j][e] = fma2(kd[e], u2, mul2(decay2, st[j][e]));
+                if (sub == j)
+                    a.o[(int64_t)(q.row0 + t0 + t) * a.o_rs + (int64_t)h * a.o_hs + row0 + 4 * j + rg] =
+                        to16<T>(fmaf(qk, u, decay * qS));
+            }
+            store(s_save[t]);
+        }
+    }
+    store(a.slot_out[s]);
+}
+
+template <int T, int DK, int DV>
+cudaError_t go(const DeltaArgs &a, cudaStream_t st) {
+    constexpr int parts = DV / (4 * 4 * (32 / (DK / 8)));
+    k_delta_step<T, DK, DV><<<(unsigned)((int64_t)a.n_seq * a.n_head * parts), kStepThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+template <int T>
+cudaError_t pick(const DeltaArgs &a, int dk, int dv, cudaStream_t st) {
+    if (dk == 64) return dv == 64 ? go<T, 64, 64>(a, st) : go<T, 64, 128>(a, st);
+    return dv == 64 ? go<T, 128, 64>(a, st) : go<T, 128, 128>(a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_delta_step(const DeltaArgs &a, int dtype, int dim_k, int dim_v, cudaStream_t st) {
+    return dtype == PAGED_F16 ? pick<PAGED_F16>(a, dim_k, dim_v, st) : pick<PAGED_BF16>(a, dim_k, dim_v, st);
+}
+
+}  // namespace dflash

@@ -348,6 +348,19 @@ def paged_gather(cache, batch, k, v, stream=None):
     _check(_load().paged_gather(ctypes.addressof(a), _stream(stream, dev)))
 
 
+def _workspace(given, size, st, stream, dev, device):
+    """The workspace given, or one of size() bytes for stream ``st``."""
+    if given is None:
+        # from the pool of the stream that the work runs on, which alone may have it next
+        if stream is None:
+            return torch.empty(size(), dtype=torch.uint8, device=device)
+        with torch.cuda.stream(torch.cuda.ExternalStream(st) if st else torch.cuda.default_stream(dev)):
+            return torch.empty(size(), dtype=torch.uint8, device=device)
+    if given.get_device() != dev or given.dtype != torch.uint8 or not given.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 CUDA tensor of the call's device")
+    return given
+
+
 def paged_attend_workspace(cache, batch, n_head) -> int:
     """Bytes of workspace that :func:`paged_attend` needs."""
     _one_device(cache, batch)
@@ -372,16 +385,7 @@ def paged_attend(cache, batch, q, o, mask="causal", window=0, scale=0.0, tree=No
     if not 0 <= window < 1 << 31:
         raise ValueError(f"window {window} out of range")
     st = _stream(stream, dev)
-    if workspace is None:
-        # from the pool of the stream that the work runs on, which alone may have it next
-        size = paged_attend_workspace(cache, batch, heads)
-        if stream is None:
-            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-        else:
-            with torch.cuda.stream(torch.cuda.ExternalStream(st) if st else torch.cuda.default_stream(dev)):
-                workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-    elif workspace.get_device() != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous uint8 CUDA tensor of the call's device")
+    workspace = _workspace(workspace, lambda: paged_attend_workspace(cache, batch, heads), st, stream, dev, q.device)
     a = PagedAttendArgs(cache.address, batch.address, qp, op, qr, qh, orow, oh, tp, lp, workspace.data_ptr(),
                         workspace.numel(), n, scale, heads, _TYPES[dtype], MASKS.get(mask, mask), window, 0)
     _check(_load().paged_attend(ctypes.addressof(a), st))
