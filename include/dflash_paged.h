@@ -247,6 +247,29 @@ int paged_attend(const paged_attend_args *args, void *stream);
 int paged_attend_workspace(const paged_cache *cache, const paged_batch *batch, int32_t n_head,
                            int64_t *bytes);
 
+/*
+ * paged_attend_shared -- paged_attend for a batch whose sequences share beginnings (samples of one
+ * prompt, questions about one document, requests behind one system prompt).  A prefix's K and V
+ * are read once for all its rows: a first pass attends to the prefixes, a second one to
+ * the sequences' own pages and joins the two softmaxes, exactly as over one context.
+ *   args->batch   as in paged_attend, of each sequence's own part: kv_len counts the positions
+ *            behind its prefix, the new tokens included, and pages holds them from the first on (a part of
+ *            a page that the prefix fills does not go on here: the own part begins in a page of its
+ *            own).  mask, tree and c refer to own positions; every token sees its whole prefix.
+ *   prefix   rows q_start[i] .. q_start[i+1]-1 (n_seq prefixes; bounds of rows, over any number of
+ *            sequences) begin with the kv_len[i] >= 0 positions of pages[i].  max_q: upper bound of one
+ *            prefix's rows; max_kv of their lengths.  Rows that no prefix has stand for themselves.
+ *   window   0 (EINVAL otherwise).
+ *   lse      of both parts.
+ *   workspace   paged_attend_shared_workspace() bytes.
+ * A prefix whose bounds contradict each other (see paged_attend; its length may be below its number of rows)
+ * is left out, PAGED_ERR_PAGE: its rows get their own part alone.
+ * With paged_append and paged_norm_rope, positions[] counts the prefix.  Errors: EINVAL, ECUDA.
+ */
+int paged_attend_shared(const paged_attend_args *args, const paged_batch *prefix, void *stream);
+int paged_attend_shared_workspace(const paged_cache *cache, const paged_batch *batch, const paged_batch *prefix,
+                                  int64_t n_rows, int32_t n_head, int64_t *bytes);
+
 /* paged_device_error -- synchronise, read and clear the current device's error word of these
  * operators.  RING_OK, or RING_EDEVICE with the bits in *bits (may be NULL). */
 int paged_device_error(uint32_t *bits);

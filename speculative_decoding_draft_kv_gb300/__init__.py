@@ -43,7 +43,8 @@ from .ring import (  # noqa: F401
 
 # names of .paged and .delta, which need PyTorch (building and loading the library do not): imported
 # on first use
-_PAGED = ("PagedBatch", "PagedCache", "PagedRope", "paged_append", "paged_attend", "paged_attend_workspace",
+_PAGED = ("PagedBatch", "PagedCache", "PagedRope", "paged_append", "paged_attend", "paged_attend_shared",
+          "paged_attend_shared_workspace", "paged_attend_workspace",
           "paged_device_error", "paged_gather", "paged_last_error", "paged_norm_rope", "rope_frequencies")
 _DELTA = ("DeltaBatch", "DeltaState", "delta_device_error", "delta_last_error", "delta_rule", "delta_rule_workspace")
 

@@ -29,13 +29,14 @@ struct PagedBatchDev {
 };
 
 // A sequence's new rows and lengths, as far as the arrays can be believed: rows within
-// [0, n_rows), a length within the block table.  ok is false where they were not.
+// [0, n_rows), a length within the block table.  ok is false where they were not.  prefix: the length does
+// not count the rows, which all come behind it.
 struct PagedSeq {
     int row0, n, kv;
     bool ok;
 };
 
-__device__ __forceinline__ PagedSeq paged_seq(const PagedBatchDev &b, int page_shift, int s) {
+__device__ __forceinline__ PagedSeq paged_seq(const PagedBatchDev &b, int page_shift, int s, bool prefix = false) {
     PagedSeq q;
     const int64_t r0 = b.q_start[s], r1 = b.q_start[s + 1];
     const int64_t kv = b.kv_len[s], cap = (int64_t)b.max_pages << page_shift;
@@ -44,7 +45,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedBatchDev &b, int page_s
     q.row0 = (int)lo;
     q.n = (int)(hi - lo);
     q.kv = (int)(kv < 0 ? 0 : (kv > cap ? cap : kv));
-    q.ok = lo == r0 && hi == r1 && q.kv == kv && (q.n == 0 || kv >= q.n);
+    q.ok = lo == r0 && hi == r1 && q.kv == kv && (prefix || q.n == 0 || kv >= q.n);
     return q;
 }
 
@@ -95,11 +96,24 @@ struct PagedAttendArgs {
     int ctas, min_tiles, item_cost;   // fewest units of a share; units of an item beyond its tiles
     int tile_tokens, tile_rows;       // tokens and rows (tokens times group, at most) of an item
     float scale_log2;
+    // A batch whose sequences share beginnings is attended to in two passes, all rows of a prefix over its
+    // positions (kPrefix, the mask a full one) and each sequence over its own (kOwn), which k_paged_levels joins.
+    // A pass writes down where an item's states are, and those of items that are not cut beside the cut ones'.
+    int level;
+    float *level_acc;                 // [n_rows][n_head][head_dim] numerators
+    float2 *level_ml;                 // [n_rows][n_head] (max in log2 units, sum)
+    int2 *level_items;                // [n_rows][kv heads] of an item's first row: the CTAs with its first and last
+                                      // tile; .y negative: not cut, its states are in the arrays above
 };
+enum { kOnly = 0, kPrefix = 1, kOwn = 2 };
+
 template <int T> cudaError_t paged_attend_setup_t();
 template <int T>
 cudaError_t launch_paged_attend_t(const PagedAttendArgs &a, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                                   int head_dim, cudaStream_t st);
+
+template <int T>
+cudaError_t launch_paged_levels_t(const PagedAttendArgs &prefix, const PagedAttendArgs &own, int head_dim, cudaStream_t st);
 
 template <int T> cudaError_t paged_prefill_setup_t();
 template <int T>

@@ -123,7 +123,10 @@ k_paged_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     pdl_trigger();                       // the join may settle; it waits for this grid's end
     const PagedShare share = paged_share<kDecTile, C::kThreads>(a, s_plan);
     if (threadIdx.x == 0 && share.units == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    if (share.units == 0) return;
+    if (share.units == 0) {
+        if (a.level == kOwn) pdl_wait();
+        return;
+    }
 
     PagedWalk<kDecTile> w;
     w.init(a, share);
@@ -665,7 +668,7 @@ k_paged_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         if (ksl == 0) {
             // column of accumulator (n, e): 16-bit pages n * 8 + 2c + e; codes in the even / odd
             // order, 16 (n / 2) + 4c + 2e + (n & 1)
-            const bool whole = w.first && w.last;
+            const bool uncut = w.first && w.last, whole = uncut && a.level == kOnly;
             const int64_t part = ((int64_t)blockIdx.x * 2 + (w.first ? 1 : 0)) * C::kRows;
 #pragma unroll
             for (int jj = 0; jj < 2; ++jj) {
@@ -691,6 +694,12 @@ k_paged_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                             L[jj] == 0.f ? -INFINITY : (M[jj] + log2f(L[jj])) * 0.6931471805599453f;
                 } else {
                     float *acc = a.part_acc + (part + r) * D;
+                    float2 *ml = a.part_ml + part + r;
+                    if (uncut) {
+                        const int64_t at = (int64_t)(q.row0 + f / a.group) * a.n_head + w.head * a.group + f % a.group;
+                        acc = a.level_acc + at * D;
+                        ml = a.level_ml + at;
+                    }
 #pragma unroll
                     for (int n = 0; n < D / 8; n += 2) {
                         if constexpr (FMT == kFmt16) {
@@ -702,9 +711,10 @@ k_paged_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                                 make_float4(oacc[n][2 * jj], oacc[n + 1][2 * jj], oacc[n][2 * jj + 1], oacc[n + 1][2 * jj + 1]);
                         }
                     }
-                    if (c == 0) a.part_ml[part + r] = make_float2(M[jj], L[jj]);
+                    if (c == 0) *ml = make_float2(M[jj], L[jj]);
                 }
             }
+            if (a.level != kOnly && w.first && threadIdx.x == 0) w.note(a);
             if (w.first && !w.last) {
                 began = true;
                 if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(w.seq, w.head, w.rt, w.last_cta());
@@ -712,6 +722,8 @@ k_paged_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         }
     }
     if (threadIdx.x == 0 && !began) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    // (the second of two passes begins beside the first: what waits for it waits for both)
+    if (a.level == kOwn) pdl_wait();
 }
 
 // Join of the items that a share's border cut: block (c, y) takes rows of the item that CTA c began
@@ -808,6 +820,138 @@ k_paged_join(const __grid_constant__ PagedAttendArgs a) {
         *reinterpret_cast<uint32_t *>(o) = pack16<T>(acc[0] * inv, acc[1] * inv);
     if (a.lse && lane == 0)
         a.lse[(int64_t)(q.row0 + tok) * a.n_head + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// Join of two passes over a batch whose sequences share beginnings: W warps take a (row, head), look up the
+// items that hold its states over its prefix and over its own positions, and join all their pieces as k_paged_join
+// does.  Bound by latency with few rows (row bounds, items, maxima, numerators: four loads one behind another;
+// four rows of 32 heads LEVEL_SMALL us with eight warps to a row, LEVEL_SMALL_1 with one), by L2 with many.
+template <int D, int T, int W>
+__global__ void __launch_bounds__(256)
+k_paged_levels(const __grid_constant__ PagedAttendArgs prefix, const __grid_constant__ PagedAttendArgs own) {
+    constexpr int N = D / 32;
+    __shared__ float s_acc[W > 1 ? W : 1][D];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % W;
+    const int64_t unit = (int64_t)blockIdx.x * (8 / W) + warp / W;
+    pdl_wait();
+    if (unit >= own.batch.n_rows * own.n_head) return;           // whole blocks with W = 8
+    const int row = (int)(unit / own.n_head), head = (int)(unit % own.n_head), hk = head / own.group;
+    // a pass's pieces of the row: n of them, the first in CTA c0; n = 0: none, c0 negative: in the level's arrays
+    struct Pieces {
+        bool ok;
+        int n, c0;
+        int64_t r;                                                // the row in its item
+    };
+    auto find = [&](const PagedAttendArgs &a) {
+        // the last sequence that begins at the row or in front of it, 32 bounds at a time
+        int s = 0, left = a.batch.n_seq;
+        while (left > 1) {
+            const int step = (left + 31) / 32, at = lane * step;
+            const uint32_t b = __ballot_sync(0xffffffffu, at < left && a.batch.q_start[s + at] <= row);
+            const int top = b ? (31 - __clz(b)) * step : 0;
+            s += top;
+            left = min(step, left - top);
+        }
+        const PagedSeq q = paged_seq(a.batch, a.pool.page_shift, s, a.level == kPrefix);
+        Pieces p = {false, 0, 0, 0};
+        if (!q.ok || q.n > a.max_q || q.kv == 0 || row < q.row0 || row >= q.row0 + q.n) return p;
+        const int tok = row - q.row0, rt = tok / a.tile_tokens;
+        const int2 c = a.level_items[(int64_t)(q.row0 + rt * a.tile_tokens) * a.pool.n_head_kv + hk];
+        p.ok = true;
+        p.r = (tok - rt * a.tile_tokens) * a.group + head % a.group;
+        p.c0 = c.y < 0 ? -1 : min(max(c.x, 0), a.ctas - 1);      // (in range, should the pass have given up)
+        p.n = c.y < 0 ? 1 : max(1, min(c.y, a.ctas - 1) - p.c0 + 1);
+        return p;
+    };
+    const Pieces po = find(own);
+    if (!po.ok) return;                                          // not in the batch, or left alone
+    const Pieces pp = find(prefix);
+    const int total = pp.n + po.n;
+    // where piece i is, in rows of either pass's arrays
+    auto slot = [&](int i, bool &cut) {
+        const Pieces &p = i < pp.n ? pp : po;
+        const int k = i < pp.n ? i : i - pp.n;
+        cut = p.c0 >= 0;
+        return cut ? ((int64_t)(p.c0 + k) * 2 + (k == 0 ? 1 : 0)) * (i < pp.n ? prefix.tile_rows : own.tile_rows) + p.r : unit;
+    };
+    float m = -INFINITY, l = 0.f, acc[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) acc[e] = 0.f;
+    for (int base = 0; base < total; base += 32) {
+        const int n = min(32, total - base);
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (lane < n) {
+            bool cut;
+            const int64_t at = slot(base + lane, cut);
+            const PagedAttendArgs &a = base + lane < pp.n ? prefix : own;
+            ml = cut ? a.part_ml[at] : a.level_ml[at];
+        }
+        constexpr int PER = 32 / W, U = PER < 4 ? PER : 4;
+        float x[U][N];
+        auto fetch = [&](int i) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int p = part + (i + u) * W;
+                if (p >= n) continue;
+                bool cut;
+                const int64_t at = slot(base + p, cut);
+                const PagedAttendArgs &a = base + p < pp.n ? prefix : own;
+                const float *src = (cut ? a.part_acc : a.level_acc) + at * D + lane * N;
+                if constexpr (N == 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(src);
+                    x[u][0] = v.x; x[u][1] = v.y; x[u][2] = v.z; x[u][3] = v.w;
+                } else {
+                    const float2 v = *reinterpret_cast<const float2 *>(src);
+                    x[u][0] = v.x; x[u][1] = v.y;
+                }
+            }
+        };
+        fetch(0);
+        float top = ml.x;
+#pragma unroll
+        for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+        const float mnew = fmaxf(m, top);
+        const float mu = mnew == -INFINITY ? 0.f : mnew;
+        const float wgt = ml.x == -INFINITY ? (ml.y != ml.y ? ml.y : 0.f) : exp2f(ml.x - mu);
+        float sum = ml.y * wgt;
+#pragma unroll
+        for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+        const float keep = m == -INFINITY ? 0.f : exp2f(m - mu);
+        l = l * keep + sum;
+#pragma unroll
+        for (int e = 0; e < N; ++e) acc[e] *= keep;
+        m = mnew;
+        for (int i = 0; part + i * W < n; i += U) {
+            if (i) fetch(i);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int p = part + (i + u) * W;
+                const float f4 = __shfl_sync(0xffffffffu, wgt, p & 31);
+                if (p >= n) continue;
+#pragma unroll
+                for (int e = 0; e < N; ++e) acc[e] = fmaf(x[u][e], f4, acc[e]);
+            }
+        }
+    }
+    if constexpr (W > 1) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) s_acc[warp][lane * N + e] = acc[e];
+        __syncthreads();
+        if (warp) return;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            acc[e] = 0.f;
+#pragma unroll
+            for (int i = 0; i < W; ++i) acc[e] += s_acc[i][lane * N + e];
+        }
+    }
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    uint16_t *o = own.o + (int64_t)row * own.o_rs + (int64_t)head * own.o_hs + lane * N;
+    if constexpr (N == 4)
+        *reinterpret_cast<uint2 *>(o) = make_uint2(pack16<T>(acc[0] * inv, acc[1] * inv), pack16<T>(acc[2] * inv, acc[3] * inv));
+    else
+        *reinterpret_cast<uint32_t *>(o) = pack16<T>(acc[0] * inv, acc[1] * inv);
+    if (own.lse && lane == 0) own.lse[unit] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 }  // namespace dflash

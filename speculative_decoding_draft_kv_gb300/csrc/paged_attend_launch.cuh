@@ -24,6 +24,41 @@ cudaError_t launch_join(const PagedAttendArgs &a, int head_dim, cudaStream_t st)
                           : cudaLaunchKernelEx(&cfg, k_paged_join<128, T, W>, a);
 }
 
+// Two passes' join, which settles as the other one does.  More warps to a row where there are few: see the kernel.
+template <int T>
+cudaError_t launch_paged_levels_t(const PagedAttendArgs &prefix, const PagedAttendArgs &own, int head_dim, cudaStream_t st) {
+    const int64_t units = own.batch.n_rows * own.n_head;
+    const int w = units <= 2048 ? 8 : 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((units * w + 7) / 8), 1, 1);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    auto go = [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, prefix, own); };
+    if (head_dim == 64) return w == 8 ? go(k_paged_levels<64, T, 8>) : go(k_paged_levels<64, T, 1>);
+    return w == 8 ? go(k_paged_levels<128, T, 8>) : go(k_paged_levels<128, T, 1>);
+}
+
+// A pass of the attention.  The second of two may begin while the first one runs: it reads nothing of that.
+template <class K, class... Args>
+cudaError_t launch_pass(K kernel, const PagedAttendArgs &a, int threads, int smem, cudaStream_t st, const Args &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.ctas, 1, 1);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.level == kOwn ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // fn(kernel, its shared memory, threads, rows) for one of the instances
 template <int T, int D, int MT, int FMT, class F>
 cudaError_t with_attend(F &&fn) {
@@ -58,10 +93,8 @@ template <int T>
 cudaError_t launch_paged_attend_t(const PagedAttendArgs &a, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                                   int head_dim, cudaStream_t st) {
     auto go = [&](auto kernel, int smem, int threads, int) {
-        kernel<<<a.ctas, threads, smem, st>>>(tm_k, tm_v, a);
-        cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-        return launch_join<T, 8>(a, head_dim, st);
+        const cudaError_t e = launch_pass(kernel, a, threads, smem, st, tm_k, tm_v, a);
+        return e == cudaSuccess && a.level == kOnly ? launch_join<T, 8>(a, head_dim, st) : e;
     };
     const int mt = a.tile_rows <= 16 ? 1 : 2;
     return head_dim == 64 ? pick_attend<T, 64>(a.pool.format, mt, go) : pick_attend<T, 128>(a.pool.format, mt, go);

@@ -444,6 +444,11 @@ extern "C" int paged_gather(const paged_gather_args *g, void *stream) {
     return e == cudaSuccess ? RING_OK : fail(RING_ECUDA, "%s: launch: %s", who, cudaGetErrorString(e));
 }
 
+// Of each of two passes: the states of its items that are not cut, and where its items' states are.
+static int64_t level_bytes(const paged_cache *c, int64_t n_rows, int n_head) {
+    return up256(n_rows * n_head * c->head_dim * 4) + up256(n_rows * n_head * 8) + up256(n_rows * c->n_head_kv * 8);
+}
+
 extern "C" int paged_attend_workspace(const paged_cache *cache, const paged_batch *batch, int32_t n_head, int64_t *bytes) {
     static const char *who = "paged_attend_workspace";
     if (!bytes) return fail(RING_EINVAL, "%s: bytes is NULL", who);
@@ -456,11 +461,65 @@ extern "C" int paged_attend_workspace(const paged_cache *cache, const paged_batc
     return RING_OK;
 }
 
-extern "C" int paged_attend(const paged_attend_args *g, void *stream) {
-    static const char *who = "paged_attend";
-    if (!g) return fail(RING_EINVAL, "%s: args is NULL", who);
+extern "C" int paged_attend_shared_workspace(const paged_cache *cache, const paged_batch *batch, const paged_batch *prefix,
+                                             int64_t n_rows, int32_t n_head, int64_t *bytes) {
+    static const char *who = "paged_attend_shared_workspace";
+    if (!bytes) return fail(RING_EINVAL, "%s: bytes is NULL", who);
+    TRY(check_cache(who, cache));
+    TRY(check_batch(who, cache, batch, n_rows));
+    TRY(check_batch(who, cache, prefix, n_rows));
+    TRY(check_heads(who, cache, n_head));
+    DeviceInfo d;
+    TRY(device_info(who, &d));
+    const int group = n_head / cache->n_head_kv;
+    *bytes = 2 * level_bytes(cache, n_rows, n_head) + workspace_of(plan_of(cache, batch, group, d.sms), cache->head_dim) +
+             workspace_of(plan_of(cache, prefix, group, d.sms), cache->head_dim);
+    return RING_OK;
+}
+
+// One pass: what the kernels take of it, and its launch.  a: as filled from the call.
+static int attend_pass(const char *who, const paged_attend_args *g, const paged_batch *b, const AttendPlan &p, PagedAttendArgs &a,
+                       uint8_t *ws, cudaStream_t st) {
+    const int64_t parts = (int64_t)p.ctas * 2 * p.rows;
+    const int dim = g->cache->head_dim;
+    a.batch = batch_of(b, g->n_rows);
+    a.part_acc = reinterpret_cast<float *>(ws);
+    ws += up256(parts * dim * 4);
+    a.part_ml = reinterpret_cast<float2 *>(ws);
+    ws += up256(parts * 8);
+    a.desc = reinterpret_cast<int4 *>(ws);
+    if (a.level != kOnly) {
+        ws += up256((int64_t)p.ctas * 16);
+        a.level_acc = reinterpret_cast<float *>(ws);
+        ws += up256(g->n_rows * g->n_head * dim * 4);
+        a.level_ml = reinterpret_cast<float2 *>(ws);
+        ws += up256(g->n_rows * g->n_head * 8);
+        a.level_items = reinterpret_cast<int2 *>(ws);
+    }
+    a.max_q = b->max_q;
+    a.ctas = p.ctas;
+    a.min_tiles = p.min_tiles;
+    a.item_cost = p.item_cost;
+    a.tile_tokens = p.tokens;
+    a.tile_rows = p.rows;
+    CUtensorMap tk, tv, tq;
+    const int box = p.wide ? 128 : 64;
+    if (!encode_pool(&tk, g->cache, g->cache->k, box) || !encode_pool(&tv, g->cache, g->cache->v, box) ||
+        (p.wide && !encode_queries(&tq, g, dim, a.group, 128 / a.group)))
+        return fail(RING_ECUDA, "%s: cuTensorMapEncodeTiled failed", who);
+    const bool f16 = g->dtype == PAGED_F16;
+    const cudaError_t e = p.wide ? (f16 ? launch_paged_prefill_t<PAGED_F16>(a, tk, tv, tq, dim, st)
+                                        : launch_paged_prefill_t<PAGED_BF16>(a, tk, tv, tq, dim, st))
+                                 : (f16 ? launch_paged_attend_t<PAGED_F16>(a, tk, tv, dim, st)
+                                        : launch_paged_attend_t<PAGED_BF16>(a, tk, tv, dim, st));
+    return e == cudaSuccess ? RING_OK : fail(RING_ECUDA, "%s: launch: %s", who, cudaGetErrorString(e));
+}
+
+// prefix: NULL, or what paged_attend_shared has beside the arguments.
+static int attend(const char *who, const paged_attend_args *g, const paged_batch *prefix, void *stream) {
     TRY(check_cache(who, g->cache));
     TRY(check_batch(who, g->cache, g->batch, g->n_rows));
+    if (prefix) TRY(check_batch(who, g->cache, prefix, g->n_rows));
     TRY(check_heads(who, g->cache, g->n_head));
     if (!is16(g->dtype)) return fail(RING_EINVAL, "%s: q and o must be F16 or BF16", who);
     if (is16(g->cache->format) && g->cache->format != g->dtype)
@@ -472,6 +531,7 @@ extern "C" int paged_attend(const paged_attend_args *g, void *stream) {
     if (g->mask == PAGED_TREE && g->batch->max_q > 64)
         return fail(RING_EINVAL, "%s: a token tree has at most 64 nodes, max_q is %d", who, g->batch->max_q);
     if (g->window < 0) return fail(RING_EINVAL, "%s: negative window", who);
+    if (prefix && g->window) return fail(RING_EINVAL, "%s: no windows over shared beginnings", who);
     // (in log2 units it has to be finite too)
     if (!(g->scale >= 0.f) || !std::isfinite(g->scale * 1.5f)) return fail(RING_EINVAL, "%s: scale must be finite and not negative", who);
     if (!rows_ok(g->q, g->q_row_stride, g->q_head_stride, 2, g->n_rows, g->n_head) ||
@@ -481,11 +541,16 @@ extern "C" int paged_attend(const paged_attend_args *g, void *stream) {
     if (g->n_rows == 0 || g->batch->n_seq == 0 || g->batch->max_q == 0) return RING_OK;
     DeviceInfo d;
     TRY(device_info(who, &d));
-    const int group = g->n_head / g->cache->n_head_kv;
+    const int group = g->n_head / g->cache->n_head_kv, dim = g->cache->head_dim;
     const AttendPlan p = plan_of(g->cache, g->batch, group, d.sms);
-    const int kind = (g->dtype == PAGED_BF16) + 2 * p.wide;
-    if (!d.set_up[kind]) TRY(set_up_attend(who, kind));
-    const int64_t need = workspace_of(p, g->cache->head_dim);
+    const AttendPlan pp = prefix ? plan_of(g->cache, prefix, group, d.sms) : p;
+    for (const AttendPlan *x : {&p, &pp}) {
+        const int kind = (g->dtype == PAGED_BF16) + 2 * x->wide;
+        if (!d.set_up[kind]) TRY(set_up_attend(who, kind));
+        d.set_up[kind] = true;
+    }
+    const int64_t level = prefix ? level_bytes(g->cache, g->n_rows, g->n_head) : 0, first = workspace_of(pp, dim) + level;
+    const int64_t need = workspace_of(p, dim) + level + (prefix ? first : 0);
     if (!g->workspace || (reinterpret_cast<uintptr_t>(g->workspace) & 255) || g->workspace_bytes < need)
         return fail(RING_EINVAL, "%s: needs %lld bytes of 256-byte aligned workspace", who, (long long)need);
     PagedAttendArgs a{};
@@ -496,41 +561,39 @@ extern "C" int paged_attend(const paged_attend_args *g, void *stream) {
     a.q_rs = g->q_row_stride; a.q_hs = g->q_head_stride;
     a.o_rs = g->o_row_stride; a.o_hs = g->o_head_stride;
     a.pool = pool_of(g->cache);
-    a.batch = batch_of(g->batch, g->n_rows);
     a.err = d.err;
-    uint8_t *ws = static_cast<uint8_t *>(g->workspace);
-    const int64_t parts = (int64_t)p.ctas * 2 * p.rows;
-    a.part_acc = reinterpret_cast<float *>(ws);
-    ws += up256(parts * g->cache->head_dim * 4);
-    a.part_ml = reinterpret_cast<float2 *>(ws);
-    ws += up256(parts * 8);
-    a.desc = reinterpret_cast<int4 *>(ws);
     a.n_head = g->n_head;
     a.group = group;
     a.mask = g->mask;
     // one that reaches back past any position is none (and sums of positions and windows stay in 32 bits)
     a.window = g->window > INT32_MAX / 2 ? 0 : g->window;
-    a.max_q = g->batch->max_q;
-    a.ctas = p.ctas;
-    a.min_tiles = p.min_tiles;
-    a.item_cost = p.item_cost;
-    a.tile_tokens = p.tokens;
-    a.tile_rows = p.rows;
-    const double scale = g->scale > 0.f ? (double)g->scale : 1.0 / std::sqrt((double)g->cache->head_dim);
+    const double scale = g->scale > 0.f ? (double)g->scale : 1.0 / std::sqrt((double)dim);
     a.scale_log2 = (float)(scale * 1.4426950408889634);
-    CUtensorMap tk, tv, tq;
-    const int box = p.wide ? 128 : 64;
-    if (!encode_pool(&tk, g->cache, g->cache->k, box) || !encode_pool(&tv, g->cache, g->cache->v, box) ||
-        (p.wide && !encode_queries(&tq, g, g->cache->head_dim, group, 128 / group)))
-        return fail(RING_ECUDA, "%s: cuTensorMapEncodeTiled failed", who);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool f16 = g->dtype == PAGED_F16;
-    const int dim = g->cache->head_dim;
-    const cudaError_t e = p.wide ? (f16 ? launch_paged_prefill_t<PAGED_F16>(a, tk, tv, tq, dim, st)
-                                        : launch_paged_prefill_t<PAGED_BF16>(a, tk, tv, tq, dim, st))
-                                 : (f16 ? launch_paged_attend_t<PAGED_F16>(a, tk, tv, dim, st)
-                                        : launch_paged_attend_t<PAGED_BF16>(a, tk, tv, dim, st));
+    uint8_t *ws = static_cast<uint8_t *>(g->workspace);
+    if (!prefix || prefix->n_seq == 0) return attend_pass(who, g, g->batch, p, a, ws, st);
+    PagedAttendArgs b = a;
+    b.level = kPrefix;
+    b.mask = PAGED_FULL;
+    a.level = kOwn;
+    TRY(attend_pass(who, g, prefix, pp, b, ws, st));
+    TRY(attend_pass(who, g, g->batch, p, a, ws + first, st));
+    const cudaError_t e = g->dtype == PAGED_F16 ? launch_paged_levels_t<PAGED_F16>(b, a, dim, st)
+                                                : launch_paged_levels_t<PAGED_BF16>(b, a, dim, st);
     return e == cudaSuccess ? RING_OK : fail(RING_ECUDA, "%s: launch: %s", who, cudaGetErrorString(e));
+}
+
+extern "C" int paged_attend(const paged_attend_args *g, void *stream) {
+    static const char *who = "paged_attend";
+    if (!g) return fail(RING_EINVAL, "%s: args is NULL", who);
+    return attend(who, g, nullptr, stream);
+}
+
+extern "C" int paged_attend_shared(const paged_attend_args *g, const paged_batch *prefix, void *stream) {
+    static const char *who = "paged_attend_shared";
+    if (!g) return fail(RING_EINVAL, "%s: args is NULL", who);
+    if (!prefix) return fail(RING_EINVAL, "%s: prefix is NULL", who);
+    return attend(who, g, prefix, stream);
 }
 
 extern "C" int paged_device_error(uint32_t *bits) {

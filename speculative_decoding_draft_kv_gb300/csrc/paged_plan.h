@@ -59,7 +59,7 @@ struct PagedShape {
 
     // a sequence whose lengths contradict each other has no tiles: its rows stay as they are
     __device__ __forceinline__ void load(const PagedAttendArgs &a, int s) {
-        q = paged_seq(a.batch, a.pool.page_shift, s);
+        q = paged_seq(a.batch, a.pool.page_shift, s, a.level == kPrefix);
         q.ok = q.ok && q.n <= a.max_q;
         if (!q.ok) q.n = 0;
         ctx = q.kv - q.n;
@@ -67,7 +67,7 @@ struct PagedShape {
     __device__ __forceinline__ int row_tiles(const PagedAttendArgs &a) const {
         return (q.n + a.tile_tokens - 1) / a.tile_tokens;
     }
-    // positions that some row of the tile sees lie in [lo, hi); 0 <= lo < hi
+    // positions that some row of the tile sees lie in [lo, hi); 0 <= lo < hi (a prefix may be empty)
     __device__ __forceinline__ int lo(const PagedAttendArgs &a, int rt) const {
         if (a.window == 0) return 0;
         return max(0, a.mask == PAGED_CAUSAL ? ctx + rt * a.tile_tokens - a.window + 1 : ctx - a.window);
@@ -283,6 +283,11 @@ struct PagedWalk {
             if (nt > 0) return true;
         }
         return false;
+    }
+    // an item's first piece of one of two passes: where the join finds its states
+    __device__ __forceinline__ void note(const PagedAttendArgs &a) const {
+        a.level_items[(int64_t)(sh.q.row0 + rt * a.tile_tokens) * a.pool.n_head_kv + head] =
+            make_int2((int)blockIdx.x, last ? -1 : last_cta());
     }
     // the CTA that has the item's last tile (a piece that leaves some ends its CTA's share)
     __device__ __forceinline__ int last_cta() const { return (int)blockIdx.x + (rest + per - 1) / per; }

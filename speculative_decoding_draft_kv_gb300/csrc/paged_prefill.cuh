@@ -1004,12 +1004,18 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     m = mm;
                     if (kCodes) add *= *odd_ref;
                 }
-                const bool whole = w.first && w.last;
+                const bool uncut = w.first && w.last, whole = uncut && a.level == kOnly;
                 const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
                 const int head = w.head * a.group + f - tok * a.group;
                 const int64_t part = ((int64_t)blockIdx.x * 2 + (w.first ? 1 : 0)) * a.tile_rows + local;
                 uint16_t *o = a.o + (int64_t)(q.row0 + tok) * a.o_rs + (int64_t)head * a.o_hs;
                 float *acc = a.part_acc + part * D;
+                float2 *ml = a.part_ml + part;
+                if (uncut && !whole) {
+                    const int64_t at = (int64_t)(q.row0 + tok) * a.n_head + head;
+                    acc = a.level_acc + at * D;
+                    ml = a.level_ml + at;
+                }
                 if (whole) {
                     keep *= inv;
                     add *= inv;
@@ -1047,7 +1053,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                             a.lse[(int64_t)(q.row0 + tok) * a.n_head + head] =
                                 l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
                     } else {
-                        a.part_ml[part] = make_float2(m, l);
+                        *ml = make_float2(m, l);
                     }
                 }
                 tc_fence_before();
@@ -1057,6 +1063,7 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 __syncwarp();
                 if (lane == 0) mbar_arrive(odd_free);
             }
+            if (a.level != kOnly && threadIdx.x == 0 && w.first) w.note(a);
             if (threadIdx.x == 0 && w.first && !w.last) {
                 began = true;
                 a.desc[blockIdx.x] = make_int4(w.seq, w.head, w.rt, w.last_cta());
@@ -1071,6 +1078,8 @@ k_paged_prefill(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     if (warp == 9) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
+        // (the second of two passes begins beside the first: what waits for it waits for both)
+        if (a.level == kOwn) pdl_wait();
     }
 }
 

@@ -47,9 +47,8 @@ template <int T>
 cudaError_t launch_paged_prefill_t(const PagedAttendArgs &a, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                                    const CUtensorMap &tm_q, int head_dim, cudaStream_t st) {
     return pick_prefill<T>(head_dim, a.pool.format, a.tile_rows <= 128, [&](auto kernel, int smem, int threads, int) {
-        kernel<<<a.ctas, threads, smem, st>>>(tm_k, tm_v, tm_q, a);
-        const cudaError_t e = cudaGetLastError();
-        return e == cudaSuccess ? launch_join<T, 1>(a, head_dim, st) : e;
+        const cudaError_t e = launch_pass(kernel, a, threads, smem, st, tm_k, tm_v, tm_q, a);
+        return e == cudaSuccess && a.level == kOnly ? launch_join<T, 1>(a, head_dim, st) : e;
     });
 }
 

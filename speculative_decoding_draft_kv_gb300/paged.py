@@ -28,7 +28,7 @@ _TYPES = {torch.float16: PAGED_F16, torch.bfloat16: PAGED_BF16, torch.float32: P
           torch.int8: PAGED_INT8, torch.float8_e4m3fn: PAGED_E4M3}
 
 EXPORTED = ("paged_rope_init", "paged_norm_rope", "paged_append", "paged_gather", "paged_attend", "paged_attend_workspace",
-            "paged_device_error", "paged_last_error")
+            "paged_attend_shared", "paged_attend_shared_workspace", "paged_device_error", "paged_last_error")
 
 _vp, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 
@@ -91,6 +91,8 @@ def _load():
             fn.argtypes, fn.restype = [_vp, _vp], ctypes.c_int
         lib.paged_rope_init.argtypes = [_vp, ctypes.POINTER(ctypes.c_double), ctypes.c_double, _i32, _i32]
         lib.paged_attend_workspace.argtypes = [_vp, _vp, _i32, ctypes.POINTER(_i64)]
+        lib.paged_attend_shared.argtypes = [_vp, _vp, _vp]
+        lib.paged_attend_shared_workspace.argtypes = [_vp, _vp, _vp, _i64, _i32, ctypes.POINTER(_i64)]
         lib.paged_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint32)]
         lib.paged_last_error.restype = ctypes.c_char_p
         _LIB = lib
@@ -376,6 +378,13 @@ def paged_attend(cache, batch, q, o, mask="causal", window=0, scale=0.0, tree=No
     token); ``window``: 0 or the length of a sliding window; ``lse``: None or float32
     [rows, n_head].  ``workspace``: a uint8 tensor of :func:`paged_attend_workspace` bytes that no
     other call uses at the same time, or None for one of the call's own from PyTorch's allocator."""
+    a, st = _attend_args(cache, batch, q, o, mask, window, scale, tree, lse, workspace, stream,
+                         lambda n, heads: paged_attend_workspace(cache, batch, heads))
+    _check(_load().paged_attend(ctypes.addressof(a), st))
+
+
+def _attend_args(cache, batch, q, o, mask, window, scale, tree, lse, workspace, stream, size):
+    """(the call's struct, stream); size(rows, heads): bytes of workspace."""
     dev = _one_device(cache, batch)
     dtype, (n, heads, _) = q.dtype, q.shape
     qp, qr, qh = _rows(q, "q", n, heads, cache.head_dim, _half(dtype), dev)
@@ -385,10 +394,31 @@ def paged_attend(cache, batch, q, o, mask="causal", window=0, scale=0.0, tree=No
     if not 0 <= window < 1 << 31:
         raise ValueError(f"window {window} out of range")
     st = _stream(stream, dev)
-    workspace = _workspace(workspace, lambda: paged_attend_workspace(cache, batch, heads), st, stream, dev, q.device)
-    a = PagedAttendArgs(cache.address, batch.address, qp, op, qr, qh, orow, oh, tp, lp, workspace.data_ptr(),
-                        workspace.numel(), n, scale, heads, _TYPES[dtype], MASKS.get(mask, mask), window, 0)
-    _check(_load().paged_attend(ctypes.addressof(a), st))
+    workspace = _workspace(workspace, lambda: size(n, heads), st, stream, dev, q.device)
+    return PagedAttendArgs(cache.address, batch.address, qp, op, qr, qh, orow, oh, tp, lp, workspace.data_ptr(),
+                           workspace.numel(), n, scale, heads, _TYPES[dtype], MASKS.get(mask, mask), window, 0), st
+
+
+def paged_attend_shared_workspace(cache, batch, prefix, n_rows, n_head) -> int:
+    """Bytes of workspace that :func:`paged_attend_shared` needs."""
+    _one_device(cache, batch)
+    _one_device(cache, prefix)
+    n = _i64()
+    _check(_load().paged_attend_shared_workspace(cache.address, batch.address, prefix.address, int(n_rows), int(n_head),
+                                                 ctypes.byref(n)))
+    return n.value
+
+
+def paged_attend_shared(cache, batch, prefix, q, o, mask="causal", scale=0.0, tree=None, lse=None, workspace=None,
+                        stream=None):
+    """:func:`paged_attend` for sequences that share beginnings: ``batch`` describes what each has of its own (``kv_len``
+    and ``pages`` count from behind the beginning), ``prefix`` -- a :class:`PagedBatch` too -- the beginnings:
+    ``q_start``: bounds of the rows that have each one, ``kv_len``: their lengths, ``pages``: where they lie; ``max_q``:
+    bound of one's rows."""
+    _one_device(cache, prefix)
+    a, st = _attend_args(cache, batch, q, o, mask, 0, scale, tree, lse, workspace, stream,
+                         lambda n, heads: paged_attend_shared_workspace(cache, batch, prefix, n, heads))
+    _check(_load().paged_attend_shared(ctypes.addressof(a), prefix.address, st))
 
 
 def paged_device_error() -> int:
