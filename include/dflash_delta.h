@@ -32,7 +32,8 @@ extern "C" {
 /* Bits of the device error word. */
 enum {
     DELTA_ERR_BATCH = 1, /* row bounds that decrease, pass the rows, or hold more than max_q */
-    DELTA_ERR_SLOT = 2   /* a slot number past the pool                                       */
+    DELTA_ERR_SLOT = 2,  /* a slot number past the pool                                       */
+    DELTA_ERR_WAIT = 4   /* a wait inside a kernel ran out (2 s); the call's output is not valid */
 };
 
 /*
@@ -63,6 +64,8 @@ typedef struct delta_state {
  *             state behind its last accepted token.)
  *   max_q     upper bound of the sequences' new tokens, now and at every replay of a captured
  *             call.
+ * Sequences that have rows in common (bounds that decrease between them, which is reported) may end
+ * with anything.
  * A slot that one sequence writes may be read by that sequence, as its slot_in, and by no
  * other of the call; a slot that is written twice holds either state, or rows of both.
  */
@@ -91,7 +94,7 @@ typedef struct delta_batch {
  * two 16-bit parts, 22 bits together.  Keys that are not normalised want beta |k|^2 of at most 2, as the
  * recurrence itself does: beyond, it grows with every token.
  * An infinity or NaN in a token's rows reaches the token's value elements (in v) or all of its head (in the
- * others) from there on, and where max_q is above 8 the same elements of up to 63 tokens in front of it.
+ * others) from there on, and where max_q is above 8 the same elements of up to 31 tokens in front of it.
  * A sequence whose row bounds contradict each other (DELTA_ERR_BATCH), or whose slot_in is past the pool
  * (DELTA_ERR_SLOT), is left alone: its rows of o and its slots stay as they were.  A slot past
  * the pool in slot_out or save is not written (DELTA_ERR_SLOT).

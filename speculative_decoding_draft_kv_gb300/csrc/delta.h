@@ -24,7 +24,15 @@ struct DeltaArgs {
     float scale, eps;
     int n_seq, max_q, n_slots, n_head, n_head_k, group;   // group: heads of a key head
     int normalise;
+    // chunks of many tokens: what k_delta_prep leaves for k_delta_scan
+    uint8_t *tiles;                      // [chunks][n_head_k][K, Q] F16 tiles of 32 rows
+    uint8_t *heads;                      // [chunks][n_head] blocks of kDeltaHeadBytes
 };
+
+constexpr int kDeltaChunk = 32;          // tokens
+constexpr int kDeltaHeadBytes = 2 * 6 * 32 * 16 + 2 * 16 * 16 + 32 * 4 + 16;
+// Chunks, with room for each sequence's ragged last one: sequence s has those from q_start[s] / 32 + s on.
+inline int64_t delta_chunks(int64_t n_rows, int n_seq) { return n_rows / kDeltaChunk + n_seq; }
 
 constexpr float kDeltaLeast = -1e4f;     // log decays below it count as it: exp() of both is 0
 
@@ -45,6 +53,8 @@ __device__ __forceinline__ DeltaSeq delta_seq(const DeltaArgs &a, int s, uint32_
     return q;
 }
 
+cudaError_t delta_chunk_setup();
+cudaError_t launch_delta_chunk(const DeltaArgs &a, int dtype, int dim_k, int dim_v, int sms, cudaStream_t st);
 cudaError_t launch_delta_step(const DeltaArgs &a, int dtype, int dim_k, int dim_v, cudaStream_t st);
 
 }  // namespace dflash

@@ -1,0 +1,747 @@
+// The gated delta rule over many tokens: 32 at a time, as matrix products.
+//
+// With G_i the sum of a chunk's log decays up to token i, S the state in front of the chunk, and every
+// sum over tokens of the chunk, the recurrence's updates are the solution of a triangular system,
+//   u_i = beta_i (v_i - exp(G_i) S k_i) - sum_{j<i} beta_i exp(G_i - G_j) (k_i . k_j) u_j,
+// so U = T R with R = beta (V - exp(G) K S^T) and T the inverse of a unit lower triangular 32 x 32 matrix
+// that does not depend on S.  Then
+//   o_i = exp(G_i) S q_i + sum_{j<=i} exp(G_i - G_j) (q_i . k_j) u_j,
+//   S  <- exp(G_last) S + sum_j u_j (exp(G_last - G_j) k_j)^T.
+//
+// k_delta_prep does what the state is not needed for, all chunks at once: norms, keys and queries as F16
+// tiles, k . k and q . k, decays, T.  k_delta_scan walks a sequence's chunks with the state in registers.
+// A warp has 16 value elements (rows of S) and shares nothing with the others: S as the A operand of
+// S [K Q]^T, U of U T^T, U A^T and U K, are accumulators of the product before, in the same layout
+// (mma.sync m16n8k16; its accumulators feed the next product without leaving the thread, where tensor
+// memory would be written, fenced and read between any two of the four dependent products of a chunk).
+//
+// Precision.  The state, its update and all sums are float32.  Operands are F16 pairs hi + lo, 22 bits together,
+// after powers of two that bring the largest value of a warp's operand to [2^12, 2^13); keys and queries are
+// one F16 each: exact for F16 rows, and for bf16 rows after a power of two by the row's norm (elements below
+// 2^-14 of the norm are off by 2^-25 of it at most).  What a product adds up starts at zero and joins the
+// state by one fused multiply-add: tensor-core sums are cut off, not rounded, and hundreds of chunks would
+// add that up.  Decays are exponentials of sums over just the tokens between, in two float32 parts, so neither
+// a long chunk nor a state that was dropped costs later tokens their precision.
+#include "delta.h"
+
+#include "ring_internal.h"
+#include "ptx.h"
+#include "paged_ptx.h"
+
+#include <type_traits>
+
+namespace dflash {
+namespace {
+
+constexpr int C = kDeltaChunk;                         // tokens of a chunk
+static_assert(C == 32, "a lane per token");
+
+template <int T> __device__ __forceinline__ float from16(uint32_t x) {
+    if constexpr (T == PAGED_F16) return __half2float(__ushort_as_half((unsigned short)x));
+    else return __uint_as_float(x << 16);
+}
+__device__ __forceinline__ float2 half2_floats(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2 *>(&x)); }
+
+// byte offset of 16-byte chunk ch of row r in a tile of DK F16 columns: conflict-free for ldmatrix
+template <int DK> __device__ __forceinline__ uint32_t tile_at(int r, int ch) { return (uint32_t)(r * DK * 2 + ((ch ^ (r & 7)) << 4)); }
+
+// Of T or A, the (token tile, key step) blocks with something in them, in the order of use.
+constexpr int kBlocks = 6;
+__host__ __device__ constexpr int block_n(int b) { return b < 4 ? b : b - 2; }     // 0 1 2 3 2 3
+__host__ __device__ constexpr int block_k(int b) { return b < 4 ? 0 : 1; }
+
+// A head's part of a chunk in the workspace: B operands a lane's words beside one another, then scalars.
+struct HeadBlock {
+    uint4 t[kBlocks][32];                              // T: hi, hi, lo, lo
+    uint4 a[kBlocks][32];                              // exp(G_i - G_j) q_i . k_j: likewise
+    float4 r[C / 2];                                   // of tokens 2i, 2i+1: beta, beta exp(G) |k|
+    float4 o[C / 2];                                   // |q|, |q| exp(G)
+    float w[C];                                        // exp(G_last - G) |k|
+    float last, t_unit, a_unit, pad;                   // exp(G_last); what T and A are to be multiplied by
+};
+static_assert(sizeof(HeadBlock) == kDeltaHeadBytes, "as the workspace is laid out");
+
+__device__ __forceinline__ int chunk_base(int row0, int s) { return row0 / C + s; }
+
+// the power of two that brings m > 0 (as bits) to [2^12, 2^13), as far as float32 has it and its inverse
+__device__ __forceinline__ float unit_of(uint32_t bits) {
+    const int e = (int)(bits >> 23);                   // biased
+    return bits == 0u || e == 255 ? 1.f : __uint_as_float((uint32_t)min(241, max(13, 254 + 12 - e)) << 23);
+}
+__device__ __forceinline__ float inverse_unit(float u) { return __uint_as_float((254u << 23) - __float_as_uint(u)); }
+
+// x0, x1 times a power of two as two F16 pairs
+__device__ __forceinline__ void split(float x0, float x1, float unit, uint32_t &hi, uint32_t &lo) {
+    x0 *= unit;
+    x1 *= unit;
+    hi = pack_half2(x0, x1);
+    const float2 h = half2_floats(hi);
+    lo = pack_half2(x0 - h.x, x1 - h.y);
+}
+
+// ---------------------------------------------------------------- what the state is not needed for
+
+template <int T, int DK>
+__global__ void __launch_bounds__(128, 5)
+k_delta_prep(const __grid_constant__ DeltaArgs a) {
+    // K and Q, then two heads' systems and A
+    __shared__ __align__(128) union {
+        uint8_t tile[2][C * DK * 2];
+        float la[2][2][C * 36];
+    } s;
+    __shared__ float s_kk[C * 32], s_qk[C * 32];
+    __shared__ float s_kn[C], s_qn[C];                             // what the F16 rows are to be multiplied by
+    __shared__ uint32_t s_amax[2][2];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int hk = blockIdx.x % a.n_head_k, at = blockIdx.x / a.n_head_k;
+    pdl_trigger();
+    // the last sequence whose chunks begin at this one or in front of it
+    int seq = 0, end = a.n_seq;
+    while (end - seq > 1) {
+        const int mid = (seq + end) >> 1;
+        if (chunk_base(a.q_start[mid], mid) <= at) seq = mid;
+        else end = mid;
+    }
+    uint32_t bits;
+    const DeltaSeq q = delta_seq(a, seq, bits);
+    const int t0 = (at - chunk_base(q.row0, seq)) * C;
+    if (!q.ok || t0 < 0 || t0 >= q.n) return;
+    const int nv = min(C, q.n - t0);
+
+    {   // rows: four lanes to one, eight rows to a warp
+        const int r = warp * 8 + (lane >> 2), p = lane & 3;
+        constexpr int N = DK / 32;                                 // 16-byte pieces of a lane
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            uint4 x[N];
+            float ss = 0.f;
+#pragma unroll
+            for (int j = 0; j < N; ++j) x[j] = make_uint4(0, 0, 0, 0);
+            if (r < nv) {
+                const int64_t row = q.row0 + t0 + r;
+                const uint16_t *src = w ? a.q + row * a.q_rs + (int64_t)hk * a.q_hs : a.k + row * a.k_rs + (int64_t)hk * a.k_hs;
+#pragma unroll
+                for (int j = 0; j < N; ++j) x[j] = *reinterpret_cast<const uint4 *>(src + (p + 4 * j) * 8);
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const uint32_t v[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float f0 = from16<T>(v[e] & 0xffffu), f1 = from16<T>(v[e] >> 16);
+                    ss = fmaf(f0, f0, ss);
+                    ss = fmaf(f1, f1, ss);
+                }
+            }
+            ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+            ss += __shfl_xor_sync(0xffffffffu, ss, 2);
+            float norm = a.normalise ? 1.f / sqrtf(ss + a.eps) : 1.f;
+            if (T == PAGED_BF16) {
+                // to a norm in [1, 2) by a power of two; a square sum past float32 makes the row 0, as its norm does
+                const uint32_t e = __float_as_uint(sqrtf(ss)) >> 23;
+                float down = e == 0u ? 1.f : (e == 255u ? 0x1p-126f : __uint_as_float((254u - min(e, 253u)) << 23));
+                if (e == 255u && a.normalise) down = 0.f;
+                norm = r < nv ? norm * (e == 0u || down == 0.f ? 1.f : __uint_as_float((254u << 23) - __float_as_uint(down))) : 0.f;
+                if (down == 0.f) norm = 1.f;
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    uint32_t v[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+                    for (int e2 = 0; e2 < 4; ++e2)
+                        v[e2] = pack_half2(from16<T>(v[e2] & 0xffffu) * down, from16<T>(v[e2] >> 16) * down);
+                    x[j] = make_uint4(v[0], v[1], v[2], v[3]);
+                }
+            }
+            uint8_t *tile = a.tiles + (((int64_t)at * a.n_head_k + hk) * 2 + w) * (C * DK * 2);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const uint32_t off = tile_at<DK>(r, p + 4 * j);
+                *reinterpret_cast<uint4 *>(s.tile[w] + off) = x[j];
+                *reinterpret_cast<uint4 *>(tile + off) = x[j];
+            }
+            if (p == 0) (w ? s_qn : s_kn)[r] = r < nv ? (w ? norm * a.scale : norm) : 0.f;
+        }
+    }
+    __syncthreads();
+    {   // k . k and q . k: a warp has eight columns
+        // K, Q; rows 0-15, 16-31; two sums, each cut off half as often
+        float acc[2][2][2][4] = {};
+        const uint32_t k0 = smem_u32(s.tile[0]), q0 = smem_u32(s.tile[1]);
+#pragma unroll
+        for (int ks = 0; ks < DK / 16; ++ks) {
+            uint32_t b[4], f[4];
+            // (two of the four matrices are this step's, the rest the next one's: fetched anew, for plainness)
+            ldsm_x4(k0 + tile_at<DK>(warp * 8 + (lane & 7), ks * 2 + ((lane >> 3) & 1)), b[0], b[1], b[2], b[3]);
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    if (m == 0 && warp >= 2) continue;             // above the diagonal
+                    ldsm_x4((w ? q0 : k0) + tile_at<DK>(m * 16 + (lane & 15), ks * 2 + (lane >> 4)), f[0], f[1], f[2], f[3]);
+                    mma16816(acc[w][m][ks & 1], f, b[0], b[1]);
+                }
+        }
+        const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    (w ? s_qk : s_kk)[(m * 16 + g + 8 * (e >> 1)) * 32 + warp * 8 + 2 * t + (e & 1)] = acc[w][m][0][e] + acc[w][m][1][e];
+    }
+    __syncthreads();
+    // heads of this key head, two at a time: two warps to one, a lane per token
+    const int i = lane, role = warp & 1;
+    float *l = s.la[warp >> 1][0], *am = s.la[warp >> 1][1];
+    const float kn = s_kn[i], qn = s_qn[i];
+    for (int h0 = 0; h0 < a.group; h0 += 2) {
+        const int hh = h0 + (warp >> 1), h = hk * a.group + hh;
+        const bool mine = hh < a.group;
+        float g = 0.f, beta = 0.f;
+        if (mine && i < nv) {
+            const int64_t row = q.row0 + t0 + i;
+            g = a.g[row * a.g_rs + h];
+            if (g < kDeltaLeast) g = kDeltaLeast;
+            beta = a.beta[row * a.beta_rs + h];
+        }
+        if (h0) __syncthreads();                                   // the heads before these are written
+        // exp(G_i - G_j) for j = i - d, each warp half of the d: sums over just the tokens between, in two parts
+        float sum = 0.f, rest = 0.f, left = 0.f, amax = 0.f;
+        const float bk = beta * kn;
+        auto add = [&](int d) {
+            const float next = __shfl_up_sync(0xffffffffu, g, d);
+            if (i >= d) {
+                const float y = sum + next, z = y - sum;
+                rest += (sum - (y - z)) + (next - z);
+                sum = y;
+            }
+        };
+        if (role)
+            for (int d = 0; d < C / 2; ++d) add(d);
+#pragma unroll 4
+        for (int d = role * (C / 2); d < (role + 1) * (C / 2); ++d) {
+            const float e = expf(sum), decay = fmaf(e, rest, e);
+            const float last = __shfl_sync(0xffffffffu, decay, C - 1);
+            if (i == C - 1 - d) left = last;
+            if (i >= d) {
+                const int j = i - d;
+                const float dk = decay * s_kn[j];
+                const float x = dk * s_qk[i * 32 + j];
+                l[i * 36 + j] = bk * dk * s_kk[i * 32 + j];
+                am[i * 36 + j] = x;
+                amax = fmaxf(amax, fabsf(x));
+            } else {
+                am[i * 36 + i + C - d] = 0.f;
+            }
+            add(d);
+        }
+        HeadBlock *out = reinterpret_cast<HeadBlock *>(a.heads + ((int64_t)at * a.n_head + h) * kDeltaHeadBytes);
+        if (role == 0) {
+            if (mine && i >= C / 2) out->w[i] = left * kn;         // j = 31 - d
+            for (int d = C / 2; d < C; ++d) add(d);
+        } else if (mine && i < C / 2) {
+            out->w[i] = left * kn;
+        }
+        const float e = expf(sum), gone = fmaf(e, rest, e);        // exp(G_i)
+        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
+        if (lane == 0) s_amax[warp >> 1][role] = top;
+        __syncthreads();
+        if (!mine) continue;                                       // (the last round)
+        const int gq = lane >> 2, tq = lane & 3;
+        auto blocks = [&](const float *from, float unit, uint4 (*to)[32]) {
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                const float *src = from + (block_n(b) * 8 + gq) * 36 + block_k(b) * 16 + 2 * tq;
+                const float2 lo = *reinterpret_cast<const float2 *>(src), hi = *reinterpret_cast<const float2 *>(src + 8);
+                uint4 v;
+                split(lo.x, lo.y, unit, v.x, v.z);
+                split(hi.x, hi.y, unit, v.y, v.w);
+                to[b][lane] = v;
+            }
+        };
+        if (role) {
+            const float au = unit_of(max(s_amax[warp >> 1][0], s_amax[warp >> 1][1]));
+            blocks(am, au, out->a);
+            reinterpret_cast<float2 *>(out->r)[i] = make_float2(beta, bk * gone);
+            reinterpret_cast<float2 *>(out->o)[i] = make_float2(qn, qn * gone);
+            if (i == C - 1) {
+                out->last = gone;
+                out->a_unit = inverse_unit(au);
+            }
+            continue;
+        }
+        // T by columns: a lane has one
+        float x[C];
+        float tmax = 0.f;
+#pragma unroll
+        for (int r = 0; r < C; ++r) {
+            float y0 = r == i ? 1.f : 0.f, y1 = 0.f, y2 = 0.f, y3 = 0.f;
+#pragma unroll
+            for (int m = 0; m < r; m += 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(l + r * 36 + m);
+                y0 = fmaf(-f.x, x[m], y0);
+                if (m + 1 < r) y1 = fmaf(-f.y, x[m + 1], y1);
+                if (m + 2 < r) y2 = fmaf(-f.z, x[m + 2], y2);
+                if (m + 3 < r) y3 = fmaf(-f.w, x[m + 3], y3);
+            }
+            x[r] = (y0 + y1) + (y2 + y3);
+            tmax = fmaxf(tmax, fabsf(x[r]));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int r = 0; r < C; ++r) l[r * 36 + i] = x[r];
+        const float tu = unit_of(__reduce_max_sync(0xffffffffu, __float_as_uint(tmax)));
+        __syncwarp();
+        blocks(l, tu, out->t);
+        if (i == 0) out->t_unit = inverse_unit(tu);
+    }
+}
+
+// ---------------------------------------------------------------- the state's walk
+
+// W groups of 16 value elements to a CTA, KS warps to a group: each has DK / KS of the key elements.
+template <int DK, int W, int KS>
+struct ScanCfg {
+    static constexpr int kWarps = W * KS;
+    static constexpr int kThreads = (kWarps + 1) * 32;
+    static constexpr int kTileBytes = 2 * C * DK * 2;
+    static constexpr int kStageBytes = kTileBytes + kDeltaHeadBytes;
+    static constexpr int kVBytes = C * 32;                         // [C tokens][16 values], two to a warp
+    static constexpr int kXWords = KS == 2 ? 24 * 32 : 0;          // what a warp hands its partner, twice
+    // (one CTA per SM where few are wanted: several would find room beside one another, and slow each other
+    // down, while other SMs have none)
+    static constexpr int kStages = KS == 2 ? (DK == 128 ? 6 : 9) : (DK == 128 ? 3 : 4);
+    static constexpr int kOffV = kStages * kStageBytes;
+    static constexpr int kOffX = kOffV + kWarps * 2 * kVBytes;
+    static constexpr int kOffBars = kOffX + kWarps * 2 * kXWords * 4;
+    static constexpr int kSmem = kOffBars + 2 * kStages * 8;
+    static_assert(kSmem <= 227 * 1024, "");
+};
+
+__device__ __forceinline__ uint32_t v_at(int r, int half) { return (uint32_t)(r * 32 + ((half ^ ((r >> 2) & 1)) << 4)); }
+
+__device__ __forceinline__ void stsm_x4_t(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r0), "r"(r1), "r"(r2),
+                 "r"(r3) : "memory");
+}
+
+template <int N> __device__ __forceinline__ float top_of(const float (&x)[N][4]) {
+    float m = 0.f;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m = fmaxf(m, fabsf(x[n][e]));  // (NaN is passed over)
+    return m;
+}
+
+// The unit for a warp's values, m the largest magnitude of this lane's: by the largest finite one of all.
+template <int N> __device__ __forceinline__ float warp_unit(const float (&x)[N][4], float m) {
+    uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+    if (top >= 0x7f800000u) {                                      // an infinity: the other rows go by what else there is
+        m = 0.f;
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (fabsf(x[n][e]) < INFINITY) m = fmaxf(m, fabsf(x[n][e]));
+        top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+    }
+    return unit_of(top);
+}
+
+// Accumulators of 32 columns as an A operand of two steps, in two parts, times a power of two.
+__device__ __forceinline__ void operand(const float (&x)[4][4], float unit, uint32_t (&hi)[2][4], uint32_t (&lo)[2][4]) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) split(x[n][2 * e], x[n][2 * e + 1], unit, hi[n >> 1][(n & 1) * 2 + e], lo[n >> 1][(n & 1) * 2 + e]);
+}
+
+template <int T, int DK, int W, int KS>
+__global__ void __launch_bounds__((W * KS + 1) * 32, KS == 1 ? 2 : 1)
+k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
+    using F = ScanCfg<DK, W, KS>;
+    constexpr int S = F::kStages, NT = DK / 8 / KS, STEPS = DK / 16 / KS;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const uint32_t full = smem_u32(smem + F::kOffBars), empty = full + 8 * S;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int part = blockIdx.x % parts, sh = blockIdx.x / parts, h = sh % a.n_head, s = sh / a.n_head;
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < S; ++k) {
+            mbar_init(full + 8 * k, 1);
+            mbar_init(empty + 8 * k, F::kWarps);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    uint32_t bits;
+    const DeltaSeq q = delta_seq(a, s, bits);
+    if (bits && threadIdx.x == 0 && h == 0 && part == 0) atomicOr(a.err, bits);
+    __syncthreads();
+    const int chunks = q.ok ? (q.n + C - 1) / C : 0;
+    const int64_t base = chunk_base(q.row0, s);
+    auto timed_out = [&]() { atomicOr(a.err, (uint32_t)DELTA_ERR_WAIT); };
+
+    if (warp == F::kWarps) {
+        // ---------------- copies ----------------
+        pdl_wait();                                                // the chunks are prepared
+        if (lane == 0) {
+            const int hk = h / a.group;
+            int c = 0;
+            for (; c < chunks; ++c) {
+                const int k = c % S;
+                if (!mbar_wait(empty + 8 * k, ((uint32_t)(c / S) & 1u) ^ 1u)) {
+                    timed_out();
+                    break;
+                }
+                const uint32_t dst = smem_u32(smem + k * F::kStageBytes);
+                mbar_expect_tx(full + 8 * k, F::kStageBytes);
+                bulk_g2s(dst, a.tiles + ((base + c) * a.n_head_k + hk) * F::kTileBytes, F::kTileBytes, full + 8 * k);
+                bulk_g2s(dst + F::kTileBytes, a.heads + ((base + c) * a.n_head + h) * kDeltaHeadBytes, kDeltaHeadBytes, full + 8 * k);
+            }
+            // no copy may land after the CTA is gone
+            for (int k = max(0, c - S); k < c; ++k)
+                if (!mbar_wait(full + 8 * (k % S), (uint32_t)(k / S) & 1u)) {
+                    timed_out();
+                    break;
+                }
+        }
+        __syncwarp();
+        return;
+    }
+    if (!q.ok) return;
+
+    // ---------------- the state ----------------
+    const int g = lane >> 2, t = lane & 3, kp = warp % KS;
+    const int row0 = (part * W + warp / KS) * 16;                  // the group's value elements: rows g and g + 8 of it
+    auto place = [&](int slot) {
+        return a.state + (int64_t)slot * a.slot_stride + (int64_t)h * a.head_stride + (int64_t)(row0 + g) * DK + kp * (DK / KS) + 2 * t;
+    };
+    float st[NT][4];
+    {
+        const float *src = q.slot < 0 ? nullptr : place(q.slot);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float2 x = make_float2(0.f, 0.f), y = x;
+            if (src) {
+                x = *reinterpret_cast<const float2 *>(src + n * 8);
+                y = *reinterpret_cast<const float2 *>(src + 8 * DK + n * 8);
+            }
+            st[n][0] = x.x; st[n][1] = x.y; st[n][2] = y.x; st[n][3] = y.y;
+        }
+    }
+    const uint32_t v0 = smem_u32(smem + F::kOffV + warp * 2 * F::kVBytes);
+    float *xs = reinterpret_cast<float *>(smem + F::kOffX) + lane;
+    // values of chunk c: two 16-byte pieces a token, zeros behind the last one
+    auto fetch_v = [&](int c) {
+        if (c < chunks) {
+            const int nv = min(C, q.n - c * C);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = (lane >> 1) + 16 * e, half = lane & 1;
+                const uint16_t *src = a.v + (int64_t)(q.row0 + c * C + min(r, nv - 1)) * a.v_rs + (int64_t)h * a.v_hs + row0 + half * 8;
+                cp_async16(v0 + (c & 1) * F::kVBytes + v_at(r, half), src, r < nv ? 16 : 0);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    fetch_v(0);
+    bool alive = true;
+    float smax = top_of<NT>(st);                                   // this lane's
+    for (int c = 0; c < chunks; ++c) {
+        const int k = c % S, nv = min(C, q.n - c * C);
+        __syncwarp();                                              // the other half's outputs are on their way
+        fetch_v(c + 1);
+        // S in units of a power of two
+        const float su = warp_unit<NT>(st, smax), si = inverse_unit(su);
+        const bool here = __all_sync(0xffffffffu, mbar_wait(full + 8 * k, (uint32_t)(c / S) & 1u));
+        if (!here && lane == 0) timed_out();
+        if (KS == 1 && !here) {
+            alive = false;
+            break;
+        }
+        const uint32_t kt = smem_u32(smem + k * F::kStageBytes), qt = kt + C * DK * 2;
+        const HeadBlock *hb = reinterpret_cast<const HeadBlock *>(smem + k * F::kStageBytes + F::kTileBytes);
+        // S K^T and S Q^T: 16 value elements by 32 tokens each.  (lo's sum apart: it is small, and hi's is cut off half
+        // as often.)  bf16 outputs take S's hi alone for S Q^T: off by 2^-11 of the products, an eighth of their
+        // own rounding, for a seventh of a chunk's products.
+        float pk[4][4] = {}, pl[4][4] = {}, pq[4][4] = {};
+        uint32_t fk[2][2][4], fq[2][2][4];
+        auto fetch = [&](int ks) {
+#pragma unroll
+            for (int np = 0; np < 2; ++np) {
+                const uint32_t off = tile_at<DK>(np * 16 + (lane & 7) + ((lane >> 4) << 3), (kp * STEPS + ks) * 2 + ((lane >> 3) & 1));
+                uint32_t (&x)[4] = fk[ks & 1][np], (&y)[4] = fq[ks & 1][np];
+                ldsm_x4(kt + off, x[0], x[1], x[2], x[3]);
+                ldsm_x4(qt + off, y[0], y[1], y[2], y[3]);
+            }
+        };
+        fetch(0);
+#pragma unroll
+        for (int ks = 0; ks < STEPS; ++ks) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) split(st[2 * ks + (e >> 1)][2 * (e & 1)], st[2 * ks + (e >> 1)][2 * (e & 1) + 1], su, hi[e], lo[e]);
+            if (ks + 1 < STEPS) fetch(ks + 1);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) mma16816(pk[n], hi, fk[ks & 1][n >> 1][2 * (n & 1)], fk[ks & 1][n >> 1][2 * (n & 1) + 1]);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) mma16816(pl[n], lo, fk[ks & 1][n >> 1][2 * (n & 1)], fk[ks & 1][n >> 1][2 * (n & 1) + 1]);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) mma16816(pq[n], hi, fq[ks & 1][n >> 1][2 * (n & 1)], fq[ks & 1][n >> 1][2 * (n & 1) + 1]);
+            if (T == PAGED_F16) {
+#pragma unroll
+                for (int n = 0; n < 4; ++n) mma16816(pq[n], lo, fq[ks & 1][n >> 1][2 * (n & 1)], fq[ks & 1][n >> 1][2 * (n & 1) + 1]);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                pk[n][e] = (pk[n][e] + pl[n][e]) * si;
+                pq[n][e] *= si;
+            }
+        if constexpr (KS == 2) {
+            // the partner's half of the sums: of S K^T all, of S Q^T those of the 16 tokens whose outputs are this warp's
+            float *mine = xs + (warp * 2 + (c & 1)) * F::kXWords, *other = xs + ((warp ^ 1) * 2 + (c & 1)) * F::kXWords;
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mine[(n * 4 + e) * 32] = pk[n][e];
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mine[(16 + m * 4 + e) * 32] = kp ? pq[m][e] : pq[2 + m][e];
+            // (a wait that ran out in either: both leave)
+            if (bar_any(1 + warp / 2, 64, !here)) {
+                alive = false;
+                break;
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) pk[n][e] += other[(n * 4 + e) * 32];
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float x = other[(16 + m * 4 + e) * 32];
+                    if (kp) pq[2 + m][e] += x;
+                    else pq[m][e] += x;
+                }
+        }
+        // R = beta V - beta exp(G) |k| (S K^T)
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncwarp();
+        const uint32_t vt = v0 + (c & 1) * F::kVBytes;
+        float r[4][4];
+#pragma unroll
+        for (int np = 0; np < 2; ++np) {
+            uint32_t v[4];
+            ldsm_x4_t(vt + v_at(np * 16 + (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1), v[0], v[1], v[2], v[3]);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const int n = 2 * np + m;
+                const float4 f = hb->r[n * 4 + t];                 // beta, beta exp(G) |k| of tokens 8n + 2t, + 1
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float x0 = from16<T>(v[2 * m + e] & 0xffffu), x1 = from16<T>(v[2 * m + e] >> 16);
+                    r[n][2 * e] = fmaf(f.x, x0, -f.y * pk[n][2 * e]);
+                    r[n][2 * e + 1] = fmaf(f.z, x1, -f.w * pk[n][2 * e + 1]);
+                }
+            }
+        }
+        // U = R T^T
+        float u[4][4] = {};
+        uint32_t hi[2][4], lo[2][4];
+        {
+            uint4 f[kBlocks];
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) f[b] = hb->t[b][lane];
+            const float ru = warp_unit<4>(r, top_of<4>(r));
+            operand(r, ru, hi, lo);
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) mma16816(u[block_n(b)], hi[block_k(b)], f[b].x, f[b].y);
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) mma16816(u[block_n(b)], lo[block_k(b)], f[b].x, f[b].y);
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) mma16816(u[block_n(b)], hi[block_k(b)], f[b].z, f[b].w);
+            const float back = inverse_unit(ru) * hb->t_unit;
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) u[n][e] *= back;
+        }
+        // o = |q| (exp(G) S q + A u), of two warps of a group 16 tokens each
+        {
+            const float uu = warp_unit<4>(u, top_of<4>(u));
+            operand(u, uu, hi, lo);
+            float x[4][4] = {};
+            auto products = [&](auto first, auto last) {
+                constexpr int B0 = decltype(first)::value, B1 = decltype(last)::value;
+                uint4 f[B1 - B0];
+#pragma unroll
+                for (int b = B0; b < B1; ++b) f[b - B0] = hb->a[b][lane];
+#pragma unroll
+                for (int b = B0; b < B1; ++b) mma16816(x[block_n(b)], hi[block_k(b)], f[b - B0].x, f[b - B0].y);
+#pragma unroll
+                for (int b = B0; b < B1; ++b) mma16816(x[block_n(b)], lo[block_k(b)], f[b - B0].x, f[b - B0].y);
+#pragma unroll
+                for (int b = B0; b < B1; ++b) mma16816(x[block_n(b)], hi[block_k(b)], f[b - B0].z, f[b - B0].w);
+            };
+            using I0 = std::integral_constant<int, 0>;
+            using I2 = std::integral_constant<int, 2>;
+            using I6 = std::integral_constant<int, 6>;
+            const float back = inverse_unit(uu) * hb->a_unit;
+            // through the values' place, which has been read, into rows
+            auto rows = [&](auto half) {
+                constexpr int NP = decltype(half)::value;
+                uint32_t o16[2][2];
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const int n = 2 * NP + m;
+                    const float4 f = hb->o[n * 4 + t];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float y0 = fmaf(f.x, x[n][2 * e] * back, f.y * pq[n][2 * e]);
+                        const float y1 = fmaf(f.z, x[n][2 * e + 1] * back, f.w * pq[n][2 * e + 1]);
+                        o16[m][e] = T == PAGED_F16 ? pack_half2(y0, y1) : pack_bf162(y0, y1);
+                    }
+                }
+                stsm_x4_t(vt + v_at(NP * 16 + (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1), o16[0][0], o16[0][1], o16[1][0], o16[1][1]);
+                __syncwarp();
+                const int row = NP * 16 + (lane >> 1), piece = lane & 1;
+                uint4 y;
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w) : "r"(vt + v_at(row, piece)));
+                if (row < nv)
+                    *reinterpret_cast<uint4 *>(a.o + (int64_t)(q.row0 + c * C + row) * a.o_rs + (int64_t)h * a.o_hs + row0 + piece * 8) = y;
+            };
+            if constexpr (KS == 1) {
+                products(I0{}, I6{});
+                __syncwarp();
+                rows(std::integral_constant<int, 0>{});
+                rows(std::integral_constant<int, 1>{});
+            } else if (kp) {
+                products(I2{}, I6{});
+                __syncwarp();
+                rows(std::integral_constant<int, 1>{});
+            } else {
+                products(I0{}, I2{});
+                __syncwarp();
+                rows(std::integral_constant<int, 0>{});
+            }
+        }
+        // S <- exp(G_last) S + U (exp(G_last - G) |k| K)
+        {
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const float2 f = *reinterpret_cast<const float2 *>(&hb->w[n * 8 + 2 * t]);
+                u[n][0] *= f.x; u[n][1] *= f.y; u[n][2] *= f.x; u[n][3] *= f.y;
+            }
+            const float uu = warp_unit<4>(u, top_of<4>(u)), back = inverse_unit(uu), last = hb->last;
+            operand(u, uu, hi, lo);
+            smax = 0.f;
+            // four key tiles at a time, their operands fetched ahead
+            uint32_t f[2][2][2][4];                                // [buffer][step][pair of tiles]
+            auto fetch_k = [&](int n4) {
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        uint32_t (&x)[4] = f[n4 & 1][ks][p];
+                        ldsm_x4_t(kt + tile_at<DK>(ks * 16 + (lane & 15), kp * NT + n4 * 4 + p * 2 + (lane >> 4)), x[0], x[1], x[2], x[3]);
+                    }
+            };
+            fetch_k(0);
+#pragma unroll
+            for (int n4 = 0; n4 < NT / 4; ++n4) {
+                if (n4 + 1 < NT / 4) fetch_k(n4 + 1);
+                float x[4][4] = {};
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) mma16816(x[m], hi[ks], f[n4 & 1][ks][m >> 1][2 * (m & 1)], f[n4 & 1][ks][m >> 1][2 * (m & 1) + 1]);
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) mma16816(x[m], lo[ks], f[n4 & 1][ks][m >> 1][2 * (m & 1)], f[n4 & 1][ks][m >> 1][2 * (m & 1) + 1]);
+                }
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float &y = st[4 * n4 + m][e];
+                        y = fmaf(x[m][e], back, last * y);
+                        smax = fmaxf(smax, fabsf(y));
+                    }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty + 8 * k);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    const int out = a.slot_out[s];
+    if (!alive || out < 0) return;
+    if (out >= a.n_slots) {
+        if (threadIdx.x == 0 && h == 0 && part == 0) atomicOr(a.err, (uint32_t)DELTA_ERR_SLOT);
+        return;
+    }
+    float *dst = place(out);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        *reinterpret_cast<float2 *>(dst + n * 8) = make_float2(st[n][0], st[n][1]);
+        *reinterpret_cast<float2 *>(dst + 8 * DK + n * 8) = make_float2(st[n][2], st[n][3]);
+    }
+}
+
+template <int T, int DK, int W, int KS>
+cudaError_t scan(const DeltaArgs &a, int dv, cudaStream_t st) {
+    using F = ScanCfg<DK, W, KS>;
+    const int parts = dv / (16 * W);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((int64_t)a.n_seq * a.n_head * parts), 1, 1);
+    cfg.blockDim = dim3(F::kThreads);
+    cfg.dynamicSmemBytes = F::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_delta_scan<T, DK, W, KS>, a, parts);
+}
+
+template <int T, int DK>
+cudaError_t go(const DeltaArgs &a, int dv, int sms, cudaStream_t st) {
+    const int64_t chunks = delta_chunks(a.n_rows, a.n_seq);
+    k_delta_prep<T, DK><<<(unsigned)(chunks * a.n_head_k), 128, 0, st>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    // few sequences times heads: more and smaller CTAs
+    if ((int64_t)a.n_seq * a.n_head * dv / 32 > sms) return scan<T, DK, 4, 1>(a, dv, st);
+    return scan<T, DK, 2, 2>(a, dv, st);
+}
+
+template <int T, int DK, int W, int KS> cudaError_t allow() {
+    return cudaFuncSetAttribute(k_delta_scan<T, DK, W, KS>, cudaFuncAttributeMaxDynamicSharedMemorySize, ScanCfg<DK, W, KS>::kSmem);
+}
+template <int T> cudaError_t allow_all() {
+    cudaError_t e = allow<T, 64, 2, 2>();
+    if (e == cudaSuccess) e = allow<T, 64, 4, 1>();
+    if (e == cudaSuccess) e = allow<T, 128, 2, 2>();
+    if (e == cudaSuccess) e = allow<T, 128, 4, 1>();
+    return e;
+}
+
+}  // namespace
+
+cudaError_t delta_chunk_setup() {
+    const cudaError_t e = allow_all<PAGED_F16>();
+    return e == cudaSuccess ? allow_all<PAGED_BF16>() : e;
+}
+
+cudaError_t launch_delta_chunk(const DeltaArgs &a, int dtype, int dim_k, int dim_v, int sms, cudaStream_t st) {
+    if (dtype == PAGED_F16) return dim_k == 64 ? go<PAGED_F16, 64>(a, dim_v, sms, st) : go<PAGED_F16, 128>(a, dim_v, sms, st);
+    return dim_k == 64 ? go<PAGED_BF16, 64>(a, dim_v, sms, st) : go<PAGED_BF16, 128>(a, dim_v, sms, st);
+}
+
+}  // namespace dflash

@@ -14,7 +14,8 @@ __device__ uint32_t g_delta_err;
 
 constexpr int kMaxDevices = 64;
 struct DeviceInfo {
-    bool ready;
+    bool ready, chunk;                   // chunk: the kernels of many tokens are set up
+    int sms;
     uint32_t *err;
 };
 std::mutex g_mu;
@@ -40,12 +41,25 @@ int device_info(const char *who, DeviceInfo *out) {
     if (!d.ready) {
         void *p = nullptr;
         e = cudaGetSymbolAddress(&p, g_delta_err);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
         if (e != cudaSuccess) return fail(RING_ECUDA, "%s: set-up: %s", who, cudaGetErrorString(e));
         d.err = static_cast<uint32_t *>(p);
         d.ready = true;
     }
     *out = d;
     return RING_OK;
+}
+
+// The kernels of many tokens, once per device and when first called for.
+int set_up_chunk(const char *who) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) {
+        std::lock_guard<std::mutex> lock(g_mu);
+        e = delta_chunk_setup();
+        if (e == cudaSuccess) g_dev[dev].chunk = true;
+    }
+    return e == cudaSuccess ? RING_OK : fail(RING_ECUDA, "%s: set-up: %s", who, cudaGetErrorString(e));
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -79,10 +93,24 @@ int check_batch(const char *who, const delta_state *s, const delta_batch *b, int
     if (n_rows < 0 || n_rows > INT32_MAX / 2) return fail(RING_EINVAL, "%s: n_rows out of range", who);
     if (n_head_k <= 0 || s->n_head % n_head_k)
         return fail(RING_EINVAL, "%s: %d key heads (a divisor of the %d heads)", who, n_head_k, s->n_head);
+    if (delta_chunks(n_rows, b->n_seq) * s->n_head > INT32_MAX)
+        return fail(RING_EINVAL, "%s: more than 2^31 chunks of 32 rows times heads", who);
     return RING_OK;
 }
 
-int64_t workspace_of(const delta_state *, const delta_batch *, int64_t, int) { return 0; }
+int64_t up256(int64_t x) { return (x + 255) & ~(int64_t)255; }
+
+// Which kernels serve a batch: token by token up to 8, and where states are kept behind single tokens.
+bool by_chunks(const delta_batch *b) { return b->max_q > 8 && !b->save; }
+
+int64_t tile_bytes(const delta_state *s, int64_t chunks, int n_head_k) {
+    return up256(chunks * n_head_k * 2 * kDeltaChunk * s->dim_k * 2);
+}
+int64_t workspace_of(const delta_state *s, const delta_batch *b, int64_t n_rows, int n_head_k) {
+    if (!by_chunks(b) || b->n_seq == 0) return 0;
+    const int64_t chunks = delta_chunks(n_rows, b->n_seq);
+    return tile_bytes(s, chunks, n_head_k) + up256(chunks * s->n_head * kDeltaHeadBytes);
+}
 
 }  // namespace
 }  // namespace dflash
@@ -161,7 +189,15 @@ extern "C" int delta_rule(const delta_rule_args *g, void *stream) {
     a.group = s->n_head / g->n_head_k;
     a.normalise = g->normalise;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = launch_delta_step(a, g->dtype, s->dim_k, s->dim_v, st);
+    cudaError_t e;
+    if (by_chunks(b)) {
+        if (!d.chunk) TRY(set_up_chunk(who));
+        a.tiles = static_cast<uint8_t *>(g->workspace);
+        a.heads = a.tiles + tile_bytes(s, delta_chunks(g->n_rows, b->n_seq), g->n_head_k);
+        e = launch_delta_chunk(a, g->dtype, s->dim_k, s->dim_v, d.sms, st);
+    } else {
+        e = launch_delta_step(a, g->dtype, s->dim_k, s->dim_v, st);
+    }
     return e == cudaSuccess ? RING_OK : fail(RING_ECUDA, "%s: launch: %s", who, cudaGetErrorString(e));
 }
 

@@ -824,8 +824,8 @@ k_paged_join(const __grid_constant__ PagedAttendArgs a) {
 
 // Join of two passes over a batch whose sequences share beginnings: W warps take a (row, head), look up the
 // items that hold its states over its prefix and over its own positions, and join all their pieces as k_paged_join
-// does.  Bound by latency with few rows (row bounds, items, maxima, numerators: four loads one behind another;
-// four rows of 32 heads LEVEL_SMALL us with eight warps to a row, LEVEL_SMALL_1 with one), by L2 with many.
+// does.  Bound by latency with few rows (row bounds, items, maxima, numerators: four loads one behind another),
+// by L2 with many.
 template <int D, int T, int W>
 __global__ void __launch_bounds__(256)
 k_paged_levels(const __grid_constant__ PagedAttendArgs prefix, const __grid_constant__ PagedAttendArgs own) {

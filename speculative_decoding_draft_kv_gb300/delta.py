@@ -17,7 +17,7 @@ import torch
 from .paged import _TYPES, _device, _half, _rows, _stream, _vector, _workspace
 from .ring import RING_EDEVICE, RING_OK, RingError, _load as _load_ring
 
-DELTA_ERR_BATCH, DELTA_ERR_SLOT = 1, 2
+DELTA_ERR_BATCH, DELTA_ERR_SLOT, DELTA_ERR_WAIT = 1, 2, 4
 
 EXPORTED = ("delta_rule", "delta_rule_workspace", "delta_device_error", "delta_last_error")
 

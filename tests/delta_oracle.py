@@ -51,8 +51,13 @@ class DeltaWorld:
         2^-24 sqrt(dim_k) = 2^-20.5 of |S| for 128) or operands of 22 bits (2^-22 of |S| and of |u|, each a few
         times), all relative to |S|_F + |v|.  These roundings are independent, so their squares add:
             E^2 <- exp(2 g) E^2 + (2^-20 (|S|_F + |v|))^2,
-        and four times that is allowed.  An output is off by |q| times the state's error and by its own
-        rounding, and q . S's sum like k . S's."""
+        and four times that is allowed.  What is not independent is the norm of a key that comes again: its rounding
+        (2^-23) and the cut-off ends of the sums that k . k and S k are (16 of up to 2^-24 each, always towards
+        zero: 2^-21 on average) are the same each time, and change S k by a factor, so these errors add as they are:
+            F <- exp(g) F + 2^-20 beta |S k|.
+        An output is off by |q| times the state's error and by its own
+        rounding, and q . S's sum like k . S's; over many tokens bf16 outputs take S as one F16, half a step (2^-11) of
+        each product, together at most 2^-11 |S_row| |q|."""
         n = len(self.lens)
         pool = self.pool.double().clone()
         out = torch.zeros(self.total, self.heads, self.dim_v, dtype=torch.float64, device="cuda")
@@ -66,21 +71,24 @@ class DeltaWorld:
         for s in range(n):
             at = self.slot_in[s]
             S = pool[at].clone() if at >= 0 else torch.zeros_like(pool[0])
-            E = torch.zeros(self.heads, dtype=torch.float64, device="cuda")
+            E, F = torch.zeros(2, self.heads, dtype=torch.float64, device="cuda")
             for r in range(self.starts[s], self.starts[s + 1]):
                 a = torch.exp(self.decay[r].double())
                 unit = 2.0 ** -20 * (torch.linalg.matrix_norm(S) + self.v[r].double().norm(dim=-1))
                 S = S * a[:, None, None]
-                u = self.beta[r].double()[:, None] * (self.v[r].double() - (S @ k[r][..., None])[..., 0])
+                sk = (S @ k[r][..., None])[..., 0]
+                u = self.beta[r].double()[:, None] * (self.v[r].double() - sk)
+                F = a * F + 2.0 ** -20 * self.beta[r].double() * sk.norm(dim=-1)
                 S = S + u[..., None] * k[r][:, None]
                 E = torch.sqrt((a * E) ** 2 + unit ** 2)
                 out[r] = (S @ q[r][..., None])[..., 0]
-                tol[r] = UNIT[self.dtype] * out[r].abs() + (4 * (E + unit) * q[r].norm(dim=-1))[:, None] + (
+                tol[r] = UNIT[self.dtype] * out[r].abs() + ((4 * (E + unit) + F) * q[r].norm(dim=-1))[:, None] + (
+                    2.0 ** -11 * S.norm(dim=-1) * q[r].norm(dim=-1)[:, None] if self.dtype == torch.bfloat16 else 0.0) + (
                     2.0 ** -25 if self.dtype == torch.float16 else 0.0)
                 if self.save is not None and 0 <= self.save[r] < self.n_slots:
-                    slots[self.save[r]] = (S.clone(), 4 * E)
+                    slots[self.save[r]] = (S.clone(), 4 * E + F)
             if 0 <= self.slot_out[s] < self.n_slots:
-                slots[self.slot_out[s]] = (S, 4 * E)
+                slots[self.slot_out[s]] = (S, 4 * E + F)
         return out, tol, slots
 
     def check(self, D, normalise=True, eps=1e-6, scale=0.0, o=None, max_q=None, errors=0, run=None):

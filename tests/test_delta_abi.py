@@ -42,7 +42,7 @@ def test_layouts_match_the_binding(tmp_path):
     for c, py in structs.items():
         lines.append(f'    printf("{c} size %zu\\n", sizeof({c}));')
         lines += [f'    printf("{c} {f} %zu\\n", offsetof({c}, {f}));' for f, _ in py._fields_]
-    names = {"DELTA_ERR_BATCH": 1, "DELTA_ERR_SLOT": 2}
+    names = {"DELTA_ERR_BATCH": 1, "DELTA_ERR_SLOT": 2, "DELTA_ERR_WAIT": 4}
     lines += [f'    printf("const {n} %d\\n", (int){n});' for n in names] + ["    return 0;", "}"]
     src, exe = tmp_path / "layout.c", tmp_path / "layout"
     src.write_text("\n".join(lines) + "\n")
