@@ -113,7 +113,8 @@ cudaError_t launch_paged_attend_t(const PagedAttendArgs &a, const CUtensorMap &t
                                   int head_dim, cudaStream_t st);
 
 template <int T>
-cudaError_t launch_paged_levels_t(const PagedAttendArgs &prefix, const PagedAttendArgs &own, int head_dim, cudaStream_t st);
+cudaError_t launch_paged_levels_t(const PagedAttendArgs &prefix, const PagedAttendArgs &own, int head_dim, int sms,
+                                  cudaStream_t st);
 
 template <int T> cudaError_t paged_prefill_setup_t();
 template <int T>

@@ -24,13 +24,16 @@ cudaError_t launch_join(const PagedAttendArgs &a, int head_dim, cudaStream_t st)
                           : cudaLaunchKernelEx(&cfg, k_paged_join<128, T, W>, a);
 }
 
-// Two passes' join, which settles as the other one does.  More warps to a row where there are few: see the kernel.
+// Two passes' join, which settles as the other one does.  Rows to a block: as few as leave one wave of blocks, five to
+// an SM; warps to a (row, query head): what a block has left.
 template <int T>
-cudaError_t launch_paged_levels_t(const PagedAttendArgs &prefix, const PagedAttendArgs &own, int head_dim, cudaStream_t st) {
-    const int64_t units = own.batch.n_rows * own.n_head;
-    const int w = units <= 2048 ? 8 : 1;
+cudaError_t launch_paged_levels_t(const PagedAttendArgs &prefix, const PagedAttendArgs &own, int head_dim, int sms, cudaStream_t st) {
+    const int64_t n = own.batch.n_rows;
+    int rows = 1, wide = 8;
+    while (rows < 16 && (n + rows - 1) / rows * own.pool.n_head_kv > 5 * sms) rows *= 2;
+    while (wide > 1 && rows * own.group * wide > 8) wide /= 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((units * w + 7) / 8), 1, 1);
+    cfg.gridDim = dim3((unsigned)((n + rows - 1) / rows * own.pool.n_head_kv), 1, 1);
     cfg.blockDim = dim3(256);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -38,9 +41,8 @@ cudaError_t launch_paged_levels_t(const PagedAttendArgs &prefix, const PagedAtte
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    auto go = [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, prefix, own); };
-    if (head_dim == 64) return w == 8 ? go(k_paged_levels<64, T, 8>) : go(k_paged_levels<64, T, 1>);
-    return w == 8 ? go(k_paged_levels<128, T, 8>) : go(k_paged_levels<128, T, 1>);
+    return head_dim == 64 ? cudaLaunchKernelEx(&cfg, k_paged_levels<64, T>, prefix, own, rows, wide)
+                          : cudaLaunchKernelEx(&cfg, k_paged_levels<128, T>, prefix, own, rows, wide);
 }
 
 // A pass of the attention.  The second of two may begin while the first one runs: it reads nothing of that.
