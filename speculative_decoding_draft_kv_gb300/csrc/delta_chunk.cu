@@ -16,11 +16,12 @@
 // memory would be written, fenced and read between any two of the four dependent products of a chunk).
 //
 // Precision.  The state, its update and all sums are float32.  Operands are F16 pairs hi + lo, 22 bits together,
-// after powers of two that bring the largest value of a warp's operand to [2^12, 2^13); keys and queries are
-// one F16 each: exact for F16 rows, and for bf16 rows after a power of two by the row's norm (elements below
-// 2^-14 of the norm are off by 2^-25 of it at most).  What a product adds up starts at zero and joins the
-// state by one fused multiply-add: tensor-core sums are cut off, not rounded, and hundreds of chunks would
-// add that up.  Decays are exponentials of sums over just the tokens between, in two float32 parts, so neither
+// after powers of two that bring them below 2^14; the state is kept times its own.  R's is by its largest
+// value; U's and the state's are by bounds (T's largest row sum, the decays' sum), which may be 2^16 above
+// the values before an F16 pair loses bits, and the state's is set right every fourth chunk.  Keys and queries
+// are one F16 each, after a power of two by the row's norm: exact but for elements below 2^-14 of the norm, which
+// are off by 2^-25 of it at most.  What a product adds up starts at zero and joins the state by one fused
+// multiply-add: tensor-core sums are cut off, not rounded, and hundreds of chunks would add that up.  Decays are exponentials of sums over just the tokens between, in two float32 parts, so neither
 // a long chunk nor a state that was dropped costs later tokens their precision.
 #include "delta.h"
 
@@ -42,6 +43,12 @@ template <int T> __device__ __forceinline__ float from16(uint32_t x) {
 }
 __device__ __forceinline__ float2 half2_floats(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2 *>(&x)); }
 
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    return x;
+}
+
 // byte offset of 16-byte chunk ch of row r in a tile of DK F16 columns: conflict-free for ldmatrix
 template <int DK> __device__ __forceinline__ uint32_t tile_at(int r, int ch) { return (uint32_t)(r * DK * 2 + ((ch ^ (r & 7)) << 4)); }
 
@@ -54,10 +61,10 @@ __host__ __device__ constexpr int block_k(int b) { return b < 4 ? 0 : 1; }
 struct HeadBlock {
     uint4 t[kBlocks][32];                              // T: hi, hi, lo, lo
     uint4 a[kBlocks][32];                              // exp(G_i - G_j) q_i . k_j: likewise
-    float4 r[C / 2];                                   // of tokens 2i, 2i+1: beta, beta exp(G) |k|
-    float4 o[C / 2];                                   // |q|, |q| exp(G)
+    float4 r[C / 2];                                   // of tokens 2i, 2i+1: beta twice, -beta exp(G) |k| twice
+    float4 o[C / 2];                                   // |q| twice, |q| exp(G) twice
     float w[C];                                        // exp(G_last - G) |k|
-    float last, t_unit, a_unit, pad;                   // exp(G_last); what T and A are to be multiplied by
+    float last, t_unit, a_unit, w_sum;                 // exp(G_last); what T and A are to be multiplied by; sum of w
 };
 static_assert(sizeof(HeadBlock) == kDeltaHeadBytes, "as the workspace is laid out");
 
@@ -70,14 +77,15 @@ __device__ __forceinline__ float unit_of(uint32_t bits) {
 }
 __device__ __forceinline__ float inverse_unit(float u) { return __uint_as_float((254u << 23) - __float_as_uint(u)); }
 
-// x0, x1 times a power of two as two F16 pairs
-__device__ __forceinline__ void split(float x0, float x1, float unit, uint32_t &hi, uint32_t &lo) {
-    x0 *= unit;
-    x1 *= unit;
+// x0, x1 as two F16 pairs
+__device__ __forceinline__ void split(float x0, float x1, uint32_t &hi, uint32_t &lo) {
     hi = pack_half2(x0, x1);
     const float2 h = half2_floats(hi);
-    lo = pack_half2(x0 - h.x, x1 - h.y);
+    float l0, l1;
+    upk2(fma2(pk2(h.x, h.y), pk2(-1.f, -1.f), pk2(x0, x1)), l0, l1);
+    lo = pack_half2(l0, l1);
 }
+__device__ __forceinline__ void scale2(float &x0, float &x1, float f0, float f1) { upk2(mul2(pk2(x0, x1), pk2(f0, f1)), x0, x1); }
 
 // ---------------------------------------------------------------- what the state is not needed for
 
@@ -92,6 +100,7 @@ k_delta_prep(const __grid_constant__ DeltaArgs a) {
     __shared__ float s_kk[C * 32], s_qk[C * 32];
     __shared__ float s_kn[C], s_qn[C];                             // what the F16 rows are to be multiplied by
     __shared__ uint32_t s_amax[2][2];
+    __shared__ float s_wsum[2][2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int hk = blockIdx.x % a.n_head_k, at = blockIdx.x / a.n_head_k;
     pdl_trigger();
@@ -136,21 +145,17 @@ k_delta_prep(const __grid_constant__ DeltaArgs a) {
             ss += __shfl_xor_sync(0xffffffffu, ss, 1);
             ss += __shfl_xor_sync(0xffffffffu, ss, 2);
             float norm = a.normalise ? 1.f / sqrtf(ss + a.eps) : 1.f;
-            if (T == PAGED_BF16) {
-                // to a norm in [1, 2) by a power of two; a square sum past float32 makes the row 0, as its norm does
-                const uint32_t e = __float_as_uint(sqrtf(ss)) >> 23;
-                float down = e == 0u ? 1.f : (e == 255u ? 0x1p-126f : __uint_as_float((254u - min(e, 253u)) << 23));
-                if (e == 255u && a.normalise) down = 0.f;
-                norm = r < nv ? norm * (e == 0u || down == 0.f ? 1.f : __uint_as_float((254u << 23) - __float_as_uint(down))) : 0.f;
-                if (down == 0.f) norm = 1.f;
+            // to a norm in [1, 2) by a power of two; a square sum past float32 makes the row 0, as its norm does
+            const uint32_t e = __float_as_uint(sqrtf(ss)) >> 23;
+            float down = e == 0u ? 1.f : (e == 255u ? 0x1p-126f : __uint_as_float((254u - min(e, 253u)) << 23));
+            if (e == 255u && a.normalise) down = 0.f;
+            norm = down == 0.f ? 1.f : (e == 0u ? norm : norm * __uint_as_float((254u << 23) - __float_as_uint(down)));
 #pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    uint32_t v[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+            for (int j = 0; j < N; ++j) {
+                uint32_t v[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
 #pragma unroll
-                    for (int e2 = 0; e2 < 4; ++e2)
-                        v[e2] = pack_half2(from16<T>(v[e2] & 0xffffu) * down, from16<T>(v[e2] >> 16) * down);
-                    x[j] = make_uint4(v[0], v[1], v[2], v[3]);
-                }
+                for (int e2 = 0; e2 < 4; ++e2) v[e2] = pack_half2(from16<T>(v[e2] & 0xffffu) * down, from16<T>(v[e2] >> 16) * down);
+                x[j] = make_uint4(v[0], v[1], v[2], v[3]);
             }
             uint8_t *tile = a.tiles + (((int64_t)at * a.n_head_k + hk) * 2 + w) * (C * DK * 2);
 #pragma unroll
@@ -237,15 +242,18 @@ k_delta_prep(const __grid_constant__ DeltaArgs a) {
             add(d);
         }
         HeadBlock *out = reinterpret_cast<HeadBlock *>(a.heads + ((int64_t)at * a.n_head + h) * kDeltaHeadBytes);
-        if (role == 0) {
-            if (mine && i >= C / 2) out->w[i] = left * kn;         // j = 31 - d
+        // (j = 31 - d; the other half's are 0)
+        float w_sum = left * kn;
+        if (mine && (i >= C / 2) == (role == 0)) out->w[i] = w_sum;
+        w_sum = warp_sum(w_sum);
+        if (role == 0)
             for (int d = C / 2; d < C; ++d) add(d);
-        } else if (mine && i < C / 2) {
-            out->w[i] = left * kn;
-        }
         const float e = expf(sum), gone = fmaf(e, rest, e);        // exp(G_i)
         const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
-        if (lane == 0) s_amax[warp >> 1][role] = top;
+        if (lane == 0) {
+            s_amax[warp >> 1][role] = top;
+            s_wsum[warp >> 1][role] = w_sum;
+        }
         __syncthreads();
         if (!mine) continue;                                       // (the last round)
         const int gq = lane >> 2, tq = lane & 3;
@@ -255,25 +263,28 @@ k_delta_prep(const __grid_constant__ DeltaArgs a) {
                 const float *src = from + (block_n(b) * 8 + gq) * 36 + block_k(b) * 16 + 2 * tq;
                 const float2 lo = *reinterpret_cast<const float2 *>(src), hi = *reinterpret_cast<const float2 *>(src + 8);
                 uint4 v;
-                split(lo.x, lo.y, unit, v.x, v.z);
-                split(hi.x, hi.y, unit, v.y, v.w);
+                split(lo.x * unit, lo.y * unit, v.x, v.z);
+                split(hi.x * unit, hi.y * unit, v.y, v.w);
                 to[b][lane] = v;
             }
         };
         if (role) {
             const float au = unit_of(max(s_amax[warp >> 1][0], s_amax[warp >> 1][1]));
             blocks(am, au, out->a);
-            reinterpret_cast<float2 *>(out->r)[i] = make_float2(beta, bk * gone);
-            reinterpret_cast<float2 *>(out->o)[i] = make_float2(qn, qn * gone);
+            const int to = (i >> 1) * 4 + (i & 1);
+            reinterpret_cast<float *>(out->r)[to] = beta;
+            reinterpret_cast<float *>(out->r)[to + 2] = -(bk * gone);
+            reinterpret_cast<float *>(out->o)[to] = qn;
+            reinterpret_cast<float *>(out->o)[to + 2] = qn * gone;
             if (i == C - 1) {
                 out->last = gone;
                 out->a_unit = inverse_unit(au);
+                out->w_sum = s_wsum[warp >> 1][0] + s_wsum[warp >> 1][1];
             }
             continue;
         }
         // T by columns: a lane has one
         float x[C];
-        float tmax = 0.f;
 #pragma unroll
         for (int r = 0; r < C; ++r) {
             float y0 = r == i ? 1.f : 0.f, y1 = 0.f, y2 = 0.f, y3 = 0.f;
@@ -286,13 +297,19 @@ k_delta_prep(const __grid_constant__ DeltaArgs a) {
                 if (m + 3 < r) y3 = fmaf(-f.w, x[m + 3], y3);
             }
             x[r] = (y0 + y1) + (y2 + y3);
-            tmax = fmaxf(tmax, fabsf(x[r]));
         }
         __syncwarp();
 #pragma unroll
         for (int r = 0; r < C; ++r) l[r * 36 + i] = x[r];
-        const float tu = unit_of(__reduce_max_sync(0xffffffffu, __float_as_uint(tmax)));
         __syncwarp();
+        // the largest row sum of magnitudes, 1 at least, to (1/2, 1]
+        float row = 0.f;
+#pragma unroll
+        for (int m = 0; m < C; m += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(l + i * 36 + m);
+            row += fabsf(f.x) + fabsf(f.y) + fabsf(f.z) + fabsf(f.w);
+        }
+        const float tu = unit_of(__reduce_max_sync(0xffffffffu, __float_as_uint(row))) * 0x1p-13f;
         blocks(l, tu, out->t);
         if (i == 0) out->t_unit = inverse_unit(tu);
     }
@@ -308,7 +325,7 @@ struct ScanCfg {
     static constexpr int kTileBytes = 2 * C * DK * 2;
     static constexpr int kStageBytes = kTileBytes + kDeltaHeadBytes;
     static constexpr int kVBytes = C * 32;                         // [C tokens][16 values], two to a warp
-    static constexpr int kXWords = KS == 2 ? 24 * 32 : 0;          // what a warp hands its partner, twice
+    static constexpr int kXWords = KS == 2 ? 24 * 32 : 0;          // what a warp hands its partner, two chunks' worth
     // (one CTA per SM where few are wanted: several would find room beside one another, and slow each other
     // down, while other SMs have none)
     static constexpr int kStages = KS == 2 ? (DK == 128 ? 6 : 9) : (DK == 128 ? 3 : 4);
@@ -335,8 +352,8 @@ template <int N> __device__ __forceinline__ float top_of(const float (&x)[N][4])
     return m;
 }
 
-// The unit for a warp's values, m the largest magnitude of this lane's: by the largest finite one of all.
-template <int N> __device__ __forceinline__ float warp_unit(const float (&x)[N][4], float m) {
+// The largest finite magnitude of a warp's values, as bits; m: the largest of this lane's.
+template <int N> __device__ __forceinline__ uint32_t warp_top(const float (&x)[N][4], float m) {
     uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
     if (top >= 0x7f800000u) {                                      // an infinity: the other rows go by what else there is
         m = 0.f;
@@ -347,15 +364,15 @@ template <int N> __device__ __forceinline__ float warp_unit(const float (&x)[N][
                 if (fabsf(x[n][e]) < INFINITY) m = fmaxf(m, fabsf(x[n][e]));
         top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
     }
-    return unit_of(top);
+    return top;
 }
 
-// Accumulators of 32 columns as an A operand of two steps, in two parts, times a power of two.
-__device__ __forceinline__ void operand(const float (&x)[4][4], float unit, uint32_t (&hi)[2][4], uint32_t (&lo)[2][4]) {
+// Accumulators of 32 columns as an A operand of two steps, in two parts.
+__device__ __forceinline__ void operand(const float (&x)[4][4], uint32_t (&hi)[2][4], uint32_t (&lo)[2][4]) {
 #pragma unroll
     for (int n = 0; n < 4; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) split(x[n][2 * e], x[n][2 * e + 1], unit, hi[n >> 1][(n & 1) * 2 + e], lo[n >> 1][(n & 1) * 2 + e]);
+        for (int e = 0; e < 2; ++e) split(x[n][2 * e], x[n][2 * e + 1], hi[n >> 1][(n & 1) * 2 + e], lo[n >> 1][(n & 1) * 2 + e]);
 }
 
 template <int T, int DK, int W, int KS>
@@ -432,7 +449,7 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
         }
     }
     const uint32_t v0 = smem_u32(smem + F::kOffV + warp * 2 * F::kVBytes);
-    float *xs = reinterpret_cast<float *>(smem + F::kOffX) + lane;
+    float4 *xs = reinterpret_cast<float4 *>(smem + F::kOffX) + lane;
     // values of chunk c: two 16-byte pieces a token, zeros behind the last one
     auto fetch_v = [&](int c) {
         if (c < chunks) {
@@ -448,13 +465,18 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
     };
     fetch_v(0);
     bool alive = true;
-    float smax = top_of<NT>(st);                                   // this lane's
+    // the state times a power of two, and a bound of its magnitudes without that
+    uint32_t stop = warp_top<NT>(st, top_of<NT>(st));
+    float su = unit_of(stop), si = inverse_unit(su), sb = __uint_as_float(stop);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        scale2(st[n][0], st[n][1], su, su);
+        scale2(st[n][2], st[n][3], su, su);
+    }
     for (int c = 0; c < chunks; ++c) {
         const int k = c % S, nv = min(C, q.n - c * C);
         __syncwarp();                                              // the other half's outputs are on their way
         fetch_v(c + 1);
-        // S in units of a power of two
-        const float su = warp_unit<NT>(st, smax), si = inverse_unit(su);
         const bool here = __all_sync(0xffffffffu, mbar_wait(full + 8 * k, (uint32_t)(c / S) & 1u));
         if (!here && lane == 0) timed_out();
         if (KS == 1 && !here) {
@@ -482,7 +504,7 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
         for (int ks = 0; ks < STEPS; ++ks) {
             uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) split(st[2 * ks + (e >> 1)][2 * (e & 1)], st[2 * ks + (e >> 1)][2 * (e & 1) + 1], su, hi[e], lo[e]);
+            for (int e = 0; e < 4; ++e) split(st[2 * ks + (e >> 1)][2 * (e & 1)], st[2 * ks + (e >> 1)][2 * (e & 1) + 1], hi[e], lo[e]);
             if (ks + 1 < STEPS) fetch(ks + 1);
 #pragma unroll
             for (int n = 0; n < 4; ++n) mma16816(pk[n], hi, fk[ks & 1][n >> 1][2 * (n & 1)], fk[ks & 1][n >> 1][2 * (n & 1) + 1]);
@@ -498,38 +520,43 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
 #pragma unroll
         for (int n = 0; n < 4; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                pk[n][e] = (pk[n][e] + pl[n][e]) * si;
-                pq[n][e] *= si;
-            }
+            for (int e = 0; e < 4; e += 2) upk2(add2(pk2(pk[n][e], pk[n][e + 1]), pk2(pl[n][e], pl[n][e + 1])), pk[n][e], pk[n][e + 1]);
+        float ks1 = si;                                            // what the sums are to be multiplied by
         if constexpr (KS == 2) {
             // the partner's half of the sums: of S K^T all, of S Q^T those of the 16 tokens whose outputs are this warp's
-            float *mine = xs + (warp * 2 + (c & 1)) * F::kXWords, *other = xs + ((warp ^ 1) * 2 + (c & 1)) * F::kXWords;
+            ks1 = 1.f;
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) mine[(n * 4 + e) * 32] = pk[n][e];
+                for (int e = 0; e < 4; e += 2) {
+                    scale2(pk[n][e], pk[n][e + 1], si, si);
+                    scale2(pq[n][e], pq[n][e + 1], si, si);
+                }
+            float4 *mine = xs + (warp * 2 + (c & 1)) * (F::kXWords / 4);
+            const float4 *other = xs + ((warp ^ 1) * 2 + (c & 1)) * (F::kXWords / 4);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) mine[n * 32] = make_float4(pk[n][0], pk[n][1], pk[n][2], pk[n][3]);
 #pragma unroll
             for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) mine[(16 + m * 4 + e) * 32] = kp ? pq[m][e] : pq[2 + m][e];
+                mine[(4 + m) * 32] = kp ? make_float4(pq[m][0], pq[m][1], pq[m][2], pq[m][3])
+                                        : make_float4(pq[2 + m][0], pq[2 + m][1], pq[2 + m][2], pq[2 + m][3]);
             // (a wait that ran out in either: both leave)
             if (bar_any(1 + warp / 2, 64, !here)) {
                 alive = false;
                 break;
             }
+            auto join = [](float (&x)[4], const float4 &y) {
+                upk2(add2(pk2(x[0], x[1]), pk2(y.x, y.y)), x[0], x[1]);
+                upk2(add2(pk2(x[2], x[3]), pk2(y.z, y.w)), x[2], x[3]);
+            };
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
+            for (int n = 0; n < 4; ++n) join(pk[n], other[n * 32]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) pk[n][e] += other[(n * 4 + e) * 32];
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float x = other[(16 + m * 4 + e) * 32];
-                    if (kp) pq[2 + m][e] += x;
-                    else pq[m][e] += x;
-                }
+            for (int m = 0; m < 2; ++m) {
+                const float4 y = other[(4 + m) * 32];
+                if (kp) join(pq[2 + m], y);
+                else join(pq[m], y);
+            }
         }
         // R = beta V - beta exp(G) |k| (S K^T)
         asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -543,43 +570,47 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
                 const int n = 2 * np + m;
-                const float4 f = hb->r[n * 4 + t];                 // beta, beta exp(G) |k| of tokens 8n + 2t, + 1
+                const float4 f = hb->r[n * 4 + t];                 // beta, then -beta exp(G) |k| of tokens 8n + 2t, + 1
+                const uint64_t b2 = pk2(f.x, f.y), c2 = mul2(pk2(f.z, f.w), pk2(ks1, ks1));
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float x0 = from16<T>(v[2 * m + e] & 0xffffu), x1 = from16<T>(v[2 * m + e] >> 16);
-                    r[n][2 * e] = fmaf(f.x, x0, -f.y * pk[n][2 * e]);
-                    r[n][2 * e + 1] = fmaf(f.z, x1, -f.w * pk[n][2 * e + 1]);
+                    const uint64_t x = pk2(from16<T>(v[2 * m + e] & 0xffffu), from16<T>(v[2 * m + e] >> 16));
+                    upk2(fma2(b2, x, mul2(c2, pk2(pk[n][2 * e], pk[n][2 * e + 1]))), r[n][2 * e], r[n][2 * e + 1]);
                 }
             }
         }
-        // U = R T^T
+        // U = R T^T, times R's unit and T's, by which it is below 2^13
         float u[4][4] = {};
         uint32_t hi[2][4], lo[2][4];
+        const uint32_t rtop = warp_top<4>(r, top_of<4>(r));
+        const float ru = unit_of(rtop), ui = inverse_unit(ru) * hb->t_unit;
         {
             uint4 f[kBlocks];
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b) f[b] = hb->t[b][lane];
-            const float ru = warp_unit<4>(r, top_of<4>(r));
-            operand(r, ru, hi, lo);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                scale2(r[n][0], r[n][1], ru, ru);
+                scale2(r[n][2], r[n][3], ru, ru);
+            }
+            operand(r, hi, lo);
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b) mma16816(u[block_n(b)], hi[block_k(b)], f[b].x, f[b].y);
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b) mma16816(u[block_n(b)], lo[block_k(b)], f[b].x, f[b].y);
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b) mma16816(u[block_n(b)], hi[block_k(b)], f[b].z, f[b].w);
-            const float back = inverse_unit(ru) * hb->t_unit;
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) u[n][e] *= back;
         }
+        // The state's next unit: its bound is the old one's decayed and, with |k| below 2 a token, 2 sum(w) max|u|.
+        const float last = hb->last;
+        sb = fmaf(last, sb, 2.f * hb->w_sum * (__uint_as_float(rtop) * hb->t_unit));
+        const float nu = unit_of(__float_as_uint(sb)), ni = inverse_unit(nu);
         // o = |q| (exp(G) S q + A u), of two warps of a group 16 tokens each
         {
-            const float uu = warp_unit<4>(u, top_of<4>(u));
-            operand(u, uu, hi, lo);
+            operand(u, hi, lo);
             float x[4][4] = {};
-            auto products = [&](auto first, auto last) {
-                constexpr int B0 = decltype(first)::value, B1 = decltype(last)::value;
+            auto products = [&](auto first, auto end) {
+                constexpr int B0 = decltype(first)::value, B1 = decltype(end)::value;
                 uint4 f[B1 - B0];
 #pragma unroll
                 for (int b = B0; b < B1; ++b) f[b - B0] = hb->a[b][lane];
@@ -593,7 +624,7 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
             using I0 = std::integral_constant<int, 0>;
             using I2 = std::integral_constant<int, 2>;
             using I6 = std::integral_constant<int, 6>;
-            const float back = inverse_unit(uu) * hb->a_unit;
+            const float back = ui * hb->a_unit;
             // through the values' place, which has been read, into rows
             auto rows = [&](auto half) {
                 constexpr int NP = decltype(half)::value;
@@ -602,10 +633,11 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
                 for (int m = 0; m < 2; ++m) {
                     const int n = 2 * NP + m;
                     const float4 f = hb->o[n * 4 + t];
+                    const uint64_t fa = mul2(pk2(f.x, f.y), pk2(back, back)), fs = mul2(pk2(f.z, f.w), pk2(ks1, ks1));
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float y0 = fmaf(f.x, x[n][2 * e] * back, f.y * pq[n][2 * e]);
-                        const float y1 = fmaf(f.z, x[n][2 * e + 1] * back, f.w * pq[n][2 * e + 1]);
+                        float y0, y1;
+                        upk2(fma2(fa, pk2(x[n][2 * e], x[n][2 * e + 1]), mul2(fs, pk2(pq[n][2 * e], pq[n][2 * e + 1]))), y0, y1);
                         o16[m][e] = T == PAGED_F16 ? pack_half2(y0, y1) : pack_bf162(y0, y1);
                     }
                 }
@@ -632,16 +664,18 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
                 rows(std::integral_constant<int, 0>{});
             }
         }
-        // S <- exp(G_last) S + U (exp(G_last - G) |k| K)
+        // S <- exp(G_last) S + U (exp(G_last - G) |k| K), all times the new unit
         {
+            const float wf = ui * nu, keep = last * (si * nu);
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 const float2 f = *reinterpret_cast<const float2 *>(&hb->w[n * 8 + 2 * t]);
-                u[n][0] *= f.x; u[n][1] *= f.y; u[n][2] *= f.x; u[n][3] *= f.y;
+                float f0, f1;
+                upk2(mul2(pk2(f.x, f.y), pk2(wf, wf)), f0, f1);
+                scale2(u[n][0], u[n][1], f0, f1);
+                scale2(u[n][2], u[n][3], f0, f1);
             }
-            const float uu = warp_unit<4>(u, top_of<4>(u)), back = inverse_unit(uu), last = hb->last;
-            operand(u, uu, hi, lo);
-            smax = 0.f;
+            operand(u, hi, lo);
             // four key tiles at a time, their operands fetched ahead
             uint32_t f[2][2][2][4];                                // [buffer][step][pair of tiles]
             auto fetch_k = [&](int n4) {
@@ -654,6 +688,7 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
                     }
             };
             fetch_k(0);
+            const uint64_t keep2 = pk2(keep, keep);
 #pragma unroll
             for (int n4 = 0; n4 < NT / 4; ++n4) {
                 if (n4 + 1 < NT / 4) fetch_k(n4 + 1);
@@ -668,15 +703,17 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
 #pragma unroll
                 for (int m = 0; m < 4; ++m)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float &y = st[4 * n4 + m][e];
-                        y = fmaf(x[m][e], back, last * y);
-                        smax = fmaxf(smax, fabsf(y));
+                    for (int e = 0; e < 4; e += 2) {
+                        float (&y)[4] = st[4 * n4 + m];
+                        upk2(fma2(keep2, pk2(y[e], y[e + 1]), pk2(x[m][e], x[m][e + 1])), y[e], y[e + 1]);
                     }
             }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(empty + 8 * k);
+        su = nu;
+        si = ni;
+        if ((c & 3) == 3) sb = __uint_as_float(warp_top<NT>(st, top_of<NT>(st))) * si;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     const int out = a.slot_out[s];
@@ -688,8 +725,8 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
     float *dst = place(out);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        *reinterpret_cast<float2 *>(dst + n * 8) = make_float2(st[n][0], st[n][1]);
-        *reinterpret_cast<float2 *>(dst + 8 * DK + n * 8) = make_float2(st[n][2], st[n][3]);
+        *reinterpret_cast<float2 *>(dst + n * 8) = make_float2(st[n][0] * si, st[n][1] * si);
+        *reinterpret_cast<float2 *>(dst + 8 * DK + n * 8) = make_float2(st[n][2] * si, st[n][3] * si);
     }
 }
 

@@ -16,30 +16,16 @@
 
 #include "ring_internal.h"
 #include "ptx.h"
+#include "paged_ptx.h"
 
 namespace dflash {
 namespace {
 
 constexpr int kStepThreads = 128, kStepTokens = 8;
 
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
 __device__ __forceinline__ float2 unpack2(uint64_t x) {
     float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    upk2(x, r.x, r.y);
     return r;
 }
 
@@ -89,8 +75,8 @@ k_delta_step(const __grid_constant__ DeltaArgs a) {
 #pragma unroll
             for (int e = 0; e < E / 4; ++e) {
                 const float4 x = *reinterpret_cast<const float4 *>(src + j * 4 * DK + e * 32);
-                st[j][2 * e] = pack2(x.x, x.y);
-                st[j][2 * e + 1] = pack2(x.z, x.w);
+                st[j][2 * e] = pk2(x.x, x.y);
+                st[j][2 * e + 1] = pk2(x.z, x.w);
             }
     } else {
 #pragma unroll
@@ -185,7 +171,7 @@ k_delta_step(const __grid_constant__ DeltaArgs a) {
                 }
             }
             const float decay = s_decay[t], beta = s_beta[t], qk = s_qk[t];
-            const uint64_t decay2 = pack2(decay, decay);
+            const uint64_t decay2 = pk2(decay, decay);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 const float2 x = unpack2(ks[j]), y = unpack2(qs[j]);
@@ -196,7 +182,7 @@ k_delta_step(const __grid_constant__ DeltaArgs a) {
                     qS += __shfl_xor_sync(0xffffffffu, qS, d);
                 }
                 const float u = beta * (s_v[t][warp * 4 * J + 4 * j + rg] - decay * kS);
-                const uint64_t u2 = pack2(u, u);
+                const uint64_t u2 = pk2(u, u);
 #pragma unroll
                 for (int e = 0; e < E / 2; ++e) st[j][e] = fma2(kd[e], u2, mul2(decay2, st[j][e]));
                 if (sub == j)
