@@ -21,8 +21,9 @@
 // the values before an F16 pair loses bits, and the state's is set right every fourth chunk.  Keys and queries
 // are one F16 each, after a power of two by the row's norm: exact but for elements below 2^-14 of the norm, which
 // are off by 2^-25 of it at most.  What a product adds up starts at zero and joins the state by one fused
-// multiply-add: tensor-core sums are cut off, not rounded, and hundreds of chunks would add that up.  Decays are exponentials of sums over just the tokens between, in two float32 parts, so neither
-// a long chunk nor a state that was dropped costs later tokens their precision.
+// multiply-add: tensor-core sums are cut off, not rounded, and hundreds of chunks would add that up.  Decays are
+// exponentials of sums over just the tokens between, so neither a long chunk nor a state that was dropped costs
+// later tokens their precision.
 #include "delta.h"
 
 #include "ring_internal.h"
@@ -89,18 +90,22 @@ __device__ __forceinline__ void scale2(float &x0, float &x1, float f0, float f1)
 
 // ---------------------------------------------------------------- what the state is not needed for
 
+// A CTA of two warps takes a chunk of a key head: both make the tiles and the products, then a warp has a head, a
+// lane a token.  Decays between tokens, exp(G_i - G_j), are products of two factors with a border between
+// the tokens: at the highest bit in which i and j differ, the sum up to i from the border on and that from j on up to
+// it, both of at most 16 log decays and never a difference of long sums.  So a lane takes seven exponentials, not 32.
 template <int T, int DK>
-__global__ void __launch_bounds__(128, 5)
+__global__ void __launch_bounds__(64, 8)
 k_delta_prep(const __grid_constant__ DeltaArgs a) {
-    // K and Q, then two heads' systems and A
+    constexpr int LP = 68;                                         // of two rows of the system, side by side
+    // K and Q, then each warp's system (and T) and A
     __shared__ __align__(128) union {
         uint8_t tile[2][C * DK * 2];
         float la[2][2][C * 36];
     } s;
-    __shared__ float s_kk[C * 32], s_qk[C * 32];
+    __shared__ float s_kk[C * 33], s_qk[C * 33];
     __shared__ float s_kn[C], s_qn[C];                             // what the F16 rows are to be multiplied by
-    __shared__ uint32_t s_amax[2][2];
-    __shared__ float s_wsum[2][2];
+    __shared__ float s_b[2][5][C];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int hk = blockIdx.x % a.n_head_k, at = blockIdx.x / a.n_head_k;
     pdl_trigger();
@@ -117,31 +122,38 @@ k_delta_prep(const __grid_constant__ DeltaArgs a) {
     if (!q.ok || t0 < 0 || t0 >= q.n) return;
     const int nv = min(C, q.n - t0);
 
-    {   // rows: four lanes to one, eight rows to a warp
-        const int r = warp * 8 + (lane >> 2), p = lane & 3;
+    // rows: four lanes to one, eight rows to a warp
+#pragma unroll
+    for (int pass = 0; pass < 2; ++pass) {
+        const int r = pass * 16 + warp * 8 + (lane >> 2), p = lane & 3;
         constexpr int N = DK / 32;                                 // 16-byte pieces of a lane
+        uint4 x[2][N];
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-            uint4 x[N];
-            float ss = 0.f;
 #pragma unroll
-            for (int j = 0; j < N; ++j) x[j] = make_uint4(0, 0, 0, 0);
+            for (int j = 0; j < N; ++j) x[w][j] = make_uint4(0, 0, 0, 0);
             if (r < nv) {
                 const int64_t row = q.row0 + t0 + r;
                 const uint16_t *src = w ? a.q + row * a.q_rs + (int64_t)hk * a.q_hs : a.k + row * a.k_rs + (int64_t)hk * a.k_hs;
 #pragma unroll
-                for (int j = 0; j < N; ++j) x[j] = *reinterpret_cast<const uint4 *>(src + (p + 4 * j) * 8);
+                for (int j = 0; j < N; ++j) x[w][j] = *reinterpret_cast<const uint4 *>(src + (p + 4 * j) * 8);
             }
+        }
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            uint64_t ss2 = 0ull;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                const uint32_t v[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+                const uint32_t v[4] = {x[w][j].x, x[w][j].y, x[w][j].z, x[w][j].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float f0 = from16<T>(v[e] & 0xffffu), f1 = from16<T>(v[e] >> 16);
-                    ss = fmaf(f0, f0, ss);
-                    ss = fmaf(f1, f1, ss);
+                    const uint64_t f = pk2(from16<T>(v[e] & 0xffffu), from16<T>(v[e] >> 16));
+                    ss2 = fma2(f, f, ss2);
                 }
             }
+            float ss, s1;
+            upk2(ss2, ss, s1);
+            ss += s1;
             ss += __shfl_xor_sync(0xffffffffu, ss, 1);
             ss += __shfl_xor_sync(0xffffffffu, ss, 2);
             float norm = a.normalise ? 1.f / sqrtf(ss + a.eps) : 1.f;
@@ -150,40 +162,41 @@ k_delta_prep(const __grid_constant__ DeltaArgs a) {
             float down = e == 0u ? 1.f : (e == 255u ? 0x1p-126f : __uint_as_float((254u - min(e, 253u)) << 23));
             if (e == 255u && a.normalise) down = 0.f;
             norm = down == 0.f ? 1.f : (e == 0u ? norm : norm * __uint_as_float((254u << 23) - __float_as_uint(down)));
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                uint32_t v[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-#pragma unroll
-                for (int e2 = 0; e2 < 4; ++e2) v[e2] = pack_half2(from16<T>(v[e2] & 0xffffu) * down, from16<T>(v[e2] >> 16) * down);
-                x[j] = make_uint4(v[0], v[1], v[2], v[3]);
-            }
             uint8_t *tile = a.tiles + (((int64_t)at * a.n_head_k + hk) * 2 + w) * (C * DK * 2);
+            const uint64_t down2 = pk2(down, down);
 #pragma unroll
             for (int j = 0; j < N; ++j) {
+                uint32_t v[4] = {x[w][j].x, x[w][j].y, x[w][j].z, x[w][j].w};
+#pragma unroll
+                for (int e2 = 0; e2 < 4; ++e2) {
+                    float f0, f1;
+                    upk2(mul2(pk2(from16<T>(v[e2] & 0xffffu), from16<T>(v[e2] >> 16)), down2), f0, f1);
+                    v[e2] = pack_half2(f0, f1);
+                }
                 const uint32_t off = tile_at<DK>(r, p + 4 * j);
-                *reinterpret_cast<uint4 *>(s.tile[w] + off) = x[j];
-                *reinterpret_cast<uint4 *>(tile + off) = x[j];
+                const uint4 y = make_uint4(v[0], v[1], v[2], v[3]);
+                *reinterpret_cast<uint4 *>(s.tile[w] + off) = y;
+                *reinterpret_cast<uint4 *>(tile + off) = y;
             }
             if (p == 0) (w ? s_qn : s_kn)[r] = r < nv ? (w ? norm * a.scale : norm) : 0.f;
         }
     }
     __syncthreads();
-    {   // k . k and q . k: a warp has eight columns
-        // K, Q; rows 0-15, 16-31; two sums, each cut off half as often
-        float acc[2][2][2][4] = {};
+    {   // k . k and q . k: a warp has 16 columns, without what is above the diagonal; two sums, each cut off half as often
+        float acc[2][2][2][2][4] = {};                             // K, Q; rows 0-15, 16-31; columns; even and odd steps
         const uint32_t k0 = smem_u32(s.tile[0]), q0 = smem_u32(s.tile[1]);
 #pragma unroll
         for (int ks = 0; ks < DK / 16; ++ks) {
             uint32_t b[4], f[4];
-            // (two of the four matrices are this step's, the rest the next one's: fetched anew, for plainness)
-            ldsm_x4(k0 + tile_at<DK>(warp * 8 + (lane & 7), ks * 2 + ((lane >> 3) & 1)), b[0], b[1], b[2], b[3]);
+            ldsm_x4(k0 + tile_at<DK>(warp * 16 + (lane & 7) + ((lane >> 4) << 3), ks * 2 + ((lane >> 3) & 1)), b[0], b[1], b[2], b[3]);
 #pragma unroll
             for (int w = 0; w < 2; ++w)
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
-                    if (m == 0 && warp >= 2) continue;             // above the diagonal
+                    if (m == 0 && warp) continue;
                     ldsm_x4((w ? q0 : k0) + tile_at<DK>(m * 16 + (lane & 15), ks * 2 + (lane >> 4)), f[0], f[1], f[2], f[3]);
-                    mma16816(acc[w][m][ks & 1], f, b[0], b[1]);
+                    mma16816(acc[w][m][0][ks & 1], f, b[0], b[1]);
+                    mma16816(acc[w][m][1][ks & 1], f, b[2], b[3]);
                 }
         }
         const int g = lane >> 2, t = lane & 3;
@@ -192,111 +205,74 @@ k_delta_prep(const __grid_constant__ DeltaArgs a) {
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    (w ? s_qk : s_kk)[(m * 16 + g + 8 * (e >> 1)) * 32 + warp * 8 + 2 * t + (e & 1)] = acc[w][m][0][e] + acc[w][m][1][e];
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (m || !warp)
+                            (w ? s_qk : s_kk)[(m * 16 + g + 8 * (e >> 1)) * 33 + warp * 16 + n * 8 + 2 * t + (e & 1)] =
+                                acc[w][m][n][0][e] + acc[w][m][n][1][e];
     }
     __syncthreads();
-    // heads of this key head, two at a time: two warps to one, a lane per token
-    const int i = lane, role = warp & 1;
-    float *l = s.la[warp >> 1][0], *am = s.la[warp >> 1][1];
+    const int i = lane;
+    float *l = s.la[warp][0], *am = s.la[warp][1];
     const float kn = s_kn[i], qn = s_qn[i];
-    for (int h0 = 0; h0 < a.group; h0 += 2) {
-        const int hh = h0 + (warp >> 1), h = hk * a.group + hh;
-        const bool mine = hh < a.group;
+    for (int hh = warp; hh < a.group; hh += 2) {
+        const int h = hk * a.group + hh;
         float g = 0.f, beta = 0.f;
-        if (mine && i < nv) {
+        if (i < nv) {
             const int64_t row = q.row0 + t0 + i;
             g = a.g[row * a.g_rs + h];
             if (g < kDeltaLeast) g = kDeltaLeast;
             beta = a.beta[row * a.beta_rs + h];
         }
-        if (h0) __syncthreads();                                   // the heads before these are written
-        // exp(G_i - G_j) for j = i - d, each warp half of the d: sums over just the tokens between, in two parts
-        float sum = 0.f, rest = 0.f, left = 0.f, amax = 0.f;
-        const float bk = beta * kn;
-        auto add = [&](int d) {
-            const float next = __shfl_up_sync(0xffffffffu, g, d);
-            if (i >= d) {
-                const float y = sum + next, z = y - sum;
-                rest += (sum - (y - z)) + (next - z);
-                sum = y;
-            }
-        };
-        if (role)
-            for (int d = 0; d < C / 2; ++d) add(d);
-#pragma unroll 4
-        for (int d = role * (C / 2); d < (role + 1) * (C / 2); ++d) {
-            const float e = expf(sum), decay = fmaf(e, rest, e);
-            const float last = __shfl_sync(0xffffffffu, decay, C - 1);
-            if (i == C - 1 - d) left = last;
-            if (i >= d) {
-                const int j = i - d;
-                const float dk = decay * s_kn[j];
-                const float x = dk * s_qk[i * 32 + j];
-                l[i * 36 + j] = bk * dk * s_kk[i * 32 + j];
-                am[i * 36 + j] = x;
-                amax = fmaxf(amax, fabsf(x));
-            } else {
-                am[i * 36 + i + C - d] = 0.f;
-            }
-            add(d);
-        }
-        HeadBlock *out = reinterpret_cast<HeadBlock *>(a.heads + ((int64_t)at * a.n_head + h) * kDeltaHeadBytes);
-        // (j = 31 - d; the other half's are 0)
-        float w_sum = left * kn;
-        if (mine && (i >= C / 2) == (role == 0)) out->w[i] = w_sum;
-        w_sum = warp_sum(w_sum);
-        if (role == 0)
-            for (int d = C / 2; d < C; ++d) add(d);
-        const float e = expf(sum), gone = fmaf(e, rest, e);        // exp(G_i)
-        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
-        if (lane == 0) {
-            s_amax[warp >> 1][role] = top;
-            s_wsum[warp >> 1][role] = w_sum;
-        }
-        __syncthreads();
-        if (!mine) continue;                                       // (the last round)
-        const int gq = lane >> 2, tq = lane & 3;
-        auto blocks = [&](const float *from, float unit, uint4 (*to)[32]) {
+        __syncwarp();                                              // the head before this one is written
+        // of the aligned runs of 1, 2, 4, ... tokens: sums up to this token, from behind it on, and of all
+        float upto = g, behind = 0.f, all = g, part[5];
 #pragma unroll
-            for (int b = 0; b < kBlocks; ++b) {
-                const float *src = from + (block_n(b) * 8 + gq) * 36 + block_k(b) * 16 + 2 * tq;
-                const float2 lo = *reinterpret_cast<const float2 *>(src), hi = *reinterpret_cast<const float2 *>(src + 8);
-                uint4 v;
-                split(lo.x * unit, lo.y * unit, v.x, v.z);
-                split(hi.x * unit, hi.y * unit, v.y, v.w);
-                to[b][lane] = v;
-            }
-        };
-        if (role) {
-            const float au = unit_of(max(s_amax[warp >> 1][0], s_amax[warp >> 1][1]));
-            blocks(am, au, out->a);
-            const int to = (i >> 1) * 4 + (i & 1);
-            reinterpret_cast<float *>(out->r)[to] = beta;
-            reinterpret_cast<float *>(out->r)[to + 2] = -(bk * gone);
-            reinterpret_cast<float *>(out->o)[to] = qn;
-            reinterpret_cast<float *>(out->o)[to + 2] = qn * gone;
-            if (i == C - 1) {
-                out->last = gone;
-                out->a_unit = inverse_unit(au);
-                out->w_sum = s_wsum[warp >> 1][0] + s_wsum[warp >> 1][1];
-            }
-            continue;
+        for (int v = 0; v < 5; ++v) {
+            part[v] = expf(i >> v & 1 ? upto : behind);
+            s_b[warp][v][i] = part[v] * kn;
+            const float other = __shfl_xor_sync(0xffffffffu, all, 1 << v);
+            if (i >> v & 1) upto += other;
+            else behind += other;
+            all += other;
         }
-        // T by columns: a lane has one
+        const float gone = expf(upto), w = expf(behind) * kn, last = expf(all), bk = beta * kn;
+        const float w_sum = warp_sum(w);
+        __syncwarp();
+        float amax = fabsf(kn * s_qk[i * 33 + i]);
+        am[i * 36 + i] = kn * s_qk[i * 33 + i];
+#pragma unroll
+        for (int v = 4; v >= 0; --v)
+            if (i >> v & 1) {
+                const int j0 = i >> (v + 1) << (v + 1);
+#pragma unroll
+                for (int d = 0; d < 1 << v; ++d) {
+                    const int j = j0 + d;
+                    const float x = part[v] * s_b[warp][v][j], y = x * s_qk[i * 33 + j];
+                    l[(i >> 1) * LP + j * 2 + (i & 1)] = bk * x * s_kk[i * 33 + j];
+                    am[i * 36 + j] = y;
+                    amax = fmaxf(amax, fabsf(y));
+                }
+            }
+        const float au = unit_of(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+        __syncwarp();
+        // T by columns, a lane has one, and two rows at a time
+        uint64_t nx[C];                                            // -x twice
         float x[C];
 #pragma unroll
-        for (int r = 0; r < C; ++r) {
-            float y0 = r == i ? 1.f : 0.f, y1 = 0.f, y2 = 0.f, y3 = 0.f;
+        for (int r = 0; r < C; r += 2) {
+            uint64_t y0 = pk2(r == i ? 1.f : 0.f, r + 1 == i ? 1.f : 0.f), y1 = 0ull;
 #pragma unroll
-            for (int m = 0; m < r; m += 4) {
-                const float4 f = *reinterpret_cast<const float4 *>(l + r * 36 + m);
-                y0 = fmaf(-f.x, x[m], y0);
-                if (m + 1 < r) y1 = fmaf(-f.y, x[m + 1], y1);
-                if (m + 2 < r) y2 = fmaf(-f.z, x[m + 2], y2);
-                if (m + 3 < r) y3 = fmaf(-f.w, x[m + 3], y3);
+            for (int m = 0; m < r; m += 2) {
+                const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(l + (r >> 1) * LP + m * 2);
+                y0 = fma2(f.x, nx[m], y0);
+                y1 = fma2(f.y, nx[m + 1], y1);
             }
-            x[r] = (y0 + y1) + (y2 + y3);
+            upk2(add2(y0, y1), x[r], x[r + 1]);
+            x[r + 1] = fmaf(-l[(r >> 1) * LP + r * 2 + 1], x[r], x[r + 1]);
+            nx[r] = pk2(-x[r], -x[r]);
+            nx[r + 1] = pk2(-x[r + 1], -x[r + 1]);
         }
         __syncwarp();
 #pragma unroll
@@ -310,37 +286,67 @@ k_delta_prep(const __grid_constant__ DeltaArgs a) {
             row += fabsf(f.x) + fabsf(f.y) + fabsf(f.z) + fabsf(f.w);
         }
         const float tu = unit_of(__reduce_max_sync(0xffffffffu, __float_as_uint(row))) * 0x1p-13f;
-        blocks(l, tu, out->t);
-        if (i == 0) out->t_unit = inverse_unit(tu);
+        HeadBlock *out = reinterpret_cast<HeadBlock *>(a.heads + ((int64_t)at * a.n_head + h) * kDeltaHeadBytes);
+        const int gq = lane >> 2, tq = lane & 3;
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
+            const int ri = block_n(b) * 8 + gq, ci = block_k(b) * 16 + 2 * tq, from = ri * 36 + ci;
+            uint4 v;
+            float2 lo = *reinterpret_cast<const float2 *>(l + from), hi = *reinterpret_cast<const float2 *>(l + from + 8);
+            split(lo.x * tu, lo.y * tu, v.x, v.z);
+            split(hi.x * tu, hi.y * tu, v.y, v.w);
+            out->t[b][lane] = v;
+            lo = *reinterpret_cast<const float2 *>(am + from);
+            hi = *reinterpret_cast<const float2 *>(am + from + 8);
+            if (block_n(b) < 2 || block_k(b)) {                    // nothing above the diagonal has been written
+                lo.x = ci <= ri ? lo.x : 0.f;
+                lo.y = ci + 1 <= ri ? lo.y : 0.f;
+                hi.x = ci + 8 <= ri ? hi.x : 0.f;
+                hi.y = ci + 9 <= ri ? hi.y : 0.f;
+            }
+            split(lo.x * au, lo.y * au, v.x, v.z);
+            split(hi.x * au, hi.y * au, v.y, v.w);
+            out->a[b][lane] = v;
+        }
+        const int to = (i >> 1) * 4 + (i & 1);
+        reinterpret_cast<float *>(out->r)[to] = beta;
+        reinterpret_cast<float *>(out->r)[to + 2] = -(bk * gone);
+        reinterpret_cast<float *>(out->o)[to] = qn;
+        reinterpret_cast<float *>(out->o)[to + 2] = qn * gone;
+        out->w[i] = w;
+        if (i == 0) *reinterpret_cast<float4 *>(&out->last) = make_float4(last, inverse_unit(tu), inverse_unit(au), w_sum);
     }
 }
 
 // ---------------------------------------------------------------- the state's walk
 
-// W groups of 16 value elements to a CTA, KS warps to a group: each has DK / KS of the key elements.
+// W groups of 16 value elements to a CTA, KS warps to a group: each has DK / KS of the key elements of the
+// state, and makes the outputs of 32 / KS of a chunk's tokens.
 template <int DK, int W, int KS>
 struct ScanCfg {
     static constexpr int kWarps = W * KS;
     static constexpr int kThreads = (kWarps + 1) * 32;
     static constexpr int kTileBytes = 2 * C * DK * 2;
     static constexpr int kStageBytes = kTileBytes + kDeltaHeadBytes;
-    static constexpr int kVBytes = C * 32;                         // [C tokens][16 values], two to a warp
-    static constexpr int kXWords = KS == 2 ? 24 * 32 : 0;          // what a warp hands its partner, two chunks' worth
+    static constexpr int kVBytes = C * 32;                         // [C tokens][16 values], two to a group
+    static constexpr int kOBytes = C / KS * 32;                    // a warp's outputs on their way
+    static constexpr int kXWords = KS > 1 ? 8 * 4 * 32 : 0;        // what a warp hands its group, two chunks' worth
     // (one CTA per SM where few are wanted: several would find room beside one another, and slow each other
     // down, while other SMs have none)
-    static constexpr int kStages = KS == 2 ? (DK == 128 ? 6 : 9) : (DK == 128 ? 3 : 4);
+    static constexpr int kStages = KS > 1 ? (DK == 128 ? 4 : 6) : (DK == 128 ? 3 : 4);
     static constexpr int kOffV = kStages * kStageBytes;
-    static constexpr int kOffX = kOffV + kWarps * 2 * kVBytes;
+    static constexpr int kOffO = kOffV + W * 2 * kVBytes;
+    static constexpr int kOffX = kOffO + kWarps * kOBytes;
     static constexpr int kOffBars = kOffX + kWarps * 2 * kXWords * 4;
-    static constexpr int kSmem = kOffBars + 2 * kStages * 8;
+    static constexpr int kUsed = kOffBars + 2 * kStages * 8;
+    static constexpr int kSmem = KS > 1 && kUsed < 120 * 1024 ? 120 * 1024 : kUsed;
     static_assert(kSmem <= 227 * 1024, "");
 };
 
 __device__ __forceinline__ uint32_t v_at(int r, int half) { return (uint32_t)(r * 32 + ((half ^ ((r >> 2) & 1)) << 4)); }
 
-__device__ __forceinline__ void stsm_x4_t(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r0), "r"(r1), "r"(r2),
-                 "r"(r3) : "memory");
+__device__ __forceinline__ void stsm_x2_t(uint32_t addr, uint32_t r0, uint32_t r1) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1, %2};" ::"r"(addr), "r"(r0), "r"(r1) : "memory");
 }
 
 template <int N> __device__ __forceinline__ float top_of(const float (&x)[N][4]) {
@@ -448,14 +454,14 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
             st[n][0] = x.x; st[n][1] = x.y; st[n][2] = y.x; st[n][3] = y.y;
         }
     }
-    const uint32_t v0 = smem_u32(smem + F::kOffV + warp * 2 * F::kVBytes);
+    const uint32_t v0 = smem_u32(smem + F::kOffV + warp / KS * 2 * F::kVBytes), o0 = smem_u32(smem + F::kOffO + warp * F::kOBytes);
     float4 *xs = reinterpret_cast<float4 *>(smem + F::kOffX) + lane;
     // values of chunk c: two 16-byte pieces a token, zeros behind the last one
     auto fetch_v = [&](int c) {
         if (c < chunks) {
             const int nv = min(C, q.n - c * C);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = kp; e < 2; e += KS) {
                 const int r = (lane >> 1) + 16 * e, half = lane & 1;
                 const uint16_t *src = a.v + (int64_t)(q.row0 + c * C + min(r, nv - 1)) * a.v_rs + (int64_t)h * a.v_hs + row0 + half * 8;
                 cp_async16(v0 + (c & 1) * F::kVBytes + v_at(r, half), src, r < nv ? 16 : 0);
@@ -475,8 +481,6 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
     }
     for (int c = 0; c < chunks; ++c) {
         const int k = c % S, nv = min(C, q.n - c * C);
-        __syncwarp();                                              // the other half's outputs are on their way
-        fetch_v(c + 1);
         const bool here = __all_sync(0xffffffffu, mbar_wait(full + 8 * k, (uint32_t)(c / S) & 1u));
         if (!here && lane == 0) timed_out();
         if (KS == 1 && !here) {
@@ -521,46 +525,51 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
         for (int n = 0; n < 4; ++n)
 #pragma unroll
             for (int e = 0; e < 4; e += 2) upk2(add2(pk2(pk[n][e], pk[n][e + 1]), pk2(pl[n][e], pl[n][e + 1])), pk[n][e], pk[n][e + 1]);
+        asm volatile("cp.async.wait_all;" ::: "memory");           // this chunk's values
+        constexpr int OT = 4 / KS;                                 // token tiles whose outputs are this warp's
         float ks1 = si;                                            // what the sums are to be multiplied by
-        if constexpr (KS == 2) {
-            // the partner's half of the sums: of S K^T all, of S Q^T those of the 16 tokens whose outputs are this warp's
+        if constexpr (KS > 1) {
+            // sums over the group: of S K^T all, of S Q^T those of this warp's tiles
             ks1 = 1.f;
+            float4 *mine = xs + (warp * 2 + (c & 1)) * (F::kXWords / 4);
+            const float4 *group = xs + (warp / KS * KS * 2 + (c & 1)) * (F::kXWords / 4);
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
+            for (int n = 0; n < 4; ++n) {
 #pragma unroll
                 for (int e = 0; e < 4; e += 2) {
                     scale2(pk[n][e], pk[n][e + 1], si, si);
                     scale2(pq[n][e], pq[n][e + 1], si, si);
                 }
-            float4 *mine = xs + (warp * 2 + (c & 1)) * (F::kXWords / 4);
-            const float4 *other = xs + ((warp ^ 1) * 2 + (c & 1)) * (F::kXWords / 4);
-#pragma unroll
-            for (int n = 0; n < 4; ++n) mine[n * 32] = make_float4(pk[n][0], pk[n][1], pk[n][2], pk[n][3]);
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-                mine[(4 + m) * 32] = kp ? make_float4(pq[m][0], pq[m][1], pq[m][2], pq[m][3])
-                                        : make_float4(pq[2 + m][0], pq[2 + m][1], pq[2 + m][2], pq[2 + m][3]);
-            // (a wait that ran out in either: both leave)
-            if (bar_any(1 + warp / 2, 64, !here)) {
+                mine[n * 32] = make_float4(pk[n][0], pk[n][1], pk[n][2], pk[n][3]);
+                mine[(4 + n) * 32] = make_float4(pq[n][0], pq[n][1], pq[n][2], pq[n][3]);
+            }
+            // (a wait that ran out in one: all leave)
+            if (bar_any(1 + warp / KS, 32 * KS, !here)) {
                 alive = false;
                 break;
             }
-            auto join = [](float (&x)[4], const float4 &y) {
-                upk2(add2(pk2(x[0], x[1]), pk2(y.x, y.y)), x[0], x[1]);
-                upk2(add2(pk2(x[2], x[3]), pk2(y.z, y.w)), x[2], x[3]);
-            };
+            // the same order in every warp: they go on with the same bits
 #pragma unroll
-            for (int n = 0; n < 4; ++n) join(pk[n], other[n * 32]);
+            for (int p = 0; p < KS; ++p) {
+                const float4 *from = group + p * 2 * (F::kXWords / 4);
+                auto join = [&](float (&x)[4], const float4 &y) {
+                    if (p == 0) {
+                        x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
+                        return;
+                    }
+                    upk2(add2(pk2(x[0], x[1]), pk2(y.x, y.y)), x[0], x[1]);
+                    upk2(add2(pk2(x[2], x[3]), pk2(y.z, y.w)), x[2], x[3]);
+                };
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const float4 y = other[(4 + m) * 32];
-                if (kp) join(pq[2 + m], y);
-                else join(pq[m], y);
+                for (int n = 0; n < 4; ++n) join(pk[n], from[n * 32]);
+#pragma unroll
+                for (int m = 0; m < OT; ++m) join(pq[m], from[(4 + kp * OT + m) * 32]);
             }
+        } else {
+            __syncwarp();
         }
+        fetch_v(c + 1);                                            // (the group is through with the chunk before)
         // R = beta V - beta exp(G) |k| (S K^T)
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-        __syncwarp();
         const uint32_t vt = v0 + (c & 1) * F::kVBytes;
         float r[4][4];
 #pragma unroll
@@ -605,63 +614,53 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
         const float last = hb->last;
         sb = fmaf(last, sb, 2.f * hb->w_sum * (__uint_as_float(rtop) * hb->t_unit));
         const float nu = unit_of(__float_as_uint(sb)), ni = inverse_unit(nu);
-        // o = |q| (exp(G) S q + A u), of two warps of a group 16 tokens each
+        // o = |q| (exp(G) S q + A u)
         {
             operand(u, hi, lo);
-            float x[4][4] = {};
-            auto products = [&](auto first, auto end) {
-                constexpr int B0 = decltype(first)::value, B1 = decltype(end)::value;
-                uint4 f[B1 - B0];
+            float x[OT][4] = {};
+            uint4 f[OT][2];
 #pragma unroll
-                for (int b = B0; b < B1; ++b) f[b - B0] = hb->a[b][lane];
+            for (int m = 0; m < OT; ++m) {
+                const int n = kp * OT + m;                         // blocks n and, from token 16 on, n + 2
+                f[m][0] = hb->a[n][lane];
+                if (n >= 2) f[m][1] = hb->a[n + 2][lane];
+            }
+            auto product = [&](int ks, const uint32_t (&op)[2][4], bool low) {
 #pragma unroll
-                for (int b = B0; b < B1; ++b) mma16816(x[block_n(b)], hi[block_k(b)], f[b - B0].x, f[b - B0].y);
-#pragma unroll
-                for (int b = B0; b < B1; ++b) mma16816(x[block_n(b)], lo[block_k(b)], f[b - B0].x, f[b - B0].y);
-#pragma unroll
-                for (int b = B0; b < B1; ++b) mma16816(x[block_n(b)], hi[block_k(b)], f[b - B0].z, f[b - B0].w);
+                for (int m = 0; m < OT; ++m)
+                    if (ks == 0 || kp * OT + m >= 2) mma16816(x[m], op[ks], low ? f[m][ks].z : f[m][ks].x, low ? f[m][ks].w : f[m][ks].y);
             };
-            using I0 = std::integral_constant<int, 0>;
-            using I2 = std::integral_constant<int, 2>;
-            using I6 = std::integral_constant<int, 6>;
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                product(ks, hi, false);
+                product(ks, lo, false);
+                product(ks, hi, true);
+            }
             const float back = ui * hb->a_unit;
-            // through the values' place, which has been read, into rows
-            auto rows = [&](auto half) {
-                constexpr int NP = decltype(half)::value;
-                uint32_t o16[2][2];
+            // through shared memory into rows
+            uint32_t o16[OT][2];
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const int n = 2 * NP + m;
-                    const float4 f = hb->o[n * 4 + t];
-                    const uint64_t fa = mul2(pk2(f.x, f.y), pk2(back, back)), fs = mul2(pk2(f.z, f.w), pk2(ks1, ks1));
+            for (int m = 0; m < OT; ++m) {
+                const float4 w = hb->o[(kp * OT + m) * 4 + t];
+                const uint64_t fa = mul2(pk2(w.x, w.y), pk2(back, back)), fs = mul2(pk2(w.z, w.w), pk2(ks1, ks1));
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float y0, y1;
-                        upk2(fma2(fa, pk2(x[n][2 * e], x[n][2 * e + 1]), mul2(fs, pk2(pq[n][2 * e], pq[n][2 * e + 1]))), y0, y1);
-                        o16[m][e] = T == PAGED_F16 ? pack_half2(y0, y1) : pack_bf162(y0, y1);
-                    }
+                for (int e = 0; e < 2; ++e) {
+                    float y0, y1;
+                    upk2(fma2(fa, pk2(x[m][2 * e], x[m][2 * e + 1]), mul2(fs, pk2(pq[m][2 * e], pq[m][2 * e + 1]))), y0, y1);
+                    o16[m][e] = T == PAGED_F16 ? pack_half2(y0, y1) : pack_bf162(y0, y1);
                 }
-                stsm_x4_t(vt + v_at(NP * 16 + (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1), o16[0][0], o16[0][1], o16[1][0], o16[1][1]);
-                __syncwarp();
-                const int row = NP * 16 + (lane >> 1), piece = lane & 1;
+            }
+#pragma unroll
+            for (int m = 0; m < OT; ++m) stsm_x2_t(o0 + v_at(m * 8 + (lane & 7), (lane >> 3) & 1), o16[m][0], o16[m][1]);
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < (OT + 1) / 2; ++e) {
+                const int row = (lane >> 1) + 16 * e, piece = lane & 1, token = kp * OT * 8 + row;
+                if (OT == 1 && lane >= 16) break;
                 uint4 y;
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w) : "r"(vt + v_at(row, piece)));
-                if (row < nv)
-                    *reinterpret_cast<uint4 *>(a.o + (int64_t)(q.row0 + c * C + row) * a.o_rs + (int64_t)h * a.o_hs + row0 + piece * 8) = y;
-            };
-            if constexpr (KS == 1) {
-                products(I0{}, I6{});
-                __syncwarp();
-                rows(std::integral_constant<int, 0>{});
-                rows(std::integral_constant<int, 1>{});
-            } else if (kp) {
-                products(I2{}, I6{});
-                __syncwarp();
-                rows(std::integral_constant<int, 1>{});
-            } else {
-                products(I0{}, I2{});
-                __syncwarp();
-                rows(std::integral_constant<int, 0>{});
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w) : "r"(o0 + v_at(row, piece)) : "memory");
+                if (token < nv)
+                    *reinterpret_cast<uint4 *>(a.o + (int64_t)(q.row0 + c * C + token) * a.o_rs + (int64_t)h * a.o_hs + row0 + piece * 8) = y;
             }
         }
         // S <- exp(G_last) S + U (exp(G_last - G) |k| K), all times the new unit
@@ -750,10 +749,10 @@ cudaError_t scan(const DeltaArgs &a, int dv, cudaStream_t st) {
 template <int T, int DK>
 cudaError_t go(const DeltaArgs &a, int dv, int sms, cudaStream_t st) {
     const int64_t chunks = delta_chunks(a.n_rows, a.n_seq);
-    k_delta_prep<T, DK><<<(unsigned)(chunks * a.n_head_k), 128, 0, st>>>(a);
+    k_delta_prep<T, DK><<<(unsigned)(chunks * a.n_head_k), 64, 0, st>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    // few sequences times heads: more and smaller CTAs
+    // few sequences times heads: smaller CTAs, and several warps to a group
     if ((int64_t)a.n_seq * a.n_head * dv / 32 > sms) return scan<T, DK, 4, 1>(a, dv, st);
     return scan<T, DK, 2, 2>(a, dv, st);
 }
