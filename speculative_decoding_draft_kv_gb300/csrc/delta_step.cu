@@ -11,7 +11,10 @@
 // memory.
 //
 // Bound by the state's bytes, 64 KB read and written per head of 128 x 128, as long as a sequence has
-// few tokens: a token takes 3 flops per state element beside 8 bytes of it.
+// few tokens: a token takes 3 flops per state element beside 8 bytes of it.  What counts is bytes under way: eight
+// CTAs to an SM (64 sequences of 32 heads, a token each: 62 us with five, 51 with eight; ten spill, 59), and states that
+// pass through L2 as what is not read again (46 us; 5.8 TB/s, 87 % of the copy rate).  With states kept behind every
+// token (64 branches of up to 9 tokens) the one that all read stays there: 103 us, 6.6 TB/s, and 108 otherwise.
 #include "delta.h"
 
 #include "ring_internal.h"
@@ -46,7 +49,7 @@ __device__ __forceinline__ float warp_sum(float x) {
 
 // DK key elements, DV value elements
 template <int T, int DK, int DV>
-__global__ void __launch_bounds__(kStepThreads)
+__global__ void __launch_bounds__(kStepThreads, DK == 64 ? 6 : 8)
 k_delta_step(const __grid_constant__ DeltaArgs a) {
     constexpr int E = DK / 8;                          // of a lane's part of a row
     constexpr int J = 32 / E;                          // rows of a lane
@@ -74,7 +77,8 @@ k_delta_step(const __grid_constant__ DeltaArgs a) {
         for (int j = 0; j < J; ++j)
 #pragma unroll
             for (int e = 0; e < E / 4; ++e) {
-                const float4 x = *reinterpret_cast<const float4 *>(src + j * 4 * DK + e * 32);
+                const float4 *from = reinterpret_cast<const float4 *>(src + j * 4 * DK + e * 32);
+                const float4 x = a.save ? *from : __ldcs(from);
                 st[j][2 * e] = pk2(x.x, x.y);
                 st[j][2 * e + 1] = pk2(x.z, x.w);
             }
@@ -96,7 +100,7 @@ k_delta_step(const __grid_constant__ DeltaArgs a) {
 #pragma unroll
             for (int e = 0; e < E / 4; ++e) {
                 const float2 x = unpack2(st[j][2 * e]), y = unpack2(st[j][2 * e + 1]);
-                *reinterpret_cast<float4 *>(dst + j * 4 * DK + e * 32) = make_float4(x.x, x.y, y.x, y.y);
+                __stcs(reinterpret_cast<float4 *>(dst + j * 4 * DK + e * 32), make_float4(x.x, x.y, y.x, y.y));
             }
     };
 
