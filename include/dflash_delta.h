@@ -94,7 +94,7 @@ typedef struct delta_batch {
  * two 16-bit parts, 22 bits together.  Keys that are not normalised want beta |k|^2 of at most 2, as the
  * recurrence itself does: beyond, it grows with every token.
  * An infinity or NaN in a token's rows reaches the token's value elements (in v) or all of its head (in the
- * others) from there on, and where max_q is above 8 the same elements of up to 31 tokens in front of it.
+ * others) from there on, and in a sequence of more than 8 tokens the same elements of up to 31 in front of it.
  * A sequence whose row bounds contradict each other (DELTA_ERR_BATCH), or whose slot_in is past the pool
  * (DELTA_ERR_SLOT), is left alone: its rows of o and its slots stay as they were.  A slot past
  * the pool in slot_out or save is not written (DELTA_ERR_SLOT).

@@ -24,6 +24,7 @@ struct DeltaArgs {
     float scale, eps;
     int n_seq, max_q, n_slots, n_head, n_head_k, group;   // group: heads of a key head
     int normalise;
+    int split;                           // sequences of up to kDeltaFew tokens are one kernel's, longer ones the other's
     // chunks of many tokens: what k_delta_prep leaves for k_delta_scan
     uint8_t *tiles;                      // [chunks][n_head_k][K, Q] F16 tiles of 32 rows
     uint8_t *heads;                      // [chunks][n_head] blocks of kDeltaHeadBytes
@@ -34,6 +35,10 @@ constexpr int kDeltaHeadBytes = 2 * 6 * 32 * 16 + 2 * 16 * 16 + 32 * 4 + 16;
 // Chunks, with room for each sequence's ragged last one: sequence s has those from q_start[s] / 32 + s on.
 inline int64_t delta_chunks(int64_t n_rows, int n_seq) { return n_rows / kDeltaChunk + n_seq; }
 
+// Sequences of up to so many tokens go token by token, also beside longer ones, whose batch has two kernels run side by
+// side; above it chunks are faster (32 sequences of 32 heads of 128 x 128, us: 8 tokens each 49 by tokens and 62
+// by chunks, 12 tokens 68 and 63, 16 tokens 86 and 62; heads of 64 x 64: 21 and 29, 27 and 29, 33 and 29).
+constexpr int kDeltaFew = 8;
 constexpr float kDeltaLeast = -1e4f;     // log decays below it count as it: exp() of both is 0
 
 // A sequence's rows and the slot that it begins from, as far as the arrays can be believed.

@@ -119,7 +119,7 @@ k_delta_prep(const __grid_constant__ DeltaArgs a) {
     uint32_t bits;
     const DeltaSeq q = delta_seq(a, seq, bits);
     const int t0 = (at - chunk_base(q.row0, seq)) * C;
-    if (!q.ok || t0 < 0 || t0 >= q.n) return;
+    if (!q.ok || q.n <= kDeltaFew || t0 < 0 || t0 >= q.n) return;
     const int nv = min(C, q.n - t0);
 
     // rows: four lanes to one, eight rows to a warp
@@ -331,16 +331,13 @@ struct ScanCfg {
     static constexpr int kVBytes = C * 32;                         // [C tokens][16 values], two to a group
     static constexpr int kOBytes = C / KS * 32;                    // a warp's outputs on their way
     static constexpr int kXWords = KS > 1 ? 8 * 4 * 32 : 0;        // what a warp hands its group, two chunks' worth
-    // (one CTA per SM where few are wanted: several would find room beside one another, and slow each other
-    // down, while other SMs have none)
-    static constexpr int kStages = KS > 1 ? (DK == 128 ? 4 : 6) : (DK == 128 ? 3 : 4);
+    static constexpr int kStages = DK == 128 ? 3 : 4;
     static constexpr int kOffV = kStages * kStageBytes;
     static constexpr int kOffO = kOffV + W * 2 * kVBytes;
     static constexpr int kOffX = kOffO + kWarps * kOBytes;
     static constexpr int kOffBars = kOffX + kWarps * 2 * kXWords * 4;
-    static constexpr int kUsed = kOffBars + 2 * kStages * 8;
-    static constexpr int kSmem = KS > 1 && kUsed < 120 * 1024 ? 120 * 1024 : kUsed;
-    static_assert(kSmem <= 227 * 1024, "");
+    static constexpr int kSmem = kOffBars + 2 * kStages * 8;
+    static_assert(kSmem <= 113 * 1024, "two CTAs per SM");
 };
 
 __device__ __forceinline__ uint32_t v_at(int r, int half) { return (uint32_t)(r * 32 + ((half ^ ((r >> 2) & 1)) << 4)); }
@@ -399,8 +396,10 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     uint32_t bits;
-    const DeltaSeq q = delta_seq(a, s, bits);
+    DeltaSeq q = delta_seq(a, s, bits);
     if (bits && threadIdx.x == 0 && h == 0 && part == 0) atomicOr(a.err, bits);
+    q.ok = q.ok && q.n > kDeltaFew;                                // the others are k_delta_step's
+    pdl_trigger();
     __syncthreads();
     const int chunks = q.ok ? (q.n + C - 1) / C : 0;
     const int64_t base = chunk_base(q.row0, s);
@@ -729,14 +728,18 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
     }
 }
 
+constexpr int kAlone = 120 * 1024;       // more than half of an SM's shared memory
+
 template <int T, int DK, int W, int KS>
-cudaError_t scan(const DeltaArgs &a, int dv, cudaStream_t st) {
+cudaError_t scan(const DeltaArgs &a, int dv, int sms, cudaStream_t st) {
     using F = ScanCfg<DK, W, KS>;
     const int parts = dv / (16 * W);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((int64_t)a.n_seq * a.n_head * parts), 1, 1);
     cfg.blockDim = dim3(F::kThreads);
-    cfg.dynamicSmemBytes = F::kSmem;
+    // (one CTA per SM where there are no more: beginning beside the kernel in front of it, two would find room on one SM,
+    // and slow each other down, while others have none)
+    cfg.dynamicSmemBytes = cfg.gridDim.x <= (unsigned)sms ? kAlone : F::kSmem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -752,13 +755,13 @@ cudaError_t go(const DeltaArgs &a, int dv, int sms, cudaStream_t st) {
     k_delta_prep<T, DK><<<(unsigned)(chunks * a.n_head_k), 64, 0, st>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    // few sequences times heads: smaller CTAs, and several warps to a group
-    if ((int64_t)a.n_seq * a.n_head * dv / 32 > sms) return scan<T, DK, 4, 1>(a, dv, st);
-    return scan<T, DK, 2, 2>(a, dv, st);
+    // few sequences times heads, up to two small CTAs for every SM: two warps to a group
+    if ((int64_t)a.n_seq * a.n_head * dv / 32 > 2 * sms) return scan<T, DK, 4, 1>(a, dv, sms, st);
+    return scan<T, DK, 2, 2>(a, dv, sms, st);
 }
 
 template <int T, int DK, int W, int KS> cudaError_t allow() {
-    return cudaFuncSetAttribute(k_delta_scan<T, DK, W, KS>, cudaFuncAttributeMaxDynamicSharedMemorySize, ScanCfg<DK, W, KS>::kSmem);
+    return cudaFuncSetAttribute(k_delta_scan<T, DK, W, KS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAlone);
 }
 template <int T> cudaError_t allow_all() {
     cudaError_t e = allow<T, 64, 2, 2>();

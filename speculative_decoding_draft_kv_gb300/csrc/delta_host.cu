@@ -100,8 +100,9 @@ int check_batch(const char *who, const delta_state *s, const delta_batch *b, int
 
 int64_t up256(int64_t x) { return (x + 255) & ~(int64_t)255; }
 
-// Which kernels serve a batch: token by token up to 8, and where states are kept behind single tokens.
-bool by_chunks(const delta_batch *b) { return b->max_q > 8 && !b->save; }
+// Which kernels serve a batch: token by token alone where no sequence is longer than kDeltaFew, and where states are
+// kept behind single tokens.
+bool by_chunks(const delta_batch *b) { return b->max_q > kDeltaFew && !b->save; }
 
 int64_t tile_bytes(const delta_state *s, int64_t chunks, int n_head_k) {
     return up256(chunks * n_head_k * 2 * kDeltaChunk * s->dim_k * 2);
@@ -195,6 +196,8 @@ extern "C" int delta_rule(const delta_rule_args *g, void *stream) {
         a.tiles = static_cast<uint8_t *>(g->workspace);
         a.heads = a.tiles + tile_bytes(s, delta_chunks(g->n_rows, b->n_seq), g->n_head_k);
         e = launch_delta_chunk(a, g->dtype, s->dim_k, s->dim_v, d.sms, st);
+        a.split = 1;
+        if (e == cudaSuccess) e = launch_delta_step(a, g->dtype, s->dim_k, s->dim_v, st);
     } else {
         e = launch_delta_step(a, g->dtype, s->dim_k, s->dim_v, st);
     }

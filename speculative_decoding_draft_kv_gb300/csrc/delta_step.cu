@@ -64,7 +64,9 @@ k_delta_step(const __grid_constant__ DeltaArgs a) {
     uint32_t bits;
     const DeltaSeq q = delta_seq(a, s, bits);
     if (bits && threadIdx.x == 0 && h == 0 && part == 0) atomicOr(a.err, bits);
-    if (!q.ok) return;
+    // (beside the kernel of longer sequences: what waits for this one waits for that too)
+    if (a.split && threadIdx.x == 0 && blockIdx.x == 0) pdl_wait();
+    if (!q.ok || (a.split && q.n > kDeltaFew)) return;
     const int sub = lane & 7, rg = lane >> 3;          // the lane's part of a row, its row of four
     const int row0 = part * kRows + warp * 4 * J;      // the warp's rows: row0 + 4 j + rg
     auto place = [&](int slot) {
@@ -202,8 +204,16 @@ k_delta_step(const __grid_constant__ DeltaArgs a) {
 template <int T, int DK, int DV>
 cudaError_t go(const DeltaArgs &a, cudaStream_t st) {
     constexpr int parts = DV / (4 * 4 * (32 / (DK / 8)));
-    k_delta_step<T, DK, DV><<<(unsigned)((int64_t)a.n_seq * a.n_head * parts), kStepThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((int64_t)a.n_seq * a.n_head * parts), 1, 1);
+    cfg.blockDim = dim3(kStepThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.split ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, k_delta_step<T, DK, DV>, a);
 }
 template <int T>
 cudaError_t pick(const DeltaArgs &a, int dk, int dv, cudaStream_t st) {

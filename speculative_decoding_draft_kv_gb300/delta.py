@@ -14,7 +14,7 @@ import ctypes
 
 import torch
 
-from .paged import _TYPES, _device, _half, _rows, _stream, _vector, _workspace
+from .paged import _TYPES, _current_device, _device, _half, _packer, _rows, _stream, _vector, _workspace
 from .ring import RING_EDEVICE, RING_OK, RingError, _load as _load_ring
 
 DELTA_ERR_BATCH, DELTA_ERR_SLOT, DELTA_ERR_WAIT = 1, 2, 4
@@ -42,6 +42,7 @@ class DeltaRuleArgs(ctypes.Structure):
                 [(n, _f32) for n in ("scale", "eps")] + [(n, _i32) for n in ("n_head_k", "dtype", "normalise", "reserved")])
 
 
+_pack_rule = _packer(DeltaRuleArgs)
 _LIB = None
 
 
@@ -109,7 +110,7 @@ class DeltaBatch:
 
 
 def _one_device(state, batch):
-    d = torch.cuda.current_device()
+    d = _current_device()
     if state.device != d or batch.device != d:
         raise ValueError(f"state (device {state.device}) and batch (device {batch.device}) must be on the current "
                          f"device, {d}")
@@ -151,9 +152,9 @@ def delta_rule(state, batch, q, k, v, g, beta, o, normalise=True, eps=1e-6, scal
         raise ValueError(f"save must have {n} entries, got {batch.rows}")
     st = _stream(stream, dev)
     workspace = _workspace(workspace, lambda: delta_rule_workspace(state, batch, n, heads_k), st, stream, dev, q.device)
-    a = DeltaRuleArgs(state.address, batch.address, qp, kp, vp, op, qr, qh, kr, kh, vr, vh, orow, oh, gp, bp, gr, br,
-                      workspace.data_ptr(), workspace.numel(), n, scale, eps, heads_k, _TYPES[dtype], bool(normalise), 0)
-    _check(_load().delta_rule(ctypes.addressof(a), st))
+    a = _pack_rule(state.address, batch.address, qp, kp, vp, op, qr, qh, kr, kh, vr, vh, orow, oh, gp, bp, gr, br,
+                   workspace.data_ptr(), workspace.numel(), n, scale, eps, heads_k, _TYPES[dtype], bool(normalise), 0)
+    _check(_load().delta_rule(a, st))
 
 
 def delta_device_error() -> int:
