@@ -16,7 +16,7 @@
 // memory would be written, fenced and read between any two of the four dependent products of a chunk).
 //
 // Precision.  The state, its update and all sums are float32.  Operands are F16 pairs hi + lo, 22 bits together,
-// after powers of two that bring them below 2^14; the state is kept times its own.  R's is by its largest
+// after powers of two that bring them below 2^15; the state is kept times its own.  R's is by its largest
 // value; U's and the state's are by bounds (T's largest row sum, the decays' sum), which may be 2^16 above
 // the values before an F16 pair loses bits, and the state's is set right every fourth chunk.  Keys and queries
 // are one F16 each, after a power of two by the row's norm: exact but for elements below 2^-14 of the norm, which
@@ -24,69 +24,12 @@
 // multiply-add: tensor-core sums are cut off, not rounded, and hundreds of chunks would add that up.  Decays are
 // exponentials of sums over just the tokens between, so neither a long chunk nor a state that was dropped costs
 // later tokens their precision.
-#include "delta.h"
-
-#include "ring_internal.h"
-#include "ptx.h"
-#include "paged_ptx.h"
+#include "delta_chunk.cuh"
 
 #include <type_traits>
 
 namespace dflash {
 namespace {
-
-constexpr int C = kDeltaChunk;                         // tokens of a chunk
-static_assert(C == 32, "a lane per token");
-
-template <int T> __device__ __forceinline__ float from16(uint32_t x) {
-    if constexpr (T == PAGED_F16) return __half2float(__ushort_as_half((unsigned short)x));
-    else return __uint_as_float(x << 16);
-}
-__device__ __forceinline__ float2 half2_floats(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2 *>(&x)); }
-
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    return x;
-}
-
-// byte offset of 16-byte chunk ch of row r in a tile of DK F16 columns: conflict-free for ldmatrix
-template <int DK> __device__ __forceinline__ uint32_t tile_at(int r, int ch) { return (uint32_t)(r * DK * 2 + ((ch ^ (r & 7)) << 4)); }
-
-// Of T or A, the (token tile, key step) blocks with something in them, in the order of use.
-constexpr int kBlocks = 6;
-__host__ __device__ constexpr int block_n(int b) { return b < 4 ? b : b - 2; }     // 0 1 2 3 2 3
-__host__ __device__ constexpr int block_k(int b) { return b < 4 ? 0 : 1; }
-
-// A head's part of a chunk in the workspace: B operands a lane's words beside one another, then scalars.
-struct HeadBlock {
-    uint4 t[kBlocks][32];                              // T: hi, hi, lo, lo
-    uint4 a[kBlocks][32];                              // exp(G_i - G_j) q_i . k_j: likewise
-    float4 r[C / 2];                                   // of tokens 2i, 2i+1: beta twice, -beta exp(G) |k| twice
-    float4 o[C / 2];                                   // |q| twice, |q| exp(G) twice
-    float w[C];                                        // exp(G_last - G) |k|
-    float last, t_unit, a_unit, w_sum;                 // exp(G_last); what T and A are to be multiplied by; sum of w
-};
-static_assert(sizeof(HeadBlock) == kDeltaHeadBytes, "as the workspace is laid out");
-
-__device__ __forceinline__ int chunk_base(int row0, int s) { return row0 / C + s; }
-
-// the power of two that brings m > 0 (as bits) to [2^12, 2^13), as far as float32 has it and its inverse
-__device__ __forceinline__ float unit_of(uint32_t bits) {
-    const int e = (int)(bits >> 23);                   // biased
-    return bits == 0u || e == 255 ? 1.f : __uint_as_float((uint32_t)min(241, max(13, 254 + 12 - e)) << 23);
-}
-__device__ __forceinline__ float inverse_unit(float u) { return __uint_as_float((254u << 23) - __float_as_uint(u)); }
-
-// x0, x1 as two F16 pairs
-__device__ __forceinline__ void split(float x0, float x1, uint32_t &hi, uint32_t &lo) {
-    hi = pack_half2(x0, x1);
-    const float2 h = half2_floats(hi);
-    float l0, l1;
-    upk2(fma2(pk2(h.x, h.y), pk2(-1.f, -1.f), pk2(x0, x1)), l0, l1);
-    lo = pack_half2(l0, l1);
-}
-__device__ __forceinline__ void scale2(float &x0, float &x1, float f0, float f1) { upk2(mul2(pk2(x0, x1), pk2(f0, f1)), x0, x1); }
 
 // ---------------------------------------------------------------- what the state is not needed for
 
@@ -173,7 +116,7 @@ k_delta_prep(const __grid_constant__ DeltaArgs a) {
                     upk2(mul2(pk2(from16<T>(v[e2] & 0xffffu), from16<T>(v[e2] >> 16)), down2), f0, f1);
                     v[e2] = pack_half2(f0, f1);
                 }
-                const uint32_t off = tile_at<DK>(r, p + 4 * j);
+                const uint32_t off = tile_at(r, p + 4 * j);
                 const uint4 y = make_uint4(v[0], v[1], v[2], v[3]);
                 *reinterpret_cast<uint4 *>(s.tile[w] + off) = y;
                 *reinterpret_cast<uint4 *>(tile + off) = y;
@@ -188,13 +131,13 @@ k_delta_prep(const __grid_constant__ DeltaArgs a) {
 #pragma unroll
         for (int ks = 0; ks < DK / 16; ++ks) {
             uint32_t b[4], f[4];
-            ldsm_x4(k0 + tile_at<DK>(warp * 16 + (lane & 7) + ((lane >> 4) << 3), ks * 2 + ((lane >> 3) & 1)), b[0], b[1], b[2], b[3]);
+            ldsm_x4(k0 + tile_at(warp * 16 + (lane & 7) + ((lane >> 4) << 3), ks * 2 + ((lane >> 3) & 1)), b[0], b[1], b[2], b[3]);
 #pragma unroll
             for (int w = 0; w < 2; ++w)
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
                     if (m == 0 && warp) continue;
-                    ldsm_x4((w ? q0 : k0) + tile_at<DK>(m * 16 + (lane & 15), ks * 2 + (lane >> 4)), f[0], f[1], f[2], f[3]);
+                    ldsm_x4((w ? q0 : k0) + tile_at(m * 16 + (lane & 15), ks * 2 + (lane >> 4)), f[0], f[1], f[2], f[3]);
                     mma16816(acc[w][m][0][ks & 1], f, b[0], b[1]);
                     mma16816(acc[w][m][1][ks & 1], f, b[2], b[3]);
                 }
@@ -278,35 +221,62 @@ k_delta_prep(const __grid_constant__ DeltaArgs a) {
 #pragma unroll
         for (int r = 0; r < C; ++r) l[r * 36 + i] = x[r];
         __syncwarp();
-        // the largest row sum of magnitudes, 1 at least, to (1/2, 1]
+        // the largest row sum of magnitudes, 1 at least, to [2^8, 2^9): with R below 2^6 U stays below 2^15, and neither
+        // operand's low part falls below F16's smallest numbers before it is 2^-33 of the largest values
         float row = 0.f;
 #pragma unroll
         for (int m = 0; m < C; m += 4) {
             const float4 f = *reinterpret_cast<const float4 *>(l + i * 36 + m);
             row += fabsf(f.x) + fabsf(f.y) + fabsf(f.z) + fabsf(f.w);
         }
-        const float tu = unit_of(__reduce_max_sync(0xffffffffu, __float_as_uint(row))) * 0x1p-13f;
-        HeadBlock *out = reinterpret_cast<HeadBlock *>(a.heads + ((int64_t)at * a.n_head + h) * kDeltaHeadBytes);
-        const int gq = lane >> 2, tq = lane & 3;
+        const float tu = unit_of(__reduce_max_sync(0xffffffffu, __float_as_uint(row))) * 0x1p-4f;
+        uint8_t *block = a.heads + ((int64_t)at * a.n_head + h) * kDeltaHeadBytes;
+        HeadScalars *out;
+        if (a.wide) {                                              // a lane has a row, nothing above the diagonal
+            WideBlock *wide = reinterpret_cast<WideBlock *>(block);
+            out = &wide->s;
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-            const int ri = block_n(b) * 8 + gq, ci = block_k(b) * 16 + 2 * tq, from = ri * 36 + ci;
-            uint4 v;
-            float2 lo = *reinterpret_cast<const float2 *>(l + from), hi = *reinterpret_cast<const float2 *>(l + from + 8);
-            split(lo.x * tu, lo.y * tu, v.x, v.z);
-            split(hi.x * tu, hi.y * tu, v.y, v.w);
-            out->t[b][lane] = v;
-            lo = *reinterpret_cast<const float2 *>(am + from);
-            hi = *reinterpret_cast<const float2 *>(am + from + 8);
-            if (block_n(b) < 2 || block_k(b)) {                    // nothing above the diagonal has been written
-                lo.x = ci <= ri ? lo.x : 0.f;
-                lo.y = ci + 1 <= ri ? lo.y : 0.f;
-                hi.x = ci + 8 <= ri ? hi.x : 0.f;
-                hi.y = ci + 9 <= ri ? hi.y : 0.f;
+            for (int ch = 0; ch < 4; ++ch)
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const float *from = (w ? am : l) + i * 36 + ch * 8, unit = w ? au : tu;
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float2 x = *reinterpret_cast<const float2 *>(from + 2 * e);
+                        const int j = ch * 8 + 2 * e;
+                        x.x = j <= i ? x.x : 0.f;
+                        x.y = j + 1 <= i ? x.y : 0.f;
+                        split(x.x * unit, x.y * unit, hi[e], lo[e]);
+                    }
+                    uint4 (*to)[8] = w ? wide->a : wide->t;
+                    to[i][ch ^ (i & 7)] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    to[i][(ch + 4) ^ (i & 7)] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+        } else {
+            HeadBlock *narrow = reinterpret_cast<HeadBlock *>(block);
+            out = &narrow->s;
+            const int gq = lane >> 2, tq = lane & 3;
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                const int ri = block_n(b) * 8 + gq, ci = block_k(b) * 16 + 2 * tq, from = ri * 36 + ci;
+                uint4 v;
+                float2 lo = *reinterpret_cast<const float2 *>(l + from), hi = *reinterpret_cast<const float2 *>(l + from + 8);
+                split(lo.x * tu, lo.y * tu, v.x, v.z);
+                split(hi.x * tu, hi.y * tu, v.y, v.w);
+                narrow->t[b][lane] = v;
+                lo = *reinterpret_cast<const float2 *>(am + from);
+                hi = *reinterpret_cast<const float2 *>(am + from + 8);
+                if (block_n(b) < 2 || block_k(b)) {                // nothing above the diagonal has been written
+                    lo.x = ci <= ri ? lo.x : 0.f;
+                    lo.y = ci + 1 <= ri ? lo.y : 0.f;
+                    hi.x = ci + 8 <= ri ? hi.x : 0.f;
+                    hi.y = ci + 9 <= ri ? hi.y : 0.f;
+                }
+                split(lo.x * au, lo.y * au, v.x, v.z);
+                split(hi.x * au, hi.y * au, v.y, v.w);
+                narrow->a[b][lane] = v;
             }
-            split(lo.x * au, lo.y * au, v.x, v.z);
-            split(hi.x * au, hi.y * au, v.y, v.w);
-            out->a[b][lane] = v;
         }
         const int to = (i >> 1) * 4 + (i & 1);
         reinterpret_cast<float *>(out->r)[to] = beta;
@@ -327,7 +297,7 @@ struct ScanCfg {
     static constexpr int kWarps = W * KS;
     static constexpr int kThreads = (kWarps + 1) * 32;
     static constexpr int kTileBytes = 2 * C * DK * 2;
-    static constexpr int kStageBytes = kTileBytes + kDeltaHeadBytes;
+    static constexpr int kStageBytes = kTileBytes + (int)sizeof(HeadBlock);
     static constexpr int kVBytes = C * 32;                         // [C tokens][16 values], two to a group
     static constexpr int kOBytes = C / KS * 32;                    // a warp's outputs on their way
     static constexpr int kXWords = KS > 1 ? 8 * 4 * 32 : 0;        // what a warp hands its group, two chunks' worth
@@ -420,7 +390,7 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
                 const uint32_t dst = smem_u32(smem + k * F::kStageBytes);
                 mbar_expect_tx(full + 8 * k, F::kStageBytes);
                 bulk_g2s(dst, a.tiles + ((base + c) * a.n_head_k + hk) * F::kTileBytes, F::kTileBytes, full + 8 * k);
-                bulk_g2s(dst + F::kTileBytes, a.heads + ((base + c) * a.n_head + h) * kDeltaHeadBytes, kDeltaHeadBytes, full + 8 * k);
+                bulk_g2s(dst + F::kTileBytes, a.heads + ((base + c) * a.n_head + h) * kDeltaHeadBytes, (uint32_t)sizeof(HeadBlock), full + 8 * k);
             }
             // no copy may land after the CTA is gone
             for (int k = max(0, c - S); k < c; ++k)
@@ -496,7 +466,7 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
         auto fetch = [&](int ks) {
 #pragma unroll
             for (int np = 0; np < 2; ++np) {
-                const uint32_t off = tile_at<DK>(np * 16 + (lane & 7) + ((lane >> 4) << 3), (kp * STEPS + ks) * 2 + ((lane >> 3) & 1));
+                const uint32_t off = tile_at(np * 16 + (lane & 7) + ((lane >> 4) << 3), (kp * STEPS + ks) * 2 + ((lane >> 3) & 1));
                 uint32_t (&x)[4] = fk[ks & 1][np], (&y)[4] = fq[ks & 1][np];
                 ldsm_x4(kt + off, x[0], x[1], x[2], x[3]);
                 ldsm_x4(qt + off, y[0], y[1], y[2], y[3]);
@@ -578,7 +548,7 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
                 const int n = 2 * np + m;
-                const float4 f = hb->r[n * 4 + t];                 // beta, then -beta exp(G) |k| of tokens 8n + 2t, + 1
+                const float4 f = hb->s.r[n * 4 + t];                 // beta, then -beta exp(G) |k| of tokens 8n + 2t, + 1
                 const uint64_t b2 = pk2(f.x, f.y), c2 = mul2(pk2(f.z, f.w), pk2(ks1, ks1));
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -587,11 +557,11 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
                 }
             }
         }
-        // U = R T^T, times R's unit and T's, by which it is below 2^13
+        // U = R T^T, times R's unit and T's, by which it is below 2^15
         float u[4][4] = {};
         uint32_t hi[2][4], lo[2][4];
         const uint32_t rtop = warp_top<4>(r, top_of<4>(r));
-        const float ru = unit_of(rtop), ui = inverse_unit(ru) * hb->t_unit;
+        const float ru = unit_of(rtop) * 0x1p-7f, ui = inverse_unit(ru) * hb->s.t_unit;
         {
             uint4 f[kBlocks];
 #pragma unroll
@@ -609,9 +579,10 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b) mma16816(u[block_n(b)], hi[block_k(b)], f[b].z, f[b].w);
         }
-        // The state's next unit: its bound is the old one's decayed and, with |k| below 2 a token, 2 sum(w) max|u|.
-        const float last = hb->last;
-        sb = fmaf(last, sb, 2.f * hb->w_sum * (__uint_as_float(rtop) * hb->t_unit));
+        // The state's next unit: its bound is the old one's decayed and, with |k| below 2 a token, 2 sum(w) max|u|,
+        // which is below max|r| times T's largest row sum (that is below 2^9 t_unit).
+        const float last = hb->s.last;
+        sb = fmaf(last, sb, 1024.f * hb->s.w_sum * (__uint_as_float(rtop) * hb->s.t_unit));
         const float nu = unit_of(__float_as_uint(sb)), ni = inverse_unit(nu);
         // o = |q| (exp(G) S q + A u)
         {
@@ -635,12 +606,12 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
                 product(ks, lo, false);
                 product(ks, hi, true);
             }
-            const float back = ui * hb->a_unit;
+            const float back = ui * hb->s.a_unit;
             // through shared memory into rows
             uint32_t o16[OT][2];
 #pragma unroll
             for (int m = 0; m < OT; ++m) {
-                const float4 w = hb->o[(kp * OT + m) * 4 + t];
+                const float4 w = hb->s.o[(kp * OT + m) * 4 + t];
                 const uint64_t fa = mul2(pk2(w.x, w.y), pk2(back, back)), fs = mul2(pk2(w.z, w.w), pk2(ks1, ks1));
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -667,7 +638,7 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
             const float wf = ui * nu, keep = last * (si * nu);
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                const float2 f = *reinterpret_cast<const float2 *>(&hb->w[n * 8 + 2 * t]);
+                const float2 f = *reinterpret_cast<const float2 *>(&hb->s.w[n * 8 + 2 * t]);
                 float f0, f1;
                 upk2(mul2(pk2(f.x, f.y), pk2(wf, wf)), f0, f1);
                 scale2(u[n][0], u[n][1], f0, f1);
@@ -682,7 +653,7 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
 #pragma unroll
                     for (int p = 0; p < 2; ++p) {
                         uint32_t (&x)[4] = f[n4 & 1][ks][p];
-                        ldsm_x4_t(kt + tile_at<DK>(ks * 16 + (lane & 15), kp * NT + n4 * 4 + p * 2 + (lane >> 4)), x[0], x[1], x[2], x[3]);
+                        ldsm_x4_t(kt + tile_at(ks * 16 + (lane & 15), kp * NT + n4 * 4 + p * 2 + (lane >> 4)), x[0], x[1], x[2], x[3]);
                     }
             };
             fetch_k(0);
@@ -728,6 +699,7 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
     }
 }
 
+constexpr int kWideFrom = 40;            // sequences times heads that k_delta_wide takes
 constexpr int kAlone = 120 * 1024;       // more than half of an SM's shared memory
 
 template <int T, int DK, int W, int KS>
@@ -755,6 +727,7 @@ cudaError_t go(const DeltaArgs &a, int dv, int sms, cudaStream_t st) {
     k_delta_prep<T, DK><<<(unsigned)(chunks * a.n_head_k), 64, 0, st>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    if (a.wide) return launch_delta_wide(a, T, DK, st);
     // few sequences times heads, up to two small CTAs for every SM: two warps to a group
     if ((int64_t)a.n_seq * a.n_head * dv / 32 > 2 * sms) return scan<T, DK, 4, 1>(a, dv, sms, st);
     return scan<T, DK, 2, 2>(a, dv, sms, st);
@@ -774,11 +747,14 @@ template <int T> cudaError_t allow_all() {
 }  // namespace
 
 cudaError_t delta_chunk_setup() {
-    const cudaError_t e = allow_all<PAGED_F16>();
+    cudaError_t e = delta_wide_setup();
+    if (e == cudaSuccess) e = allow_all<PAGED_F16>();
     return e == cudaSuccess ? allow_all<PAGED_BF16>() : e;
 }
 
-cudaError_t launch_delta_chunk(const DeltaArgs &a, int dtype, int dim_k, int dim_v, int sms, cudaStream_t st) {
+cudaError_t launch_delta_chunk(const DeltaArgs &args, int dtype, int dim_k, int dim_v, int sms, cudaStream_t st) {
+    DeltaArgs a = args;
+    a.wide = dim_v == 128 && (int64_t)a.n_seq * a.n_head >= kWideFrom;
     if (dtype == PAGED_F16) return dim_k == 64 ? go<PAGED_F16, 64>(a, dim_v, sms, st) : go<PAGED_F16, 128>(a, dim_v, sms, st);
     return dim_k == 64 ? go<PAGED_BF16, 64>(a, dim_v, sms, st) : go<PAGED_BF16, 128>(a, dim_v, sms, st);
 }

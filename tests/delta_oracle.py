@@ -55,6 +55,14 @@ class DeltaWorld:
         (2^-23) and the cut-off ends of the sums that k . k and S k are (16 of up to 2^-24 each, always towards
         zero: 2^-21 on average) are the same each time, and change S k by a factor, so these errors add as they are:
             F <- exp(g) F + 2^-20 beta |S k|.
+        A sequence of more than 8 tokens is worked on 32 at a time, through the inverse T of I + L, L_ij = beta_i exp(..)
+        k_i . k_j: its updates are u = T r, r_j = beta_j (v_j - exp(..) S k_j).  T_ij = -beta_i k_i . (what a key passes
+        through between) k_j, at most beta_i.  Substitution gets a row of T from those above it: 31 products of L and
+        T, each rounded (2^-24 beta_i beta, together sqrt(32) of it), and what is off there comes on multiplied by
+        a row of T again (sqrt(32) beta): 2^-24 32 beta^3 = 2^-19 beta^3 an entry; as an operand it has 22 bits, 2^-22 beta.
+        Entries and tokens are independent, so a token adds
+            E^2 <- E^2 + (2^-19 max(beta^3, beta / 8))^2 sum of |r_j|^2 over the chunk's tokens up to it.
+        (It takes keys alike and beta of 2 for that to count beside the rest.)
         An output is off by |q| times the state's error and by its own
         rounding, and q . S's sum like k . S's; over many tokens bf16 outputs take S as one F16, half a step (2^-11) of
         each product, together at most 2^-11 |S_row| |q|."""
@@ -72,7 +80,10 @@ class DeltaWorld:
             at = self.slot_in[s]
             S = pool[at].clone() if at >= 0 else torch.zeros_like(pool[0])
             E, F = torch.zeros(2, self.heads, dtype=torch.float64, device="cuda")
+            long = self.lens[s] > 8 and self.save is None
             for r in range(self.starts[s], self.starts[s + 1]):
+                if (r - self.starts[s]) % 32 == 0:
+                    S0, rr = S, torch.zeros_like(E)
                 a = torch.exp(self.decay[r].double())
                 unit = 2.0 ** -20 * (torch.linalg.matrix_norm(S) + self.v[r].double().norm(dim=-1))
                 S = S * a[:, None, None]
@@ -80,7 +91,10 @@ class DeltaWorld:
                 u = self.beta[r].double()[:, None] * (self.v[r].double() - sk)
                 F = a * F + 2.0 ** -20 * self.beta[r].double() * sk.norm(dim=-1)
                 S = S + u[..., None] * k[r][:, None]
-                E = torch.sqrt((a * E) ** 2 + unit ** 2)
+                b = self.beta[r].double().abs()
+                rr = rr + (b * (self.v[r].double().norm(dim=-1) + (S0 @ k[r][..., None])[..., 0].norm(dim=-1))) ** 2
+                solve = 2.0 ** -19 * torch.maximum(b ** 3, b / 8) if long else torch.zeros_like(E)
+                E = torch.sqrt((a * E) ** 2 + unit ** 2 + solve ** 2 * rr)
                 out[r] = (S @ q[r][..., None])[..., 0]
                 tol[r] = UNIT[self.dtype] * out[r].abs() + ((4 * (E + unit) + F) * q[r].norm(dim=-1))[:, None] + (
                     2.0 ** -11 * S.norm(dim=-1) * q[r].norm(dim=-1)[:, None] if self.dtype == torch.bfloat16 else 0.0) + (
