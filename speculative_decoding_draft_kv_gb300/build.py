@@ -25,7 +25,7 @@ SOURCES = ["ring_host.cu", "ring_kernels.cu", "attn_kernels.cu", "step_kernels.c
            "static_attend.cu", "produce_kernels.cu", "produce_tc.cu", "paged_host.cu",
            "paged_rows.cu", "paged_attend_f16.cu", "paged_attend_bf16.cu", "paged_prefill_f16.cu",
            "paged_prefill_bf16.cu", "delta_host.cu", "delta_step.cu",
-           "delta_chunk.cu", "delta_wide.cu"]
+           "delta_chunk.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

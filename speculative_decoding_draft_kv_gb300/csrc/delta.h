@@ -28,11 +28,10 @@ struct DeltaArgs {
     // chunks of many tokens: what k_delta_prep leaves for k_delta_scan
     uint8_t *tiles;                      // [chunks][n_head_k][K, Q] F16 tiles of 32 rows
     uint8_t *heads;                      // [chunks][n_head] blocks of kDeltaHeadBytes
-    int wide;                            // the blocks are k_delta_wide's
 };
 
 constexpr int kDeltaChunk = 32;          // tokens
-constexpr int kDeltaHeadBytes = 8960;
+constexpr int kDeltaHeadBytes = 2 * 6 * 32 * 16 + 2 * 16 * 16 + 32 * 4 + 16;
 // Chunks, with room for each sequence's ragged last one: sequence s has those from q_start[s] / 32 + s on.
 inline int64_t delta_chunks(int64_t n_rows, int n_seq) { return n_rows / kDeltaChunk + n_seq; }
 
@@ -60,8 +59,6 @@ __device__ __forceinline__ DeltaSeq delta_seq(const DeltaArgs &a, int s, uint32_
 }
 
 cudaError_t delta_chunk_setup();
-cudaError_t delta_wide_setup();
-cudaError_t launch_delta_wide(const DeltaArgs &a, int dtype, int dim_k, cudaStream_t st);
 cudaError_t launch_delta_chunk(const DeltaArgs &a, int dtype, int dim_k, int dim_v, int sms, cudaStream_t st);
 cudaError_t launch_delta_step(const DeltaArgs &a, int dtype, int dim_k, int dim_v, cudaStream_t st);
 

@@ -12,8 +12,11 @@
 // tiles, k . k and q . k, decays, T.  k_delta_scan walks a sequence's chunks with the state in registers.
 // A warp has 16 value elements (rows of S) and shares nothing with the others: S as the A operand of
 // S [K Q]^T, U of U T^T, U A^T and U K, are accumulators of the product before, in the same layout
-// (mma.sync m16n8k16; its accumulators feed the next product without leaving the thread, where tensor
-// memory would be written, fenced and read between any two of the four dependent products of a chunk).
+// (mma.sync m16n8k16: its accumulators feed the next product without leaving the thread).  On tcgen05.mma, which was
+// built too, with 128 value elements as rows and the left operands in tensor memory, a product of 16 steps along
+// K took some 98 cycles whatever its columns, 32 or 64, and a chunk has 40 of them and three hand-overs to the threads
+// and back: 4,900 cycles for a head's chunk and SM, where this takes 5,900 with many heads (eight prompts 552 us, 588
+// here) and 2,800 with few (48 heads of 14,142 tokens 1,136 us, 972 here).
 //
 // Precision.  The state, its update and all sums are float32.  Operands are F16 pairs hi + lo, 22 bits together,
 // after powers of two that bring them below 2^15; the state is kept times its own.  R's is by its largest
@@ -24,12 +27,74 @@
 // multiply-add: tensor-core sums are cut off, not rounded, and hundreds of chunks would add that up.  Decays are
 // exponentials of sums over just the tokens between, so neither a long chunk nor a state that was dropped costs
 // later tokens their precision.
-#include "delta_chunk.cuh"
+#include "delta.h"
+
+#include "ring_internal.h"
+#include "ptx.h"
+#include "paged_ptx.h"
 
 #include <type_traits>
 
 namespace dflash {
 namespace {
+
+constexpr int C = kDeltaChunk;                         // tokens of a chunk
+static_assert(C == 32, "a lane per token");
+
+template <int T> __device__ __forceinline__ float from16(uint32_t x) {
+    if constexpr (T == PAGED_F16) return __half2float(__ushort_as_half((unsigned short)x));
+    else return __uint_as_float(x << 16);
+}
+__device__ __forceinline__ float2 half2_floats(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2 *>(&x)); }
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    return x;
+}
+
+// Byte offset of 16-byte chunk ch of row r in a tile of 32 rows of F16: runs of 64 columns one behind another, with the
+// 128-byte swizzle, conflict-free for ldmatrix along rows as along columns.
+__device__ __forceinline__ uint32_t tile_at(int r, int ch) { return (uint32_t)((ch >> 3) * C * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)); }
+
+// Of T or A, the (token tile, key step) blocks with something in them, in the order of use.
+constexpr int kBlocks = 6;
+__host__ __device__ constexpr int block_n(int b) { return b < 4 ? b : b - 2; }     // 0 1 2 3 2 3
+__host__ __device__ constexpr int block_k(int b) { return b < 4 ? 0 : 1; }
+
+// What a head's chunk needs beside T and A.
+struct HeadScalars {
+    float4 r[C / 2];                                   // of tokens 2i, 2i+1: beta twice, -beta exp(G) |k| twice
+    float4 o[C / 2];                                   // |q| twice, |q| exp(G) twice
+    float w[C];                                        // exp(G_last - G) |k|
+    float last, t_unit, a_unit, w_sum;                 // exp(G_last); what T and A are to be multiplied by; sum of w
+};
+// A head's part of a chunk in the workspace, for mma.sync: B operands of T and of A (exp(G_i - G_j) q_i . k_j), a lane's
+// words beside one another (hi, hi, lo, lo).
+struct HeadBlock {
+    uint4 t[kBlocks][32], a[kBlocks][32];
+    HeadScalars s;
+};
+static_assert(sizeof(HeadBlock) == kDeltaHeadBytes, "as the workspace is laid out");
+
+__device__ __forceinline__ int chunk_base(int row0, int s) { return row0 / C + s; }
+
+// the power of two that brings m > 0 (as bits) to [2^12, 2^13), as far as float32 has it and its inverse
+__device__ __forceinline__ float unit_of(uint32_t bits) {
+    const int e = (int)(bits >> 23);                   // biased
+    return bits == 0u || e == 255 ? 1.f : __uint_as_float((uint32_t)min(241, max(13, 254 + 12 - e)) << 23);
+}
+__device__ __forceinline__ float inverse_unit(float u) { return __uint_as_float((254u << 23) - __float_as_uint(u)); }
+
+// x0, x1 as two F16 pairs
+__device__ __forceinline__ void split(float x0, float x1, uint32_t &hi, uint32_t &lo) {
+    hi = pack_half2(x0, x1);
+    const float2 h = half2_floats(hi);
+    float l0, l1;
+    upk2(fma2(pk2(h.x, h.y), pk2(-1.f, -1.f), pk2(x0, x1)), l0, l1);
+    lo = pack_half2(l0, l1);
+}
+__device__ __forceinline__ void scale2(float &x0, float &x1, float f0, float f1) { upk2(mul2(pk2(x0, x1), pk2(f0, f1)), x0, x1); }
 
 // ---------------------------------------------------------------- what the state is not needed for
 
@@ -230,53 +295,28 @@ k_delta_prep(const __grid_constant__ DeltaArgs a) {
             row += fabsf(f.x) + fabsf(f.y) + fabsf(f.z) + fabsf(f.w);
         }
         const float tu = unit_of(__reduce_max_sync(0xffffffffu, __float_as_uint(row))) * 0x1p-4f;
-        uint8_t *block = a.heads + ((int64_t)at * a.n_head + h) * kDeltaHeadBytes;
-        HeadScalars *out;
-        if (a.wide) {                                              // a lane has a row, nothing above the diagonal
-            WideBlock *wide = reinterpret_cast<WideBlock *>(block);
-            out = &wide->s;
+        HeadBlock *block = reinterpret_cast<HeadBlock *>(a.heads + ((int64_t)at * a.n_head + h) * kDeltaHeadBytes);
+        HeadScalars *out = &block->s;
+        const int gq = lane >> 2, tq = lane & 3;
 #pragma unroll
-            for (int ch = 0; ch < 4; ++ch)
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const float *from = (w ? am : l) + i * 36 + ch * 8, unit = w ? au : tu;
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float2 x = *reinterpret_cast<const float2 *>(from + 2 * e);
-                        const int j = ch * 8 + 2 * e;
-                        x.x = j <= i ? x.x : 0.f;
-                        x.y = j + 1 <= i ? x.y : 0.f;
-                        split(x.x * unit, x.y * unit, hi[e], lo[e]);
-                    }
-                    uint4 (*to)[8] = w ? wide->a : wide->t;
-                    to[i][ch ^ (i & 7)] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    to[i][(ch + 4) ^ (i & 7)] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                }
-        } else {
-            HeadBlock *narrow = reinterpret_cast<HeadBlock *>(block);
-            out = &narrow->s;
-            const int gq = lane >> 2, tq = lane & 3;
-#pragma unroll
-            for (int b = 0; b < kBlocks; ++b) {
-                const int ri = block_n(b) * 8 + gq, ci = block_k(b) * 16 + 2 * tq, from = ri * 36 + ci;
-                uint4 v;
-                float2 lo = *reinterpret_cast<const float2 *>(l + from), hi = *reinterpret_cast<const float2 *>(l + from + 8);
-                split(lo.x * tu, lo.y * tu, v.x, v.z);
-                split(hi.x * tu, hi.y * tu, v.y, v.w);
-                narrow->t[b][lane] = v;
-                lo = *reinterpret_cast<const float2 *>(am + from);
-                hi = *reinterpret_cast<const float2 *>(am + from + 8);
-                if (block_n(b) < 2 || block_k(b)) {                // nothing above the diagonal has been written
-                    lo.x = ci <= ri ? lo.x : 0.f;
-                    lo.y = ci + 1 <= ri ? lo.y : 0.f;
-                    hi.x = ci + 8 <= ri ? hi.x : 0.f;
-                    hi.y = ci + 9 <= ri ? hi.y : 0.f;
-                }
-                split(lo.x * au, lo.y * au, v.x, v.z);
-                split(hi.x * au, hi.y * au, v.y, v.w);
-                narrow->a[b][lane] = v;
+        for (int b = 0; b < kBlocks; ++b) {
+            const int ri = block_n(b) * 8 + gq, ci = block_k(b) * 16 + 2 * tq, from = ri * 36 + ci;
+            uint4 v;
+            float2 lo = *reinterpret_cast<const float2 *>(l + from), hi = *reinterpret_cast<const float2 *>(l + from + 8);
+            split(lo.x * tu, lo.y * tu, v.x, v.z);
+            split(hi.x * tu, hi.y * tu, v.y, v.w);
+            block->t[b][lane] = v;
+            lo = *reinterpret_cast<const float2 *>(am + from);
+            hi = *reinterpret_cast<const float2 *>(am + from + 8);
+            if (block_n(b) < 2 || block_k(b)) {                // nothing above the diagonal has been written
+                lo.x = ci <= ri ? lo.x : 0.f;
+                lo.y = ci + 1 <= ri ? lo.y : 0.f;
+                hi.x = ci + 8 <= ri ? hi.x : 0.f;
+                hi.y = ci + 9 <= ri ? hi.y : 0.f;
             }
+            split(lo.x * au, lo.y * au, v.x, v.z);
+            split(hi.x * au, hi.y * au, v.y, v.w);
+            block->a[b][lane] = v;
         }
         const int to = (i >> 1) * 4 + (i & 1);
         reinterpret_cast<float *>(out->r)[to] = beta;
@@ -699,7 +739,6 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
     }
 }
 
-constexpr int kWideFrom = 40;            // sequences times heads that k_delta_wide takes
 constexpr int kAlone = 120 * 1024;       // more than half of an SM's shared memory
 
 template <int T, int DK, int W, int KS>
@@ -727,7 +766,6 @@ cudaError_t go(const DeltaArgs &a, int dv, int sms, cudaStream_t st) {
     k_delta_prep<T, DK><<<(unsigned)(chunks * a.n_head_k), 64, 0, st>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    if (a.wide) return launch_delta_wide(a, T, DK, st);
     // few sequences times heads, up to two small CTAs for every SM: two warps to a group
     if ((int64_t)a.n_seq * a.n_head * dv / 32 > 2 * sms) return scan<T, DK, 4, 1>(a, dv, sms, st);
     return scan<T, DK, 2, 2>(a, dv, sms, st);
@@ -747,14 +785,11 @@ template <int T> cudaError_t allow_all() {
 }  // namespace
 
 cudaError_t delta_chunk_setup() {
-    cudaError_t e = delta_wide_setup();
-    if (e == cudaSuccess) e = allow_all<PAGED_F16>();
+    const cudaError_t e = allow_all<PAGED_F16>();
     return e == cudaSuccess ? allow_all<PAGED_BF16>() : e;
 }
 
-cudaError_t launch_delta_chunk(const DeltaArgs &args, int dtype, int dim_k, int dim_v, int sms, cudaStream_t st) {
-    DeltaArgs a = args;
-    a.wide = dim_v == 128 && (int64_t)a.n_seq * a.n_head >= kWideFrom;
+cudaError_t launch_delta_chunk(const DeltaArgs &a, int dtype, int dim_k, int dim_v, int sms, cudaStream_t st) {
     if (dtype == PAGED_F16) return dim_k == 64 ? go<PAGED_F16, 64>(a, dim_v, sms, st) : go<PAGED_F16, 128>(a, dim_v, sms, st);
     return dim_k == 64 ? go<PAGED_BF16, 64>(a, dim_v, sms, st) : go<PAGED_BF16, 128>(a, dim_v, sms, st);
 }

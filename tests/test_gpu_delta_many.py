@@ -1,5 +1,4 @@
-"""delta_rule over many tokens with many sequences and heads, where one CTA has a head's whole state: the same bounds
-as elsewhere, at sizes of its own."""
+"""delta_rule over many tokens with many sequences and heads at once: the same bounds as elsewhere."""
 
 import math
 
