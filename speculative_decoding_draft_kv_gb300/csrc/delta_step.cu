@@ -7,8 +7,7 @@
 // has four rows beside one another, eight lanes to a row, each lane a run of four key elements in
 // every 32, so that a row is read and written in whole 128-byte lines.  S k and S q come out of one pass
 // over the old state, o = a (S q) + (q . k) u, whose two sums over the eight lanes are the only words
-// that lanes exchange.  Keys and queries are normed once per CTA, eight tokens at a time, in shared
-// memory.
+// that lanes exchange.  Keys and queries are normed once per CTA, eight tokens at a time, in shared memory.
 //
 // Bound by the state's bytes, 64 KB read and written per head of 128 x 128, as long as a sequence has
 // few tokens: a token takes 3 flops per state element beside 8 bytes of it.  What counts is bytes under way: eight
@@ -52,7 +51,8 @@ template <int T, int DK, int DV>
 __global__ void __launch_bounds__(kStepThreads, DK == 64 ? 6 : 8)
 k_delta_step(const __grid_constant__ DeltaArgs a) {
     constexpr int E = DK / 8;                          // of a lane's part of a row
-    constexpr int J = 32 / E;                          // rows of a lane
+    constexpr int J = 32 / E;                          // rows of a lane: 2 or 4
+    constexpr int WHICH = J == 4 ? 1 : 2;              // of a lane's number among eight: whether it ends with a k . S or a q . S
     constexpr int kRows = 4 * 4 * J;                   // of a CTA
     constexpr int kParts = DV / kRows;
     constexpr int TB = kStepTokens;
@@ -176,24 +176,42 @@ k_delta_step(const __grid_constant__ DeltaArgs a) {
                     qs[j] = fma2(qx.y, st[j][2 * e + 1], qs[j]);
                 }
             }
-            const float decay = s_decay[t], beta = s_beta[t], qk = s_qk[t];
+            // 2 J sums over eight lanes: a round hands half of them over and keeps the other half, so that lane 2j WHICH (+ WHICH)
+            // of the eight ends with row j's k . S (q . S): four or seven shuffles, where one sum after the other takes
+            // three each.
+            float x[2 * J];
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const float2 a0 = unpack2(ks[j]), a1 = unpack2(qs[j]);
+                x[2 * j] = a0.x + a0.y;
+                x[2 * j + 1] = a1.x + a1.y;
+            }
+#pragma unroll
+            for (int d = 4, n = J; d; d >>= 1, n >>= 1) {
+                if (n == 0) {
+                    x[0] += __shfl_xor_sync(0xffffffffu, x[0], d);
+                    continue;
+                }
+                const bool up = sub & d;
+#pragma unroll
+                for (int i = 0; i < n; ++i) {
+                    const float give = up ? x[i] : x[i + n], keep = up ? x[i + n] : x[i];
+                    x[i] = keep + __shfl_xor_sync(0xffffffffu, give, d);
+                }
+            }
+            const float decay = s_decay[t], other = __shfl_xor_sync(0xffffffffu, x[0], WHICH);
+            const float kS = sub & WHICH ? other : x[0], qS = sub & WHICH ? x[0] : other;
+            const int r = warp * 4 * J + 4 * (sub / (2 * WHICH)) + rg;
+            const float mine = s_beta[t] * (s_v[t][r] - decay * kS);
+            if (sub % (2 * WHICH) == 0)
+                a.o[(int64_t)(q.row0 + t0 + t) * a.o_rs + (int64_t)h * a.o_hs + part * kRows + r] = to16<T>(fmaf(s_qk[t], mine, decay * qS));
             const uint64_t decay2 = pk2(decay, decay);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                const float2 x = unpack2(ks[j]), y = unpack2(qs[j]);
-                float kS = x.x + x.y, qS = y.x + y.y;
-#pragma unroll
-                for (int d = 4; d; d >>= 1) {
-                    kS += __shfl_xor_sync(0xffffffffu, kS, d);
-                    qS += __shfl_xor_sync(0xffffffffu, qS, d);
-                }
-                const float u = beta * (s_v[t][warp * 4 * J + 4 * j + rg] - decay * kS);
+                const float u = __shfl_sync(0xffffffffu, mine, (lane & 24) + 2 * WHICH * j);
                 const uint64_t u2 = pk2(u, u);
 #pragma unroll
                 for (int e = 0; e < E / 2; ++e) st[j][e] = fma2(kd[e], u2, mul2(decay2, st[j][e]));
-                if (sub == j)
-                    a.o[(int64_t)(q.row0 + t0 + t) * a.o_rs + (int64_t)h * a.o_hs + row0 + 4 * j + rg] =
-                        to16<T>(fmaf(qk, u, decay * qS));
             }
             store(s_save[t]);
         }
