@@ -21,7 +21,7 @@
 // Precision.  The state, its update and all sums are float32.  Operands are F16 pairs hi + lo, 22 bits together,
 // after powers of two that bring them below 2^15; the state is kept times its own.  R's is by its largest
 // value; U's and the state's are by bounds (T's largest row sum, the decays' sum), which may be 2^16 above
-// the values before an F16 pair loses bits, and the state's is set right every fourth chunk.  Keys and queries
+// the values before an F16 pair loses bits, and the state's is set right every eighth chunk.  Keys and queries
 // are one F16 each, after a power of two by the row's norm: exact but for elements below 2^-14 of the norm, which
 // are off by 2^-25 of it at most.  What a product adds up starts at zero and joins the state by one fused
 // multiply-add: tensor-core sums are cut off, not rounded, and hundreds of chunks would add that up.  Decays are
@@ -340,7 +340,7 @@ struct ScanCfg {
     static constexpr int kStageBytes = kTileBytes + (int)sizeof(HeadBlock);
     static constexpr int kVBytes = C * 32;                         // [C tokens][16 values], two to a group
     static constexpr int kOBytes = C / KS * 32;                    // a warp's outputs on their way
-    static constexpr int kXWords = KS > 1 ? 8 * 4 * 32 : 0;        // what a warp hands its group, two chunks' worth
+    static constexpr int kXWords = KS == 2 ? 6 * 4 * 32 : 0;       // what a warp hands its partner, two chunks' worth
     static constexpr int kStages = DK == 128 ? 3 : 4;
     static constexpr int kOffV = kStages * kStageBytes;
     static constexpr int kOffO = kOffV + W * 2 * kVBytes;
@@ -354,6 +354,14 @@ __device__ __forceinline__ uint32_t v_at(int r, int half) { return (uint32_t)(r 
 
 __device__ __forceinline__ void stsm_x2_t(uint32_t addr, uint32_t r0, uint32_t r1) {
     asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1, %2};" ::"r"(addr), "r"(r0), "r"(r1) : "memory");
+}
+
+// whether the phase is over, without waiting at all
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
 }
 
 template <int N> __device__ __forceinline__ float top_of(const float (&x)[N][4]) {
@@ -488,9 +496,10 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
         scale2(st[n][0], st[n][1], su, su);
         scale2(st[n][2], st[n][3], su, su);
     }
+    bool ready = false;                                            // the chunk was seen to be there while the one before it was worked on
     for (int c = 0; c < chunks; ++c) {
         const int k = c % S, nv = min(C, q.n - c * C);
-        const bool here = __all_sync(0xffffffffu, mbar_wait(full + 8 * k, (uint32_t)(c / S) & 1u));
+        const bool here = __all_sync(0xffffffffu, ready) || __all_sync(0xffffffffu, mbar_wait(full + 8 * k, (uint32_t)(c / S) & 1u));
         if (!here && lane == 0) timed_out();
         if (KS == 1 && !here) {
             alive = false;
@@ -537,43 +546,46 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
         asm volatile("cp.async.wait_all;" ::: "memory");           // this chunk's values
         constexpr int OT = 4 / KS;                                 // token tiles whose outputs are this warp's
         float ks1 = si;                                            // what the sums are to be multiplied by
-        if constexpr (KS > 1) {
-            // sums over the group: of S K^T all, of S Q^T those of this warp's tiles
+        if constexpr (KS == 2) {
+            // the partner's half of the sums: of S K^T all, of S Q^T those of the 16 tokens whose outputs are this warp's
             ks1 = 1.f;
             float4 *mine = xs + (warp * 2 + (c & 1)) * (F::kXWords / 4);
-            const float4 *group = xs + (warp / KS * KS * 2 + (c & 1)) * (F::kXWords / 4);
+            const float4 *other = xs + ((warp ^ 1) * 2 + (c & 1)) * (F::kXWords / 4);
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
+                scale2(pk[n][0], pk[n][1], si, si);
+                scale2(pk[n][2], pk[n][3], si, si);
+                mine[n * 32] = make_float4(pk[n][0], pk[n][1], pk[n][2], pk[n][3]);
+            }
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
                 for (int e = 0; e < 4; e += 2) {
-                    scale2(pk[n][e], pk[n][e + 1], si, si);
-                    scale2(pq[n][e], pq[n][e + 1], si, si);
+                    scale2(pq[m][e], pq[m][e + 1], si, si);
+                    scale2(pq[2 + m][e], pq[2 + m][e + 1], si, si);
                 }
-                mine[n * 32] = make_float4(pk[n][0], pk[n][1], pk[n][2], pk[n][3]);
-                mine[(4 + n) * 32] = make_float4(pq[n][0], pq[n][1], pq[n][2], pq[n][3]);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                mine[(4 + m) * 32] = kp ? make_float4(pq[m][0], pq[m][1], pq[m][2], pq[m][3])
+                                        : make_float4(pq[2 + m][0], pq[2 + m][1], pq[2 + m][2], pq[2 + m][3]);
+                // (what stays, to the front)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) pq[m][e] = kp ? pq[2 + m][e] : pq[m][e];
             }
-            // (a wait that ran out in one: all leave)
-            if (bar_any(1 + warp / KS, 32 * KS, !here)) {
+            // (a wait that ran out in either: both leave)
+            if (bar_any(1 + warp / 2, 64, !here)) {
                 alive = false;
                 break;
             }
-            // the same order in every warp: they go on with the same bits
+            // (the same sums in both warps: addition does not mind the order of two)
+            auto join = [](float (&x)[4], const float4 &y) {
+                upk2(add2(pk2(x[0], x[1]), pk2(y.x, y.y)), x[0], x[1]);
+                upk2(add2(pk2(x[2], x[3]), pk2(y.z, y.w)), x[2], x[3]);
+            };
 #pragma unroll
-            for (int p = 0; p < KS; ++p) {
-                const float4 *from = group + p * 2 * (F::kXWords / 4);
-                auto join = [&](float (&x)[4], const float4 &y) {
-                    if (p == 0) {
-                        x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
-                        return;
-                    }
-                    upk2(add2(pk2(x[0], x[1]), pk2(y.x, y.y)), x[0], x[1]);
-                    upk2(add2(pk2(x[2], x[3]), pk2(y.z, y.w)), x[2], x[3]);
-                };
+            for (int n = 0; n < 4; ++n) join(pk[n], other[n * 32]);
 #pragma unroll
-                for (int n = 0; n < 4; ++n) join(pk[n], from[n * 32]);
-#pragma unroll
-                for (int m = 0; m < OT; ++m) join(pq[m], from[(4 + kp * OT + m) * 32]);
-            }
+            for (int m = 0; m < OT; ++m) join(pq[m], other[(4 + m) * 32]);
         } else {
             __syncwarp();
         }
@@ -673,6 +685,8 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
                     *reinterpret_cast<uint4 *>(a.o + (int64_t)(q.row0 + c * C + token) * a.o_rs + (int64_t)h * a.o_hs + row0 + piece * 8) = y;
             }
         }
+        // (the next chunk: the answer is there by the time it is asked for)
+        ready = c + 1 < chunks && mbar_test(full + 8 * ((c + 1) % S), (uint32_t)((c + 1) / S) & 1u);
         // S <- exp(G_last) S + U (exp(G_last - G) |k| K), all times the new unit
         {
             const float wf = ui * nu, keep = last * (si * nu);
@@ -722,7 +736,7 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
         if (lane == 0) mbar_arrive(empty + 8 * k);
         su = nu;
         si = ni;
-        if ((c & 3) == 3) sb = __uint_as_float(warp_top<NT>(st, top_of<NT>(st))) * si;
+        if ((c & 7) == 7) sb = __uint_as_float(warp_top<NT>(st, top_of<NT>(st))) * si;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     const int out = a.slot_out[s];
