@@ -732,6 +732,9 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
                     }
             }
         }
+        // (the stage's next copy writes through another proxy: an arrival alone does not hold it back behind reads still
+        // on their way, and a warp's last ones were overwritten when a new CTA's first loads delayed them; 8 of 728 us)
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(empty + 8 * k);
         su = nu;

@@ -200,3 +200,19 @@ def test_the_same_call_gives_the_same_bits():
         D.delta_rule(state, batch, w.q, w.k, w.v, w.decay, w.beta, o)
         got.append((o.view(torch.int16).clone(), w.pool[2:4].view(torch.int32).clone()))
     assert all(torch.equal(a, b) for x in got[1:] for a, b in zip(x, got[0]))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("lens,heads", [([4000, 3900, 2400, 830, 3300, 1800, 240, 2700], 32), ([6000, 4000], 32), ([12000], 48)])
+def test_long_sequences_give_the_same_bits(dtype, lens, heads):
+    """Sequences that end while others go on: the CTAs behind them start beside warps in the midst of their chunks."""
+    w = DeltaWorld(lens, heads=heads, heads_k=16, dtype=dtype, seed=15)
+    state, batch = w.handles(D)
+    n, want = len(lens), None
+    for _ in range(12):
+        o = torch.empty_like(w.v)
+        D.delta_rule(state, batch, w.q, w.k, w.v, w.decay, w.beta, o)
+        got = (o.view(torch.int16), w.pool[n:2 * n].view(torch.int32).clone())
+        want = want or got
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert D.delta_device_error() == 0 and torch.isfinite(o).all()
