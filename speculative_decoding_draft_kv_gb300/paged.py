@@ -87,7 +87,13 @@ def _packer(args):
     codes = {_vp: "Q", _i64: "q", _i32: "i", _f32: "f"}
     s = struct.Struct("@" + "".join(codes[t] for _, t in args._fields_))
     assert s.size == ctypes.sizeof(args)
-    return s.pack
+
+    def pack(*values):
+        try:
+            return s.pack(*values)
+        except struct.error as e:
+            raise TypeError(f"{args.__name__}: {e}") from None
+    return pack
 
 
 _pack_attend = _packer(PagedAttendArgs)
