@@ -104,6 +104,8 @@ struct PagedAttendArgs {
     float2 *level_ml;                 // [n_rows][n_head] (max in log2 units, sum)
     int2 *level_items;                // [n_rows][kv heads] of an item's first row: the CTAs with its first and last
                                       // tile; .y negative: not cut, its states are in the arrays above
+    const PagedAttendArgs *first;     // kOwn, on the host: the first pass's, whose join goes behind this one
+    int sms;
 };
 enum { kOnly = 0, kPrefix = 1, kOwn = 2 };
 
@@ -111,10 +113,6 @@ template <int T> cudaError_t paged_attend_setup_t();
 template <int T>
 cudaError_t launch_paged_attend_t(const PagedAttendArgs &a, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                                   int head_dim, cudaStream_t st);
-
-template <int T>
-cudaError_t launch_paged_levels_t(const PagedAttendArgs &prefix, const PagedAttendArgs &own, int head_dim, int sms,
-                                  cudaStream_t st);
 
 template <int T> cudaError_t paged_prefill_setup_t();
 template <int T>

@@ -5,5 +5,4 @@ namespace dflash {
 template cudaError_t paged_attend_setup_t<PAGED_F16>();
 template cudaError_t launch_paged_attend_t<PAGED_F16>(const PagedAttendArgs &, const CUtensorMap &, const CUtensorMap &, int,
                                                 cudaStream_t);
-template cudaError_t launch_paged_levels_t<PAGED_F16>(const PagedAttendArgs &, const PagedAttendArgs &, int, int, cudaStream_t);
 }  // namespace dflash

@@ -27,10 +27,10 @@ cudaError_t launch_join(const PagedAttendArgs &a, int head_dim, cudaStream_t st)
 // Two passes' join, which settles as the other one does.  Rows to a block: as few as leave one wave of blocks, five to
 // an SM; warps to a (row, query head): what a block has left.
 template <int T>
-cudaError_t launch_paged_levels_t(const PagedAttendArgs &prefix, const PagedAttendArgs &own, int head_dim, int sms, cudaStream_t st) {
+cudaError_t launch_levels(const PagedAttendArgs &prefix, const PagedAttendArgs &own, int head_dim, cudaStream_t st) {
     const int64_t n = own.batch.n_rows;
     int rows = 1, wide = 8;
-    while (rows < 16 && (n + rows - 1) / rows * own.pool.n_head_kv > 5 * sms) rows *= 2;
+    while (rows < 16 && (n + rows - 1) / rows * own.pool.n_head_kv > 5 * own.sms) rows *= 2;
     while (wide > 1 && rows * own.group * wide > 8) wide /= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((n + rows - 1) / rows * own.pool.n_head_kv), 1, 1);
@@ -43,6 +43,13 @@ cudaError_t launch_paged_levels_t(const PagedAttendArgs &prefix, const PagedAtte
     cfg.numAttrs = 1;
     return head_dim == 64 ? cudaLaunchKernelEx(&cfg, k_paged_levels<64, T>, prefix, own, rows, wide)
                           : cudaLaunchKernelEx(&cfg, k_paged_levels<128, T>, prefix, own, rows, wide);
+}
+
+// What joins a pass's states: of the only one those of cut items, behind the second of two both passes'.
+template <int T, int W>
+cudaError_t launch_behind(const PagedAttendArgs &a, int head_dim, cudaStream_t st) {
+    if (a.level == kOnly) return launch_join<T, W>(a, head_dim, st);
+    return a.level == kOwn ? launch_levels<T>(*a.first, a, head_dim, st) : cudaSuccess;
 }
 
 // A pass of the attention.  The second of two may begin while the first one runs: it reads nothing of that.
@@ -96,7 +103,7 @@ cudaError_t launch_paged_attend_t(const PagedAttendArgs &a, const CUtensorMap &t
                                   int head_dim, cudaStream_t st) {
     auto go = [&](auto kernel, int smem, int threads, int) {
         const cudaError_t e = launch_pass(kernel, a, threads, smem, st, tm_k, tm_v, a);
-        return e == cudaSuccess && a.level == kOnly ? launch_join<T, 8>(a, head_dim, st) : e;
+        return e == cudaSuccess ? launch_behind<T, 8>(a, head_dim, st) : e;
     };
     const int mt = a.tile_rows <= 16 ? 1 : 2;
     return head_dim == 64 ? pick_attend<T, 64>(a.pool.format, mt, go) : pick_attend<T, 128>(a.pool.format, mt, go);

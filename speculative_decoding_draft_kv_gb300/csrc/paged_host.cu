@@ -577,10 +577,9 @@ static int attend(const char *who, const paged_attend_args *g, const paged_batch
     b.mask = PAGED_FULL;
     a.level = kOwn;
     TRY(attend_pass(who, g, prefix, pp, b, ws, st));
-    TRY(attend_pass(who, g, g->batch, p, a, ws + first, st));
-    const cudaError_t e = g->dtype == PAGED_F16 ? launch_paged_levels_t<PAGED_F16>(b, a, dim, d.sms, st)
-                                                : launch_paged_levels_t<PAGED_BF16>(b, a, dim, d.sms, st);
-    return e == cudaSuccess ? RING_OK : fail(RING_ECUDA, "%s: launch: %s", who, cudaGetErrorString(e));
+    a.first = &b;
+    a.sms = d.sms;
+    return attend_pass(who, g, g->batch, p, a, ws + first, st);
 }
 
 extern "C" int paged_attend(const paged_attend_args *g, void *stream) {

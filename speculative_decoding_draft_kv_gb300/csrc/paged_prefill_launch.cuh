@@ -48,7 +48,7 @@ cudaError_t launch_paged_prefill_t(const PagedAttendArgs &a, const CUtensorMap &
                                    const CUtensorMap &tm_q, int head_dim, cudaStream_t st) {
     return pick_prefill<T>(head_dim, a.pool.format, a.tile_rows <= 128, [&](auto kernel, int smem, int threads, int) {
         const cudaError_t e = launch_pass(kernel, a, threads, smem, st, tm_k, tm_v, tm_q, a);
-        return e == cudaSuccess && a.level == kOnly ? launch_join<T, 1>(a, head_dim, st) : e;
+        return e == cudaSuccess ? launch_behind<T, 1>(a, head_dim, st) : e;
     });
 }
 
