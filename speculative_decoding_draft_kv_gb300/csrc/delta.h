@@ -59,7 +59,9 @@ __device__ __forceinline__ DeltaSeq delta_seq(const DeltaArgs &a, int s, uint32_
 }
 
 cudaError_t delta_chunk_setup();
-cudaError_t launch_delta_chunk(const DeltaArgs &a, int dtype, int dim_k, int dim_v, int sms, cudaStream_t st);
+// The kernels of a long batch, each beside the end of the one in front: prep, k_delta_step (split), scan.
+cudaError_t launch_delta_prep(const DeltaArgs &a, int dtype, int dim_k, cudaStream_t st);
+cudaError_t launch_delta_scan(const DeltaArgs &a, int dtype, int dim_k, int dim_v, int sms, cudaStream_t st);
 cudaError_t launch_delta_step(const DeltaArgs &a, int dtype, int dim_k, int dim_v, cudaStream_t st);
 
 }  // namespace dflash

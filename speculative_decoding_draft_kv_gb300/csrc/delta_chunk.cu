@@ -12,11 +12,14 @@
 // tiles, k . k and q . k, decays, T.  k_delta_scan walks a sequence's chunks with the state in registers.
 // A warp has 16 value elements (rows of S) and shares nothing with the others: S as the A operand of
 // S [K Q]^T, U of U T^T, U A^T and U K, are accumulators of the product before, in the same layout
-// (mma.sync m16n8k16: its accumulators feed the next product without leaving the thread).  On tcgen05.mma, which was
-// built too, with 128 value elements as rows and the left operands in tensor memory, a product of 16 steps along
-// K took some 98 cycles whatever its columns, 32 or 64, and a chunk has 40 of them and three hand-overs to the threads
-// and back: 4,900 cycles for a head's chunk and SM, where this takes 5,900 with many heads (eight prompts 552 us, 588
-// here) and 2,800 with few (48 heads of 14,142 tokens 1,136 us, 972 here).
+// (mma.sync m16n8k16: its accumulators feed the next product without leaving the thread).  A form on tcgen05.mma, with
+// 128 value elements as rows and the left operands in tensor memory, was built too: there a product of 16 steps along K
+// takes some 98 cycles whatever its columns, 32 or 64, and a chunk has 40 of them and three hand-overs to the threads
+// and back, 4,900 cycles for a head's chunk and SM.  It took 552 us for eight prompts, which take 540 here, and
+// 1,136 for 48 heads of 14,142 tokens (972).
+//
+// Bound by the walk's chain: a chunk of a head of 128 x 128 takes two warps to a group 1.2 us when they have the SM to
+// themselves, two CTAs with a warp to a group 3.4 us for both, of which the tensor pipe is busy about half.
 //
 // Precision.  The state, its update and all sums are float32.  Operands are F16 pairs hi + lo, 22 bits together,
 // after powers of two that bring them below 2^15; the state is kept times its own.  R's is by its largest
@@ -33,6 +36,7 @@
 #include "ptx.h"
 #include "paged_ptx.h"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace dflash {
@@ -396,15 +400,35 @@ __device__ __forceinline__ void operand(const float (&x)[4][4], uint32_t (&hi)[2
         for (int e = 0; e < 2; ++e) split(x[n][2 * e], x[n][2 * e + 1], hi[n >> 1][(n & 1) * 2 + e], lo[n >> 1][(n & 1) * 2 + e]);
 }
 
+constexpr int kSorted = 128;             // sequences
+
 template <int T, int DK, int W, int KS>
 __global__ void __launch_bounds__((W * KS + 1) * 32, KS == 1 ? 2 : 1)
 k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
     using F = ScanCfg<DK, W, KS>;
+    static_assert(F::kThreads >= kSorted);
     constexpr int S = F::kStages, NT = DK / 8 / KS, STEPS = DK / 16 / KS;
     extern __shared__ __align__(128) uint8_t smem[];
     const uint32_t full = smem_u32(smem + F::kOffBars), empty = full + 8 * S;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int part = blockIdx.x % parts, sh = blockIdx.x / parts, h = sh % a.n_head, s = sh / a.n_head;
+    const int part = blockIdx.x % parts, sh = blockIdx.x / parts, h = sh % a.n_head;
+    int s = sh / a.n_head;
+    // The longest sequences first, so that none begins when the others end (eight prompts of 239 to 4,096 tokens by rising
+    // length, us: 652 as they come, 552 so; falling 542 and 551).  Each CTA counts the longer ones, as many
+    // sequences as it has threads for; with more of them the last ones weigh less.
+    if (a.n_seq > 1 && a.n_seq <= kSorted) {
+        __shared__ int s_len[kSorted], s_seq;
+        const int me = threadIdx.x;
+        if (me < a.n_seq) s_len[me] = (int)((uint32_t)a.q_start[me + 1] - (uint32_t)a.q_start[me]);
+        __syncthreads();
+        if (me < a.n_seq) {
+            int before = 0;
+            for (int j = 0; j < a.n_seq; ++j) before += s_len[j] > s_len[me] || (s_len[j] == s_len[me] && j < me);
+            if (before == s) s_seq = me;
+        }
+        __syncthreads();
+        s = s_seq;
+    }
     if (threadIdx.x == 0) {
         for (int k = 0; k < S; ++k) {
             mbar_init(full + 8 * k, 1);
@@ -418,6 +442,7 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
     if (bits && threadIdx.x == 0 && h == 0 && part == 0) atomicOr(a.err, bits);
     q.ok = q.ok && q.n > kDeltaFew;                                // the others are k_delta_step's
     pdl_trigger();
+    if (!q.ok && blockIdx.x) return;                               // (one waits for the kernel in front, as the one behind counts on)
     __syncthreads();
     const int chunks = q.ok ? (q.n + C - 1) / C : 0;
     const int64_t base = chunk_base(q.row0, s);
@@ -758,16 +783,21 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
 
 constexpr int kAlone = 120 * 1024;       // more than half of an SM's shared memory
 
+template <int T, int DK>
+cudaError_t prep(const DeltaArgs &a, cudaStream_t st) {
+    const int64_t chunks = delta_chunks(a.n_rows, a.n_seq);
+    k_delta_prep<T, DK><<<(unsigned)(chunks * a.n_head_k), 64, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
 template <int T, int DK, int W, int KS>
-cudaError_t scan(const DeltaArgs &a, int dv, int sms, cudaStream_t st) {
+cudaError_t scan(const DeltaArgs &a, int dv, bool alone, cudaStream_t st) {
     using F = ScanCfg<DK, W, KS>;
     const int parts = dv / (16 * W);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((int64_t)a.n_seq * a.n_head * parts), 1, 1);
     cfg.blockDim = dim3(F::kThreads);
-    // (one CTA per SM where there are no more: beginning beside the kernel in front of it, two would find room on one SM,
-    // and slow each other down, while others have none)
-    cfg.dynamicSmemBytes = cfg.gridDim.x <= (unsigned)sms ? kAlone : F::kSmem;
+    cfg.dynamicSmemBytes = alone ? kAlone : F::kSmem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -777,15 +807,17 @@ cudaError_t scan(const DeltaArgs &a, int dv, int sms, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, k_delta_scan<T, DK, W, KS>, a, parts);
 }
 
+// By the CTAs of four groups that all rows make when each takes as long as the longest sequence's: up to half the SMs'
+// number, two warps to a group and half the groups to a CTA; up to little more than the SMs', each CTA has an SM to
+// itself (beginning beside the kernel in front, two long ones would find room on one while others have none); then
+// two to an SM.  32 heads of 128, us, in these three forms: one sequence of 2,000 tokens 107, 153, 208, with seven of
+// 200 172, 166, 223, two 197, 170, 224, four of 2,000 to 500 228, 209, 232, three 287, 307, 237; of 64: two 104,
+// 113, 151, three 178, 123, 160, six 275, 228, 192.
 template <int T, int DK>
-cudaError_t go(const DeltaArgs &a, int dv, int sms, cudaStream_t st) {
-    const int64_t chunks = delta_chunks(a.n_rows, a.n_seq);
-    k_delta_prep<T, DK><<<(unsigned)(chunks * a.n_head_k), 64, 0, st>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    // few sequences times heads, up to two small CTAs for every SM: two warps to a group
-    if ((int64_t)a.n_seq * a.n_head * dv / 32 > 2 * sms) return scan<T, DK, 4, 1>(a, dv, sms, st);
-    return scan<T, DK, 2, 2>(a, dv, sms, st);
+cudaError_t walk(const DeltaArgs &a, int dv, int sms, cudaStream_t st) {
+    const int64_t rows = std::min(a.n_rows, (int64_t)a.n_seq * a.max_q), work = rows * a.n_head * dv / 64, one = (int64_t)a.max_q * sms;
+    if (2 * work <= one) return scan<T, DK, 2, 2>(a, dv, true, st);
+    return scan<T, DK, 4, 1>(a, dv, 10 * work <= 11 * one, st);
 }
 
 template <int T, int DK, int W, int KS> cudaError_t allow() {
@@ -806,9 +838,13 @@ cudaError_t delta_chunk_setup() {
     return e == cudaSuccess ? allow_all<PAGED_BF16>() : e;
 }
 
-cudaError_t launch_delta_chunk(const DeltaArgs &a, int dtype, int dim_k, int dim_v, int sms, cudaStream_t st) {
-    if (dtype == PAGED_F16) return dim_k == 64 ? go<PAGED_F16, 64>(a, dim_v, sms, st) : go<PAGED_F16, 128>(a, dim_v, sms, st);
-    return dim_k == 64 ? go<PAGED_BF16, 64>(a, dim_v, sms, st) : go<PAGED_BF16, 128>(a, dim_v, sms, st);
+cudaError_t launch_delta_prep(const DeltaArgs &a, int dtype, int dim_k, cudaStream_t st) {
+    if (dtype == PAGED_F16) return dim_k == 64 ? prep<PAGED_F16, 64>(a, st) : prep<PAGED_F16, 128>(a, st);
+    return dim_k == 64 ? prep<PAGED_BF16, 64>(a, st) : prep<PAGED_BF16, 128>(a, st);
+}
+cudaError_t launch_delta_scan(const DeltaArgs &a, int dtype, int dim_k, int dim_v, int sms, cudaStream_t st) {
+    if (dtype == PAGED_F16) return dim_k == 64 ? walk<PAGED_F16, 64>(a, dim_v, sms, st) : walk<PAGED_F16, 128>(a, dim_v, sms, st);
+    return dim_k == 64 ? walk<PAGED_BF16, 64>(a, dim_v, sms, st) : walk<PAGED_BF16, 128>(a, dim_v, sms, st);
 }
 
 }  // namespace dflash

@@ -195,9 +195,11 @@ extern "C" int delta_rule(const delta_rule_args *g, void *stream) {
         if (!d.chunk) TRY(set_up_chunk(who));
         a.tiles = static_cast<uint8_t *>(g->workspace);
         a.heads = a.tiles + tile_bytes(s, delta_chunks(g->n_rows, b->n_seq), g->n_head_k);
-        e = launch_delta_chunk(a, g->dtype, s->dim_k, s->dim_v, d.sms, st);
+        // (few tokens are a matter of bytes, what is done before the longer ones' walk is not: side by side)
         a.split = 1;
+        e = launch_delta_prep(a, g->dtype, s->dim_k, st);
         if (e == cudaSuccess) e = launch_delta_step(a, g->dtype, s->dim_k, s->dim_v, st);
+        if (e == cudaSuccess) e = launch_delta_scan(a, g->dtype, s->dim_k, s->dim_v, d.sms, st);
     } else {
         e = launch_delta_step(a, g->dtype, s->dim_k, s->dim_v, st);
     }

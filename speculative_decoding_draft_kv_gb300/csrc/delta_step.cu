@@ -64,8 +64,11 @@ k_delta_step(const __grid_constant__ DeltaArgs a) {
     uint32_t bits;
     const DeltaSeq q = delta_seq(a, s, bits);
     if (bits && threadIdx.x == 0 && h == 0 && part == 0) atomicOr(a.err, bits);
-    // (beside the kernel of longer sequences: what waits for this one waits for that too)
-    if (a.split && threadIdx.x == 0 && blockIdx.x == 0) pdl_wait();
+    // (between the kernels of longer sequences: what waits for this one waits for the one in front too)
+    if (a.split) {
+        pdl_trigger();
+        if (threadIdx.x == 0 && blockIdx.x == 0) pdl_wait();
+    }
     if (!q.ok || (a.split && q.n > kDeltaFew)) return;
     const int sub = lane & 7, rg = lane >> 3;          // the lane's part of a row, its row of four
     const int row0 = part * kRows + warp * 4 * J;      // the warp's rows: row0 + 4 j + rg

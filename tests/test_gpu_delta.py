@@ -316,3 +316,15 @@ def test_many_sequences():
     w.slot_out = list(range(2 * n - 1, n - 1, -1))
     w.slot_out[0] = n + 1399
     w.check(D)
+
+
+@pytest.mark.parametrize("n", [1, 5, 40])
+def test_a_pool_past_32_bits(n):
+    """Slots 2^30 floats apart: the last one's byte offset is past 2^33, its element offset past 2^31."""
+    w = DeltaWorld([n, n], slots=4, seed=21)
+    far = torch.empty(3 * (1 << 30) + w.pool[0].numel(), device="cuda")
+    pool = far.as_strided(w.pool.shape, (1 << 30, *w.pool.stride()[1:]))
+    pool.copy_(w.pool)
+    w.pool = pool
+    w.slot_in, w.slot_out = [0, 1], [2, 3]
+    w.check(D)

@@ -216,3 +216,16 @@ def test_long_sequences_give_the_same_bits(dtype, lens, heads):
         want = want or got
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert D.delta_device_error() == 0 and torch.isfinite(o).all()
+
+
+@pytest.mark.parametrize("dim_k", [64, 128])
+@pytest.mark.parametrize("lens", [[300], [300, 20, 9, 12, 40, 1, 0, 33], [20, 9, 300, 8, 150, 300, 1], [40] * 12, [9] * 126 + [70, 33],
+                                  [9] * 127 + [70, 33]])
+def test_shapes_of_a_batch(dim_k, lens):
+    """One long sequence, a few among short ones, all alike, as many as are put in order and one more."""
+    DeltaWorld(lens, heads=8, heads_k=4, dim_k=dim_k, seed=16).check(D)
+
+
+@pytest.mark.parametrize("lens", [[300, 20, 9, 12], [40] * 30, [5, 300]])
+def test_a_bound_far_above_the_lengths(lens):
+    DeltaWorld(lens, heads=16, heads_k=8, seed=17).check(D, max_q=100_000)
