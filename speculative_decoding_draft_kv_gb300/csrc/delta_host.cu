@@ -100,9 +100,9 @@ int check_batch(const char *who, const delta_state *s, const delta_batch *b, int
 
 int64_t up256(int64_t x) { return (x + 255) & ~(int64_t)255; }
 
-// Which kernels serve a batch: token by token alone where no sequence is longer than kDeltaFew, and where states are
+// Which kernels serve a batch: token by token alone where no sequence is longer than kDeltaTokens, and where states are
 // kept behind single tokens.
-bool by_chunks(const delta_batch *b) { return b->max_q > kDeltaFew && !b->save; }
+bool by_chunks(const delta_batch *b) { return b->max_q > kDeltaTokens && !b->save; }
 
 int64_t tile_bytes(const delta_state *s, int64_t chunks, int n_head_k) {
     return up256(chunks * n_head_k * 2 * kDeltaChunk * s->dim_k * 2);
