@@ -63,7 +63,7 @@ typedef struct delta_state {
  *             token, negative: none.  (A drafted block whose tail is rejected goes on from the
  *             state behind its last accepted token.)
  *   max_q     upper bound of the sequences' new tokens, now and at every replay of a captured
- *             call.
+ *             call.  How the work is shared out goes by it: far above the lengths it costs speed.
  * Sequences that have rows in common (bounds that decrease between them, which is reported) may end
  * with anything.
  * A slot that one sequence writes may be read by that sequence, as its slot_in, and by no
@@ -94,7 +94,7 @@ typedef struct delta_batch {
  * two 16-bit parts, 22 bits together.  Keys that are not normalised want beta |k|^2 of at most 2, as the
  * recurrence itself does: beyond, it grows with every token.
  * An infinity or NaN in a token's rows reaches the token's value elements (in v) or all of its head (in the
- * others) from there on, and in a sequence of more than 8 tokens the same elements of up to 31 in front of it.
+ * others) from there on, and in a batch with max_q above 12 the same elements of up to 31 in front of it.
  * A sequence whose row bounds contradict each other (DELTA_ERR_BATCH), or whose slot_in is past the pool
  * (DELTA_ERR_SLOT), is left alone: its rows of o and its slots stay as they were.  A slot past
  * the pool in slot_out or save is not written (DELTA_ERR_SLOT).
