@@ -399,13 +399,13 @@ def paged_attend(cache, batch, q, o, mask="causal", window=0, scale=0.0, tree=No
     token); ``window``: 0 or the length of a sliding window; ``lse``: None or float32
     [rows, n_head].  ``workspace``: a uint8 tensor of :func:`paged_attend_workspace` bytes that no
     other call uses at the same time, or None for one of the call's own from PyTorch's allocator."""
-    a, st = _attend_args(cache, batch, q, o, mask, window, scale, tree, lse, workspace, stream,
-                         lambda n, heads: paged_attend_workspace(cache, batch, heads))
+    a, st, workspace = _attend_args(cache, batch, q, o, mask, window, scale, tree, lse, workspace, stream,
+                                    lambda n, heads: paged_attend_workspace(cache, batch, heads))
     _check(_load().paged_attend(a, st))
 
 
 def _attend_args(cache, batch, q, o, mask, window, scale, tree, lse, workspace, stream, size):
-    """(the call's struct as bytes, stream); size(rows, heads): bytes of workspace."""
+    """(the call's struct as bytes, stream, workspace, to be kept until the call is made); size(rows, heads): its bytes."""
     dev = _one_device(cache, batch)
     dtype, (n, heads, _) = q.dtype, q.shape
     qp, qr, qh = _rows(q, "q", n, heads, cache.head_dim, _half(dtype), dev)
@@ -417,7 +417,7 @@ def _attend_args(cache, batch, q, o, mask, window, scale, tree, lse, workspace, 
     st = _stream(stream, dev)
     workspace = _workspace(workspace, lambda: size(n, heads), st, stream, dev, q.device)
     return _pack_attend(cache.address, batch.address, qp, op, qr, qh, orow, oh, tp, lp, workspace.data_ptr(), workspace.numel(),
-                        n, scale, heads, _TYPES[dtype], MASKS.get(mask, mask), window, 0), st
+                        n, scale, heads, _TYPES[dtype], MASKS.get(mask, mask), window, 0), st, workspace
 
 
 def paged_attend_shared_workspace(cache, batch, prefix, n_rows, n_head) -> int:
@@ -437,8 +437,8 @@ def paged_attend_shared(cache, batch, prefix, q, o, mask="causal", scale=0.0, tr
     ``q_start``: bounds of the rows that have each one, ``kv_len``: their lengths, ``pages``: where they lie; ``max_q``:
     bound of one's rows."""
     _one_device(cache, prefix)
-    a, st = _attend_args(cache, batch, q, o, mask, 0, scale, tree, lse, workspace, stream,
-                         lambda n, heads: paged_attend_shared_workspace(cache, batch, prefix, n, heads))
+    a, st, workspace = _attend_args(cache, batch, q, o, mask, 0, scale, tree, lse, workspace, stream,
+                                    lambda n, heads: paged_attend_shared_workspace(cache, batch, prefix, n, heads))
     _check(_load().paged_attend_shared(a, prefix.address, st))
 
 

@@ -275,3 +275,30 @@ def test_the_same_call_gives_the_same_bits():
         P.paged_attend_shared(*handles, q, o)
         got.append(o.view(torch.int16))
     assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+
+
+def test_a_call_keeps_its_own_workspace_until_it_is_launched(monkeypatch):
+    """Another thread's allocations in front of the launch must not find it free."""
+    s = Shared([(1, 50)] * 33, [(2000, 33)], seed=18)
+    q = s.w.randn(s.w.heads)
+    o = torch.empty_like(q)
+    cache, batch, prefix = s.handles()
+    lib, seen = P._load(), []
+
+    class Watched:
+        def __getattr__(self, name):
+            f = getattr(lib, name)
+            if name.endswith("workspace"):
+                return f
+            return lambda *a: (seen.append(torch.cuda.memory_allocated()), f(*a))[1]
+
+    monkeypatch.setattr(P, "_load", Watched)
+    for call, size in ((lambda: P.paged_attend(cache, batch, q, o), P.paged_attend_workspace(cache, batch, s.w.heads)),
+                       (lambda: P.paged_attend_shared(cache, batch, prefix, q, o),
+                        P.paged_attend_shared_workspace(cache, batch, prefix, s.w.rows, s.w.heads))):
+        before = torch.cuda.memory_allocated()
+        del seen[:]
+        call()
+        assert len(seen) == 1 and seen[0] >= before + size
+    monkeypatch.undo()
+    assert P.paged_device_error() == 0
