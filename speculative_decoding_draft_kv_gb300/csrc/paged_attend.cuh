@@ -606,6 +606,8 @@ k_paged_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                     }
                 }
             }
+            // (the next copy into the stage writes through another proxy: behind the reads still on their way; no cost measured)
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(bar0 + 8 * (S + stg));
         }
