@@ -15,11 +15,11 @@
 // (mma.sync m16n8k16: its accumulators feed the next product without leaving the thread).  A form on tcgen05.mma, with
 // 128 value elements as rows and the left operands in tensor memory, was built too: there a product of 16 steps along K
 // takes some 98 cycles whatever its columns, 32 or 64, and a chunk has 40 of them and three hand-overs to the threads
-// and back, 4,900 cycles for a head's chunk and SM.  It took 552 us for eight prompts, which take 540 here, and
+// and back, 4,900 cycles for a head's chunk and SM.  It took 552 us for eight prompts, which take 533 here, and
 // 1,136 for 48 heads of 14,142 tokens (972).
 //
 // Bound by the walk's chain: a chunk of a head of 128 x 128 takes two warps to a group 1.2 us when they have the SM to
-// themselves, two CTAs with a warp to a group 3.4 us for both, of which the tensor pipe is busy about half.
+// themselves, two CTAs with a warp to a group 3.3 us for both, of which the tensor pipe is busy about half.
 //
 // Precision.  The state, its update and all sums are float32.  Operands are F16 pairs hi + lo, 22 bits together,
 // after powers of two that bring them below 2^15; the state is kept times its own.  R's is by its largest
@@ -368,6 +368,18 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
+// mbar_wait of the copy warp, which has two chunks' time and leaves the issue slots to the warps beside it (eight prompts
+// 540 us without a pause, 536 with 100 ns, 533 with 400)
+__device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity) {
+    const uint64_t t0 = global_ns();
+    for (uint32_t it = 1; it < (1u << 30); ++it) {
+        if (mbar_test(bar, parity)) return true;
+        __nanosleep(400);
+        if ((it & 255u) == 0 && global_ns() - t0 > kWaitNs) return false;
+    }
+    return false;
+}
+
 template <int N> __device__ __forceinline__ float top_of(const float (&x)[N][4]) {
     float m = 0.f;
 #pragma unroll
@@ -456,7 +468,7 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
             int c = 0;
             for (; c < chunks; ++c) {
                 const int k = c % S;
-                if (!mbar_wait(empty + 8 * k, ((uint32_t)(c / S) & 1u) ^ 1u)) {
+                if (!mbar_wait_idle(empty + 8 * k, ((uint32_t)(c / S) & 1u) ^ 1u)) {
                     timed_out();
                     break;
                 }
