@@ -121,12 +121,14 @@ k_delta_prep(const __grid_constant__ DeltaArgs a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int hk = blockIdx.x % a.n_head_k, at = blockIdx.x / a.n_head_k;
     pdl_trigger();
-    // the last sequence whose chunks begin at this one or in front of it
-    int seq = 0, end = a.n_seq;
-    while (end - seq > 1) {
-        const int mid = (seq + end) >> 1;
-        if (chunk_base(a.q_start[mid], mid) <= at) seq = mid;
-        else end = mid;
+    // the last sequence whose chunks begin at this one or in front of it, a lane looking at every 32nd part of what is left
+    int seq = 0;
+    for (int left = a.n_seq; left > 1;) {
+        const int part = (left + 31) >> 5, from = lane * part;
+        const bool before = lane == 0 || (from < left && chunk_base(a.q_start[seq + from], seq + from) <= at);
+        const int last = 31 - __clz((int)__ballot_sync(0xffffffffu, before));
+        seq += last * part;
+        left = min(part, left - last * part);
     }
     uint32_t bits;
     const DeltaSeq q = delta_seq(a, seq, bits);
