@@ -24,7 +24,7 @@ struct DeltaArgs {
     float scale, eps;
     int n_seq, max_q, n_slots, n_head, n_head_k, group;   // group: heads of a key head
     int normalise;
-    int split;                           // sequences of up to kDeltaFew tokens are one kernel's, longer ones the other's
+    int split;                           // sequences of up to kDeltaFew tokens (and unprepared ones) are one kernel's, longer ones the other's
     // chunks of many tokens: what k_delta_prep leaves for k_delta_scan
     uint8_t *tiles;                      // [chunks][n_head_k][K, Q] F16 tiles of 32 rows
     uint8_t *heads;                      // [chunks][n_head] blocks of kDeltaHeadBytes
@@ -58,6 +58,33 @@ __device__ __forceinline__ DeltaSeq delta_seq(const DeltaArgs &a, int s, uint32_
     q.row0 = rows ? (int)r0 : 0;
     q.n = rows ? (int)(r1 - r0) : 0;
     return q;
+}
+
+// Where a sequence's chunks begin among all (see delta_chunks).
+__device__ __forceinline__ int delta_base(int row0, int s) { return row0 / kDeltaChunk + s; }
+
+// The sequence that chunks at .. to are prepared for: the last one whose chunks begin at them or in front of them, as long as bounds
+// do not decrease; -1 where at and to find different ones.  Whole warps, a lane looking at every 32nd part of what is left.
+__device__ __forceinline__ int delta_owner(const DeltaArgs &a, int at, int to) {
+    const int lane = threadIdx.x & 31;
+    int seq = 0;
+    for (int left = a.n_seq; left > 1;) {
+        const int part = (left + 31) >> 5, from = lane * part;
+        const int begin = lane == 0 ? INT32_MIN : from < left ? delta_base(a.q_start[seq + from], seq + from) : INT32_MAX;
+        const int last = 31 - __clz((int)__ballot_sync(0xffffffffu, begin <= at));
+        if (to != at && __any_sync(0xffffffffu, lane > last && begin <= to)) return -1;
+        seq += last * part;
+        left = min(part, left - last * part);
+    }
+    return seq;
+}
+
+// Whether sequence s, in order and of some tokens, has its chunks prepared.  Where bounds decrease (which is reported), the search may
+// find another sequence in its place for some of them: then it goes token by token.  (Found for its first chunk and for its
+// last one, it is found for all between: a lane's answer only ever turns to yes as `at` grows.)
+__device__ __forceinline__ bool delta_prepared(const DeltaArgs &a, int s, const DeltaSeq &q) {
+    const int base = delta_base(q.row0, s);
+    return delta_owner(a, base, base + (q.n - 1) / kDeltaChunk) == s;
 }
 
 cudaError_t delta_chunk_setup();

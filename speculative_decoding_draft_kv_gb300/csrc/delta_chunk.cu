@@ -81,8 +81,6 @@ struct HeadBlock {
 };
 static_assert(sizeof(HeadBlock) == kDeltaHeadBytes, "as the workspace is laid out");
 
-__device__ __forceinline__ int chunk_base(int row0, int s) { return row0 / C + s; }
-
 // the power of two that brings m > 0 (as bits) to [2^12, 2^13), as far as float32 has it and its inverse
 __device__ __forceinline__ float unit_of(uint32_t bits) {
     const int e = (int)(bits >> 23);                   // biased
@@ -121,18 +119,10 @@ k_delta_prep(const __grid_constant__ DeltaArgs a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int hk = blockIdx.x % a.n_head_k, at = blockIdx.x / a.n_head_k;
     pdl_trigger();
-    // the last sequence whose chunks begin at this one or in front of it, a lane looking at every 32nd part of what is left
-    int seq = 0;
-    for (int left = a.n_seq; left > 1;) {
-        const int part = (left + 31) >> 5, from = lane * part;
-        const bool before = lane == 0 || (from < left && chunk_base(a.q_start[seq + from], seq + from) <= at);
-        const int last = 31 - __clz((int)__ballot_sync(0xffffffffu, before));
-        seq += last * part;
-        left = min(part, left - last * part);
-    }
+    const int seq = delta_owner(a, at, at);
     uint32_t bits;
     const DeltaSeq q = delta_seq(a, seq, bits);
-    const int t0 = (at - chunk_base(q.row0, seq)) * C;
+    const int t0 = (at - delta_base(q.row0, seq)) * C;
     if (!q.ok || q.n <= kDeltaFew || t0 < 0 || t0 >= q.n) return;
     const int nv = min(C, q.n - t0);
 
@@ -457,9 +447,15 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
     q.ok = q.ok && q.n > kDeltaFew;                                // the others are k_delta_step's
     pdl_trigger();
     if (!q.ok && blockIdx.x) return;                               // (one waits for the kernel in front, as the one behind counts on)
+    __shared__ bool s_prepared;
+    if (warp == F::kWarps && q.ok) {
+        const bool prepared = delta_prepared(a, s, q);
+        if (lane == 0) s_prepared = prepared;
+    }
     __syncthreads();
+    q.ok = q.ok && s_prepared;                                     // unprepared ones too
     const int chunks = q.ok ? (q.n + C - 1) / C : 0;
-    const int64_t base = chunk_base(q.row0, s);
+    const int64_t base = delta_base(q.row0, s);
     auto timed_out = [&]() { atomicOr(a.err, (uint32_t)DELTA_ERR_WAIT); };
 
     if (warp == F::kWarps) {

@@ -69,7 +69,7 @@ k_delta_step(const __grid_constant__ DeltaArgs a) {
         pdl_trigger();
         if (threadIdx.x == 0 && blockIdx.x == 0) pdl_wait();
     }
-    if (!q.ok || (a.split && q.n > kDeltaFew)) return;
+    if (!q.ok || (a.split && q.n > kDeltaFew && delta_prepared(a, s, q))) return;
     const int sub = lane & 7, rg = lane >> 3;          // the lane's part of a row, its row of four
     const int row0 = part * kRows + warp * 4 * J;      // the warp's rows: row0 + 4 j + rg
     auto place = [&](int slot) {
