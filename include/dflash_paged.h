@@ -264,6 +264,8 @@ int paged_attend_workspace(const paged_cache *cache, const paged_batch *batch, i
  *   workspace   paged_attend_shared_workspace() bytes.
  * A prefix whose bounds contradict each other (see paged_attend; its length may be below its number of rows)
  * is left out, PAGED_ERR_PAGE: its rows get their own part alone.
+ * Beside bounds that decrease, sequences and prefixes whose own ones are right are served all the same; two of
+ * them that have rows in common may end with anything.
  * With paged_append and paged_norm_rope, positions[] counts the prefix.  Errors: EINVAL, ECUDA.
  */
 int paged_attend_shared(const paged_attend_args *args, const paged_batch *prefix, void *stream);

@@ -104,6 +104,7 @@ struct PagedAttendArgs {
     float2 *level_ml;                 // [n_rows][n_head] (max in log2 units, sum)
     int2 *level_items;                // [n_rows][kv heads] of an item's first row: the CTAs with its first and last
                                       // tile; .y negative: not cut, its states are in the arrays above
+    int *level_broken;                // 1 where some sequence (or prefix) contradicts itself, else 0
     const PagedAttendArgs *first;     // kOwn, on the host: the first pass's, whose join goes behind this one
     int sms;
 };

@@ -844,8 +844,18 @@ k_paged_levels(const __grid_constant__ PagedAttendArgs prefix, const __grid_cons
     const PagedAttendArgs &a = level ? own : prefix;
     int64_t item = -1;
     int3 piece = make_int3(0, 0, 0);
+    const int row = first + mine;
+    // whether the row is one of sequence s
+    auto is_of = [&](int s) {
+        const PagedSeq q = paged_seq(a.batch, a.pool.page_shift, s, level == 0);
+        if (!q.ok || q.n > a.max_q || row < q.row0 || row >= q.row0 + q.n) return false;
+        const int tok = row - q.row0, rt = tok / a.tile_tokens;
+        if (q.kv > 0) item = (int64_t)(q.row0 + rt * a.tile_tokens) * kvh + hk;
+        piece.z = (tok - rt * a.tile_tokens) * a.group;
+        return true;
+    };
+    bool found = level >= 2;
     if (level < 2) {
-        const int row = first + mine;
         // the last sequence that begins at the row or in front of it
         int s = 0, end = a.batch.n_seq;
         while (end - s > 1) {
@@ -853,14 +863,13 @@ k_paged_levels(const __grid_constant__ PagedAttendArgs prefix, const __grid_cons
             if (a.batch.q_start[mid] <= row) s = mid;
             else end = mid;
         }
-        const PagedSeq q = paged_seq(a.batch, a.pool.page_shift, s, level == 0);
-        if (q.ok && q.n <= a.max_q && q.kv > 0 && row >= q.row0 && row < q.row0 + q.n) {
-            const int tok = row - q.row0, rt = tok / a.tile_tokens;
-            item = (int64_t)(q.row0 + rt * a.tile_tokens) * kvh + hk;
-            piece.z = (tok - rt * a.tile_tokens) * a.group;
-        }
+        found = is_of(s);
     }
     pdl_wait();
+    // (where bounds decrease the search may miss the row's sequence: one after the other then)
+    if (!found && *a.level_broken)
+        for (int s = 0; s < a.batch.n_seq && !is_of(s); ++s) {
+        }
     if (level < 2) {
         if (item >= 0) {
             const int2 c = a.level_items[item];

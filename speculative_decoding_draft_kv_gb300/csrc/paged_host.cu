@@ -444,9 +444,10 @@ extern "C" int paged_gather(const paged_gather_args *g, void *stream) {
     return e == cudaSuccess ? RING_OK : fail(RING_ECUDA, "%s: launch: %s", who, cudaGetErrorString(e));
 }
 
-// Of each of two passes: the states of its items that are not cut, and where its items' states are.
+// Of each of two passes: the states of its items that are not cut, where its items' states are, and a word.
 static int64_t level_bytes(const paged_cache *c, int64_t n_rows, int n_head) {
-    return up256(n_rows * n_head * c->head_dim * 4) + up256(n_rows * n_head * 8) + up256(n_rows * c->n_head_kv * 8);
+    return up256(n_rows * n_head * c->head_dim * 4) + up256(n_rows * n_head * 8) + up256(n_rows * c->n_head_kv * 8) +
+           up256(4);
 }
 
 extern "C" int paged_attend_workspace(const paged_cache *cache, const paged_batch *batch, int32_t n_head, int64_t *bytes) {
@@ -495,6 +496,8 @@ static int attend_pass(const char *who, const paged_attend_args *g, const paged_
         a.level_ml = reinterpret_cast<float2 *>(ws);
         ws += up256(g->n_rows * g->n_head * 8);
         a.level_items = reinterpret_cast<int2 *>(ws);
+        ws += up256(g->n_rows * g->cache->n_head_kv * 8);
+        a.level_broken = reinterpret_cast<int *>(ws);
     }
     a.max_q = b->max_q;
     a.ctas = p.ctas;

@@ -123,6 +123,10 @@ __device__ __forceinline__ PagedShare paged_share(const PagedAttendArgs &a, int6
             mine = sh.head_units(a) * a.pool.n_head_kv;
             if (!sh.q.ok && blockIdx.x == 0 && warp == 0) atomicOr(a.err, (uint32_t)PAGED_ERR_PAGE);
         }
+        if (a.level != kOnly && blockIdx.x == 0 && warp == 0) {
+            const bool broken = __any_sync(0xffffffffu, !sh.q.ok);
+            if (lane == 0) *a.level_broken = broken;
+        }
         int64_t incl = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -164,7 +168,12 @@ __device__ __forceinline__ PagedShare paged_share(const PagedAttendArgs &a, int6
     }
     if (lane == 31) scratch[warp] = incl;
     if (tid == 0) scratch[WARPS + 1] = -1;
-    __syncthreads();
+    if (a.level != kOnly) {
+        const int broken = __syncthreads_or(!ok);
+        if (blockIdx.x == 0 && tid == 0) *a.level_broken = broken;
+    } else {
+        __syncthreads();
+    }
     int64_t base = 0, total = 0;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
