@@ -165,7 +165,9 @@ k_delta_prep(const __grid_constant__ DeltaArgs a) {
             const uint32_t e = __float_as_uint(sqrtf(ss)) >> 23;
             float down = e == 0u ? 1.f : (e == 255u ? 0x1p-126f : __uint_as_float((254u - min(e, 253u)) << 23));
             if (e == 255u && a.normalise) down = 0.f;
-            norm = down == 0.f ? 1.f : (e == 0u ? norm : norm * __uint_as_float((254u << 23) - __float_as_uint(down)));
+            norm = down == 0.f ? 1.f : norm * __uint_as_float((254u << 23) - __float_as_uint(down));
+            // no length at all: its factor is of no row (1 / sqrt(eps) would count in the bounds of what the row adds), but for 0 / 0
+            if (e == 0u) norm = norm < INFINITY ? 0.f : norm;
             uint8_t *tile = a.tiles + (((int64_t)at * a.n_head_k + hk) * 2 + w) * (C * DK * 2);
             const uint64_t down2 = pk2(down, down);
 #pragma unroll
