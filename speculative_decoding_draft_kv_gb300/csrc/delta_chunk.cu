@@ -672,7 +672,8 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
         // which is below max|r| times T's largest row sum (that is below 2^9 t_unit).
         const float last = hb->s.last;
         sb = fmaf(last, sb, 1024.f * hb->s.w_sum * (__uint_as_float(rtop) * hb->s.t_unit));
-        const float nu = unit_of(__float_as_uint(sb)), ni = inverse_unit(nu);
+        // (and not so large that what U is multiplied by would pass float32, should all that U adds vanish by decays)
+        const float nu = fminf(unit_of(__float_as_uint(sb)), 0x1p127f * inverse_unit(ui)), ni = inverse_unit(nu);
         // o = |q| (exp(G) S q + A u)
         {
             operand(u, hi, lo);
@@ -726,7 +727,8 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
         ready = c + 1 < chunks && mbar_test(full + 8 * ((c + 1) % S), (uint32_t)((c + 1) / S) & 1u);
         // S <- exp(G_last) S + U (exp(G_last - G) |k| K), all times the new unit
         {
-            const float wf = ui * nu, keep = last * (si * nu);
+            // (units far apart: the state has vanished, and their product alone may pass float32)
+            const float wf = ui * nu, step = si * nu, keep = step < INFINITY ? last * step : last * si * nu;
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 const float2 f = *reinterpret_cast<const float2 *>(&hb->s.w[n * 8 + 2 * t]);
