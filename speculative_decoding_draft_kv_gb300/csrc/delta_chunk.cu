@@ -81,10 +81,10 @@ struct HeadBlock {
 };
 static_assert(sizeof(HeadBlock) == kDeltaHeadBytes, "as the workspace is laid out");
 
-// the power of two that brings m > 0 (as bits) to [2^12, 2^13), as far as float32 has it and its inverse
+// the power of two that brings m > 0 (as bits) to [2^12, 2^13), if that is 2^-115 to 2^115
 __device__ __forceinline__ float unit_of(uint32_t bits) {
     const int e = (int)(bits >> 23);                   // biased
-    return bits == 0u || e == 255 ? 1.f : __uint_as_float((uint32_t)min(241, max(13, 254 + 12 - e)) << 23);
+    return bits == 0u || e == 255 ? 1.f : __uint_as_float((uint32_t)min(242, max(12, 254 + 12 - e)) << 23);
 }
 __device__ __forceinline__ float inverse_unit(float u) { return __uint_as_float((254u << 23) - __float_as_uint(u)); }
 
@@ -671,7 +671,8 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
         // The state's next unit: its bound is the old one's decayed and, with |k| below 2 a token, 2 sum(w) max|u|,
         // which is below max|r| times T's largest row sum (that is below 2^9 t_unit).
         const float last = hb->s.last;
-        sb = fmaf(last, sb, 1024.f * hb->s.w_sum * (__uint_as_float(rtop) * hb->s.t_unit));
+        // (The bound may pass float32 where the state does not.)
+        sb = fminf(fmaf(last, sb, 1024.f * hb->s.w_sum * (__uint_as_float(rtop) * hb->s.t_unit)), 3.4e38f);
         // (and not so large that what U is multiplied by would pass float32, should all that U adds vanish by decays)
         const float nu = fminf(unit_of(__float_as_uint(sb)), 0x1p127f * inverse_unit(ui)), ni = inverse_unit(nu);
         // o = |q| (exp(G) S q + A u)

@@ -38,3 +38,10 @@ def test_a_state_that_comes_and_goes(big, shift):
         w.decay[first] = -1e4
         w.v[first:] = w.v[first:].sign() * size
     check_rows(w, D)
+
+
+@pytest.mark.parametrize("n", [5, 40, 300])
+def test_values_near_the_largest(n):
+    """Sums of a chunk's magnitudes pass float32 where the results do not."""
+    w = DeltaWorld([n], dtype=BF16, spread=3e37, seed=3)
+    check_rows(w, D)
