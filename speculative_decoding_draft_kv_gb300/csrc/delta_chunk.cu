@@ -22,14 +22,16 @@
 // themselves, two CTAs with a warp to a group 3.3 us for both, of which the tensor pipe is busy about half.
 //
 // Precision.  The state, its update and all sums are float32.  Operands are F16 pairs hi + lo, 22 bits together,
-// after powers of two that bring them below 2^15; the state is kept times its own.  R's is by its largest
-// value; U's and the state's are by bounds (T's largest row sum, the decays' sum), which may be 2^16 above
-// the values before an F16 pair loses bits, and the state's is set right every eighth chunk.  Keys and queries
+// after powers of two that bring them below 2^15.  Rows of S never meet, so each has units of its own, whatever its neighbours
+// hold (a unit for a warp's 16 rows cost a row 2^-16 of its neighbour all but ten bits; eight prompts 530 us so, 544 now, one
+// prompt 728 and 762): the state is kept times its unit, by a bound that each chunk's sum of exp(G_last - G) |u| moves and that is
+// set right every eighth chunk; R's is by the row's largest of the chunk, and where a token's is 2^10 or more below that it loses
+// bits, ending at 2^-30 of the largest; U's by R's and T's largest row sum.  Keys and queries
 // are one F16 each, after a power of two by the row's norm: exact but for elements below 2^-14 of the norm, which
 // are off by 2^-25 of it at most.  What a product adds up starts at zero and joins the state by one fused
 // multiply-add: tensor-core sums are cut off, not rounded, and hundreds of chunks would add that up.  Decays are
-// exponentials of sums over just the tokens between, so neither a long chunk nor a state that was dropped costs
-// later tokens their precision.
+// exponentials of sums over just the tokens between, so neither a long sequence nor a state that was dropped in front of
+// their chunk costs later tokens their precision.
 #include "delta.h"
 
 #include "ring_internal.h"
@@ -51,12 +53,6 @@ template <int T> __device__ __forceinline__ float from16(uint32_t x) {
 }
 __device__ __forceinline__ float2 half2_floats(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2 *>(&x)); }
 
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    return x;
-}
-
 // Byte offset of 16-byte chunk ch of row r in a tile of 32 rows of F16: runs of 64 columns one behind another, with the
 // 128-byte swizzle, conflict-free for ldmatrix along rows as along columns.
 __device__ __forceinline__ uint32_t tile_at(int r, int ch) { return (uint32_t)((ch >> 3) * C * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)); }
@@ -71,7 +67,7 @@ struct HeadScalars {
     float4 r[C / 2];                                   // of tokens 2i, 2i+1: beta twice, -beta exp(G) |k| twice
     float4 o[C / 2];                                   // |q| twice, |q| exp(G) twice
     float w[C];                                        // exp(G_last - G) |k|
-    float last, t_unit, a_unit, w_sum;                 // exp(G_last); what T and A are to be multiplied by; sum of w
+    float last, t_unit, a_unit, unused;                // exp(G_last); what T and A are to be multiplied by
 };
 // A head's part of a chunk in the workspace, for mma.sync: B operands of T and of A (exp(G_i - G_j) q_i . k_j), a lane's
 // words beside one another (hi, hi, lo, lo).
@@ -86,6 +82,9 @@ __device__ __forceinline__ float unit_of(uint32_t bits) {
     const int e = (int)(bits >> 23);                   // biased
     return bits == 0u || e == 255 ? 1.f : __uint_as_float((uint32_t)min(242, max(12, 254 + 12 - e)) << 23);
 }
+// the same for m of kLeast to infinity
+constexpr float kLeast = 0x1p-103f;
+__device__ __forceinline__ float unit_above(float m) { return __uint_as_float((266u << 23) - (__float_as_uint(m) & 0x7f800000u)); }
 __device__ __forceinline__ float inverse_unit(float u) { return __uint_as_float((254u << 23) - __float_as_uint(u)); }
 
 // x0, x1 as two F16 pairs
@@ -244,7 +243,6 @@ k_delta_prep(const __grid_constant__ DeltaArgs a) {
             all += other;
         }
         const float gone = expf(upto), w = expf(behind) * kn, last = expf(all), bk = beta * kn;
-        const float w_sum = warp_sum(w);
         __syncwarp();
         float amax = fabsf(kn * s_qk[i * 33 + i]);
         am[i * 36 + i] = kn * s_qk[i * 33 + i];
@@ -322,7 +320,7 @@ k_delta_prep(const __grid_constant__ DeltaArgs a) {
         reinterpret_cast<float *>(out->o)[to] = qn;
         reinterpret_cast<float *>(out->o)[to + 2] = qn * gone;
         out->w[i] = w;
-        if (i == 0) *reinterpret_cast<float4 *>(&out->last) = make_float4(last, inverse_unit(tu), inverse_unit(au), w_sum);
+        if (i == 0) *reinterpret_cast<float4 *>(&out->last) = make_float4(last, inverse_unit(tu), inverse_unit(au), 0.f);
     }
 }
 
@@ -374,28 +372,18 @@ __device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity) {
     return false;
 }
 
-template <int N> __device__ __forceinline__ float top_of(const float (&x)[N][4]) {
-    float m = 0.f;
+// A thread has parts of two rows, g and g + 8, the four threads of a quad the whole ones: their largest magnitudes, kLeast
+// at least (NaN is passed over).
+template <int N> __device__ __forceinline__ void row_tops(const float (&x)[N][4], float (&m)[2]) {
+    m[0] = m[1] = kLeast;
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) m = fmaxf(m, fabsf(x[n][e]));  // (NaN is passed over)
-    return m;
-}
-
-// The largest finite magnitude of a warp's values, as bits; m: the largest of this lane's.
-template <int N> __device__ __forceinline__ uint32_t warp_top(const float (&x)[N][4], float m) {
-    uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-    if (top >= 0x7f800000u) {                                      // an infinity: the other rows go by what else there is
-        m = 0.f;
+        for (int i = 0; i < 2; ++i) m[i] = max3(m[i], fabsf(x[n][2 * i]), fabsf(x[n][2 * i + 1]));
 #pragma unroll
-        for (int n = 0; n < N; ++n)
+    for (int d = 1; d < 4; d <<= 1)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (fabsf(x[n][e]) < INFINITY) m = fmaxf(m, fabsf(x[n][e]));
-        top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-    }
-    return top;
+        for (int i = 0; i < 2; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], d));
 }
 
 // Accumulators of 32 columns as an A operand of two steps, in two parts.
@@ -525,13 +513,15 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
     };
     fetch_v(0);
     bool alive = true;
-    // the state times a power of two, and a bound of its magnitudes without that
-    uint32_t stop = warp_top<NT>(st, top_of<NT>(st));
-    float su = unit_of(stop), si = inverse_unit(su), sb = __uint_as_float(stop);
+    // each row times a power of two; what takes that back, and a bound of its magnitudes without it
+    float si[2], sb[2];
+    row_tops<NT>(st, sb);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        scale2(st[n][0], st[n][1], su, su);
-        scale2(st[n][2], st[n][3], su, su);
+    for (int i = 0; i < 2; ++i) {
+        const float su = unit_above(sb[i]);
+        si[i] = inverse_unit(su);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) scale2(st[n][2 * i], st[n][2 * i + 1], su, su);
     }
     bool ready = false;                                            // the chunk was seen to be there while the one before it was worked on
     for (int c = 0; c < chunks; ++c) {
@@ -582,24 +572,24 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
             for (int e = 0; e < 4; e += 2) upk2(add2(pk2(pk[n][e], pk[n][e + 1]), pk2(pl[n][e], pl[n][e + 1])), pk[n][e], pk[n][e + 1]);
         asm volatile("cp.async.wait_all;" ::: "memory");           // this chunk's values
         constexpr int OT = 4 / KS;                                 // token tiles whose outputs are this warp's
-        float ks1 = si;                                            // what the sums are to be multiplied by
+        float ks1[2] = {si[0], si[1]};                             // what the sums are to be multiplied by
         if constexpr (KS == 2) {
             // the partner's half of the sums: of S K^T all, of S Q^T those of the 16 tokens whose outputs are this warp's
-            ks1 = 1.f;
+            ks1[0] = ks1[1] = 1.f;
             float4 *mine = xs + (warp * 2 + (c & 1)) * (F::kXWords / 4);
             const float4 *other = xs + ((warp ^ 1) * 2 + (c & 1)) * (F::kXWords / 4);
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                scale2(pk[n][0], pk[n][1], si, si);
-                scale2(pk[n][2], pk[n][3], si, si);
+                scale2(pk[n][0], pk[n][1], si[0], si[0]);
+                scale2(pk[n][2], pk[n][3], si[1], si[1]);
                 mine[n * 32] = make_float4(pk[n][0], pk[n][1], pk[n][2], pk[n][3]);
             }
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
                 for (int e = 0; e < 4; e += 2) {
-                    scale2(pq[m][e], pq[m][e + 1], si, si);
-                    scale2(pq[2 + m][e], pq[2 + m][e + 1], si, si);
+                    scale2(pq[m][e], pq[m][e + 1], si[e / 2], si[e / 2]);
+                    scale2(pq[2 + m][e], pq[2 + m][e + 1], si[e / 2], si[e / 2]);
                 }
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
@@ -638,28 +628,32 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
             for (int m = 0; m < 2; ++m) {
                 const int n = 2 * np + m;
                 const float4 f = hb->s.r[n * 4 + t];                 // beta, then -beta exp(G) |k| of tokens 8n + 2t, + 1
-                const uint64_t b2 = pk2(f.x, f.y), c2 = mul2(pk2(f.z, f.w), pk2(ks1, ks1));
+                const uint64_t b2 = pk2(f.x, f.y);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
+                    const uint64_t c2 = mul2(pk2(f.z, f.w), pk2(ks1[e], ks1[e]));
                     const uint64_t x = pk2(from16<T>(v[2 * m + e] & 0xffffu), from16<T>(v[2 * m + e] >> 16));
                     upk2(fma2(b2, x, mul2(c2, pk2(pk[n][2 * e], pk[n][2 * e + 1]))), r[n][2 * e], r[n][2 * e + 1]);
                 }
             }
         }
-        // U = R T^T, times R's unit and T's, by which it is below 2^15
+        // U = R T^T, times the row's unit of R and T's, by which it is below 2^15
         float u[4][4] = {};
         uint32_t hi[2][4], lo[2][4];
-        const uint32_t rtop = warp_top<4>(r, top_of<4>(r));
-        const float ru = unit_of(rtop) * 0x1p-7f, ui = inverse_unit(ru) * hb->s.t_unit;
+        float ui[2];
         {
+            float top[2];
+            row_tops<4>(r, top);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float ru = unit_above(top[i]) * 0x1p-7f;
+                ui[i] = inverse_unit(ru) * hb->s.t_unit;
+#pragma unroll
+                for (int n = 0; n < 4; ++n) scale2(r[n][2 * i], r[n][2 * i + 1], ru, ru);
+            }
             uint4 f[kBlocks];
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b) f[b] = hb->t[b][lane];
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                scale2(r[n][0], r[n][1], ru, ru);
-                scale2(r[n][2], r[n][3], ru, ru);
-            }
             operand(r, hi, lo);
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b) mma16816(u[block_n(b)], hi[block_k(b)], f[b].x, f[b].y);
@@ -668,13 +662,22 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b) mma16816(u[block_n(b)], hi[block_k(b)], f[b].z, f[b].w);
         }
-        // The state's next unit: its bound is the old one's decayed and, with |k| below 2 a token, 2 sum(w) max|u|,
-        // which is below max|r| times T's largest row sum (that is below 2^9 t_unit).
+        // The rows' next units: a row's bound is the old one's decayed and, with |k| below 2 a token, 2 sum(w |u|).  (It
+        // may pass float32 where the state does not.)
         const float last = hb->s.last;
-        // (The bound may pass float32 where the state does not.)
-        sb = fminf(fmaf(last, sb, 1024.f * hb->s.w_sum * (__uint_as_float(rtop) * hb->s.t_unit)), 3.4e38f);
-        // (and not so large that what U is multiplied by would pass float32, should all that U adds vanish by decays)
-        const float nu = fminf(unit_of(__float_as_uint(sb)), 0x1p127f * inverse_unit(ui)), ni = inverse_unit(nu);
+        float nu[2] = {};
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const float2 f = *reinterpret_cast<const float2 *>(&hb->s.w[n * 8 + 2 * t]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) nu[i] = fmaf(f.x, fabsf(u[n][2 * i]), fmaf(f.y, fabsf(u[n][2 * i + 1]), nu[i]));
+        }
+        float more[2];
+        auto round = [&](int d) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) more[i] = __shfl_xor_sync(0xffffffffu, nu[i], d);
+        };
+        round(1);
         // o = |q| (exp(G) S q + A u)
         {
             operand(u, hi, lo);
@@ -697,19 +700,30 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
                 product(ks, lo, false);
                 product(ks, hi, true);
             }
-            const float back = ui * hb->s.a_unit;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) nu[i] += more[i];
+            round(2);
+            const float back[2] = {ui[0] * hb->s.a_unit, ui[1] * hb->s.a_unit};
             // through shared memory into rows
             uint32_t o16[OT][2];
 #pragma unroll
             for (int m = 0; m < OT; ++m) {
                 const float4 w = hb->s.o[(kp * OT + m) * 4 + t];
-                const uint64_t fa = mul2(pk2(w.x, w.y), pk2(back, back)), fs = mul2(pk2(w.z, w.w), pk2(ks1, ks1));
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
+                    const uint64_t fa = mul2(pk2(w.x, w.y), pk2(back[e], back[e])), fs = mul2(pk2(w.z, w.w), pk2(ks1[e], ks1[e]));
                     float y0, y1;
                     upk2(fma2(fa, pk2(x[m][2 * e], x[m][2 * e + 1]), mul2(fs, pk2(pq[m][2 * e], pq[m][2 * e + 1]))), y0, y1);
                     o16[m][e] = T == PAGED_F16 ? pack_half2(y0, y1) : pack_bf162(y0, y1);
                 }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                nu[i] += more[i];
+                sb[i] = fminf(fmaf(last, sb[i], 2.f * (ui[i] * nu[i])), 3.4e38f);
+                // (and not so small that what U is multiplied by would pass float32, should all that U adds vanish by decays)
+                sb[i] = max3(sb[i], 0x1p-114f * ui[i], kLeast);
+                nu[i] = unit_above(sb[i]);
             }
 #pragma unroll
             for (int m = 0; m < OT; ++m) stsm_x2_t(o0 + v_at(m * 8 + (lane & 7), (lane >> 3) & 1), o16[m][0], o16[m][1]);
@@ -728,15 +742,24 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
         ready = c + 1 < chunks && mbar_test(full + 8 * ((c + 1) % S), (uint32_t)((c + 1) / S) & 1u);
         // S <- exp(G_last) S + U (exp(G_last - G) |k| K), all times the new unit
         {
-            // (units far apart: the state has vanished, and their product alone may pass float32)
-            const float wf = ui * nu, step = si * nu, keep = step < INFINITY ? last * step : last * si * nu;
+            float wf[2], keep[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                // (units far apart: the row has vanished, and their product alone may pass float32)
+                const float step = si[i] * nu[i];
+                keep[i] = step < INFINITY ? last * step : last * si[i] * nu[i];
+                wf[i] = ui[i] * nu[i];
+                si[i] = inverse_unit(nu[i]);
+            }
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 const float2 f = *reinterpret_cast<const float2 *>(&hb->s.w[n * 8 + 2 * t]);
-                float f0, f1;
-                upk2(mul2(pk2(f.x, f.y), pk2(wf, wf)), f0, f1);
-                scale2(u[n][0], u[n][1], f0, f1);
-                scale2(u[n][2], u[n][3], f0, f1);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float f0, f1;
+                    upk2(mul2(pk2(f.x, f.y), pk2(wf[i], wf[i])), f0, f1);
+                    scale2(u[n][2 * i], u[n][2 * i + 1], f0, f1);
+                }
             }
             operand(u, hi, lo);
             // four key tiles at a time, their operands fetched ahead
@@ -751,7 +774,7 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
                     }
             };
             fetch_k(0);
-            const uint64_t keep2 = pk2(keep, keep);
+            const uint64_t keep2[2] = {pk2(keep[0], keep[0]), pk2(keep[1], keep[1])};
 #pragma unroll
             for (int n4 = 0; n4 < NT / 4; ++n4) {
                 if (n4 + 1 < NT / 4) fetch_k(n4 + 1);
@@ -768,7 +791,7 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
 #pragma unroll
                     for (int e = 0; e < 4; e += 2) {
                         float (&y)[4] = st[4 * n4 + m];
-                        upk2(fma2(keep2, pk2(y[e], y[e + 1]), pk2(x[m][e], x[m][e + 1])), y[e], y[e + 1]);
+                        upk2(fma2(keep2[e / 2], pk2(y[e], y[e + 1]), pk2(x[m][e], x[m][e + 1])), y[e], y[e + 1]);
                     }
             }
         }
@@ -777,9 +800,11 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(empty + 8 * k);
-        su = nu;
-        si = ni;
-        if ((c & 7) == 7) sb = __uint_as_float(warp_top<NT>(st, top_of<NT>(st))) * si;
+        if ((c & 7) == 7) {
+            row_tops<NT>(st, sb);
+            sb[0] *= si[0];
+            sb[1] *= si[1];
+        }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     const int out = a.slot_out[s];
@@ -791,8 +816,8 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
     float *dst = place(out);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        *reinterpret_cast<float2 *>(dst + n * 8) = make_float2(st[n][0] * si, st[n][1] * si);
-        *reinterpret_cast<float2 *>(dst + 8 * DK + n * 8) = make_float2(st[n][2] * si, st[n][3] * si);
+        *reinterpret_cast<float2 *>(dst + n * 8) = make_float2(st[n][0] * si[0], st[n][1] * si[0]);
+        *reinterpret_cast<float2 *>(dst + 8 * DK + n * 8) = make_float2(st[n][2] * si[1], st[n][3] * si[1]);
     }
 }
 
