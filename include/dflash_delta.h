@@ -90,9 +90,16 @@ typedef struct delta_batch {
  *   n_head   of the state pool; a multiple of n_head_k.
  *   workspace   device memory of delta_rule_workspace() bytes, 256-byte aligned (NULL where
  *               that is 0); its contents before and after the call mean nothing.
- * States, sums and norms are float32; products that run on the tensor cores take their operands as
- * two 16-bit parts, 22 bits together.  Keys that are not normalised want beta |k|^2 of at most 2, as the
- * recurrence itself does: beyond, it grows with every token.
+ * States, sums and norms are float32.  A batch with max_q up to 12, or with `save`, goes token by token in float32.  In others
+ * sequences of more than 8 tokens go 32 tokens at a time through the tensor cores, whose operands are F16:
+ *   - keys and queries one each, after a power of two by their norm: exact but for elements below 2^-14 of it, off by up to 2^-25;
+ *     one whose square sum is 0 in float32 counts as zero;
+ *   - states, updates u and what weighs tokens against one another two each, 22 bits together, in units that go by the value
+ *     element, whatever its neighbours hold.  One unit serves its 32 updates beta (v - S k): those 2^10 and more below the largest
+ *     lose bits, which end at 2^-30 of that;
+ *   - for BF16 outputs the state's first part alone in S q, 11 bits: beside its own rounding an output is off by up to
+ *     2^-11 exp(G) |S| |q| then, S the value element's weights in front of the 32 tokens, G the log decays since.
+ * Keys that are not normalised want beta |k|^2 of at most 2, as the recurrence itself does: beyond, it grows with every token.
  * An infinity or NaN in a token's rows reaches the token's value elements (in v) or all of its head (in the
  * others) from there on, and in a batch with max_q above 12 the same elements of up to 31 in front of it.
  * A sequence whose row bounds contradict each other (DELTA_ERR_BATCH), or whose slot_in is past the pool

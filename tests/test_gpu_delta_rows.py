@@ -1,4 +1,5 @@
-"""delta_rule's value elements are held to a bound one by one: neighbours of far larger magnitude, tokens that stand out."""
+"""delta_rule's value elements are held to a bound one by one: neighbours of far larger magnitude, tokens that stand out, thousands of tokens,
+and the float32 of batches that go token by token."""
 
 import pytest
 import torch
@@ -40,4 +41,29 @@ def test_small_value_elements_over_thousands_of_tokens(dtype, rate):
 def test_tokens_that_stand_out(dtype, n):
     w = DeltaWorld([n, n], dtype=dtype, seed=5)
     w.v[20:2 * n:32] *= 2.0 ** 10
+    check_rows(w, D)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("lens,save", [([1, 1, 1], False), ([8, 5, 3], False), ([12, 10, 1], False), ([9, 4, 40], True)])
+def test_token_by_token(lens, save, dtype):
+    n = len(lens)
+    w = DeltaWorld(lens, dtype=dtype, seed=6, slots=2 * n + sum(lens) + 1)
+    if save:
+        w.save = [2 * n + r for r in range(w.total)]
+    check_rows(w, D)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_outputs_that_cancel(dtype):
+    """Queries along which the state has next to nothing: a token's outputs go by float32's rounding, not by the output's type."""
+    w = DeltaWorld([6, 6], heads=2, heads_k=2, dtype=dtype, seed=7)
+    for s in range(2):
+        # states of one direction, queries at right angles to it
+        d = torch.nn.functional.normalize(torch.randn(2, w.dim_k, device="cuda", generator=w.g), dim=-1)
+        w.pool[s] = torch.randn(2, w.dim_v, 1, device="cuda", generator=w.g) * d[:, None] * 10
+        r = slice(6 * s, 6 * s + 6)
+        q = w.q[r].float()
+        w.q[r] = (q - (q * d).sum(-1, keepdim=True) * d).to(dtype)
+    w.v *= 2.0 ** -10
     check_rows(w, D)
