@@ -36,6 +36,22 @@ def test_small_value_elements_over_thousands_of_tokens(dtype, rate):
     check_rows(uneven(DeltaWorld([3001, 2050], heads=2, heads_k=1, dtype=dtype, seed=2, rate=rate), 3), D)
 
 
+@pytest.mark.parametrize("rate", [1e-4, 0.1])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("lens,heads", [([5000, 33], 2), ([2500] * 6, 48)])
+def test_thousands_of_tokens(lens, heads, dtype, rate):
+    check_rows(DeltaWorld(lens, heads=heads, heads_k=heads // 2, dtype=dtype, seed=3, rate=rate), D)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_the_same_keys_over_thousands_of_tokens(dtype):
+    """Eight keys in turn: what is rounded off in one direction comes again."""
+    n = 2000
+    w = DeltaWorld([n], heads=2, heads_k=1, dtype=dtype, seed=4, rate=1e-4)
+    w.k[:n] = w.k[:8].repeat(n // 8, 1, 1)
+    check_rows(w, D)
+
+
 @pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("n", [40, 400])
 def test_tokens_that_stand_out(dtype, n):
