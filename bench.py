@@ -44,18 +44,18 @@ FALLBACK_BF16_TFLOPS = 1900.0
 # from one ncu capture, keyed by workload; valid only for the kernel code it was taken on
 # (kernel = _code_hash of attn_kernels.cu: sha256[:16] without comments and whitespace).
 NCU_TRAFFIC = {
-    "steady_decode_cap4096_s1_l5": {"bytes": 33_856_128, "kernel": "2ee0f6a3f6510f19",
+    "steady_decode_cap4096_s1_l5": {"bytes": 33_742_720, "kernel": "2cccf3c3703f0551",
                                     "source": "profiles/attend_cluster_steady_decode_cap4096_s1_l5.md"},
-    # captured on 4 of the 16 sequences (538,202,368 B read + 14,991,872 B written per
+    # captured on 4 of the 16 sequences (538,202,368 B read + 15,143,936 B written per
     # launch) and scaled by the sequences a launch processes: every sequence's visible rows
     # are read once, so the traffic grows in proportion
-    "large_ring_cap32768_s16_l5": {"bytes": 4 * (538_202_368 + 14_991_872), "kernel": "2ee0f6a3f6510f19",
+    "large_ring_cap32768_s16_l5": {"bytes": 4 * (538_202_368 + 15_143_936), "kernel": "2cccf3c3703f0551",
                                    "source": "profiles/attend_plain_large_cap32768_s4_l5.md"},
 }
 # dram__bytes_read.sum + dram__bytes_write.sum per launch of the producer kernels, keyed as
 # above (kernel = _code_hash of produce_kernels.cu or produce_tc.cu)
 PRODUCE_TRAFFIC = {
-    "steady_decode_cap4096_s1_l5": {"bytes": 84_903_552, "kernel": "1117b6f1d0ffc179",
+    "steady_decode_cap4096_s1_l5": {"bytes": 84_884_608, "kernel": "bd4aa5b08c994edb",
                                     "source": "profiles/produce_steady_decode_cap4096_s1_l5.md"},
     # the tensor-core kernel (produce_tc.cu) on the legacy recompute's 4096 rows
     "steady_decode_cap4096_s1_l5_legacy": {"bytes": 181_065_984, "kernel": "c446e1838298dba4",

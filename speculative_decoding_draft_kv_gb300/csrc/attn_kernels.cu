@@ -750,6 +750,8 @@ k_attend(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUten
                     }
                 }
             }
+            // (the next copy into the stage writes through another proxy: behind the reads still on their way)
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(release);
         };

@@ -294,6 +294,8 @@ k_produce(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
             };
             if (two_blocks) mma_stage(std::integral_constant<int, 2>{});
             else mma_stage(std::integral_constant<int, 1>{});
+            // (the next copy into the stage writes through another proxy: behind the reads still on their way)
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(bar0 + 8 * (kPStages + stg));
         }

@@ -473,6 +473,8 @@ k_attend_step(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     mma16816(oacc[dp * 2 + 1], pa, b2, b3);
                 }
             }
+            // (the next copy into the stage writes through another proxy: behind the reads still on their way)
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(bar0 + 8 * (kStages + stg));
         }
