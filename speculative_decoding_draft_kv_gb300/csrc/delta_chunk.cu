@@ -729,9 +729,8 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
             for (int m = 0; m < OT; ++m) stsm_x2_t(o0 + v_at(m * 8 + (lane & 7), (lane >> 3) & 1), o16[m][0], o16[m][1]);
             __syncwarp();
 #pragma unroll
-            for (int e = 0; e < (OT + 1) / 2; ++e) {
+            for (int e = 0; e < OT / 2; ++e) {
                 const int row = (lane >> 1) + 16 * e, piece = lane & 1, token = kp * OT * 8 + row;
-                if (OT == 1 && lane >= 16) break;
                 uint4 y;
                 asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w) : "r"(o0 + v_at(row, piece)) : "memory");
                 if (token < nv)
