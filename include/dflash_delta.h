@@ -101,7 +101,8 @@ typedef struct delta_batch {
  *     2^-11 exp(G) |S| |q| then, S the value element's weights in front of the 32 tokens, G the log decays since.
  * Keys that are not normalised want beta |k|^2 of at most 2, as the recurrence itself does: beyond, it grows with every token.
  * An infinity or NaN in a token's rows reaches the token's value elements (in v) or all of its head (in the
- * others) from there on, and in a batch with max_q above 12 the same elements of up to 31 in front of it.
+ * others) from there on, and in a batch with max_q above 12 the same elements of up to 31 in front of it, as
+ * NaN: what is a number there is right.
  * A sequence whose row bounds contradict each other (DELTA_ERR_BATCH), or whose slot_in is past the pool
  * (DELTA_ERR_SLOT), is left alone: its rows of o and its slots stay as they were.  A slot past
  * the pool in slot_out or save is not written (DELTA_ERR_SLOT).

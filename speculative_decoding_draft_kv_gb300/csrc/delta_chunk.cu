@@ -646,8 +646,9 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
             row_tops<4>(r, top);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const float ru = unit_above(top[i]) * 0x1p-7f;
-                ui[i] = inverse_unit(ru) * hb->s.t_unit;
+                const float unit = unit_above(top[i]) * 0x1p-7f;
+                ui[i] = inverse_unit(unit) * hb->s.t_unit;
+                const float ru = fmaf(top[i], 0.f, unit);          // an infinity has no unit: NaN for all its row's tokens
 #pragma unroll
                 for (int n = 0; n < 4; ++n) scale2(r[n][2 * i], r[n][2 * i + 1], ru, ru);
             }
