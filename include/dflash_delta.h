@@ -61,7 +61,9 @@ typedef struct delta_state {
  *             has its state copied.
  *   save      NULL, or device int32 [n_rows]: the slot that gets the state behind that row's
  *             token, negative: none.  (A drafted block whose tail is rejected goes on from the
- *             state behind its last accepted token.)
+ *             state behind its last accepted token.)  A call with it goes token by token, whatever the lengths and even
+ *             where no state is kept (32 heads of 128 x 128, 16,381 tokens: 12.5 ms, 0.76 without): prompts
+ *             want a call of their own.
  *   max_q     upper bound of the sequences' new tokens, now and at every replay of a captured
  *             call.  How the work is shared out goes by it: far above the lengths it costs speed.
  * Sequences that have rows in common (bounds that decrease between them, which is reported) may end

@@ -36,9 +36,9 @@ constexpr int kDeltaHeadBytes = 2 * 6 * 32 * 16 + 2 * 16 * 16 + 32 * 4 + 16;
 inline int64_t delta_chunks(int64_t n_rows, int n_seq) { return n_rows / kDeltaChunk + n_seq; }
 
 // A batch of up to kDeltaTokens tokens a sequence goes token by token: above it chunks are faster (32 sequences of 32
-// heads of 128 x 128, us: 9 tokens each 57 by tokens and 66 by chunks, 12 tokens 68 and 68, 16 tokens 86 and 68; heads
-// of 64 x 64: 23 and 31, 25 and 31, 31 and 31).  In a batch with longer ones, whose chunks are to be prepared and
-// walked anyway, only up to kDeltaFew do (32 sequences of 1 to 16 tokens, us: 58 with 8, 62 with 10, 63 with 12).
+// heads of 128 x 128, us: 9 tokens each 57 by tokens and 68 by chunks, 12 tokens 68 and 66, 16 tokens 85 and 67; heads
+// of 64 x 64: 21 and 29, 23 and 29, 29 and 29).  In a batch with longer ones, whose chunks are to be prepared and
+// walked anyway, only up to kDeltaFew do (32 sequences of 1 to 16 tokens, us: 58 with 8, 60 with 10 and with 12).
 constexpr int kDeltaTokens = 12;
 constexpr int kDeltaFew = 8;
 constexpr float kDeltaLeast = -1e4f;     // log decays below it count as it: exp() of both is 0

@@ -15,10 +15,11 @@
 // (mma.sync m16n8k16: its accumulators feed the next product without leaving the thread).  A form on tcgen05.mma, with
 // 128 value elements as rows and the left operands in tensor memory, was built too: there a product of 16 steps along K
 // takes some 98 cycles whatever its columns, 32 or 64, and a chunk has 40 of them and three hand-overs to the threads
-// and back, 4,900 cycles for a head's chunk and SM.  It took 552 us for eight prompts, which take 533 here, and
-// 1,136 for 48 heads of 14,142 tokens (972).
+// and back, 4,900 cycles for a head's chunk and SM.  It took 552 us for eight prompts and 1,136 for 48 heads of
+// 14,142 tokens, which took 533 and 972 here then (546 and 950 now).  Chunks of more tokens, which would spread a product's
+// time over more columns, were not tried.
 //
-// Bound by the walk's chain: a chunk of a head of 128 x 128 takes two warps to a group 1.2 us when they have the SM to
+// Bound by the walk's chain: a chunk of a head of 128 x 128 takes two warps to a group 1.3 us when they have the SM to
 // themselves, two CTAs with a warp to a group 3.3 us for both, of which the tensor pipe is busy about half.
 //
 // Precision.  The state, its update and all sums are float32.  Operands are F16 pairs hi + lo, 22 bits together,
@@ -361,7 +362,7 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
 }
 
 // mbar_wait of the copy warp, which has two chunks' time and leaves the issue slots to the warps beside it (eight prompts
-// 540 us without a pause, 536 with 100 ns, 533 with 400)
+// 567 us without a pause, 554 with 100 ns, 546 with 400)
 __device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity) {
     const uint64_t t0 = global_ns();
     for (uint32_t it = 1; it < (1u << 30); ++it) {
@@ -408,7 +409,7 @@ k_delta_scan(const __grid_constant__ DeltaArgs a, int parts) {
     const int part = blockIdx.x % parts, sh = blockIdx.x / parts, h = sh % a.n_head;
     int s = sh / a.n_head;
     // The longest sequences first, so that none begins when the others end (eight prompts of 239 to 4,096 tokens by rising
-    // length, us: 652 as they come, 552 so; falling 542 and 551).  Each CTA counts the longer ones, as many
+    // length, us: 645 as they come, 543 so; falling 541 and 544).  Each CTA counts the longer ones, as many
     // sequences as it has threads for; with more of them the last ones weigh less.
     if (a.n_seq > 1 && a.n_seq <= kSorted) {
         __shared__ int s_len[kSorted], s_seq;
@@ -850,9 +851,9 @@ cudaError_t scan(const DeltaArgs &a, int dv, bool alone, cudaStream_t st) {
 // By the CTAs of four groups that all rows make when each takes as long as the longest sequence's: up to half the SMs'
 // number, two warps to a group and half the groups to a CTA; up to little more than the SMs', each CTA has an SM to
 // itself (beginning beside the kernel in front, two long ones would find room on one while others have none); then
-// two to an SM.  32 heads of 128, us, in these three forms: one sequence of 2,000 tokens 107, 153, 208, with seven of
-// 200 172, 166, 223, two 197, 170, 224, four of 2,000 to 500 228, 209, 232, three 287, 307, 237; of 64: two 104,
-// 113, 151, three 178, 123, 160, six 275, 228, 192.
+// two to an SM.  32 heads of 128, us, in these three forms: one sequence of 2,000 tokens 101, 138, 199, with seven of
+// 200 172, 152, 214, two 199, 155, 216, four of 2,000 to 500 231, 194, 223, three 295, 286, 228; of 64: two 97,
+// 105, 120, three 176, 115, 155, six 275, 222, 186.
 template <int T, int DK>
 cudaError_t walk(const DeltaArgs &a, int dv, int sms, cudaStream_t st) {
     const int64_t rows = std::min(a.n_rows, (int64_t)a.n_seq * a.max_q), work = rows * a.n_head * dv / 64, one = (int64_t)a.max_q * sms;
