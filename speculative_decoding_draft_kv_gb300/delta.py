@@ -90,7 +90,7 @@ class DeltaBatch:
     """A ragged batch of new tokens (the C struct ``delta_batch``).  ``q_start``: int32
     [n_seq + 1], ``slot_in``, ``slot_out``: int32 [n_seq], ``save``: None or int32 [rows], on the
     device; ``max_q``: host bound of a sequence's new tokens now and at every replay of a captured
-    call."""
+    call.  A batch with ``save`` goes token by token, whatever its lengths: prompts want a batch of their own."""
 
     def __init__(self, q_start, slot_in, slot_out, max_q, save=None):
         self.device = _device(q_start, "q_start")
